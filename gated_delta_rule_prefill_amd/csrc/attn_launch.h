@@ -1,0 +1,59 @@
+// Host-side launch interface between the C ABI layer (gdn_api.cpp) and the kernels of the
+// softmax-attention layers (paged.hip, paged_decode.hip, latent_decode.hip,
+// latent_prefill.hip). Arguments arrive here already validated.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "key_split.h"
+
+namespace gdn {
+
+struct PlanArgs {
+    const int32_t *ctx_lens, *new_lens;
+    int n, block_size;
+    int32_t* block_table;
+    int max_blocks;
+    const int32_t* free_blocks;
+    int n_free, max_tokens;
+    int32_t *cu_seqlens, *seq_lens;
+    int64_t* slot_map;
+    int32_t* positions;
+    int32_t* counts;
+};
+hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream);
+
+// Rows of two sources written to cache slots. All sizes in 16-byte pieces.
+//   split caches (b_cache != null): source a [tokens][heads][row] to a_cache
+//     [n_blocks][heads][block_size][row], b to b_cache likewise
+//   one cache (b_cache == null, heads == 1): a_cache row = a's row followed by b's
+struct AppendArgs {
+    const void *a, *b;
+    int64_t a_stride, b_stride;
+    const int64_t* slot_map;
+    int tokens, heads, a_row, b_row;
+    void *a_cache, *b_cache;
+    int n_blocks, block_size;
+};
+hipError_t launch_append(const AppendArgs& a, hipStream_t stream);
+
+// Paged decode: rows of one unit are the n_pos x (num_heads / kv_heads) query rows that share
+// a key/value head, cut into row tiles of 16 * rt rows.
+struct PagedDecodeArgs {
+    int dtype, H, kv_heads, d, n_pos, max_blocks, n_blocks;
+    float scale;
+    const void *q, *k_cache, *v_cache;
+    const int32_t* block_table;
+    FastDiv block;       // by the page size
+    SplitShape split;    // units = kv_heads * row_tiles
+    int group, rows, rt, row_tiles, n_wg;
+    void* o;
+    float* part_o;       // [2 n_wg][16 rt][d]
+    float* part_ml;      // [2 n_wg][16 rt][2]
+};
+// Row tiles, workgroups and workspace bytes of a call (fills rt, row_tiles, n_wg, split.units).
+size_t paged_decode_layout(PagedDecodeArgs* a, void* ws);
+hipError_t launch_paged_decode(const PagedDecodeArgs& a, hipStream_t stream);
+
+}  // namespace gdn

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "../../include/gdn.h"
+#include "attn_launch.h"
 #include "gdn_launch.h"
 
 namespace {
@@ -330,6 +331,118 @@ int decode_run(const gdn_dims_t* dims, const void* q, const void* k, const void*
     return launch_status(gdn::launch_decode(a, static_cast<hipStream_t>(stream)), what);
 }
 
+// ------------------------------------------------- paged softmax attention: shared checks
+
+bool paged_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
+
+// A cache of n_blocks pages of block_size rows per head. Rows are numbered in 32 bits inside
+// the kernels (byte offsets in 64).
+int check_cache(int32_t dtype, int32_t kv_heads, int32_t n_blocks, int32_t block_size) {
+    if (dtype != GDN_DTYPE_F32 && dtype != GDN_DTYPE_BF16)
+        return fail(GDN_ERR_UNSUPPORTED, "dtype must be 0 (fp32) or 1 (bf16), got %d", dtype);
+    if (kv_heads < 1 || n_blocks < 1 || block_size < 1)
+        return fail(GDN_ERR_SHAPE, "heads, n_blocks and block_size must be >= 1 (got %d, %d, %d)",
+                    kv_heads, n_blocks, block_size);
+    const uint64_t slots = (uint64_t)n_blocks * (uint32_t)block_size;
+    if (slots > 0x7fffffffull || slots * (uint32_t)kv_heads > 0xfffffffeull)
+        return fail(GDN_ERR_UNSUPPORTED, "a cache holds at most 2^31 - 1 tokens and 2^32 - 2 rows "
+                                         "(got %d blocks of %d tokens, %d heads)", n_blocks,
+                    block_size, kv_heads);
+    return GDN_OK;
+}
+
+// The keys that a block table row can address are counted in 32 bits.
+int check_table(int32_t max_blocks, int32_t block_size) {
+    if (max_blocks < 1) return fail(GDN_ERR_SHAPE, "max_blocks must be >= 1 (got %d)", max_blocks);
+    if ((int64_t)max_blocks * block_size > 0x3fffffff)
+        return fail(GDN_ERR_UNSUPPORTED, "a block table row addresses at most 2^30 - 1 tokens "
+                                         "(got %d blocks of %d)", max_blocks, block_size);
+    return GDN_OK;
+}
+
+// Source rows of an append: `width` elements each, `stride` elements apart, 16-byte aligned.
+int check_rows(int32_t dtype, int32_t tokens, int64_t stride, int64_t width, const char* name) {
+    if (tokens < 0) return fail(GDN_ERR_SHAPE, "tokens must be >= 0 (got %d)", tokens);
+    if (width > (1 << 24))
+        return fail(GDN_ERR_UNSUPPORTED, "%s: rows of %lld elements", name, (long long)width);
+    if (tokens == 0) return GDN_OK;
+    if (stride < width)
+        return fail(GDN_ERR_SHAPE, "%s: row stride %lld is smaller than the row (%lld)", name,
+                    (long long)stride, (long long)width);
+    if (stride % (dtype == GDN_DTYPE_BF16 ? 8 : 4) != 0)
+        return fail(GDN_ERR_ALIGN, "%s: row stride %lld is not a multiple of 16 bytes", name,
+                    (long long)stride);
+    return GDN_OK;
+}
+
+int check_batch(int32_t batch, int32_t n_pos) {
+    if (batch < 0) return fail(GDN_ERR_SHAPE, "batch must be >= 0 (got %d)", batch);
+    if (n_pos < 1 || n_pos > GDN_SPEC_MAX_POS)
+        return fail(GDN_ERR_UNSUPPORTED, "n_pos must be in [1, %d] (got %d)", GDN_SPEC_MAX_POS,
+                    n_pos);
+    return GDN_OK;
+}
+
+int check_paged_dims(const gdn_paged_dims_t* d, int32_t batch, int32_t n_pos) {
+    if (d == nullptr) return fail(GDN_ERR_NULL, "dims is NULL");
+    if (d->num_heads < 1 || d->num_kv_heads < 1 || d->num_heads % d->num_kv_heads != 0)
+        return fail(GDN_ERR_SHAPE, "num_heads (%d) must be a positive multiple of num_kv_heads "
+                                   "(%d)", d->num_heads, d->num_kv_heads);
+    if (d->num_heads > GDN_ATTN_MAX_HEADS)
+        return fail(GDN_ERR_UNSUPPORTED, "num_heads must be <= %d (got %d)", GDN_ATTN_MAX_HEADS,
+                    d->num_heads);
+    if (!paged_dim_ok(d->d))
+        return fail(GDN_ERR_UNSUPPORTED, "d must be 64, 128 or 256 (got %d)", d->d);
+    if (d->dtype != GDN_DTYPE_F32 && d->dtype != GDN_DTYPE_BF16)
+        return fail(GDN_ERR_UNSUPPORTED, "dtype must be 0 (fp32) or 1 (bf16), got %d", d->dtype);
+    return check_batch(batch, n_pos);
+}
+
+gdn::PagedDecodeArgs paged_args(const gdn_paged_dims_t* d, int32_t batch, int32_t n_pos) {
+    gdn::PagedDecodeArgs a = {};
+    a.dtype = d->dtype;
+    a.H = d->num_heads;
+    a.kv_heads = d->num_kv_heads;
+    a.d = d->d;
+    a.n_pos = n_pos;
+    a.scale = d->scale;
+    a.split.batch = batch;
+    return a;
+}
+
+// Debug builds: valid cache slots of one append are distinct (as DEBUG_DISTINCT_SLOTS).
+#ifdef GDN_DEBUG_CHECKS
+int debug_distinct_cache_slots(const int64_t* slot_map, int32_t tokens, int64_t n_slots,
+                               void* stream, const char* what) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    std::vector<char> seen((size_t)n_slots, 0);
+    std::vector<int64_t> h((size_t)tokens);
+    if (hipMemcpyAsync(h.data(), slot_map, sizeof(int64_t) * h.size(), hipMemcpyDeviceToHost, s) !=
+            hipSuccess ||
+        hipStreamSynchronize(s) != hipSuccess) {
+        (void)hipGetLastError();
+        return fail(GDN_ERR_LAUNCH, "%s: debug check could not read the slot map", what);
+    }
+    for (int64_t v : h) {
+        if (v < 0 || v >= n_slots) continue;
+        if (seen[(size_t)v])
+            return fail(GDN_ERR_SHAPE, "%s: cache slot %lld used twice", what, (long long)v);
+        seen[(size_t)v] = 1;
+    }
+    return GDN_OK;
+}
+#define DEBUG_DISTINCT_CACHE_SLOTS(map, tokens, n_slots, what)                            \
+    do {                                                                                  \
+        int st_ = debug_distinct_cache_slots(map, tokens, n_slots, stream, what);         \
+        if (st_) return st_;                                                              \
+    } while (0)
+#else
+#define DEBUG_DISTINCT_CACHE_SLOTS(map, tokens, n_slots, what) \
+    do {                                                       \
+        (void)(what);                                          \
+    } while (0)
+#endif
+
 }  // namespace
 
 extern "C" {
@@ -588,6 +701,166 @@ int gdn_conv1d_silu(const void* x, const float* w, const int32_t* cu_seqlens, in
     a.y = y;
     return launch_status(gdn::launch_conv1d(a, static_cast<hipStream_t>(stream)),
                          "gdn_conv1d_silu");
+}
+
+// ---------------------------------------------------------------- paged softmax attention
+
+int gdn_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t n,
+                   int32_t block_size, int32_t* block_table, int32_t max_blocks,
+                   const int32_t* free_blocks, int32_t n_free, int32_t max_tokens,
+                   int32_t* cu_seqlens, int32_t* seq_lens, int64_t* slot_map,
+                   int32_t* positions, int32_t* counts, void* stream) {
+    if (n < 0 || max_blocks < 0 || n_free < 0 || max_tokens < 0)
+        return fail(GDN_ERR_SHAPE, "n, max_blocks, n_free and max_tokens must be >= 0 (got %d, "
+                                   "%d, %d, %d)", n, max_blocks, n_free, max_tokens);
+    if (block_size < 1) return fail(GDN_ERR_SHAPE, "block_size must be >= 1 (got %d)", block_size);
+    if (n > 0) {
+        REQUIRE_PTR(ctx_lens);
+        REQUIRE_PTR(new_lens);
+        REQUIRE_PTR(seq_lens);
+        if (max_blocks > 0) REQUIRE_PTR(block_table);
+    }
+    if (n_free > 0) REQUIRE_PTR(free_blocks);
+    REQUIRE_PTR(cu_seqlens);
+    REQUIRE_PTR(counts);
+    if (max_tokens > 0) {
+        REQUIRE_PTR(slot_map);
+        REQUIRE_PTR(positions);
+    }
+    gdn::PlanArgs a;
+    a.ctx_lens = ctx_lens;
+    a.new_lens = new_lens;
+    a.n = n;
+    a.block_size = block_size;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.free_blocks = free_blocks;
+    a.n_free = n_free;
+    a.max_tokens = max_tokens;
+    a.cu_seqlens = cu_seqlens;
+    a.seq_lens = seq_lens;
+    a.slot_map = slot_map;
+    a.positions = positions;
+    a.counts = counts;
+    return launch_status(gdn::launch_paged_plan(a, static_cast<hipStream_t>(stream)),
+                         "gdn_paged_plan");
+}
+
+int gdn_paged_append(int32_t dtype, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, const int64_t* slot_map, int32_t tokens,
+                     int32_t kv_heads, int32_t d, void* k_cache, void* v_cache,
+                     int32_t n_blocks, int32_t block_size, void* stream) {
+    const char* what = "gdn_paged_append";
+    int st = check_cache(dtype, kv_heads, n_blocks, block_size);
+    if (st) return st;
+    if (!paged_dim_ok(d)) return fail(GDN_ERR_UNSUPPORTED, "d must be 64, 128 or 256 (got %d)", d);
+    st = check_rows(dtype, tokens, k_stride, (int64_t)kv_heads * d, "k");
+    if (!st) st = check_rows(dtype, tokens, v_stride, (int64_t)kv_heads * d, "v");
+    if (st || tokens == 0) return st ? st : ok();
+    REQUIRE_PTR(k);
+    REQUIRE_PTR(v);
+    REQUIRE_PTR(slot_map);
+    REQUIRE_PTR(k_cache);
+    REQUIRE_PTR(v_cache);
+    const int per = dtype == GDN_DTYPE_BF16 ? 8 : 4;
+    gdn::AppendArgs a;
+    a.a = k;
+    a.b = v;
+    a.a_stride = k_stride / per;
+    a.b_stride = v_stride / per;
+    a.slot_map = slot_map;
+    a.tokens = tokens;
+    a.heads = kv_heads;
+    a.a_row = d / per;
+    a.b_row = d / per;
+    a.a_cache = k_cache;
+    a.b_cache = v_cache;
+    a.n_blocks = n_blocks;
+    a.block_size = block_size;
+    DEBUG_DISTINCT_CACHE_SLOTS(slot_map, tokens, (int64_t)n_blocks * block_size, what);
+    return launch_status(gdn::launch_append(a, static_cast<hipStream_t>(stream)), what);
+}
+
+int gdn_latent_append(int32_t dtype, const void* c, int64_t c_stride, const void* k_pe,
+                      int64_t pe_stride, const int64_t* slot_map, int32_t tokens, int32_t rank,
+                      int32_t d_rope, void* cache, int32_t n_blocks, int32_t block_size,
+                      void* stream) {
+    const char* what = "gdn_latent_append";
+    int st = check_cache(dtype, 1, n_blocks, block_size);
+    if (st) return st;
+    if (rank < 8 || rank % 8 != 0 || rank > 65536 || d_rope < 8 || d_rope % 8 != 0 ||
+        d_rope > 65536)
+        return fail(GDN_ERR_UNSUPPORTED, "rank and d_rope must be multiples of 8 in [8, 65536] "
+                                         "(got %d, %d)", rank, d_rope);
+    st = check_rows(dtype, tokens, c_stride, rank, "c");
+    if (!st) st = check_rows(dtype, tokens, pe_stride, d_rope, "k_pe");
+    if (st || tokens == 0) return st ? st : ok();
+    REQUIRE_PTR(c);
+    REQUIRE_PTR(k_pe);
+    REQUIRE_PTR(slot_map);
+    REQUIRE_PTR(cache);
+    const int per = dtype == GDN_DTYPE_BF16 ? 8 : 4;
+    gdn::AppendArgs a;
+    a.a = c;
+    a.b = k_pe;
+    a.a_stride = c_stride / per;
+    a.b_stride = pe_stride / per;
+    a.slot_map = slot_map;
+    a.tokens = tokens;
+    a.heads = 1;
+    a.a_row = rank / per;
+    a.b_row = d_rope / per;
+    a.a_cache = cache;
+    a.b_cache = nullptr;
+    a.n_blocks = n_blocks;
+    a.block_size = block_size;
+    DEBUG_DISTINCT_CACHE_SLOTS(slot_map, tokens, (int64_t)n_blocks * block_size, what);
+    return launch_status(gdn::launch_append(a, static_cast<hipStream_t>(stream)), what);
+}
+
+int gdn_paged_decode_workspace_bytes(const gdn_paged_dims_t* dims, int32_t batch, int32_t n_pos,
+                                     size_t* bytes) {
+    int st = check_paged_dims(dims, batch, n_pos);
+    if (st) return st;
+    if (bytes == nullptr) return fail(GDN_ERR_NULL, "bytes is NULL");
+    gdn::PagedDecodeArgs a = paged_args(dims, batch, n_pos);
+    *bytes = batch == 0 ? 0 : gdn::paged_decode_layout(&a, nullptr);
+    return ok();
+}
+
+int gdn_paged_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_cache,
+                     const void* v_cache, int32_t n_blocks, int32_t block_size,
+                     const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
+                     int32_t batch, int32_t n_pos, void* o, void* workspace, size_t ws_bytes,
+                     void* stream) {
+    int st = check_paged_dims(dims, batch, n_pos);
+    if (!st) st = check_cache(dims->dtype, dims->num_kv_heads, n_blocks, block_size);
+    if (!st) st = check_table(max_blocks, block_size);
+    if (st) return st;
+    if (batch == 0) return ok();
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(k_cache);
+    REQUIRE_PTR(v_cache);
+    REQUIRE_PTR(block_table);
+    REQUIRE_PTR(seq_lens);
+    REQUIRE_PTR(o);
+    REQUIRE_PTR(workspace);
+    gdn::PagedDecodeArgs a = paged_args(dims, batch, n_pos);
+    const size_t need = gdn::paged_decode_layout(&a, workspace);
+    if (ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.n_blocks = n_blocks;
+    a.block = gdn::FastDiv::of((uint32_t)block_size);
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.split.seq_lens = seq_lens;
+    a.split.max_keys = max_blocks * block_size;
+    a.o = o;
+    return launch_status(gdn::launch_paged_decode(a, static_cast<hipStream_t>(stream)),
+                         "gdn_paged_decode");
 }
 
 const char* gdn_status_string(int status) {

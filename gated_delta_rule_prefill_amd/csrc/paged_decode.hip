@@ -1,0 +1,499 @@
+// Attention of the newest n_pos tokens of each request over a paged key/value cache, grouped
+// heads (gdn_paged_decode).
+//
+//   o[b, p, h] = sum_j softmax_j(scale q[b, p, h] . k_j) v_j,   j < len_b - n_pos + p + 1,
+// k_j and v_j the rows of head h / group in the request's pages. The n_pos x group query rows
+// that share a key/value head form the 16-row MFMA tiles, so the cache is read once for all of
+// them; the keys are split over workgroups by key_split.h and joined by a second kernel.
+//
+// One wave takes KW keys at a time and keeps everything of them in registers:
+//   S^T = K Q^T   keys are the rows of the MFMA's A operand, read from the cache row by row in
+//                 16-byte pieces straight into registers (no LDS);
+//   softmax       running maximum and sum per query row, i.e. per accumulator column: a lane's
+//                 KW / 4 scores are reduced in registers, then over the four lane groups;
+//   O^T += V^T P^T  the accumulator layout of S^T is the B operand's with the keys renumbered
+//                 (lane group g holds keys 4 g .. 4 g + 3 of each 16), so P stays in registers.
+//                 V^T is the one operand that needs a transpose: V rows go through a per-wave
+//                 LDS tile and come back by transposing reads (bf16) or column reads (fp32).
+// Waves never wait for each other inside the key loop; the four partial results of a workgroup
+// are merged through LDS at the end of a unit.
+#include "attn_launch.h"
+#include "gdn_common.h"
+#include "gdn_launch.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int PD_THREADS = 256;
+constexpr int PD_WAVES = PD_THREADS / WAVE;
+constexpr float LOG2E = 1.4426950408889634f;
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ bf16x4 lds_read_tr(const char* p) {
+    typedef __attribute__((address_space(3))) s16x4* lptr;
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(p)));
+}
+
+// Per element type: keys per wave step, fragments, and the two products.
+template <typename T, int D> struct PdTile;
+
+template <int D> struct PdTile<bf16, D> {
+    static constexpr int KW = 32;            // keys of a wave step: one MFMA contraction of P V
+    static constexpr int NSUB = KW / 16;
+    static constexpr int NF = D / 32;        // 16-byte pieces per lane of a key or query row
+    static constexpr int ROW = D * 2;        // bytes of an LDS row
+    static constexpr int CPR = D * 2 / 16;   // 16-byte pieces per row
+    typedef bf16x8 frag;
+    __device__ __forceinline__ static int piece(int f, int g) { return f * 4 + g; }
+    __device__ __forceinline__ static f32x4 qk(const frag* k, const frag* q) {
+        f32x4 s = zero4();
+#pragma unroll
+        for (int f = 0; f < NF; f++) s = Mma<bf16>::mma(k[f], q[f], s);
+        return s;
+    }
+    // LDS position of piece c of row r: pairs of pieces (the 32 bytes a transposing read takes
+    // from a row) are rotated over the banks by the row, so that its 16 rows do not collide
+    __device__ __forceinline__ static int turn(int r) { return D >= 128 ? r & 7 : (r >> 1) & 3; }
+    __device__ __forceinline__ static int place(int r, int c) {
+        return r * ROW + ((c ^ (turn(r) << 1)) << 4);
+    }
+    // o[j] += V^T(16 dims from 16 j) P^T
+    template <int NS>
+    __device__ __forceinline__ static void pv(f32x4* o, const char* v, const float (*p)[4],
+                                              int lane) {
+        bf16x8 pb;
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) pb[t * 4 + i] = (bf16)p[t][i];
+        const int r = (lane >> 4) * 4 + ((lane >> 2) & 3);
+        const char* row = v + r * ROW + (lane & 3) * 8;
+        const int turned = turn(r) << 5;
+#pragma unroll
+        for (int j = 0; j < D / 16; j++) {
+            const char* at = row + ((j << 5) ^ turned);
+            const bf16x4 a0 = lds_read_tr(at), a1 = lds_read_tr(at + 16 * ROW);
+            bf16x8 a;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                a[i] = a0[i];
+                a[4 + i] = a1[i];
+            }
+            o[j] = Mma<bf16>::mma(a, pb, o[j]);
+        }
+    }
+};
+
+template <int D> struct PdTile<float, D> {
+    static constexpr int KW = 16;
+    static constexpr int NSUB = 1;
+    static constexpr int NF = D / 16;
+    static constexpr int ROW = D * 4 + 16;   // 4 floats of padding: rows 4 apart on other banks
+    static constexpr int CPR = D * 4 / 16;
+    typedef f32x4 frag;
+    __device__ __forceinline__ static int piece(int f, int g) { return f * 4 + g; }
+    __device__ __forceinline__ static f32x4 qk(const frag* k, const frag* q) {
+        f32x4 s = zero4();
+#pragma unroll
+        for (int f = 0; f < NF; f++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) s = Mma<float>::mma(k[f][e], q[f][e], s);
+        return s;
+    }
+    __device__ __forceinline__ static int place(int r, int c) { return r * ROW + c * 16; }
+    template <int NS>
+    __device__ __forceinline__ static void pv(f32x4* o, const char* v, const float (*p)[4],
+                                              int lane) {
+        const float* row = reinterpret_cast<const float*>(v + (lane >> 4) * 4 * ROW) + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < D / 16; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                o[j] = Mma<float>::mma(row[i * (ROW / 4) + j * 16], p[0][i], o[j]);
+    }
+};
+
+template <typename T, int D, int RT>
+struct PdLds {
+    static constexpr int VTILE = PdTile<T, D>::KW * PdTile<T, D>::ROW;
+    static constexpr int MROW = D + 4;  // floats: merge rows on different banks
+    static constexpr int MERGE = PD_WAVES * 16 * MROW * 4;
+    static constexpr int BYTES = VTILE * PD_WAVES > MERGE ? VTILE * PD_WAVES : MERGE;
+};
+
+constexpr uint32_t NO_ROW = 0xffffffffu;
+
+template <typename T, int D, int RT>
+__global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArgs a) {
+    using X = PdTile<T, D>;
+    using L = PdLds<T, D, RT>;
+    typedef typename X::frag frag;
+    constexpr int KW = X::KW, NSUB = X::NSUB, NF = X::NF, CPR = X::CPR;
+    constexpr int KB = KW * PD_WAVES;
+    constexpr int NV = KW * CPR / WAVE;  // 16-byte pieces of V per lane
+    __shared__ __align__(16) char smem[L::BYTES];
+    __shared__ float ml[PD_WAVES][16][2];
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+    const int col = lane & 15, grp = lane >> 4;
+    SplitRun run = split_run<KB, PD_THREADS>(a.split, blockIdx.x, a.n_wg);
+    const int64_t run_start = run.pos;
+    char* vlds = smem + wave * L::VTILE;
+    const float cs = a.scale * LOG2E;
+
+    while (run.pos < run.end) {
+        const int b = run.b;
+        const int nkeys = split_keys(a.split, b);
+        const int nch = (nkeys + KB - 1) / KB;
+        const int unit = (int)((run.pos - run.base) / nch);
+        const int c0 = (int)(run.pos - run.base - (int64_t)unit * nch);
+        const int c1 = (int)min((int64_t)nch, c0 + (run.end - run.pos));
+        const int kvh = unit / a.row_tiles, row0 = (unit - kvh * a.row_tiles) * 16 * RT;
+        const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
+        const int seen0 = a.split.seq_lens[b] - a.n_pos + 1;  // keys that position 0 sees
+
+        frag q[RT][NF];
+        int lim[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+            const int r = row0 + rt * 16 + col;
+            const bool live = r < a.rows;
+            const int p = live ? r / a.group : 0, h = live ? r - p * a.group : 0;
+            lim[rt] = live ? seen0 + p : 0;
+            const T* src = reinterpret_cast<const T*>(a.q) +
+                           (((size_t)b * a.n_pos + p) * a.H + (size_t)kvh * a.group + h) * D;
+#pragma unroll
+            for (int f = 0; f < NF; f++)
+                q[rt][f] = reinterpret_cast<const frag*>(src)[X::piece(f, grp)];
+        }
+
+        f32x4 acc[RT][D / 16];
+        float m[RT], l[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+            m[rt] = -INFINITY;
+            l[rt] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; j++) acc[rt][j] = zero4();
+        }
+
+        // page of this lane's key of each 16-key group of wave step c (lanes 16.. repeat 0..15)
+        int page[NSUB];
+        auto load_pages = [&](int c) {
+#pragma unroll
+            for (int t = 0; t < NSUB; t++) {
+                const int key = c * KB + wave * KW + t * 16 + col;
+                page[t] = key < nkeys ? table[a.block((uint32_t)key)] : -1;
+            }
+        };
+        uint32_t row[NSUB];
+        auto find_rows = [&](int c) {
+#pragma unroll
+            for (int t = 0; t < NSUB; t++) {
+                const uint32_t key = (uint32_t)(c * KB + wave * KW + t * 16 + col);
+                const uint32_t off = key - a.block(key) * a.block.div;
+                const bool ok = page[t] >= 0 && page[t] < a.n_blocks;
+                row[t] = ok ? ((uint32_t)page[t] * a.kv_heads + kvh) * a.block.div + off : NO_ROW;
+            }
+        };
+        frag kf[NSUB][NF];
+        auto load_k = [&]() {
+#pragma unroll
+            for (int t = 0; t < NSUB; t++) {
+                const uint32_t r = row[t] == NO_ROW ? 0u : row[t];
+                const frag* src = reinterpret_cast<const frag*>(
+                    reinterpret_cast<const T*>(a.k_cache) + (size_t)r * D);
+#pragma unroll
+                for (int f = 0; f < NF; f++) kf[t][f] = src[X::piece(f, grp)];
+            }
+        };
+        f32x4 vf[NV];
+        auto load_v = [&]() {
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int x = i * WAVE + lane, r = x / CPR, c = x % CPR;
+                uint32_t at = __shfl(row[0], r & 15, WAVE);
+                if constexpr (NSUB > 1) {
+                    const uint32_t at1 = __shfl(row[1], r & 15, WAVE);
+                    at = r < 16 ? at : at1;
+                }
+                at = at == NO_ROW ? 0u : at;
+                vf[i] = reinterpret_cast<const f32x4*>(reinterpret_cast<const T*>(a.v_cache) +
+                                                       (size_t)at * D)[c];
+            }
+        };
+        load_pages(c0);
+        find_rows(c0);
+        load_k();
+        load_v();
+        load_pages(c0 + 1 < c1 ? c0 + 1 : c0);
+
+        for (int c = c0; c < c1; c++) {
+            float s[RT][NSUB][4];
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                for (int t = 0; t < NSUB; t++) {
+                    const f32x4 x = X::qk(kf[t], q[rt]);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) s[rt][t][i] = x[i] * cs;
+                }
+            // keys of this step that exist, one bit each
+            uint32_t exist = 0;
+#pragma unroll
+            for (int t = 0; t < NSUB; t++)
+                exist |= (uint32_t)(__ballot(row[t] != NO_ROW) & 0xffff) << (16 * t);
+            constexpr uint32_t ALL = (uint32_t)((1ull << KW) - 1);
+            const int key0 = c * KB + wave * KW;
+            if (exist != ALL || key0 + KW > seen0) {
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                    for (int t = 0; t < NSUB; t++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const int k = t * 16 + grp * 4 + i;
+                            const bool keep = ((exist >> k) & 1) && key0 + k < lim[rt];
+                            s[rt][t][i] = keep ? s[rt][t][i] : -INFINITY;
+                        }
+            }
+            // V to LDS, absent keys as zeros (a zero weight does not cancel what their rows hold)
+            if (exist != ALL) {
+#pragma unroll
+                for (int i = 0; i < NV; i++) {
+                    const int r = (i * WAVE + lane) / CPR;
+                    if (!((exist >> r) & 1)) vf[i] = zero4();
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int x = i * WAVE + lane;
+                *reinterpret_cast<f32x4*>(vlds + X::place(x / CPR, x % CPR)) = vf[i];
+            }
+            if (c + 1 < c1) {
+                find_rows(c + 1);
+                load_k();
+                load_v();
+                load_pages(c + 2 < c1 ? c + 2 : c + 1);
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++) {
+                float top = s[rt][0][0];
+#pragma unroll
+                for (int t = 0; t < NSUB; t++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) top = fmaxf(top, s[rt][t][i]);
+                top = fmaxf(top, __shfl_xor(top, 16, WAVE));
+                top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+                const float m1 = fmaxf(m[rt], top);
+                const float ref = m1 == -INFINITY ? 0.f : m1;  // a row with no key so far
+                if (__any(m1 > m[rt])) {
+                    const float shrink = __builtin_amdgcn_exp2f(m[rt] - ref);
+                    l[rt] *= shrink;
+#pragma unroll
+                    for (int j = 0; j < D / 16; j++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) acc[rt][j][i] *= shrink;
+                    m[rt] = m1;
+                }
+#pragma unroll
+                for (int t = 0; t < NSUB; t++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        s[rt][t][i] = __builtin_amdgcn_exp2f(s[rt][t][i] - ref);
+                        l[rt] += s[rt][t][i];
+                    }
+                X::template pv<NSUB>(acc[rt], vlds, s[rt], lane);
+            }
+        }
+
+        // merge the four waves, one 16-row tile at a time
+        const bool whole = c0 == 0 && c1 == nch;
+        const int slot = 2 * (int)blockIdx.x + (run.pos == run_start ? 0 : 1);
+        float* mrow = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+            __syncthreads();
+            float lt = l[rt];
+            lt += __shfl_xor(lt, 16, WAVE);
+            lt += __shfl_xor(lt, 32, WAVE);
+            if (grp == 0) {
+                ml[wave][col][0] = m[rt];
+                ml[wave][col][1] = lt;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; j++)
+                *reinterpret_cast<f32x4*>(mrow + (wave * 16 + col) * L::MROW + j * 16 + grp * 4) =
+                    acc[rt][j];
+            __syncthreads();
+            const int r = tid >> 4, rr = row0 + rt * 16 + r;
+            if (rr < a.rows) {
+                float top = ml[0][r][0];
+#pragma unroll
+                for (int w = 1; w < PD_WAVES; w++) top = fmaxf(top, ml[w][r][0]);
+                const float ref = top == -INFINITY ? 0.f : top;
+                float wt[PD_WAVES], sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < PD_WAVES; w++) {
+                    wt[w] = __builtin_amdgcn_exp2f(ml[w][r][0] - ref);
+                    sum += wt[w] * ml[w][r][1];
+                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
+                const int p = rr / a.group, h = rr - p * a.group;
+                T* dst = reinterpret_cast<T*>(a.o) +
+                         (((size_t)b * a.n_pos + p) * a.H + (size_t)kvh * a.group + h) * D;
+                float* part = a.part_o + ((size_t)slot * RT * 16 + rt * 16 + r) * D;
+#pragma unroll
+                for (int j = 0; j < D / 64; j++) {
+                    const int d = j * 64 + (tid & 15) * 4;
+                    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int w = 0; w < PD_WAVES; w++) {
+                        const f32x4 y = *reinterpret_cast<const f32x4*>(
+                            mrow + (w * 16 + r) * L::MROW + d);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) x[i] = fmaf(wt[w], y[i], x[i]);
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++) x[i] *= inv;
+                        store4<T>(dst + d, x);
+                    } else {
+                        store4<float>(part + d, x);
+                    }
+                }
+                if (!whole && (tid & 15) == 0) {
+                    float* pm = a.part_ml + ((size_t)slot * RT * 16 + rt * 16 + r) * 2;
+                    pm[0] = top;
+                    pm[1] = sum;
+                }
+            }
+        }
+        __syncthreads();  // the merge rows are the next unit's V tiles
+
+        run.pos += c1 - c0;
+        if (run.pos < run.end && run.pos == run.base + (int64_t)nch * a.split.units) {
+            run.base = run.pos;
+            do run.b++;
+            while (run.b + 1 < a.split.batch && split_chunks<KB>(a.split, run.b) == 0);
+        }
+    }
+}
+
+// Joins the partial results of the units that were cut: one wave per query row. Rows of units
+// that a single workgroup finished are left alone; a request without keys gets zeros.
+template <typename T, int D>
+__global__ __launch_bounds__(PD_THREADS) void paged_join_kernel(PagedDecodeArgs a) {
+    constexpr int KB = PdTile<T, D>::KW * PD_WAVES;
+    constexpr int PER = D / WAVE;
+    const int tile = 16 * a.rt;
+    const int lane = lane_id();
+    const int64_t idx = (int64_t)blockIdx.x * PD_WAVES + wave_id();
+    const int b = (int)(idx / (a.kv_heads * a.rows));
+    if (b >= a.split.batch) return;
+    const int rest = (int)(idx - (int64_t)b * a.kv_heads * a.rows);
+    const int kvh = rest / a.rows, rr = rest - kvh * a.rows;
+    const int unit = kvh * a.row_tiles + rr / tile, r = rr % tile;
+    const int p = rr / a.group, h = rr - p * a.group;
+    T* dst = reinterpret_cast<T*>(a.o) +
+             (((size_t)b * a.n_pos + p) * a.H + (size_t)kvh * a.group + h) * D + lane * PER;
+    const int nch = split_chunks<KB>(a.split, b);
+    float x[PER];
+#pragma unroll
+    for (int i = 0; i < PER; i++) x[i] = 0.f;
+    if (nch > 0) {
+        int64_t base, total;
+        split_base<KB>(a.split, b, &base, &total);
+        const int64_t u0 = base + (int64_t)unit * nch;
+        const int n = split_wgs(total, a.n_wg);
+        const int w0 = split_owner(u0, total, n), w1 = split_owner(u0 + nch - 1, total, n);
+        if (w0 == w1) return;
+        // part of workgroup w: its first unit is this one unless it started before it (w0 only)
+        const int late = split_start(w0, total, n) < u0 ? 1 : 0;
+        auto at = [&](int w) {
+            return ((size_t)(2 * w + (w == w0 ? late : 0)) * tile + r);
+        };
+        float top = -INFINITY;
+        for (int w = w0 + lane; w <= w1; w += WAVE) top = fmaxf(top, a.part_ml[at(w) * 2]);
+#pragma unroll
+        for (int off = WAVE / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, WAVE));
+        const float ref = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+#pragma unroll 8
+        for (int w = w0; w <= w1; w++) {
+            const size_t e = at(w);
+            const float wt = __builtin_amdgcn_exp2f(a.part_ml[e * 2] - ref);
+            sum = fmaf(wt, a.part_ml[e * 2 + 1], sum);
+#pragma unroll
+            for (int i = 0; i < PER; i++) x[i] = fmaf(wt, a.part_o[e * D + lane * PER + i], x[i]);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < PER; i++) x[i] *= inv;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; i++) dst[i] = from_f32<T>(x[i]);
+}
+
+template <typename T, int D, int RT>
+hipError_t run_decode(const PagedDecodeArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((paged_decode_kernel<T, D, RT>), dim3((unsigned)a.n_wg), dim3(PD_THREADS),
+                       0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t rows = (int64_t)a.split.batch * a.kv_heads * a.rows;
+    hipLaunchKernelGGL((paged_join_kernel<T, D>), dim3((unsigned)((rows + PD_WAVES - 1) / PD_WAVES)),
+                       dim3(PD_THREADS), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t pick_rows(const PagedDecodeArgs& a, hipStream_t s) {
+    switch (a.rt) {
+        case 1: return run_decode<T, D, 1>(a, s);
+        case 2:
+            if constexpr (sizeof(T) == 2) return run_decode<T, D, 2>(a, s);
+            break;
+        case 4:
+            if constexpr (sizeof(T) == 2 && D <= 128) return run_decode<T, D, 4>(a, s);
+            break;
+    }
+    return hipErrorInvalidValue;
+}
+
+template <typename T>
+hipError_t pick_dim(const PagedDecodeArgs& a, hipStream_t s) {
+    switch (a.d) {
+        case 64: return pick_rows<T, 64>(a, s);
+        case 128: return pick_rows<T, 128>(a, s);
+        case 256: return pick_rows<T, 256>(a, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
+    a->group = a->H / a->kv_heads;
+    a->rows = a->group * a->n_pos;
+    // rows of a tile: as many as the registers hold beside the head dim
+    const int most = a->dtype == 0 ? 1 : a->d <= 128 ? 4 : 2;
+    const int tiles = (a->rows + 15) / 16;
+    a->rt = tiles >= 4 && most >= 4 ? 4 : tiles >= 2 && most >= 2 ? 2 : 1;
+    a->row_tiles = (tiles + a->rt - 1) / a->rt;
+    a->split.units = a->kv_heads * a->row_tiles;
+    a->n_wg = 2 * device_cu_count();
+    const size_t rows = (size_t)2 * a->n_wg * 16 * a->rt;
+    a->part_o = static_cast<float*>(ws);
+    a->part_ml = a->part_o == nullptr ? nullptr : a->part_o + rows * a->d;
+    return rows * (a->d + 2) * sizeof(float);
+}
+
+hipError_t launch_paged_decode(const PagedDecodeArgs& a, hipStream_t s) {
+    (void)hipGetLastError();  // report only errors raised by this call's launches
+    return a.dtype == 1 ? pick_dim<bf16>(a, s) : pick_dim<float>(a, s);
+}
+
+}  // namespace gdn

@@ -39,12 +39,19 @@ class gdn_deltalog_pool_t(ctypes.Structure):
                 ("M", ctypes.c_int32)]
 
 
+class gdn_paged_dims_t(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _DIMS = ctypes.POINTER(gdn_dims_t)
+_L = ctypes.c_int64
 _POOL = ctypes.POINTER(gdn_deltalog_pool_t)
+_PAGED = ctypes.POINTER(gdn_paged_dims_t)
 
 _SIGS = {
     "gdn_prefill_workspace_bytes": [_DIMS, _I, _I, _I, ctypes.POINTER(_SZ)],
@@ -65,6 +72,11 @@ _SIGS = {
     "gdn_deltalog_reset": [_DIMS, _POOL, _I, _P, _I, _P],
     "gdn_deltalog_materialize": [_DIMS, _POOL, _I, _P, _I, _P],
     "gdn_conv1d_silu": [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P],
+    "gdn_paged_plan": [_P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P],
+    "gdn_paged_append": [_I, _P, _L, _P, _L, _P, _I, _I, _I, _P, _P, _I, _I, _P],
+    "gdn_latent_append": [_I, _P, _L, _P, _L, _P, _I, _I, _I, _P, _I, _I, _P],
+    "gdn_paged_decode_workspace_bytes": [_PAGED, _I, _I, ctypes.POINTER(_SZ)],
+    "gdn_paged_decode": [_PAGED, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _SZ, _P],
     "gdn_status_string": [ctypes.c_int],
     "gdn_last_error": [],
     "gdn_abi_version": [],
@@ -391,3 +403,189 @@ def gdn_conv1d_silu(x, w, cu_seqlens, planes=1, y=None, stream=None):
         _ptr(x), _ptr(w), _ptr(cu_seqlens), int(cu_seqlens.numel() - 1), int(T), int(ch),
         int(w.shape[1]), int(planes), _dtype_code(x), _ptr(y), _stream(stream)))
     return y
+
+
+# ------------------------------------------------- paged softmax attention (hybrid models)
+class _Call:
+    """One launch on the tensors' own device: that device is made current, and the stream is
+    its current stream unless one is given. Buffers that the binding allocates for a call on
+    another stream are marked as used there, so the allocator does not hand them out early."""
+
+    def __init__(self, like, stream):
+        self.device = like.device
+        self.given = stream
+
+    def __enter__(self):
+        self.guard = torch.cuda.device(self.device)
+        self.guard.__enter__()
+        cur = torch.cuda.current_stream()
+        if self.given is None:
+            self.stream, self.other = cur, False
+        else:
+            self.stream = (self.given if hasattr(self.given, "cuda_stream")
+                           else torch.cuda.ExternalStream(int(self.given)))
+            self.other = self.stream.cuda_stream != cur.cuda_stream
+        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
+        return self
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+    def new(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.other:
+            t.record_stream(self.stream)
+        return t
+
+
+def _same_device(*ts):
+    _dev(*ts)
+    devs = {t.device for t in ts if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"all tensors must be on one GPU, got {sorted(map(str, devs))}")
+
+
+def _want(name, t, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def _table(block_table, n):
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [requests, max_blocks]")
+    _want("block_table", block_table, (n, block_table.shape[1]), torch.int32)
+
+
+def _rows(name, t, width):
+    """A token-major source whose rows may lie apart (a part of a fused projection): returns
+    the row stride in elements."""
+    if not t.is_cuda:
+        raise ValueError("all tensors must be on the GPU")
+    inner = t[0] if t.shape[0] else t
+    if t.shape[0] and (not inner.is_contiguous() or inner.numel() != width):
+        raise ValueError(f"{name}: rows must be contiguous with {width} elements")
+    return int(t.stride(0)) if t.shape[0] > 1 else width
+
+
+def gdn_paged_plan(ctx_lens, new_lens, block_table, free_blocks, block_size, max_tokens,
+                   cu_seqlens=None, seq_lens=None, slot_map=None, positions=None, counts=None,
+                   stream=None):
+    """Bookkeeping of one step over a paged cache, on the GPU. ctx_lens, new_lens [n] int32;
+    block_table [n, max_blocks] int32, updated in place; free_blocks [n_free] int32; max_tokens
+    is the length of the token buffers. Returns (cu_seqlens [n + 1] int32, seq_lens [n] int32,
+    slot_map [max_tokens] int64, positions [max_tokens] int32, counts [2] int32: tokens, pages
+    asked for)."""
+    n, T = int(ctx_lens.numel()), int(max_tokens)
+    i32 = torch.int32
+    _want("ctx_lens", ctx_lens, (n,), i32)
+    _want("new_lens", new_lens, (n,), i32)
+    _table(block_table, n)
+    _want("free_blocks", free_blocks, (free_blocks.numel(),), i32)
+    if T < 0:
+        raise ValueError("max_tokens must be >= 0")
+    with _Call(ctx_lens, stream) as c:
+        cu_seqlens = c.new((n + 1,), i32) if cu_seqlens is None else cu_seqlens
+        seq_lens = c.new((n,), i32) if seq_lens is None else seq_lens
+        slot_map = c.new((T,), torch.int64) if slot_map is None else slot_map
+        positions = c.new((T,), i32) if positions is None else positions
+        counts = c.new((2,), i32) if counts is None else counts
+        _want("cu_seqlens", cu_seqlens, (n + 1,), i32)
+        _want("seq_lens", seq_lens, (n,), i32)
+        _want("slot_map", slot_map, (T,), torch.int64)
+        _want("positions", positions, (T,), i32)
+        _want("counts", counts, (2,), i32)
+        _same_device(ctx_lens, new_lens, block_table, free_blocks, cu_seqlens, seq_lens, slot_map,
+                     positions, counts)
+        _check("gdn_paged_plan", lib().gdn_paged_plan(
+            _ptr(ctx_lens), _ptr(new_lens), n, int(block_size), _ptr(block_table),
+            int(block_table.shape[1]), _ptr(free_blocks), int(free_blocks.numel()), T,
+            _ptr(cu_seqlens), _ptr(seq_lens), _ptr(slot_map), _ptr(positions), _ptr(counts),
+            c.ptr))
+    return cu_seqlens, seq_lens, slot_map, positions, counts
+
+
+def gdn_paged_append(k, v, slot_map, k_cache, v_cache, stream=None):
+    """Rows of new tokens into the cache. k, v [T, kv_heads, d] (tokens may lie apart, as parts
+    of a fused projection); slot_map [T] int64; k_cache, v_cache [n_blocks, kv_heads,
+    block_size, d], updated in place."""
+    T, h, d = k.shape
+    n_blocks, _, bs, _ = k_cache.shape
+    _want("v", v, k.shape, k.dtype)
+    _want("slot_map", slot_map, (T,), torch.int64)
+    _want("k_cache", k_cache, (n_blocks, h, bs, d), k.dtype)
+    _want("v_cache", v_cache, k_cache.shape, k.dtype)
+    _same_device(slot_map, k_cache, v_cache)
+    ks, vs = _rows("k", k, h * d), _rows("v", v, h * d)
+    if k.device != k_cache.device or v.device != k_cache.device:
+        raise ValueError("all tensors must be on one GPU")
+    with _Call(k_cache, stream) as c:
+        _check("gdn_paged_append", lib().gdn_paged_append(
+            _dtype_code(k), _ptr(k), ks, _ptr(v), vs, _ptr(slot_map), int(T), int(h), int(d),
+            _ptr(k_cache), _ptr(v_cache), int(n_blocks), int(bs), c.ptr))
+
+
+def gdn_latent_append(c_kv, k_pe, slot_map, cache, stream=None):
+    """Rows of new tokens into a latent cache. c_kv [T, rank], k_pe [T, d_rope] (rows may lie
+    apart); slot_map [T] int64; cache [n_blocks, block_size, rank + d_rope], updated in
+    place."""
+    T, rank = c_kv.shape
+    rope = k_pe.shape[1]
+    n_blocks, bs, _ = cache.shape
+    _want("k_pe", k_pe, (T, rope), c_kv.dtype)
+    _want("slot_map", slot_map, (T,), torch.int64)
+    _want("cache", cache, (n_blocks, bs, rank + rope), c_kv.dtype)
+    _same_device(slot_map, cache)
+    cs, ps = _rows("c_kv", c_kv, rank), _rows("k_pe", k_pe, rope)
+    if c_kv.device != cache.device or k_pe.device != cache.device:
+        raise ValueError("all tensors must be on one GPU")
+    with _Call(cache, stream) as c:
+        _check("gdn_latent_append", lib().gdn_latent_append(
+            _dtype_code(c_kv), _ptr(c_kv), cs, _ptr(k_pe), ps, _ptr(slot_map), int(T), int(rank),
+            int(rope), _ptr(cache), int(n_blocks), int(bs), c.ptr))
+
+
+def _code(dtype):
+    if isinstance(dtype, int):
+        return dtype
+    return _dtype_code(torch.empty(0, dtype=dtype))
+
+
+def gdn_paged_decode_workspace_bytes(H, kv_heads, d, dtype, batch, n_pos=1):
+    dims = gdn_paged_dims_t(int(H), int(kv_heads), int(d), _code(dtype), 1.0)
+    out = _SZ(0)
+    _check("gdn_paged_decode_workspace_bytes", lib().gdn_paged_decode_workspace_bytes(
+        ctypes.byref(dims), int(batch), int(n_pos), ctypes.byref(out)))
+    return int(out.value)
+
+
+def _positions(q):
+    """[B, H, d] is one position per request."""
+    return q[:, None] if q.dim() == 3 else q
+
+
+def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=1.0, o=None,
+                     workspace=None, stream=None):
+    """Attention of the newest tokens over a paged cache. q [B, H, d] (a decode step) or
+    [B, P, H, d] (a verify step: the request's newest P tokens, all of them in the cache);
+    k_cache, v_cache [n_blocks, kv_heads, block_size, d]; block_table [B, max_blocks] int32;
+    seq_lens [B] int32. Returns o, shaped as q."""
+    q4 = _positions(q)
+    B, P, H, d = q4.shape
+    n_blocks, kv, bs, _ = k_cache.shape
+    _want("k_cache", k_cache, (n_blocks, kv, bs, d), q.dtype)
+    _want("v_cache", v_cache, k_cache.shape, q.dtype)
+    _table(block_table, B)
+    _want("seq_lens", seq_lens, (B,), torch.int32)
+    with _Call(q, stream) as c:
+        o = c.new(q.shape, q.dtype) if o is None else o
+        _want("o", o, q.shape, q.dtype)
+        dims = gdn_paged_dims_t(int(H), int(kv), int(d), _dtype_code(q), float(scale))
+        if workspace is None:
+            workspace = c.new((max(1, gdn_paged_decode_workspace_bytes(
+                H, kv, d, _dtype_code(q), B, P)),), torch.uint8)
+        _same_device(q, k_cache, v_cache, block_table, seq_lens, o, workspace)
+        _check("gdn_paged_decode", lib().gdn_paged_decode(
+            ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), int(n_blocks), int(bs),
+            _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(B), int(P), _ptr(o),
+            _ptr(workspace), int(workspace.numel() * workspace.element_size()), c.ptr))
+    return o

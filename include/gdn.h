@@ -414,6 +414,111 @@ int gdn_conv1d_silu(const void* x, const float* w, const int32_t* cu_seqlens, in
                     int32_t total_tokens, int32_t channels, int32_t width, int32_t planes,
                     int32_t dtype, void* y, void* stream);
 
+/* --------------------------------------------------------- paged softmax attention layers */
+
+/* A hybrid model interleaves its gated delta-rule layers with softmax-attention layers
+ * ([Handbook], title page: three linear layers to one full layer; [LA-Infra] "Linear
+ * Attention的Prefix Cache": the full layers' block tables, pages and null blocks). Their keys
+ * and values live in a paged cache: n_blocks pages of block_size tokens, shared by all
+ * requests. Conventions of the entry points below:
+ *   - block_table [n, max_blocks] int32 (device): entry p of request i is the page that holds
+ *     its tokens p * block_size .. (p + 1) * block_size - 1. An entry outside [0, n_blocks) is
+ *     a null block: its tokens do not exist, that is no query sees them. So are tokens beyond
+ *     max_blocks * block_size.
+ *   - seq_lens [n] int32 (device): tokens of each request in the cache, those of this call
+ *     included. Entries and pages beyond a request's length are neither followed nor read for
+ *     a value: they may hold anything (a NaN too).
+ *   - a cache slot is page * block_size + offset, in 64 bits.
+ *   - block_size is any number >= 1; pages that are not a multiple of a kernel's key tile only
+ *     cost their look-up.
+ * Scores, softmax statistics, weighted sums are held in fp32; with bf16 inputs the softmax
+ * weights are rounded to bf16 (relative 2^-9 each, not into the sum that divides them) as the
+ * MFMA's operand, outputs by round-to-nearest-even once. */
+
+/* Largest num_heads of the attention entry points. */
+#define GDN_ATTN_MAX_HEADS 1024
+
+/* Block tables, slot maps, positions and cu_seqlens of a step, from request lengths, in one
+ * launch. With c = ctx_lens[i] tokens in the cache and w = new_lens[i] tokens to come (negative
+ * lengths count as 0, c + w < 2^31, the sum of all w < 2^31):
+ *   held = ceil(c / block_size), all = min(ceil((c + w) / block_size), max_blocks); entries
+ *   held .. all - 1 of request i's table row become the next all - held ids of free_blocks,
+ *   which are handed out in request order; -1 once they are used up. Other entries stay.
+ *   cu_seqlens [n + 1]  prefix sums of w (what gdn_prefill_chunked takes)
+ *   seq_lens   [n]      c + w
+ *   slot_map   [max_tokens] int64: cache slot of each new token, packed by cu_seqlens; -1 for
+ *              tokens without a page (null entry, free list used up, beyond max_blocks) and for
+ *              entries from cu_seqlens[n] on (a buffer sized for the largest step)
+ *   positions  [max_tokens] int32: position of each new token in its request, 0 from
+ *              cu_seqlens[n] on
+ *   counts     [2] int32: cu_seqlens[n], and the number of pages asked of the free list (more
+ *              than n_free when it was too short; the first min of both were handed out)
+ * If the new tokens exceed max_tokens, the tokens from max_tokens on get no slot, and pages
+ * that start at one of them are not entered into the table; counts[0] tells.
+ *   ctx_lens, new_lens [n] int32; free_blocks [n_free] int32 (device; not changed);
+ *   block_table [n, max_blocks] int32 (device), updated in place. n, max_blocks, n_free and
+ *   max_tokens may be 0 (the arrays they size may then be NULL). */
+int gdn_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t n,
+                   int32_t block_size, int32_t* block_table, int32_t max_blocks,
+                   const int32_t* free_blocks, int32_t n_free, int32_t max_tokens,
+                   int32_t* cu_seqlens, int32_t* seq_lens, int64_t* slot_map,
+                   int32_t* positions, int32_t* counts, void* stream);
+
+/* Writes the keys and values of new tokens into their cache slots.
+ *   k, v       [tokens] rows of [kv_heads, d] dtype, k_stride / v_stride elements apart (so
+ *              that they may be parts of a fused projection's output; a multiple of 16 bytes)
+ *   slot_map   [tokens] int64 (device); a slot outside [0, n_blocks * block_size) skips the
+ *              token. Valid slots must be distinct within one call (the debug library checks).
+ *   k_cache, v_cache [n_blocks, kv_heads, block_size, d] dtype (device)
+ *   d          64, 128 or 256 */
+int gdn_paged_append(int32_t dtype, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, const int64_t* slot_map, int32_t tokens,
+                     int32_t kv_heads, int32_t d, void* k_cache, void* v_cache,
+                     int32_t n_blocks, int32_t block_size, void* stream);
+
+/* The same for a latent cache [n_blocks, block_size, rank + d_rope]: each token's row is its
+ * latent c (rank elements) followed by its rotary key k_pe (d_rope elements); both multiples
+ * of 8. */
+int gdn_latent_append(int32_t dtype, const void* c, int64_t c_stride, const void* k_pe,
+                      int64_t pe_stride, const int64_t* slot_map, int32_t tokens, int32_t rank,
+                      int32_t d_rope, void* cache, int32_t n_blocks, int32_t block_size,
+                      void* stream);
+
+/* num_heads query heads, a multiple of num_kv_heads; query head h reads key/value head
+ * h / (num_heads / num_kv_heads). d 64, 128 or 256; dtype of q, o and the caches; scale
+ * multiplies the scores (usually d^{-1/2}). */
+typedef struct {
+    int32_t num_heads;
+    int32_t num_kv_heads;
+    int32_t d;
+    int32_t dtype;
+    float scale;
+} gdn_paged_dims_t;
+
+/* Workspace of gdn_paged_decode for the current device (host computation). It does not depend
+ * on the lengths. */
+int gdn_paged_decode_workspace_bytes(const gdn_paged_dims_t* dims, int32_t batch, int32_t n_pos,
+                                     size_t* bytes);
+
+/* Attention of the newest n_pos tokens of every request (1: a decode step; more: the verify
+ * step of speculative decoding, as gdn_decode_spec) over the cache, which already holds them:
+ *   o[b, p, h] = sum_j softmax_j(scale q[b, p, h] . k_j) v_j  over the request's tokens
+ *   j < seq_lens[b] - n_pos + p + 1 that exist. A query that sees no token gives zeros.
+ *   q, o        [batch, n_pos, num_heads, d] dtype
+ *   k_cache, v_cache [n_blocks, num_kv_heads, block_size, d] dtype
+ *   block_table [batch, max_blocks], seq_lens [batch] int32 (device)
+ *   n_pos       1 .. GDN_SPEC_MAX_POS
+ *   workspace   device scratch; its contents need no initialisation and carry no meaning
+ *               afterwards. Calls that may overlap need one each.
+ * Later positions' keys get no weight from an earlier one, but a NaN or infinity in the value
+ * row of one of the request's own newest n_pos tokens reaches all n_pos outputs. Results do
+ * not depend on the page order and are the same from run to run. batch == 0 is a no-op. */
+int gdn_paged_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_cache,
+                     const void* v_cache, int32_t n_blocks, int32_t block_size,
+                     const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
+                     int32_t batch, int32_t n_pos, void* o, void* workspace, size_t ws_bytes,
+                     void* stream);
+
 /* ------------------------------------------------------------------------------ utility */
 
 /* Static description of a status code (never NULL). */
