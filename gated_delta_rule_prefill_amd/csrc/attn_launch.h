@@ -56,4 +56,23 @@ struct PagedDecodeArgs {
 size_t paged_decode_layout(PagedDecodeArgs* a, void* ws);
 hipError_t launch_paged_decode(const PagedDecodeArgs& a, hipStream_t stream);
 
+// Latent decode (bf16): a request's n_pos x H query rows all read the same latents; they are
+// cut into row tiles of 16 * rt rows.
+struct LatentDecodeArgs {
+    int H, rank, d_nope, d_v, n_pos, max_blocks, n_blocks;
+    float scale;
+    const void *q_nope, *q_pe, *w_kv, *cache;
+    const int32_t* block_table;
+    FastDiv block;       // by the page size
+    SplitShape split;    // units = row_tiles
+    int rows, rt, row_tiles, n_wg;
+    void* o;
+    void* q_lat;         // [batch n_pos][H][rank] bf16: queries in the latent space
+    void* o_lat;         // [batch n_pos][H][rank] bf16: outputs there, of units not cut
+    float* part_o;       // [2 n_wg][16 rt][rank]
+    float* part_ml;      // [2 n_wg][16 rt][2]
+};
+size_t latent_decode_layout(LatentDecodeArgs* a, void* ws);
+hipError_t launch_latent_decode(const LatentDecodeArgs& a, hipStream_t stream);
+
 }  // namespace gdn

@@ -410,6 +410,45 @@ gdn::PagedDecodeArgs paged_args(const gdn_paged_dims_t* d, int32_t batch, int32_
     return a;
 }
 
+int check_latent_dims(const gdn_latent_dims_t* d) {
+    if (d == nullptr) return fail(GDN_ERR_NULL, "dims is NULL");
+    if (d->num_heads < 1) return fail(GDN_ERR_SHAPE, "num_heads must be >= 1 (got %d)", d->num_heads);
+    if (d->num_heads > GDN_ATTN_MAX_HEADS)
+        return fail(GDN_ERR_UNSUPPORTED, "num_heads must be <= %d (got %d)", GDN_ATTN_MAX_HEADS,
+                    d->num_heads);
+    if (d->dtype != GDN_DTYPE_BF16)
+        return fail(GDN_ERR_UNSUPPORTED, "latent attention takes bf16 (dtype 1), got %d", d->dtype);
+    if (d->rank != 256 && d->rank != 512)
+        return fail(GDN_ERR_UNSUPPORTED, "rank must be 256 or 512 (got %d)", d->rank);
+    if (d->d_rope != 64)
+        return fail(GDN_ERR_UNSUPPORTED, "d_rope must be 64 (got %d)", d->d_rope);
+    if ((d->d_nope != 64 && d->d_nope != 128) || d->d_v != d->d_nope)
+        return fail(GDN_ERR_UNSUPPORTED, "d_nope and d_v must be equal, 64 or 128 (got %d, %d)",
+                    d->d_nope, d->d_v);
+    return GDN_OK;
+}
+
+// The row counts of a call are kept in 32 bits.
+int check_latent_rows(const gdn_latent_dims_t* d, int64_t tokens) {
+    if (tokens * d->num_heads > 0x7fffffffll)
+        return fail(GDN_ERR_UNSUPPORTED, "tokens x heads must stay below 2^31 (got %lld x %d)",
+                    (long long)tokens, d->num_heads);
+    return GDN_OK;
+}
+
+gdn::LatentDecodeArgs latent_decode_args(const gdn_latent_dims_t* d, int32_t batch,
+                                         int32_t n_pos) {
+    gdn::LatentDecodeArgs a = {};
+    a.H = d->num_heads;
+    a.rank = d->rank;
+    a.d_nope = d->d_nope;
+    a.d_v = d->d_v;
+    a.n_pos = n_pos;
+    a.scale = d->scale;
+    a.split.batch = batch;
+    return a;
+}
+
 // Debug builds: valid cache slots of one append are distinct (as DEBUG_DISTINCT_SLOTS).
 #ifdef GDN_DEBUG_CHECKS
 int debug_distinct_cache_slots(const int64_t* slot_map, int32_t tokens, int64_t n_slots,
@@ -861,6 +900,57 @@ int gdn_paged_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_
     a.o = o;
     return launch_status(gdn::launch_paged_decode(a, static_cast<hipStream_t>(stream)),
                          "gdn_paged_decode");
+}
+
+int gdn_latent_decode_workspace_bytes(const gdn_latent_dims_t* dims, int32_t batch,
+                                      int32_t n_pos, size_t* bytes) {
+    int st = check_latent_dims(dims);
+    if (!st) st = check_batch(batch, n_pos);
+    if (!st) st = check_latent_rows(dims, (int64_t)batch * n_pos);
+    if (st) return st;
+    if (bytes == nullptr) return fail(GDN_ERR_NULL, "bytes is NULL");
+    gdn::LatentDecodeArgs a = latent_decode_args(dims, batch, n_pos);
+    *bytes = batch == 0 ? 0 : gdn::latent_decode_layout(&a, nullptr);
+    return ok();
+}
+
+int gdn_latent_decode(const gdn_latent_dims_t* dims, const void* q_nope, const void* q_pe,
+                      const void* w_kv, const void* cache, int32_t n_blocks, int32_t block_size,
+                      const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
+                      int32_t batch, int32_t n_pos, void* o, void* workspace, size_t ws_bytes,
+                      void* stream) {
+    int st = check_latent_dims(dims);
+    if (!st) st = check_batch(batch, n_pos);
+    if (!st) st = check_latent_rows(dims, (int64_t)batch * n_pos);
+    if (!st) st = check_cache(dims->dtype, 1, n_blocks, block_size);
+    if (!st) st = check_table(max_blocks, block_size);
+    if (st) return st;
+    if (batch == 0) return ok();
+    REQUIRE_PTR(q_nope);
+    REQUIRE_PTR(q_pe);
+    REQUIRE_PTR(w_kv);
+    REQUIRE_PTR(cache);
+    REQUIRE_PTR(block_table);
+    REQUIRE_PTR(seq_lens);
+    REQUIRE_PTR(o);
+    REQUIRE_PTR(workspace);
+    gdn::LatentDecodeArgs a = latent_decode_args(dims, batch, n_pos);
+    const size_t need = gdn::latent_decode_layout(&a, workspace);
+    if (ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    a.q_nope = q_nope;
+    a.q_pe = q_pe;
+    a.w_kv = w_kv;
+    a.cache = cache;
+    a.n_blocks = n_blocks;
+    a.block = gdn::FastDiv::of((uint32_t)block_size);
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.split.seq_lens = seq_lens;
+    a.split.max_keys = max_blocks * block_size;
+    a.o = o;
+    return launch_status(gdn::launch_latent_decode(a, static_cast<hipStream_t>(stream)),
+                         "gdn_latent_decode");
 }
 
 const char* gdn_status_string(int status) {

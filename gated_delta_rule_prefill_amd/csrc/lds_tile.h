@@ -1,0 +1,54 @@
+// Loads from global memory straight into LDS, and transposing LDS reads, for the attention
+// kernels.
+#pragma once
+#include "gdn_common.h"
+
+namespace gdn {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+
+// 64 lanes x 16 bytes from `base` + each lane's `offset` to the 1 KiB of LDS at `lds` (wave
+// uniform, lane l's piece at 16 l). No register receives data, and the compiler does not count
+// the load: lds_loads_done() has to come before the barrier behind which the data is read.
+// m0 carries the LDS address; the compiler keeps no value in it across statements.
+// (The builtin for the same instruction makes the compiler wait for every such load before any
+// later LDS read, which would end the overlap of one tile's load with the other's use.)
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
+                 : "memory");
+}
+// The same with a 64-bit address per lane.
+__device__ __forceinline__ void load_to_lds(const void* lane_address, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(lane_address)
+                 : "memory");
+}
+__device__ __forceinline__ void lds_loads_done() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Transposing read of 16-bit elements. Every 16 lanes read a block of 4 rows x 16 columns: lane
+// i passes the address of 4 columns (4 (i & 3) ..) of row i >> 2 and receives column i of the 4
+// rows.
+__device__ __forceinline__ bf16x4 lds_read_tr(const char* p) {
+    typedef __attribute__((address_space(3))) s16x4* lptr;
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(p)));
+}
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
+    bf16x8 r;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        r[i] = a[i];
+        r[4 + i] = b[i];
+    }
+    return r;
+}
+
+}  // namespace gdn

@@ -44,6 +44,12 @@ class gdn_paged_dims_t(ctypes.Structure):
                 ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class gdn_latent_dims_t(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("d_rope", ctypes.c_int32), ("d_nope", ctypes.c_int32), ("d_v", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
@@ -52,6 +58,7 @@ _DIMS = ctypes.POINTER(gdn_dims_t)
 _L = ctypes.c_int64
 _POOL = ctypes.POINTER(gdn_deltalog_pool_t)
 _PAGED = ctypes.POINTER(gdn_paged_dims_t)
+_LATENT = ctypes.POINTER(gdn_latent_dims_t)
 
 _SIGS = {
     "gdn_prefill_workspace_bytes": [_DIMS, _I, _I, _I, ctypes.POINTER(_SZ)],
@@ -77,6 +84,8 @@ _SIGS = {
     "gdn_latent_append": [_I, _P, _L, _P, _L, _P, _I, _I, _I, _P, _I, _I, _P],
     "gdn_paged_decode_workspace_bytes": [_PAGED, _I, _I, ctypes.POINTER(_SZ)],
     "gdn_paged_decode": [_PAGED, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _SZ, _P],
+    "gdn_latent_decode_workspace_bytes": [_LATENT, _I, _I, ctypes.POINTER(_SZ)],
+    "gdn_latent_decode": [_LATENT, _P, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _SZ, _P],
     "gdn_status_string": [ctypes.c_int],
     "gdn_last_error": [],
     "gdn_abi_version": [],
@@ -588,4 +597,52 @@ def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=1.0, o=No
             ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), int(n_blocks), int(bs),
             _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(B), int(P), _ptr(o),
             _ptr(workspace), int(workspace.numel() * workspace.element_size()), c.ptr))
+    return o
+
+
+def _latent_dims(H, rank, d_rope, d_nope, d_v, scale):
+    return gdn_latent_dims_t(int(H), int(rank), int(d_rope), int(d_nope), int(d_v),
+                             GDN_DTYPE_BF16, float(scale))
+
+
+def gdn_latent_decode_workspace_bytes(H, rank, d_rope, d_nope, d_v, batch, n_pos=1):
+    dims = _latent_dims(H, rank, d_rope, d_nope, d_v, 1.0)
+    out = _SZ(0)
+    _check("gdn_latent_decode_workspace_bytes", lib().gdn_latent_decode_workspace_bytes(
+        ctypes.byref(dims), int(batch), int(n_pos), ctypes.byref(out)))
+    return int(out.value)
+
+
+def gdn_latent_decode(q_nope, q_pe, w_kv, cache, block_table, seq_lens, scale=1.0, o=None,
+                      workspace=None, stream=None):
+    """Latent attention of the newest tokens, absorbed form (bf16). q_nope [B, H, d] or
+    [B, P, H, d], q_pe likewise with d_rope; w_kv [H, d_nope + d_v, rank] (the rows of the key
+    up projection, then of the value's; d_nope == d_v); cache [n_blocks, block_size, rank +
+    d_rope]; block_table [B, max_blocks] int32; seq_lens [B] int32. Returns o, shaped as
+    q_nope."""
+    qn = _positions(q_nope)
+    B, P, H, dn = qn.shape
+    rank, rope = w_kv.shape[2], q_pe.shape[-1]
+    dv = w_kv.shape[1] - dn
+    n_blocks, bs, _ = cache.shape
+    bf = torch.bfloat16
+    _want("q_nope", q_nope, q_nope.shape, bf)
+    _want("q_pe", q_pe, (*q_nope.shape[:-1], rope), bf)
+    _want("w_kv", w_kv, (H, dn + dv, rank), bf)
+    _want("cache", cache, (n_blocks, bs, rank + rope), bf)
+    _table(block_table, B)
+    _want("seq_lens", seq_lens, (B,), torch.int32)
+    with _Call(q_nope, stream) as c:
+        shape = (*q_nope.shape[:-1], dv)
+        o = c.new(shape, bf) if o is None else o
+        _want("o", o, shape, bf)
+        dims = _latent_dims(H, rank, rope, dn, dv, scale)
+        if workspace is None:
+            workspace = c.new((max(1, gdn_latent_decode_workspace_bytes(
+                H, rank, rope, dn, dv, B, P)),), torch.uint8)
+        _same_device(q_nope, q_pe, w_kv, cache, block_table, seq_lens, o, workspace)
+        _check("gdn_latent_decode", lib().gdn_latent_decode(
+            ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(w_kv), _ptr(cache), int(n_blocks),
+            int(bs), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(B), int(P),
+            _ptr(o), _ptr(workspace), int(workspace.numel() * workspace.element_size()), c.ptr))
     return o

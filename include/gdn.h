@@ -519,6 +519,43 @@ int gdn_paged_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_
                      int32_t batch, int32_t n_pos, void* o, void* workspace, size_t ws_bytes,
                      void* stream);
 
+/* Latent attention: a token's cache row is one latent c (rank elements) that all heads share,
+ * followed by one rotary key r (d_rope). With head h's up projections W_uk,h [d_nope, rank]
+ * and W_uv,h [d_v, rank], its key is (W_uk,h c, r) and its value W_uv,h c.
+ *   num_heads  1 .. GDN_ATTN_MAX_HEADS
+ *   rank       256 or 512;  d_rope 64;  d_nope == d_v, 64 or 128;  dtype GDN_DTYPE_BF16
+ *   scale      multiplies the scores (usually (d_nope + d_rope)^{-1/2}) */
+typedef struct {
+    int32_t num_heads;
+    int32_t rank;
+    int32_t d_rope;
+    int32_t d_nope;
+    int32_t d_v;
+    int32_t dtype;
+    float scale;
+} gdn_latent_dims_t;
+
+/* Workspace of gdn_latent_decode for the current device (host computation). */
+int gdn_latent_decode_workspace_bytes(const gdn_latent_dims_t* dims, int32_t batch,
+                                      int32_t n_pos, size_t* bytes);
+
+/* Latent attention of the newest n_pos tokens of every request over the cache, which already
+ * holds them, in the absorbed form: scores against the latents themselves,
+ *   s_j = scale ((W_uk,h^T q_nope) . c_j + q_pe . r_j),  o = W_uv,h sum_j softmax_j(s) c_j,
+ * over the tokens j < seq_lens[b] - n_pos + p + 1 that exist; zeros if there is none.
+ *   q_nope      [batch, n_pos, num_heads, d_nope],  q_pe [batch, n_pos, num_heads, d_rope]
+ *   w_kv        [num_heads, d_nope + d_v, rank]: W_uk,h over W_uv,h
+ *   cache       [n_blocks, block_size, rank + d_rope]
+ *   block_table [batch, max_blocks], seq_lens [batch] int32 (device);  n_pos 1 .. GDN_SPEC_MAX_POS
+ *   o           [batch, n_pos, num_heads, d_v]
+ * all bf16. W_uk^T q_nope and the softmax-weighted latents are rounded to bf16 as MFMA
+ * operands. Workspace, determinism and the newest tokens' values as in gdn_paged_decode. */
+int gdn_latent_decode(const gdn_latent_dims_t* dims, const void* q_nope, const void* q_pe,
+                      const void* w_kv, const void* cache, int32_t n_blocks, int32_t block_size,
+                      const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
+                      int32_t batch, int32_t n_pos, void* o, void* workspace, size_t ws_bytes,
+                      void* stream);
+
 /* ------------------------------------------------------------------------------ utility */
 
 /* Static description of a status code (never NULL). */

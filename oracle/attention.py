@@ -84,3 +84,83 @@ def paged_decode(q, k_cache, v_cache, table, lens, scale):
                 for h in range(g * (H // kv), (g + 1) * (H // kv)):
                     o[b, p, h], mag[b, p, h], top[b, p, h] = attend(q[b, p, h], k[m], v[m], scale)
     return o, mag, top
+
+
+def _latent_rows(cache, table_row, n_tokens):
+    """Existing cache rows of one request: (their positions, the rows) in fp64."""
+    n_blocks, block, _ = cache.shape
+    seen = visible(table_row, n_tokens, block, n_blocks)
+    pos = np.array([x[0] for x in seen], dtype=np.int64)
+    rows = cache[[x[1] for x in seen], [x[2] for x in seen]] if seen else cache[0, :0]
+    return pos, rows
+
+
+def _weights(s):
+    e = np.exp(s - s.max())
+    return e / e.sum()
+
+
+def latent_absorbed(q_nope, q_pe, w_kv, cache, table, lens, scale):
+    """Queries taken into the latent space, outputs taken out of it; q_* [B, P, H, .]."""
+    qn, qp, w, c = _f64(q_nope), _f64(q_pe), _f64(w_kv), _f64(cache)
+    table, lens = _i32(table), _i32(lens)
+    B, P, H, dn = qn.shape
+    R = w.shape[2]
+    o = np.zeros((B, P, H, w.shape[1] - dn))
+    for b in range(B):
+        pos, rows = _latent_rows(c, table[b], int(lens[b]))
+        for p in range(P):
+            x = rows[pos < int(lens[b]) - P + p + 1]
+            if len(x) == 0:
+                continue
+            for h in range(H):
+                q = np.concatenate([qn[b, p, h] @ w[h, :dn], qp[b, p, h]])
+                o[b, p, h] = w[h, dn:] @ (_weights(scale * (x @ q)) @ x[:, :R])
+    return o
+
+
+def latent_expanded(q_nope, q_pe, w_kv, cache, table, cu, lens, scale):
+    """Every head's keys and values written out; packed q_* [T, H, .], causal: the tokens of a
+    request are its last cu[i + 1] - cu[i]."""
+    qn, qp, w, c = _f64(q_nope), _f64(q_pe), _f64(w_kv), _f64(cache)
+    table, lens, cu = _i32(table), _i32(lens), _i32(cu)
+    T, H, dn = qn.shape
+    R = w.shape[2]
+    o = np.zeros((T, H, w.shape[1] - dn))
+    for i in range(len(cu) - 1):
+        pos, rows = _latent_rows(c, table[i], int(lens[i]))
+        new = int(cu[i + 1] - cu[i])
+        for h in range(H):
+            k = np.concatenate([rows[:, :R] @ w[h, :dn].T, rows[:, R:]], axis=1)
+            v = rows[:, :R] @ w[h, dn:].T
+            for t in range(new):
+                m = pos <= int(lens[i]) - new + t
+                if not m.any():
+                    continue
+                q = np.concatenate([qn[cu[i] + t, h], qp[cu[i] + t, h]])
+                o[cu[i] + t, h] = _weights(scale * (k[m] @ q)) @ v[m]
+    return o
+
+
+def latent_error(q_nope, q_pe, w_kv, rows, o, scale, u):
+    """Standard deviations that independent roundings leave in one output, for a query (q_nope
+    [dn], q_pe) of one head (w_kv [dn + dv, R]) over fp64 cache rows, with half step u: a
+    rounding's error is at most u of the value, and spread evenly over that range u / sqrt(3) of
+    it. Counted: the latent-space query (one rounding moves the scores of all keys together) and
+    the written-out keys, each softmax weight, the mixed latent and the written-out values, the
+    output. The absorbed and the expanded form make only some of these."""
+    dn, R = q_nope.shape[0], w_kv.shape[1]
+    if len(rows) == 0:
+        return np.zeros(w_kv.shape[0] - dn)
+    c = rows[:, :R]
+    ql, k, v = q_nope @ w_kv[:dn], c @ w_kv[:dn].T, c @ w_kv[dn:].T
+    p = _weights(scale * (c @ ql + rows[:, R:] @ q_pe))
+    e = u / np.sqrt(3.0)
+    dev = v - o                                   # a weight's error moves o by p_j (v_j - o)
+    query = scale * e * np.sqrt(((ql[:, None] * ((p[:, None] * c).T @ dev)) ** 2).sum(0))
+    key = scale * e * np.sqrt(((k * q_nope) ** 2).sum(1))
+    from_scores = np.hypot(query, np.sqrt((((p * key)[:, None] * dev) ** 2).sum(0)))
+    from_weights = e * np.sqrt(((p[:, None] * v) ** 2).sum(0))
+    mixed = e * np.sqrt(np.maximum(((w_kv[dn:] * (p @ c)) ** 2).sum(1),
+                                   ((p[:, None] * v) ** 2).sum(0)))
+    return np.sqrt(from_scores ** 2 + from_weights ** 2 + mixed ** 2 + (e * o) ** 2)
