@@ -75,4 +75,24 @@ struct LatentDecodeArgs {
 size_t latent_decode_layout(LatentDecodeArgs* a, void* ws);
 hipError_t launch_latent_decode(const LatentDecodeArgs& a, hipStream_t stream);
 
+// Latent prefill (bf16). Keys are laid out in the workspace request after request, each
+// starting at a new 64-key tile; queries in tiles of 128 rows of one request.
+struct LatentPrefillArgs {
+    int H, rank, d, n_seqs, total_tokens, max_blocks, n_blocks, max_keys;
+    float scale;
+    const void *q_nope, *q_pe, *w_kv, *cache;
+    const int32_t *block_table, *cu_seqlens, *seq_lens;
+    FastDiv block;       // by the page size
+    int key_tiles, q_tiles;  // bounds from the host's totals
+    void* o;
+    int32_t* key_tile;   // [n_seqs + 1] first key tile of each request
+    int32_t* q_tile;     // [n_seqs + 1] first query tile
+    uint64_t* exist;     // [key_tiles] a bit per key
+    void* k_pe;          // [key_tiles][64][64] rotary keys
+    void* k;             // [H][key_tiles][64][d]
+    void* vt;            // [H][key_tiles][d][64], keys of each 16 in the order of the weights
+};
+size_t latent_prefill_layout(LatentPrefillArgs* a, int64_t total_keys, void* ws);
+hipError_t launch_latent_prefill(const LatentPrefillArgs& a, hipStream_t stream);
+
 }  // namespace gdn

@@ -449,6 +449,34 @@ gdn::LatentDecodeArgs latent_decode_args(const gdn_latent_dims_t* d, int32_t bat
     return a;
 }
 
+int check_latent_prefill(const gdn_latent_dims_t* d, int32_t n_seqs, int32_t total_tokens,
+                         int64_t total_keys) {
+    int st = check_latent_dims(d);
+    if (st) return st;
+    if (n_seqs < 0 || total_tokens < 0 || total_keys < 0)
+        return fail(GDN_ERR_SHAPE, "n_seqs, total_tokens and total_keys must be >= 0 (got %d, %d, "
+                                   "%lld)", n_seqs, total_tokens, (long long)total_keys);
+    // tile counts, grids and their products stay in 32 bits
+    if (total_keys + (int64_t)n_seqs * 64 > 0x3fffffff ||
+        ((int64_t)total_tokens / 128 + n_seqs + 1) * d->num_heads > 0x7fffff)
+        return fail(GDN_ERR_UNSUPPORTED, "%lld keys, %d tokens in %d sequences, %d heads: split the "
+                                         "call", (long long)total_keys, total_tokens, n_seqs,
+                    d->num_heads);
+    return check_latent_rows(d, total_tokens);
+}
+
+gdn::LatentPrefillArgs latent_prefill_args(const gdn_latent_dims_t* d, int32_t n_seqs,
+                                           int32_t total_tokens) {
+    gdn::LatentPrefillArgs a = {};
+    a.H = d->num_heads;
+    a.rank = d->rank;
+    a.d = d->d_nope;
+    a.n_seqs = n_seqs;
+    a.total_tokens = total_tokens;
+    a.scale = d->scale;
+    return a;
+}
+
 // Debug builds: valid cache slots of one append are distinct (as DEBUG_DISTINCT_SLOTS).
 #ifdef GDN_DEBUG_CHECKS
 int debug_distinct_cache_slots(const int64_t* slot_map, int32_t tokens, int64_t n_slots,
@@ -951,6 +979,57 @@ int gdn_latent_decode(const gdn_latent_dims_t* dims, const void* q_nope, const v
     a.o = o;
     return launch_status(gdn::launch_latent_decode(a, static_cast<hipStream_t>(stream)),
                          "gdn_latent_decode");
+}
+
+int gdn_latent_prefill_workspace_bytes(const gdn_latent_dims_t* dims, int32_t n_seqs,
+                                       int32_t total_tokens, int64_t total_keys, size_t* bytes) {
+    int st = check_latent_prefill(dims, n_seqs, total_tokens, total_keys);
+    if (st) return st;
+    if (bytes == nullptr) return fail(GDN_ERR_NULL, "bytes is NULL");
+    gdn::LatentPrefillArgs a = latent_prefill_args(dims, n_seqs, total_tokens);
+    *bytes = n_seqs == 0 || total_tokens == 0
+                 ? 0 : gdn::latent_prefill_layout(&a, total_keys, nullptr);
+    return ok();
+}
+
+int gdn_latent_prefill(const gdn_latent_dims_t* dims, const void* q_nope, const void* q_pe,
+                       const void* w_kv, const void* cache, int32_t n_blocks, int32_t block_size,
+                       const int32_t* block_table, int32_t max_blocks, const int32_t* cu_seqlens,
+                       const int32_t* seq_lens, int32_t n_seqs, int32_t total_tokens,
+                       int64_t total_keys, void* o, void* workspace, size_t ws_bytes,
+                       void* stream) {
+    int st = check_latent_prefill(dims, n_seqs, total_tokens, total_keys);
+    if (!st) st = check_cache(dims->dtype, 1, n_blocks, block_size);
+    if (!st) st = check_table(max_blocks, block_size);
+    if (st) return st;
+    if (n_seqs == 0 || total_tokens == 0) return ok();
+    REQUIRE_PTR(q_nope);
+    REQUIRE_PTR(q_pe);
+    REQUIRE_PTR(w_kv);
+    REQUIRE_PTR(cache);
+    REQUIRE_PTR(block_table);
+    REQUIRE_PTR(cu_seqlens);
+    REQUIRE_PTR(seq_lens);
+    REQUIRE_PTR(o);
+    REQUIRE_PTR(workspace);
+    gdn::LatentPrefillArgs a = latent_prefill_args(dims, n_seqs, total_tokens);
+    const size_t need = gdn::latent_prefill_layout(&a, total_keys, workspace);
+    if (ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    a.q_nope = q_nope;
+    a.q_pe = q_pe;
+    a.w_kv = w_kv;
+    a.cache = cache;
+    a.n_blocks = n_blocks;
+    a.block = gdn::FastDiv::of((uint32_t)block_size);
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.max_keys = max_blocks * block_size;
+    a.cu_seqlens = cu_seqlens;
+    a.seq_lens = seq_lens;
+    a.o = o;
+    return launch_status(gdn::launch_latent_prefill(a, static_cast<hipStream_t>(stream)),
+                         "gdn_latent_prefill");
 }
 
 const char* gdn_status_string(int status) {

@@ -1,0 +1,483 @@
+// Latent attention of packed prompts, expanded form, causal (gdn_latent_prefill), bf16.
+//
+// Per head h: k_j = (W_uk,h c_j, r_j), v_j = W_uv,h c_j written out once (expand), then
+//   o_i = sum_{j <= pos_i} softmax_j(scale q_i . k_j) v_j   (attend)
+// with the running maximum and sum of a softmax over 64-key tiles. Against many queries per key
+// the written-out form needs 2 (2 d + 64) operations per (query, key, head) where the absorbed
+// form needs 2 (2 rank + 64).
+//
+// Three launches: the tile tables (prefix sums of the device-resident lengths), expand, attend.
+#include "attn_launch.h"
+#include "gdn_common.h"
+#include "lds_tile.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int LP_THREADS = 256;
+constexpr int LP_WAVES = LP_THREADS / WAVE;
+constexpr int LP_ROPE = 64;
+constexpr int LP_KB = 64;    // keys of a tile
+constexpr int LP_QB = 128;   // query rows of a tile
+constexpr float LOG2E = 1.4426950408889634f;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// Keys of request i that its table can address, and its new tokens.
+__device__ __forceinline__ int lp_keys(const LatentPrefillArgs& a, int i) {
+    return min(max(a.seq_lens[i], 0), a.max_keys);
+}
+__device__ __forceinline__ int lp_new(const LatentPrefillArgs& a, int i) {
+    const int s = min(max(a.cu_seqlens[i], 0), a.total_tokens);
+    return max(min(a.cu_seqlens[i + 1], a.total_tokens) - s, 0);
+}
+
+// Last i < n with first[i] <= t.
+__device__ __forceinline__ int lp_find(const int32_t* first, int n, int t) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= t) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------------------------- tables
+// Prefix sums of each request's key and query tiles, cut off at the host's bounds (lengths
+// that break the contract then lose keys or rows, never memory).
+__global__ __launch_bounds__(LP_THREADS) void latent_tiles_kernel(LatentPrefillArgs a) {
+    __shared__ int64_t part[LP_WAVES][2];
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+    const int per = (a.n_seqs + LP_THREADS - 1) / LP_THREADS;
+    const int i0 = min(tid * per, a.n_seqs), i1 = min(i0 + per, a.n_seqs);
+    int64_t k = 0, q = 0;
+    for (int i = i0; i < i1; i++) {
+        k += (lp_keys(a, i) + LP_KB - 1) / LP_KB;
+        q += (lp_new(a, i) + LP_QB - 1) / LP_QB;
+    }
+    int64_t ks = k, qs = q;
+#pragma unroll
+    for (int off = 1; off < WAVE; off <<= 1) {
+        const int64_t x = __shfl_up(ks, off, WAVE), y = __shfl_up(qs, off, WAVE);
+        if (lane >= off) {
+            ks += x;
+            qs += y;
+        }
+    }
+    if (lane == WAVE - 1) {
+        part[wave][0] = ks;
+        part[wave][1] = qs;
+    }
+    __syncthreads();
+    for (int w = 0; w < wave; w++) {
+        ks += part[w][0];
+        qs += part[w][1];
+    }
+    ks -= k;
+    qs -= q;
+    for (int i = i0; i < i1; i++) {
+        a.key_tile[i] = (int)min(ks, (int64_t)a.key_tiles);
+        a.q_tile[i] = (int)min(qs, (int64_t)a.q_tiles);
+        ks += (lp_keys(a, i) + LP_KB - 1) / LP_KB;
+        qs += (lp_new(a, i) + LP_QB - 1) / LP_QB;
+    }
+    if (tid == LP_THREADS - 1) {
+        a.key_tile[a.n_seqs] = (int)min(ks, (int64_t)a.key_tiles);
+        a.q_tile[a.n_seqs] = (int)min(qs, (int64_t)a.q_tiles);
+    }
+}
+
+// ---------------------------------------------------------------------------------- expand
+// A 128 x 128 product per workgroup: 128 keys (two key tiles) times 128 of the H 2 d rows of
+// w_kv, contraction over the rank in steps of 64, both operands loaded straight into LDS, two
+// buffers. Keys come through the block table. A wave's 64 output columns are all of one kind:
+// for keys the weights are the MFMA's A operand, so that a lane holds 4 dims of a key; for values
+// the latents are, so that it holds 4 keys of a dim: each is stored along its rows in memory
+// order, and the values come out transposed. Keys that do not exist are stored as zeros.
+constexpr int EX_M = 128, EX_N = 128, EX_K = 64;
+
+// LDS piece (16 bytes) c of row r of a tile with 128-byte rows
+__device__ __forceinline__ int row128(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
+
+__global__ __launch_bounds__(LP_THREADS) void latent_expand_kernel(LatentPrefillArgs a) {
+    __shared__ __align__(16) char lds[2][(EX_M + EX_N) * 128];
+    __shared__ uint32_t slot_of[EX_M];
+    const int tid = threadIdx.x, lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(wave_id());
+    const int t0 = blockIdx.x * 2;
+    const int used = a.key_tile[a.n_seqs];
+    if (t0 >= used) return;
+    const int R = a.rank, row_bytes = (R + LP_ROPE) * 2;
+    const char* cache = reinterpret_cast<const char*>(a.cache);
+
+    bool ok = false;
+    if (tid < EX_M) {
+        const int t = t0 + tid / LP_KB;
+        uint32_t slot = 0;
+        if (t < used) {
+            const int i = lp_find(a.key_tile, a.n_seqs, t);
+            const int key = (t - a.key_tile[i]) * LP_KB + tid % LP_KB;
+            if (key < lp_keys(a, i)) {
+                const uint32_t p = a.block((uint32_t)key);
+                const int page = a.block_table[(size_t)i * a.max_blocks + p];
+                ok = page >= 0 && page < a.n_blocks;
+                if (ok) slot = (uint32_t)page * a.block.div + ((uint32_t)key - p * a.block.div);
+            }
+        }
+        slot_of[tid] = slot | (ok ? 0u : 0x80000000u);  // slots stay below 2^31
+    }
+    __syncthreads();
+    if (blockIdx.y == 0) {
+        // this pair's rotary keys and existence bits, once for all heads
+        if (wave < 2) {
+            const uint64_t bits = __ballot(ok);
+            if (lane == 0 && t0 + wave < used) a.exist[t0 + wave] = bits;
+        }
+        for (int x = tid; x < EX_M * 8; x += LP_THREADS) {
+            const int r = x >> 3, c = x & 7;
+            if (t0 + r / LP_KB < used)
+                *reinterpret_cast<f32x4*>(reinterpret_cast<char*>(a.k_pe) +
+                                          ((size_t)t0 * LP_KB + r) * 128 + c * 16) =
+                    *reinterpret_cast<const f32x4*>(
+                        cache + (size_t)(slot_of[r] & 0x7fffffffu) * row_bytes + R * 2 + c * 16);
+        }
+    }
+    // loads: 8 rows of 128 bytes each; wave w brings latent rows 32 w .. and weight rows 32 w ..
+    const char* src[4];
+    const char* wsrc = reinterpret_cast<const char*>(a.w_kv) + (size_t)blockIdx.y * EX_N * R * 2;
+    uint32_t woff[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = wave * 32 + i * 8 + (lane >> 3);
+        const int c = (lane & 7) ^ ((r >> 1) & 7);
+        src[i] = cache + (size_t)(slot_of[r] & 0x7fffffffu) * row_bytes + c * 16;
+        woff[i] = (uint32_t)(r * R * 2 + c * 16);
+    }
+    auto load = [&](int k, int buf) {
+        const uint32_t at = lds_offset(lds[buf]) + wave * 32 * 128;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            load_to_lds(src[i] + k * (EX_K * 2), at + i * 1024);
+            load_to_lds(wsrc + k * (EX_K * 2), woff[i], at + EX_M * 128 + i * 1024);
+        }
+    };
+    const int col = lane & 15, grp = lane >> 4;
+    const int wm = wave >> 1, wn = wave & 1;
+    const int col0 = blockIdx.y * EX_N + wn * 64;  // this wave's 64 rows of w_kv
+    const int h = col0 / (2 * a.d), in_head = col0 - h * 2 * a.d;
+    const bool value = in_head >= a.d;
+    f32x4 acc[4][4];  // [key block][column block]
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) acc[i][j] = zero4();
+    load(0, 0);
+    const int steps = R / EX_K;
+    for (int k = 0; k < steps; k++) {
+        const char* at = lds[k & 1];
+        lds_loads_done();
+        lds_barrier();
+        if (k + 1 < steps) load(k + 1, (k + 1) & 1);
+#pragma unroll
+        for (int s = 0; s < EX_K / 32; s++) {
+            bf16x8 x[4], w[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                x[i] = *reinterpret_cast<const bf16x8*>(
+                    at + row128(wm * 64 + i * 16 + col, s * 4 + grp));
+                w[i] = *reinterpret_cast<const bf16x8*>(
+                    at + EX_M * 128 + row128(wn * 64 + i * 16 + col, s * 4 + grp));
+            }
+            if (value) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) acc[i][j] = Mma<bf16>::mma(x[i], w[j], acc[i][j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) acc[i][j] = Mma<bf16>::mma(w[j], x[i], acc[i][j]);
+            }
+        }
+    }
+    const int t = t0 + wm;
+    if (t >= used) return;
+    const size_t head_tile = (size_t)h * a.key_tiles + t;
+    if (value) {
+        bf16* out = reinterpret_cast<bf16*>(a.vt) + head_tile * a.d * LP_KB;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int key = i * 16 + grp * 4 + e;
+                    y[e] = slot_of[wm * 64 + key] >> 31 ? 0.f : acc[i][j][e];
+                }
+                // keys 4 g .. 4 g + 3 of a 16: the middle two groups change places
+                const int pos = i * 16 + ((grp & 1) << 3) + ((grp >> 1) << 2);
+                store4<bf16>(out + (size_t)(in_head - a.d + j * 16 + col) * LP_KB + pos, y);
+            }
+    } else {
+        bf16* out = reinterpret_cast<bf16*>(a.k) + head_tile * LP_KB * a.d;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int key = i * 16 + col;
+            const bool absent = slot_of[wm * 64 + key] >> 31;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) y[e] = absent ? 0.f : acc[i][j][e];
+                store4<bf16>(out + (size_t)key * a.d + in_head + j * 16 + grp * 4, y);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------- attend
+// A workgroup takes 128 query rows of one head, 32 a wave; all four waves walk the same key
+// tiles, loaded straight into LDS, two buffers, one barrier a tile. With 32 x 32 x 16 MFMAs:
+//   S^T = K Q^T     queries in registers as the B operand, so a query is an accumulator column:
+//                   its scores lie in two lanes, and its statistics need one exchange a tile;
+//   O^T += V^T P^T  the accumulator layout of S^T is the B operand's with the keys of each 16
+//                   renumbered, and V^T was written out in that order: weights never leave the
+//                   registers.
+template <int D>
+struct LpTile {
+    static constexpr int K_AT = 0;                                // [64][D] keys
+    static constexpr int PE_AT = LP_KB * D * 2;                   // [64][64] rotary keys
+    static constexpr int V_AT = PE_AT + LP_KB * LP_ROPE * 2;      // [D][64] values
+    static constexpr int BYTES = V_AT + D * LP_KB * 2;
+    // pieces of a key row turned by the row (256-byte rows: 16 pieces)
+    __device__ __forceinline__ static int turn(int r) { return D == 128 ? r & 15 : (r >> 1) & 7; }
+    __device__ __forceinline__ static int key(int r, int c) {
+        return r * (D * 2) + ((c ^ turn(r)) << 4);
+    }
+};
+
+template <int D>
+__global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPrefillArgs a) {
+    using X = LpTile<D>;
+    constexpr int NK = D / 16, NR = LP_ROPE / 16;  // contraction steps of a score
+    constexpr int NO = D / 32;                     // 32-column output tiles
+    __shared__ __align__(16) char tile[2][X::BYTES];
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(wave_id());
+    const int h = blockIdx.x % a.H;
+    const int n_qt = a.q_tile[a.n_seqs];
+    const int qt = n_qt - 1 - (int)(blockIdx.x / a.H);  // late (long) rows first
+    if (qt < 0) return;
+    const int seq = lp_find(a.q_tile, a.n_seqs, qt);
+    const int q0 = (qt - a.q_tile[seq]) * LP_QB;
+    const int fresh = lp_new(a, seq);
+    const int first_pos = a.seq_lens[seq] - fresh;      // of the request's first new token
+    const int kt0 = a.key_tile[seq];
+    const int keys = min(lp_keys(a, seq), (a.key_tile[seq + 1] - kt0) * LP_KB);
+    const int last_row = min(q0 + LP_QB, fresh) - 1;
+    const int reach = min(keys, first_pos + last_row + 1);  // keys that the tile's last row sees
+    const int nt = reach > 0 ? (reach + LP_KB - 1) / LP_KB : 0;
+
+    const int col = lane & 31, half = lane >> 5;
+    const int row = q0 + wave * 32 + col;               // this lane's query row
+    const bool live = row < fresh;
+    const int pos = first_pos + row;
+    const int wave_first = first_pos + q0 + wave * 32;  // position of the wave's first row
+    const size_t token = (size_t)min(max(a.cu_seqlens[seq], 0), a.total_tokens) +
+                         (live ? row : q0);
+    bf16x8 q[NK + NR];
+    {
+        const bf16* qn = reinterpret_cast<const bf16*>(a.q_nope) + (token * a.H + h) * D;
+        const bf16* qp = reinterpret_cast<const bf16*>(a.q_pe) + (token * a.H + h) * LP_ROPE;
+#pragma unroll
+        for (int f = 0; f < NK; f++) q[f] = Mma<bf16>::load(qn + f * 16 + half * 8);
+#pragma unroll
+        for (int f = 0; f < NR; f++) q[NK + f] = Mma<bf16>::load(qp + f * 16 + half * 8);
+    }
+    const char* ksrc = reinterpret_cast<const char*>(a.k) +
+                       ((size_t)h * a.key_tiles + kt0) * (LP_KB * D * 2);
+    const char* vsrc = reinterpret_cast<const char*>(a.vt) +
+                       ((size_t)h * a.key_tiles + kt0) * (LP_KB * D * 2);
+    const char* psrc = reinterpret_cast<const char*>(a.k_pe) + (size_t)kt0 * (LP_KB * LP_ROPE * 2);
+    auto load = [&](int t, int buf) {
+        const uint32_t at = lds_offset(tile[buf]);
+        constexpr int KI = LP_KB * D * 2 / 1024 / LP_WAVES;  // 1 KiB loads per wave
+#pragma unroll
+        for (int i = 0; i < KI; i++) {
+            const int x = (wave * KI + i) * 64 + lane;       // 16-byte piece of the key tile
+            const int r = x / (D / 8), c = x % (D / 8);
+            load_to_lds(ksrc + (size_t)t * (LP_KB * D * 2),
+                        (uint32_t)(r * (D * 2) + ((c ^ X::turn(r)) << 4)),
+                        at + X::K_AT + (wave * KI + i) * 1024);
+            const int vr = x >> 3, vc = x & 7;
+            load_to_lds(vsrc + (size_t)t * (LP_KB * D * 2),
+                        (uint32_t)(vr * 128 + ((vc ^ ((vr >> 1) & 7)) << 4)),
+                        at + X::V_AT + (wave * KI + i) * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int r = (wave * 2 + i) * 8 + (lane >> 3), c = lane & 7;
+            load_to_lds(psrc + (size_t)t * (LP_KB * LP_ROPE * 2),
+                        (uint32_t)(r * 128 + ((c ^ ((r >> 1) & 7)) << 4)),
+                        at + X::PE_AT + (wave * 2 + i) * 1024);
+        }
+    };
+    f32x16 acc[NO];
+#pragma unroll
+    for (int j = 0; j < NO; j++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) acc[j][i] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    const float cs = a.scale * LOG2E;
+    uint64_t exist_next = 0;
+    if (nt > 0) {
+        exist_next = a.exist[kt0];
+        load(0, 0);
+    }
+    for (int t = 0; t < nt; t++) {
+        const char* kt = tile[t & 1];
+        lds_loads_done();
+        // (moved to scalar registers here, where nothing is in flight: a wait for the ordinary
+        // load further down would also wait for the tile loads issued behind it)
+        const uint64_t exist =
+            (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(exist_next >> 32)) << 32 |
+            (uint32_t)__builtin_amdgcn_readfirstlane((int)exist_next);
+        lds_barrier();  // tile t is whole; all waves are done with the other buffer
+        if (t + 1 < nt) {
+            exist_next = a.exist[kt0 + t + 1];
+            load(t + 1, (t + 1) & 1);
+        }
+        const int key0 = t * LP_KB;
+        if (key0 > wave_first + 31) continue;  // beyond all of this wave's rows
+        f32x16 s[2];
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) s[x][i] = 0.f;
+#pragma unroll
+        for (int f = 0; f < NK + NR; f++)
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                const int r = x * 32 + col;
+                const bf16x8 k = *reinterpret_cast<const bf16x8*>(
+                    kt + (f < NK ? X::K_AT + X::key(r, f * 2 + half)
+                                 : X::PE_AT + row128(r, (f - NK) * 2 + half)));
+                s[x] = mma32(k, q[f], s[x]);
+            }
+        if (exist != ~0ull || key0 + LP_KB - 1 > wave_first) {
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int k = x * 32 + (i >> 2) * 8 + half * 4 + (i & 3);
+                    const bool keep = ((exist >> k) & 1) && key0 + k <= pos;
+                    s[x][i] = keep ? s[x][i] * cs : -INFINITY;
+                }
+        } else {
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) s[x][i] *= cs;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) top = fmaxf(top, s[x][i]);
+        top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+        const float m1 = fmaxf(m, top);
+        const float ref = m1 == -INFINITY ? 0.f : m1;  // a row with no key so far
+        if (__any(m1 > m)) {
+            const float shrink = __builtin_amdgcn_exp2f(m - ref);
+            l *= shrink;
+#pragma unroll
+            for (int j = 0; j < NO; j++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) acc[j][i] *= shrink;
+            m = m1;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                s[x][i] = __builtin_amdgcn_exp2f(s[x][i] - ref);
+                l += s[x][i];
+            }
+#pragma unroll
+        for (int st = 0; st < LP_KB / 16; st++) {
+            bf16x8 p;
+#pragma unroll
+            for (int i = 0; i < 8; i++) p[i] = (bf16)s[st >> 1][(st & 1) * 8 + i];
+#pragma unroll
+            for (int j = 0; j < NO; j++) {
+                const bf16x8 v = *reinterpret_cast<const bf16x8*>(
+                    kt + X::V_AT + row128(j * 32 + col, st * 2 + half));
+                acc[j] = mma32(v, p, acc[j]);
+            }
+        }
+    }
+    l += __shfl_xor(l, 32, WAVE);
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros
+    if (live) {
+        bf16* out = reinterpret_cast<bf16*>(a.o) + (token * a.H + h) * D;
+#pragma unroll
+        for (int j = 0; j < NO; j++)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) y[e] = acc[j][i + e] * inv;
+                store4<bf16>(out + j * 32 + (i >> 2) * 8 + half * 4, y);
+            }
+    }
+}
+
+}  // namespace
+
+size_t latent_prefill_layout(LatentPrefillArgs* a, int64_t total_keys, void* ws) {
+    // sum_i ceil(len_i / B) <= (sum len_i + n (B - 1)) / B
+    a->key_tiles = (int)((total_keys + (int64_t)a->n_seqs * (LP_KB - 1)) / LP_KB);
+    a->q_tiles = (int)((a->total_tokens + (int64_t)a->n_seqs * (LP_QB - 1)) / LP_QB);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char* p = ws == nullptr ? nullptr : static_cast<char*>(ws) + off;
+        off += (bytes + 255) & ~(size_t)255;
+        return p;
+    };
+    const size_t tiles = (size_t)a->key_tiles;
+    a->key_tile = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * (size_t)(a->n_seqs + 1)));
+    a->q_tile = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * (size_t)(a->n_seqs + 1)));
+    a->exist = reinterpret_cast<uint64_t*>(take(sizeof(uint64_t) * tiles));
+    a->k_pe = take(tiles * LP_KB * LP_ROPE * 2);
+    a->k = take(tiles * LP_KB * a->d * 2 * a->H);
+    a->vt = take(tiles * LP_KB * a->d * 2 * a->H);
+    return off;
+}
+
+hipError_t launch_latent_prefill(const LatentPrefillArgs& a, hipStream_t s) {
+    (void)hipGetLastError();  // report only errors raised by this call's launches
+    const dim3 block(LP_THREADS);
+    hipLaunchKernelGGL(latent_tiles_kernel, dim3(1), block, 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.q_tiles == 0) return e;
+    if (a.key_tiles > 0) {
+        const unsigned columns = (unsigned)(a.H * 2 * a.d / EX_N);  // d 64 or 128: whole tiles
+        hipLaunchKernelGGL(latent_expand_kernel, dim3((unsigned)(a.key_tiles + 1) / 2, columns),
+                           block, 0, s, a);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const dim3 grid((unsigned)a.q_tiles * (unsigned)a.H);
+    if (a.d == 128) hipLaunchKernelGGL(latent_attend_kernel<128>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(latent_attend_kernel<64>, grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace gdn

@@ -86,6 +86,9 @@ _SIGS = {
     "gdn_paged_decode": [_PAGED, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _SZ, _P],
     "gdn_latent_decode_workspace_bytes": [_LATENT, _I, _I, ctypes.POINTER(_SZ)],
     "gdn_latent_decode": [_LATENT, _P, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _SZ, _P],
+    "gdn_latent_prefill_workspace_bytes": [_LATENT, _I, _I, _L, ctypes.POINTER(_SZ)],
+    "gdn_latent_prefill": [_LATENT, _P, _P, _P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _L, _P, _P,
+                           _SZ, _P],
     "gdn_status_string": [ctypes.c_int],
     "gdn_last_error": [],
     "gdn_abi_version": [],
@@ -645,4 +648,48 @@ def gdn_latent_decode(q_nope, q_pe, w_kv, cache, block_table, seq_lens, scale=1.
             ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(w_kv), _ptr(cache), int(n_blocks),
             int(bs), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(B), int(P),
             _ptr(o), _ptr(workspace), int(workspace.numel() * workspace.element_size()), c.ptr))
+    return o
+
+
+def gdn_latent_prefill_workspace_bytes(H, rank, d_rope, d_nope, d_v, n_seqs, total_tokens,
+                                       total_keys):
+    dims = _latent_dims(H, rank, d_rope, d_nope, d_v, 1.0)
+    out = _SZ(0)
+    _check("gdn_latent_prefill_workspace_bytes", lib().gdn_latent_prefill_workspace_bytes(
+        ctypes.byref(dims), int(n_seqs), int(total_tokens), int(total_keys), ctypes.byref(out)))
+    return int(out.value)
+
+
+def gdn_latent_prefill(q_nope, q_pe, w_kv, cache, block_table, cu_seqlens, seq_lens, total_keys,
+                       scale=1.0, o=None, workspace=None, stream=None):
+    """Latent attention of packed new tokens, expanded form, causal (bf16). q_nope [T, H, d],
+    q_pe [T, H, d_rope]; w_kv, cache and block_table as gdn_latent_decode; cu_seqlens [n + 1]
+    int32; seq_lens [n] int32, the new tokens included; total_keys >= the sum of seq_lens.
+    Returns o [T, H, d]."""
+    T, H, dn = q_nope.shape
+    n = int(seq_lens.numel())
+    rank, rope = w_kv.shape[2], q_pe.shape[2]
+    dv = w_kv.shape[1] - dn
+    n_blocks, bs, _ = cache.shape
+    bf = torch.bfloat16
+    _want("q_nope", q_nope, (T, H, dn), bf)
+    _want("q_pe", q_pe, (T, H, rope), bf)
+    _want("w_kv", w_kv, (H, dn + dv, rank), bf)
+    _want("cache", cache, (n_blocks, bs, rank + rope), bf)
+    _table(block_table, n)
+    _want("cu_seqlens", cu_seqlens, (n + 1,), torch.int32)
+    _want("seq_lens", seq_lens, (n,), torch.int32)
+    with _Call(q_nope, stream) as c:
+        o = c.new((T, H, dv), bf) if o is None else o
+        _want("o", o, (T, H, dv), bf)
+        dims = _latent_dims(H, rank, rope, dn, dv, scale)
+        if workspace is None:
+            workspace = c.new((max(1, gdn_latent_prefill_workspace_bytes(
+                H, rank, rope, dn, dv, n, T, total_keys)),), torch.uint8)
+        _same_device(q_nope, q_pe, w_kv, cache, block_table, cu_seqlens, seq_lens, o, workspace)
+        _check("gdn_latent_prefill", lib().gdn_latent_prefill(
+            ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(w_kv), _ptr(cache), int(n_blocks),
+            int(bs), _ptr(block_table), int(block_table.shape[1]), _ptr(cu_seqlens),
+            _ptr(seq_lens), n, int(T), int(total_keys), _ptr(o), _ptr(workspace),
+            int(workspace.numel() * workspace.element_size()), c.ptr))
     return o

@@ -556,6 +556,36 @@ int gdn_latent_decode(const gdn_latent_dims_t* dims, const void* q_nope, const v
                       int32_t batch, int32_t n_pos, void* o, void* workspace, size_t ws_bytes,
                       void* stream);
 
+/* Workspace of gdn_latent_prefill (host computation): keys and values of every head for
+ * total_keys tokens, 2 d_nope x 2 bytes each, tables and the rotary keys. */
+int gdn_latent_prefill_workspace_bytes(const gdn_latent_dims_t* dims, int32_t n_seqs,
+                                       int32_t total_tokens, int64_t total_keys, size_t* bytes);
+
+/* Latent attention of packed new tokens over the cache, which already holds them, in the
+ * expanded form: every head's keys (W_uk,h c_j, r_j) and values W_uv,h c_j are written out to
+ * the workspace (bf16) and attended causally. The new tokens of request i are its last
+ * w = cu_seqlens[i + 1] - cu_seqlens[i]; what comes before them (a cached prefix, earlier
+ * chunks of the prompt) is read from its pages like they are. New token t sees the request's
+ * tokens j <= seq_lens[i] - w + t that exist; zeros if there is none.
+ *   q_nope      [total_tokens, num_heads, d_nope],  q_pe [total_tokens, num_heads, d_rope]
+ *   w_kv, cache, block_table [n_seqs, max_blocks], seq_lens [n_seqs] as in gdn_latent_decode
+ *   cu_seqlens  [n_seqs + 1] int32 (device), as in gdn_prefill_chunked. Rows of o from
+ *               cu_seqlens[n_seqs] on (a padded batch) are left as they are.
+ *   total_keys  at least the sum of seq_lens over the requests with max_blocks * block_size
+ *               as each one's limit (the host keeps these lengths to size its pages). If the
+ *               device lengths exceed it, keys past it are not seen; no memory is touched
+ *               outside the arrays.
+ *   o           [total_tokens, num_heads, d_v]
+ * Workspace and determinism as in gdn_paged_decode. A NaN or infinity in the row of one of a
+ * request's tokens can reach the outputs of up to 63 tokens before it. n_seqs == 0 and
+ * total_tokens == 0 are no-ops. */
+int gdn_latent_prefill(const gdn_latent_dims_t* dims, const void* q_nope, const void* q_pe,
+                       const void* w_kv, const void* cache, int32_t n_blocks, int32_t block_size,
+                       const int32_t* block_table, int32_t max_blocks, const int32_t* cu_seqlens,
+                       const int32_t* seq_lens, int32_t n_seqs, int32_t total_tokens,
+                       int64_t total_keys, void* o, void* workspace, size_t ws_bytes,
+                       void* stream);
+
 /* ------------------------------------------------------------------------------ utility */
 
 /* Static description of a status code (never NULL). */

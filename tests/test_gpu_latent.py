@@ -146,3 +146,126 @@ def test_latent_decode_three_and_four_dims_agree():
     a = _run_decode(case)
     b = _run_decode((case[0][:, 0].contiguous(), case[1][:, 0].contiguous(), *case[2:]))
     assert b.shape == (2, 4, 128) and torch.equal(a[:, 0], b)
+
+
+# --------------------------------------------------------------------------------- prefill
+def _prefill_case(seed, ctx, new, H, R, d, block, poison=True, q_scale=1.5):
+    g = gen(seed)
+    lens = [c + w for c, w in zip(ctx, new)]
+    table, cache = _cache(g, lens, block, R, poison)
+    T = sum(new)
+    cu = torch.tensor([0] + np.cumsum(new).tolist(), dtype=torch.int32)
+    return (normal(g, T, H, d, scale=q_scale), normal(g, T, H, ROPE, scale=q_scale),
+            _weights(g, H, R, d), cache, table, cu, torch.tensor(lens, dtype=torch.int32),
+            (d + ROPE) ** -0.5)
+
+
+def _run_prefill(case, keys=None, **kw):
+    keys = int(case[6].clamp_min(0).sum()) if keys is None else keys
+    o = gdn.gdn_latent_prefill(*(x.to(DEV) for x in case[:7]), keys, scale=case[7], **kw)
+    torch.cuda.synchronize()
+    return o
+
+
+def _check_prefill(case, keys=None, every=1):
+    """`every`: tokens of which the tolerance is worked out (it costs a pass over the keys)."""
+    qn, qp, w, cache, table, cu, lens, scale = case
+    clean = torch.nan_to_num(cache.float()).double()
+    want = attention.latent_expanded(qn, qp, w, clean, table, cu, lens, scale)
+    o = _run_prefill(case, keys)
+    limits = []
+    for i in range(len(lens)):
+        new = int(cu[i + 1] - cu[i])
+        limits += [(i, int(lens[i]) - new + t + 1) for t in range(new)]
+    pick = list(range(0, len(limits), every))
+    tol = _tolerance(qn[pick], qp[pick], w, cache, table, [limits[t] for t in pick], want[pick],
+                     scale)
+    assert_within(o[pick], want[pick], tol)
+    assert torch.isfinite(o.float()).all()
+    return o
+
+
+@pytest.mark.parametrize("R,d", [(512, 128), (256, 64), (512, 64), (256, 128)])
+@pytest.mark.parametrize("H,block", [(1, 16), (3, 64), (2, 5), (2, 640)])
+def test_latent_prefill(R, d, H, block):
+    say(f"case latent prefill R={R} d={d} H={H} block={block}")
+    _check_prefill(_prefill_case(R + d + H, [0, 0, 70, 5, 0, 130], [1, 130, 3, 0, 65, 40], H, R,
+                                 d, block))
+
+
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 257])
+def test_latent_prefill_lengths(n):
+    say(f"case latent prefill length {n}")
+    _check_prefill(_prefill_case(n, [0], [n], 2, 256, 64, 64))
+
+
+@pytest.mark.parametrize("ctx,new", [([900], [1]), ([700], [100]), ([0], [900]), ([1], [300])])
+def test_latent_prefill_long_rows(ctx, new):
+    say(f"case latent prefill long {ctx} {new}")
+    _check_prefill(_prefill_case(9, ctx, new, 2, 512, 128, 64), every=5)
+
+
+def test_latent_prefill_many_sequences():
+    say("case latent prefill n=300")
+    g = gen(5)
+    new = torch.randint(0, 7, (300,), generator=g).tolist()
+    ctx = torch.randint(0, 30, (300,), generator=g).tolist()
+    _check_prefill(_prefill_case(6, ctx, new, 1, 256, 64, 16), every=3)
+
+
+@pytest.mark.parametrize("block", [8, 64, 100])
+def test_latent_prefill_null_blocks(block):
+    """Null entries, ids past the pool; a request whose first rows see nothing."""
+    say(f"case latent prefill null {block}")
+    case = list(_prefill_case(9, [60, 0, 0], [200, 130, 20], 2, 512, 128, block))
+    case[4][0, 0] = -1
+    case[4][0, 1] = 1 << 30
+    case[4][1, 0] = -9
+    case[4][2, :] = -1
+    o = _check_prefill(tuple(case), every=3)
+    assert torch.equal(o[330:], torch.zeros_like(o[330:]))
+    assert torch.equal(o[200], torch.zeros_like(o[200]))
+
+
+def test_latent_prefill_more_new_tokens_than_the_length():
+    """seq_lens below the packed rows: the first rows lie before the request's start."""
+    say("case latent prefill new > len")
+    case = list(_prefill_case(10, [0, 0], [40, 10], 2, 256, 64, 16, poison=False))
+    case[6] = torch.tensor([25, 0], dtype=torch.int32)
+    o = _check_prefill(tuple(case))
+    assert torch.equal(o[:15], torch.zeros_like(o[:15]))
+    assert torch.equal(o[40:], torch.zeros_like(o[40:]))
+
+
+def test_latent_prefill_leaves_rows_behind_the_last_sequence():
+    say("case latent prefill padded")
+    case = list(_prefill_case(11, [0, 20], [70, 33], 2, 256, 64, 16))
+    want = _run_prefill(tuple(case))
+    pad = [torch.cat([x, torch.full((50, *x.shape[1:]), float("nan"), dtype=BF16)])
+           for x in case[:2]]
+    o = torch.full((153, 2, 64), 7.0, dtype=BF16, device=DEV)
+    got = _run_prefill((*pad, *case[2:]), keys=1000, o=o)
+    assert torch.equal(got[:103], want)
+    assert torch.equal(got[103:], torch.full_like(got[103:], 7.0))
+
+
+def test_latent_prefill_with_too_few_keys_stays_inside():
+    """A total_keys below the lengths loses keys: outputs of the requests before are right."""
+    say("case latent prefill short total_keys")
+    case = _prefill_case(12, [0, 0], [100, 300], 2, 256, 64, 16, poison=False)
+    full = _run_prefill(case)
+    got = _run_prefill(case, keys=128)
+    assert torch.equal(got[:100], full[:100]) and torch.isfinite(got.float()).all()
+
+
+def test_latent_prefill_equals_decode_token_by_token():
+    """The two forms of the same attention agree to rounding."""
+    say("case latent prefill vs decode")
+    case = _prefill_case(13, [37], [9], 4, 512, 128, 16, poison=False)
+    a = _run_prefill(case).float()
+    qn, qp, w, cache, table, cu, lens, scale = case
+    b = gdn.gdn_latent_decode(qn[None].to(DEV), qp[None].to(DEV), w.to(DEV), cache.to(DEV),
+                              table.to(DEV), lens.to(DEV), scale=scale)[0].float()
+    torch.cuda.synchronize()
+    # each is within its roundings (a few half steps of 2^-8) of the same value
+    assert (a - b).abs().max() <= 0.05 * b.abs().max()
