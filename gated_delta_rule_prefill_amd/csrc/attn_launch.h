@@ -47,7 +47,7 @@ struct PagedDecodeArgs {
     const int32_t* block_table;
     FastDiv block;       // by the page size
     SplitShape split;    // units = kv_heads * row_tiles
-    int group, rows, rt, row_tiles, n_wg;
+    int group, rows, rt, row_tiles, n_wg, n_join;
     void* o;
     float* part_o;       // [2 n_wg][16 rt][d]
     float* part_ml;      // [2 n_wg][16 rt][2]
@@ -65,10 +65,10 @@ struct LatentDecodeArgs {
     const int32_t* block_table;
     FastDiv block;       // by the page size
     SplitShape split;    // units = row_tiles
-    int rows, rt, row_tiles, n_wg;
+    int rows, rt, row_tiles, n_wg, n_join;
     void* o;
     void* q_lat;         // [batch n_pos][H][rank] bf16: queries in the latent space
-    void* o_lat;         // [batch n_pos][H][rank] bf16: outputs there, of units not cut
+    float* o_lat;        // [batch n_pos][H][rank]: outputs there
     float* part_o;       // [2 n_wg][16 rt][rank]
     float* part_ml;      // [2 n_wg][16 rt][2]
 };

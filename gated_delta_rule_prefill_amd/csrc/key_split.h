@@ -4,7 +4,7 @@
 //
 // A unit that one workgroup covers whole is finished by it. A unit cut between workgroups
 // leaves one partial result (unnormalised output, running maximum and sum, per row) per
-// workgroup that touched it, and a second kernel joins them. A workgroup can touch at most two
+// workgroup that touched it, and a second kernel joins them (key_join.h). A workgroup can touch at most two
 // cut units (its first and its last), so it owns two partial slots: 2 w for the unit it starts
 // with, 2 w + 1 for a later one. Work is even to one chunk whatever the lengths, the slots are
 // as many as the grid is wide, and the sums run in a fixed order.
@@ -43,13 +43,6 @@ __device__ __forceinline__ int split_chunks(const SplitShape& s, int b) {
     return (split_keys(s, b) + KB - 1) / KB;
 }
 
-template <typename V>
-__device__ __forceinline__ V wave_sum(V x) {
-#pragma unroll
-    for (int off = WAVE / 2; off > 0; off >>= 1) x += __shfl_xor(x, off, WAVE);
-    return x;
-}
-
 // Workgroups that get work, the first chunk of workgroup w, and the owner of chunk x.
 __device__ __forceinline__ int split_wgs(int64_t total, int n_wg) {
     return total < n_wg ? (int)total : n_wg;
@@ -59,6 +52,13 @@ __device__ __forceinline__ int64_t split_start(int w, int64_t total, int n) {
 }
 __device__ __forceinline__ int split_owner(int64_t x, int64_t total, int n) {
     return (int)(((uint64_t)(x + 1) * (uint32_t)n - 1) / (uint64_t)total);
+}
+
+// Workgroup-uniform values moved to scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 | lo);
 }
 
 // This workgroup's run of chunks [pos, end), and the request that chunk `pos` lies in, whose
@@ -109,24 +109,13 @@ __device__ SplitRun split_run(const SplitShape& s, int w, int n_wg) {
         found_b = b;
     }
     __syncthreads();
-    r.base = found_base;
-    r.b = found_b;
-    if (r.pos >= r.end) r.b = 0;  // nothing to do (found_* may be unset)
+    // (found_* are unset when there is nothing to do)
+    const bool any = r.pos < r.end;
+    r.base = uniform(any ? found_base : 0);
+    r.b = uniform(any ? found_b : 0);
+    r.pos = uniform(r.pos);
+    r.end = uniform(r.end);
     return r;
-}
-
-// For the joining kernel: first chunk of request b and the total, by one wave.
-template <int KB>
-__device__ __forceinline__ void split_base(const SplitShape& s, int b, int64_t* base,
-                                           int64_t* total) {
-    int64_t before = 0, all = 0;
-    for (int i = lane_id(); i < s.batch; i += WAVE) {
-        const int64_t c = split_chunks<KB>(s, i);
-        all += c;
-        if (i < b) before += c;
-    }
-    *base = wave_sum(before) * s.units;
-    *total = wave_sum(all) * s.units;
 }
 
 }  // namespace gdn

@@ -7,11 +7,12 @@
 //   s_j = scale (q'_h . c_j + q_pe,h . r_j),  p = softmax(s),  u_h = sum_j p_j c_j   (core)
 //   o_h = W_uv,h u_h              (up)
 // no key or value of a head is ever written out: the core reads each cache row once for all
-// heads. Three launches; the core's work split and its join are key_split.h's, the join runs at
-// the start of `up`.
+// heads. Four launches; the core's work split is key_split.h's, the join between core and up
+// key_join.h's.
 #include "attn_launch.h"
 #include "gdn_common.h"
 #include "gdn_launch.h"
+#include "key_join.h"
 #include "lds_tile.h"
 
 namespace gdn {
@@ -92,14 +93,17 @@ __global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeA
 }
 
 // ------------------------------------------------------------------------------------ core
-// A workgroup of 4 RH waves holds one row tile (16 RT RH query rows) and walks 64 keys at a time:
-//   S^T = K Q^T   wave w takes keys 16 (w & 3) .. + 15 of the tile for the 16 RT rows of part
-//                 w >> 2; the queries stay in registers, K fragments come from LDS;
+// A workgroup holds one row tile (16 RH query rows) and walks 64 keys at a time:
+//   S^T = K Q^T   each wave takes 16 KS of the keys for 16 of the rows; the queries stay in
+//                 registers, K fragments come from LDS;
 //   softmax       the row maximum goes over the waves through LDS, weights go back as bf16;
-//   U^T += C^T P^T  wave w takes rank / (4 RH) of the output columns for all rows; C^T by
-//                 transposing LDS reads of the very tile the scores came from.
+//   U^T += C^T P^T  each wave takes its share of the rank for all rows; C^T by transposing LDS
+//                 reads of the very tile the scores came from.
 // So each cache row is read once from memory per row tile; from LDS a tile is read RH times as
 // keys and once as values. The next tile loads straight into the other LDS buffer meanwhile.
+// (64 rows with 32 rows a wave read the keys twice only, but their queries take 144 registers:
+// the compiler then spills inside the key loop, and a reload from scratch memory waits for the
+// tile loads issued before it.)
 constexpr int LD_KB = 64;
 
 template <int R>
@@ -126,58 +130,87 @@ __device__ __forceinline__ int ld_weight(int row, int piece) {
     return row * (LD_KB * 2) + ((piece ^ ((row >> 1) & 7)) << 4);
 }
 
-template <int R, int RT, int RH>
-__global__ __launch_bounds__(LD_THREADS * RH) void latent_core_kernel(LatentDecodeArgs a) {
+template <int RH, int KS>
+struct LdWaves {
+    static constexpr int KEYS = 16 * KS;            // keys of a wave
+    static constexpr int GROUPS = LD_KB / KEYS;     // waves side by side along the keys
+    static constexpr int WAVES = GROUPS * RH;
+    static constexpr int OWN = LD_KB / WAVES;       // tile rows that a wave loads
+};
+
+template <int R, int RH, int KS>
+__global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_kernel(
+    LatentDecodeArgs a) {
     using X = LdTile<R>;
-    constexpr int WAVES = 4 * RH;
-    constexpr int TILES = RT * RH, ROWS = 16 * TILES;
+    using Y = LdWaves<RH, KS>;
+    constexpr int WAVES = Y::WAVES, KEYS = Y::KEYS, OWN = Y::OWN;
+    constexpr uint32_t ALL = (uint32_t)((1ull << KEYS) - 1);
+    constexpr int ROWS = 16 * RH;
     constexpr int NL = R / 32, NF = NL + LD_ROPE / 32;  // key fragments: latent, then rotary
     constexpr int NT = R / 16 / WAVES;                  // 16-column output tiles per wave
-    constexpr int OWN = 16 / RH;                        // rows of a tile that a wave loads
     __shared__ __align__(16) char tile[2 * X::BYTES];
     __shared__ __align__(16) char wt[ROWS * LD_KB * 2];
-    __shared__ float tops[4][ROWS];
+    __shared__ float tops[Y::GROUPS][ROWS];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int col = lane & 15, grp = lane >> 4;
-    const int kq = wave & 3, part = wave >> 2;  // key quarter; row part of the scores
-    SplitRun run = split_run<LD_KB, LD_THREADS * RH>(a.split, blockIdx.x, a.n_wg);
+    const int kg = wave / RH, part = wave % RH;  // key group and 16-row part of the scores
+    const int key_row = kg * KEYS;               // first tile row of this wave's keys
+    SplitRun run = split_run<LD_KB, WAVES * WAVE>(a.split, blockIdx.x, a.n_wg);
     const int64_t run_start = run.pos;
     const float cs = a.scale * LOG2E;
     const char* cache = reinterpret_cast<const char*>(a.cache);
 
+    // LDS byte offsets of this lane's reads (the piece index is xored with a function of the
+    // row, so most of it folds into an immediate: four offsets for the key fragments, one for
+    // the transposing reads, whose second half lies 4 rows on with the lowest piece bit turned)
+    int k_at[4], pe_at[2], p_at[2];
+#pragma unroll
+    for (int f = 0; f < 4; f++) k_at[f] = X::lat(key_row + col, f * 4 + grp);
+#pragma unroll
+    for (int f = 0; f < 2; f++) {
+        pe_at[f] = X::rope(key_row + col, f * 4 + grp);
+        p_at[f] = ld_weight(col, f * 4 + grp);
+    }
+    const int v_at = X::lat(grp * 8 + ((lane >> 2) & 3), wave * NT * 2 + ((lane & 3) >> 1)) +
+                     (lane & 1) * 8;
+
     while (run.pos < run.end) {
         const int b = run.b;
-        const int nkeys = split_keys(a.split, b);
+        const int nkeys = uniform(split_keys(a.split, b));
         const int nch = (nkeys + LD_KB - 1) / LD_KB;
-        const int unit = (int)((run.pos - run.base) / nch);
+        const int unit = uniform((int)((run.pos - run.base) / nch));
         const int c0 = (int)(run.pos - run.base - (int64_t)unit * nch);
         const int c1 = (int)min((int64_t)nch, c0 + (run.end - run.pos));
         const int row0 = unit * ROWS;
         const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
-        const int seen0 = a.split.seq_lens[b] - a.n_pos + 1;  // keys that position 0 sees
+        const int seen0 = uniform(a.split.seq_lens[b]) - a.n_pos + 1;  // keys that position 0 sees
 
-        // this wave's 16 keys of a chunk: the page of lane's key (16 lanes, repeated)
+        // the page of lane's key among this wave's keys of a chunk (KEYS lanes, repeated)
         int page;
         auto load_pages = [&](int c) {
-            const int key = c * LD_KB + kq * 16 + col;
+            const int key = c * LD_KB + key_row + lane % KEYS;
             page = key < nkeys ? table[a.block((uint32_t)key)] : -1;
         };
         uint32_t exist, exist_next = 0;
         auto load_tile = [&](int c, int buf) {
-            const uint32_t key = (uint32_t)(c * LD_KB + kq * 16 + col);
+            const uint32_t key = (uint32_t)(c * LD_KB + key_row + lane % KEYS);
             const uint32_t off = key - a.block(key) * a.block.div;
             const bool ok = page >= 0 && page < a.n_blocks;
             const uint32_t slot = ok ? (uint32_t)page * a.block.div + off : 0u;
-            exist_next = (uint32_t)(__ballot(ok) & 0xffff);
+            exist_next = (uint32_t)__ballot(ok) & ALL;
             const uint32_t at = lds_offset(tile) + buf * X::BYTES;
             const int first = part * OWN;
             if constexpr (X::PIECES == 64) {
+                // turn(first + i) = turn(first) ^ turn(i); the lane part is hidden from the
+                // compiler, which would keep one register per row alive across the key loop
+                int piece = lane ^ X::turn(first);
+                asm volatile("" : "+v"(piece));
 #pragma unroll
                 for (int i = 0; i < OWN; i++) {
                     const int r = first + i;
                     const uint32_t s = __builtin_amdgcn_readlane(slot, r);
-                    load_to_lds(cache + (size_t)s * X::ROW, (uint32_t)((lane ^ X::turn(r)) << 4),
-                                at + (kq * 16 + r) * X::LAT);
+                    load_to_lds(cache + (size_t)s * X::ROW, (uint32_t)((piece ^ X::turn(i)) << 4),
+                                at + (key_row + r) * X::LAT);
                 }
             } else {  // two rows per load
 #pragma unroll
@@ -185,7 +218,7 @@ __global__ __launch_bounds__(LD_THREADS * RH) void latent_core_kernel(LatentDeco
                     const int r = first + i, rr = r + (lane >> 5);
                     const uint32_t s = __shfl(slot, rr, WAVE);
                     load_to_lds(cache + (size_t)s * X::ROW + (((lane & 31) ^ X::turn(rr)) << 4),
-                                at + (kq * 16 + r) * X::LAT);
+                                at + (key_row + r) * X::LAT);
                 }
             }
 #pragma unroll
@@ -194,34 +227,31 @@ __global__ __launch_bounds__(LD_THREADS * RH) void latent_core_kernel(LatentDeco
                 const uint32_t s = __shfl(slot, rr, WAVE);
                 load_to_lds(cache + (size_t)s * X::ROW + X::LAT +
                                 (((lane & 7) ^ ((rr >> 1) & 7)) << 4),
-                            at + X::ROPE_AT + (kq * 16 + r) * (LD_ROPE * 2));
+                            at + X::ROPE_AT + (key_row + r) * (LD_ROPE * 2));
             }
         };
         load_pages(c0);
         load_tile(c0, 0);
         load_pages(c0 + 1 < c1 ? c0 + 1 : c0);
 
-        bf16x8 q[RT][NF];
-        int lim[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; rt++) {
-            const int r = row0 + (part * RT + rt) * 16 + col;
-            const bool live = r < a.rows;
-            lim[rt] = live ? seen0 + r / a.H : 0;
-            const size_t at = (size_t)b * a.rows + (live ? r : 0);
+        bf16x8 q[NF];
+        const int q_row = row0 + part * 16 + col;
+        const bool live = q_row < a.rows;
+        const int lim = live ? seen0 + q_row / a.H : 0;
+        {
+            const size_t at = (size_t)b * a.rows + (live ? q_row : 0);
             const bf16* ql = reinterpret_cast<const bf16*>(a.q_lat) + at * R;
             const bf16* qp = reinterpret_cast<const bf16*>(a.q_pe) + at * LD_ROPE;
 #pragma unroll
             for (int f = 0; f < NF; f++)
-                q[rt][f] = Mma<bf16>::load(f < NL ? ql + f * 32 + grp * 8
-                                                  : qp + (f - NL) * 32 + grp * 8);
+                q[f] = Mma<bf16>::load(f < NL ? ql + f * 32 + grp * 8
+                                              : qp + (f - NL) * 32 + grp * 8);
         }
-        f32x4 acc[TILES][NT];
-        float m[TILES], l[RT];  // running maxima; this lane's share of its rows' running sums
+        f32x4 acc[RH][NT];
+        float m[RH], l = 0.f;  // running maxima of all rows; this lane's share of its row's sum
 #pragma unroll
-        for (int t = 0; t < TILES; t++) {
+        for (int t = 0; t < RH; t++) {
             m[t] = -INFINITY;
-            if (t < RT) l[t] = 0.f;
 #pragma unroll
             for (int j = 0; j < NT; j++) acc[t][j] = zero4();
         }
@@ -231,11 +261,11 @@ __global__ __launch_bounds__(LD_THREADS * RH) void latent_core_kernel(LatentDeco
             const char* kt = tile + buf * X::BYTES;
             exist = exist_next;
             lds_loads_done();
-            if (exist != 0xffff) {
+            if (exist != ALL) {
                 // latents of absent keys as zeros: a zero weight does not cancel what they hold
                 for (int r = part * OWN; r < part * OWN + OWN; r++)
                     if (!((exist >> r) & 1) && lane < X::PIECES)
-                        *reinterpret_cast<f32x4*>(tile + buf * X::BYTES + (kq * 16 + r) * X::LAT +
+                        *reinterpret_cast<f32x4*>(tile + buf * X::BYTES + (key_row + r) * X::LAT +
                                                   lane * 16) = zero4();
             }
             lds_barrier();  // tile c is whole; all waves are done with the other buffer
@@ -243,88 +273,83 @@ __global__ __launch_bounds__(LD_THREADS * RH) void latent_core_kernel(LatentDeco
                 load_tile(c + 1, buf ^ 1);
                 load_pages(c + 2 < c1 ? c + 2 : c + 1);
             }
-            f32x4 s[RT];
+            f32x4 s[KS];
 #pragma unroll
-            for (int rt = 0; rt < RT; rt++) s[rt] = zero4();
+            for (int x = 0; x < KS; x++) s[x] = zero4();
 #pragma unroll
-            for (int f = 0; f < NF; f++) {
-                const int r = kq * 16 + col;
-                const bf16x8 k = *reinterpret_cast<const bf16x8*>(
-                    kt + (f < NL ? X::lat(r, f * 4 + grp) : X::rope(r, (f - NL) * 4 + grp)));
+            for (int f = 0; f < NF; f++)
 #pragma unroll
-                for (int rt = 0; rt < RT; rt++) s[rt] = Mma<bf16>::mma(k, q[rt][f], s[rt]);
-            }
-            const int key0 = c * LD_KB + kq * 16;
-            const bool mask = exist != 0xffff || key0 + 16 > seen0;
+                for (int x = 0; x < KS; x++) {
+                    // (16 rows on, the pieces are turned alike)
+                    const char* at = f < NL
+                        ? kt + k_at[f & 3] + (f >> 2) * 256 + x * (16 * X::LAT)
+                        : kt + pe_at[f - NL] + x * (16 * LD_ROPE * 2);
+                    s[x] = Mma<bf16>::mma(*reinterpret_cast<const bf16x8*>(at), q[f], s[x]);
+                }
+            const int key0 = c * LD_KB + key_row;
+            const bool mask = exist != ALL || key0 + KEYS > seen0;
+            float top = -INFINITY;
 #pragma unroll
-            for (int rt = 0; rt < RT; rt++) {
-                float top = -INFINITY;
+            for (int x = 0; x < KS; x++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    s[rt][i] *= cs;
+                    s[x][i] *= cs;
                     if (mask) {
-                        const int k = grp * 4 + i;
-                        const bool keep = ((exist >> k) & 1) && key0 + k < lim[rt];
-                        s[rt][i] = keep ? s[rt][i] : -INFINITY;
+                        const int k = x * 16 + grp * 4 + i;
+                        const bool keep = ((exist >> k) & 1) && key0 + k < lim;
+                        s[x][i] = keep ? s[x][i] : -INFINITY;
                     }
-                    top = fmaxf(top, s[rt][i]);
+                    top = fmaxf(top, s[x][i]);
                 }
-                top = fmaxf(top, __shfl_xor(top, 16, WAVE));
-                top = fmaxf(top, __shfl_xor(top, 32, WAVE));
-                if (grp == 0) tops[kq][(part * RT + rt) * 16 + col] = top;
-            }
+            top = fmaxf(top, __shfl_xor(top, 16, WAVE));
+            top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+            if (grp == 0) tops[kg][part * 16 + col] = top;
             lds_barrier();
+            // all waves follow the maxima of all rows, their outputs' columns hold them all
+            float own_ref = 0.f;
 #pragma unroll
-            for (int t = 0; t < TILES; t++) {
+            for (int t = 0; t < RH; t++) {
                 float m1 = m[t];
 #pragma unroll
-                for (int w = 0; w < 4; w++) m1 = fmaxf(m1, tops[w][t * 16 + col]);
+                for (int g = 0; g < Y::GROUPS; g++) m1 = fmaxf(m1, tops[g][t * 16 + col]);
                 const float ref = m1 == -INFINITY ? 0.f : m1;  // a row with no key so far
-                const int rt = t - part * RT;
-                const bool own = RH == 1 || (rt >= 0 && rt < RT);
+                if (t == part) own_ref = ref;
                 if (__any(m1 > m[t])) {
                     const float shrink = __builtin_amdgcn_exp2f(m[t] - ref);
-#pragma unroll
-                    for (int x = 0; x < RT; x++)
-                        if (x == rt) l[x] *= shrink;
+                    if (t == part) l *= shrink;
 #pragma unroll
                     for (int j = 0; j < NT; j++)
 #pragma unroll
                         for (int i = 0; i < 4; i++) acc[t][j][i] *= shrink;
                     m[t] = m1;
                 }
-                if (own) {
+            }
 #pragma unroll
-                    for (int x = 0; x < RT; x++)
-                        if (x == rt) {
-                            float p[4];
+            for (int x = 0; x < KS; x++) {
+                float p[4];
 #pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                p[i] = __builtin_amdgcn_exp2f(s[x][i] - ref);
-                                l[x] += p[i];
-                            }
-                            *reinterpret_cast<uint64_t*>(
-                                wt + ld_weight(t * 16 + col, kq * 2 + (grp >> 1)) + (grp & 1) * 8) =
-                                bits4(p);
-                        }
+                for (int i = 0; i < 4; i++) {
+                    p[i] = __builtin_amdgcn_exp2f(s[x][i] - own_ref);
+                    l += p[i];
                 }
+                *reinterpret_cast<uint64_t*>(
+                    wt + ld_weight(part * 16 + col, (kg * KS + x) * 2 + (grp >> 1)) +
+                    (grp & 1) * 8) = bits4(p);
             }
             lds_barrier();
 #pragma unroll
             for (int ks = 0; ks < LD_KB / 32; ks++) {
-                bf16x8 pb[TILES];
+                bf16x8 pb[RH];
 #pragma unroll
-                for (int t = 0; t < TILES; t++)
-                    pb[t] = *reinterpret_cast<const bf16x8*>(
-                        wt + ld_weight(t * 16 + col, ks * 4 + grp));
-                const int r = ks * 32 + grp * 8 + ((lane >> 2) & 3);
+                for (int t = 0; t < RH; t++)
+                    pb[t] = *reinterpret_cast<const bf16x8*>(wt + p_at[ks] + t * (16 * LD_KB * 2));
 #pragma unroll
                 for (int j = 0; j < NT; j++) {
-                    const int pc = (wave * NT + j) * 2 + ((lane & 3) >> 1);
-                    const bf16x8 v = join(lds_read_tr(kt + X::lat(r, pc) + (lane & 1) * 8),
-                                          lds_read_tr(kt + X::lat(r + 4, pc) + (lane & 1) * 8));
+                    const char* v0 = kt + (v_at ^ (j << 5)) + ks * (32 * X::LAT);
+                    const char* v1 = kt + (v_at ^ (j << 5) ^ 16) + ks * (32 * X::LAT) + 4 * X::LAT;
+                    const bf16x8 v = join(lds_read_tr(v0), lds_read_tr(v1));
 #pragma unroll
-                    for (int t = 0; t < TILES; t++)
+                    for (int t = 0; t < RH; t++)
                         acc[t][j] = Mma<bf16>::mma(v, pb[t], acc[t][j]);
                 }
             }
@@ -334,32 +359,27 @@ __global__ __launch_bounds__(LD_THREADS * RH) void latent_core_kernel(LatentDeco
         const bool whole = c0 == 0 && c1 == nch;
         const int slot = 2 * (int)blockIdx.x + (run.pos == run_start ? 0 : 1);
         lds_barrier();
-#pragma unroll
-        for (int rt = 0; rt < RT; rt++) {
-            float t = l[rt];
-            t += __shfl_xor(t, 16, WAVE);
-            t += __shfl_xor(t, 32, WAVE);
-            if (grp == 0) tops[kq][(part * RT + rt) * 16 + col] = t;
-        }
+        l += __shfl_xor(l, 16, WAVE);
+        l += __shfl_xor(l, 32, WAVE);
+        if (grp == 0) tops[kg][part * 16 + col] = l;
         lds_barrier();
 #pragma unroll
-        for (int t = 0; t < TILES; t++) {
+        for (int t = 0; t < RH; t++) {
             const int rr = t * 16 + col, r = row0 + rr;
             if (r < a.rows) {
                 float sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < 4; w++) sum += tops[w][rr];
+                for (int g = 0; g < Y::GROUPS; g++) sum += tops[g][rr];
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
-                bf16* dst = reinterpret_cast<bf16*>(a.o_lat) + ((size_t)b * a.rows + r) * R;
-                float* out = a.part_o + ((size_t)slot * ROWS + rr) * R;
+                float* out = whole ? a.o_lat + ((size_t)b * a.rows + r) * R
+                                   : a.part_o + ((size_t)slot * ROWS + rr) * R;
 #pragma unroll
                 for (int j = 0; j < NT; j++) {
                     const int d = (wave * NT + j) * 16 + grp * 4;
                     float x[4];
 #pragma unroll
                     for (int i = 0; i < 4; i++) x[i] = whole ? acc[t][j][i] * inv : acc[t][j][i];
-                    if (whole) store4<bf16>(dst + d, x);
-                    else store4<float>(out + d, x);
+                    store4<float>(out + d, x);
                 }
                 if (!whole && wave == 0 && grp == 0) {
                     float* pm = a.part_ml + ((size_t)slot * ROWS + rr) * 2;
@@ -374,96 +394,79 @@ __global__ __launch_bounds__(LD_THREADS * RH) void latent_core_kernel(LatentDeco
         if (run.pos < run.end && run.pos == run.base + (int64_t)nch * a.split.units) {
             run.base = run.pos;
             do run.b++;
-            while (run.b + 1 < a.split.batch && split_chunks<LD_KB>(a.split, run.b) == 0);
+            while (run.b + 1 < a.split.batch && uniform(split_keys(a.split, run.b)) == 0);
         }
     }
 }
 
-// -------------------------------------------------------------------------------------- up
-// o = W_uv u for one head and 16 (request, position) rows. u is staged in LDS: copied where the
-// core finished the row, joined from the parts where its unit was cut, zeros where the request
-// has no key.
-template <int R, int DV>
-__global__ __launch_bounds__(LD_THREADS) void latent_up_kernel(LatentDecodeArgs a) {
-    constexpr int PITCH = R * 2 + 16;
-    constexpr int PER = R / WAVE;
-    __shared__ __align__(16) char u[16 * PITCH];
-    const int h = blockIdx.x, base_row = blockIdx.y * 16;
-    const int lane = lane_id(), wave = wave_id();
-    const int n_rows = a.split.batch * a.n_pos;
+// ------------------------------------------------------------------------------------ join
+// Weighted latents of the units that were cut, and zeros for requests without keys.
+__global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentDecodeArgs a) {
     const int tile = 16 * a.rt;
-    for (int k = 0; k < 16 / LD_WAVES; k++) {
-        const int rr = wave * (16 / LD_WAVES) + k, bp = base_row + rr;
-        float x[PER];
-#pragma unroll
-        for (int i = 0; i < PER; i++) x[i] = 0.f;
-        bool copy = false;
-        if (bp < n_rows) {
-            const int b = bp / a.n_pos, row = (bp - b * a.n_pos) * a.H + h;
-            const int unit = row / tile, r = row - unit * tile;
-            const int nch = split_chunks<LD_KB>(a.split, b);
-            if (nch > 0) {
-                int64_t base, total;
-                split_base<LD_KB>(a.split, b, &base, &total);
-                const int64_t u0 = base + (int64_t)unit * nch;
-                const int n = split_wgs(total, a.n_wg);
-                const int w0 = split_owner(u0, total, n), w1 = split_owner(u0 + nch - 1, total, n);
-                copy = w0 == w1;
-                if (copy) {
-                    const bf16* src = reinterpret_cast<const bf16*>(a.o_lat) +
-                                      ((size_t)bp * a.H + h) * R;
-#pragma unroll
-                    for (int i = 0; i < PER; i++) x[i] = (float)src[lane * PER + i];
-                } else {
-                    const int late = split_start(w0, total, n) < u0 ? 1 : 0;
-                    auto at = [&](int w) {
-                        return (size_t)(2 * w + (w == w0 ? late : 0)) * tile + r;
-                    };
-                    float top = -INFINITY;
-                    for (int w = w0 + lane; w <= w1; w += WAVE)
-                        top = fmaxf(top, a.part_ml[at(w) * 2]);
-#pragma unroll
-                    for (int off = WAVE / 2; off > 0; off >>= 1)
-                        top = fmaxf(top, __shfl_xor(top, off, WAVE));
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    float sum = 0.f;
-#pragma unroll 4
-                    for (int w = w0; w <= w1; w++) {
-                        const size_t e = at(w);
-                        const float f = __builtin_amdgcn_exp2f(a.part_ml[e * 2] - ref);
-                        sum = fmaf(f, a.part_ml[e * 2 + 1], sum);
-#pragma unroll
-                        for (int i = 0; i < PER; i++)
-                            x[i] = fmaf(f, a.part_o[e * R + lane * PER + i], x[i]);
-                    }
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-                    for (int i = 0; i < PER; i++) x[i] *= inv;
-                }
-            }
-        }
-        bf16* dst = reinterpret_cast<bf16*>(u + rr * PITCH) + lane * PER;
-#pragma unroll
-        for (int i = 0; i < PER; i++) dst[i] = (bf16)x[i];
-    }
-    __syncthreads();
+    const JoinShape s = {a.split, a.n_wg, tile, min(tile, a.rows), a.rank, a.part_o, a.part_ml};
+    join_parts<LD_KB>(
+        s, [&](int unit) { return min(tile, a.rows - unit * tile); },
+        [&](int b, int unit, int row, int col, const float x[4]) {
+            store4<float>(a.o_lat + ((size_t)b * a.rows + unit * tile + row) * a.rank + col, x);
+        },
+        [&](int b) {
+            const size_t n = (size_t)a.rows * a.rank;
+            const float z[4] = {0.f, 0.f, 0.f, 0.f};
+            for (size_t i = threadIdx.x * 4; i < n; i += JOIN_THREADS * 4)
+                store4<float>(a.o_lat + (size_t)b * n + i, z);
+        });
+}
+
+// -------------------------------------------------------------------------------------- up
+// o = W_uv u, one head per workgroup: its rows of W_uv stay in registers as the MFMA's A
+// operand while the (request, position) rows pass, 16 at a time. u is taken as the sum of two
+// bf16 numbers, its rounding and the rounding of what that leaves (2^-17 of it together): one
+// more MFMA each, in a pass that waits for memory, for an output error that is a third smaller.
+template <int R, int DV>
+__global__ __launch_bounds__(LD_THREADS) void latent_up_kernel(LatentDecodeArgs a,
+                                                               int tiles_per_wg) {
+    constexpr int NJ = DV / 16 / LD_WAVES;
+    const int h = blockIdx.x, lane = lane_id(), wave = wave_id();
     const int col = lane & 15, grp = lane >> 4;
+    const int rows = a.split.batch * a.n_pos;
     const bf16* W = reinterpret_cast<const bf16*>(a.w_kv) +
                     ((size_t)h * (a.d_nope + DV) + a.d_nope) * R;
-    const int bp = base_row + col;
+    bf16x8 w[NJ][R / 32];
 #pragma unroll
-    for (int j = 0; j < DV / 16 / LD_WAVES; j++) {
-        const int t = j * LD_WAVES + wave;
-        f32x4 d = zero4();
+    for (int j = 0; j < NJ; j++)
 #pragma unroll
         for (int k = 0; k < R / 32; k++)
-            d = Mma<bf16>::mma(Mma<bf16>::load(W + (size_t)(t * 16 + col) * R + k * 32 + grp * 8),
-                               *reinterpret_cast<const bf16x8*>(u + col * PITCH + k * 64 + grp * 16),
-                               d);
-        float y[4] = {d[0], d[1], d[2], d[3]};
-        if (bp < n_rows)
-            store4<bf16>(reinterpret_cast<bf16*>(a.o) + ((size_t)bp * a.H + h) * DV + t * 16 +
-                             grp * 4, y);
+            w[j][k] = Mma<bf16>::load(W + (size_t)((wave * NJ + j) * 16 + col) * R + k * 32 +
+                                      grp * 8);
+    const int t0 = blockIdx.y * tiles_per_wg;
+    for (int t = t0; t < t0 + tiles_per_wg && t * 16 < rows; t++) {
+        const int row = t * 16 + col;
+        const float* u = a.o_lat + ((size_t)min(row, rows - 1) * a.H + h) * R + grp * 8;
+        f32x4 d[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; j++) d[j] = zero4();
+#pragma unroll
+        for (int k = 0; k < R / 32; k++) {
+            float x[8];
+            load8<float>(u + k * 32, x);
+            bf16x8 hi, lo;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                hi[i] = (bf16)x[i];
+                lo[i] = (bf16)(x[i] - (float)hi[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; j++) {
+                d[j] = Mma<bf16>::mma(w[j][k], hi, d[j]);
+                d[j] = Mma<bf16>::mma(w[j][k], lo, d[j]);
+            }
+        }
+        bf16* out = reinterpret_cast<bf16*>(a.o) + ((size_t)row * a.H + h) * DV;
+#pragma unroll
+        for (int j = 0; j < NJ; j++) {
+            const float y[4] = {d[j][0], d[j][1], d[j][2], d[j][3]};
+            if (row < rows) store4<bf16>(out + (wave * NJ + j) * 16 + grp * 4, y);
+        }
     }
 }
 
@@ -477,23 +480,41 @@ void run_absorb(const LatentDecodeArgs& a, hipStream_t s) {
                        dim3(LD_THREADS), 0, s, a, per);
 }
 
+template <int R, int RH, int KS>
+void core_launch(const LatentDecodeArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((latent_core_kernel<R, RH, KS>), dim3((unsigned)a.n_wg),
+                       dim3(LdWaves<RH, KS>::WAVES * WAVE), 0, s, a);
+}
+
 template <int R>
 hipError_t run_core(const LatentDecodeArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)a.n_wg), block(LD_THREADS);
     switch (a.rt) {
-        case 1: hipLaunchKernelGGL((latent_core_kernel<R, 1, 1>), grid, block, 0, s, a); break;
-        case 2: hipLaunchKernelGGL((latent_core_kernel<R, 2, 1>), grid, block, 0, s, a); break;
-        case 4:
-            hipLaunchKernelGGL((latent_core_kernel<R, 2, 2>), grid, dim3(2 * LD_THREADS), 0, s, a);
-            break;
+        case 1: core_launch<R, 1, 1>(a, s); break;
+        case 2: core_launch<R, 2, 1>(a, s); break;
+        case 4: core_launch<R, 4, 2>(a, s); break;
         default: return hipErrorInvalidValue;
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const dim3 up((unsigned)a.H, (unsigned)((a.split.batch * a.n_pos + 15) / 16));
-    if (a.d_v == 128) hipLaunchKernelGGL((latent_up_kernel<R, 128>), up, block, 0, s, a);
-    else hipLaunchKernelGGL((latent_up_kernel<R, 64>), up, block, 0, s, a);
     return hipGetLastError();
+}
+
+template <int R, int DV>
+hipError_t run_up(const LatentDecodeArgs& a, hipStream_t s) {
+    const int tiles = (a.split.batch * a.n_pos + 15) / 16;
+    const int per = tiles < 4 ? tiles : 4;
+    hipLaunchKernelGGL((latent_up_kernel<R, DV>),
+                       dim3((unsigned)a.H, (unsigned)((tiles + per - 1) / per)), dim3(LD_THREADS),
+                       0, s, a, per);
+    return hipGetLastError();
+}
+
+template <int R>
+hipError_t run_rank(const LatentDecodeArgs& a, hipStream_t s) {
+    hipError_t e = run_core<R>(a, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)a.n_join), dim3(JOIN_THREADS), 0, s, a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return a.d_v == 128 ? run_up<R, 128>(a, s) : run_up<R, 64>(a, s);
 }
 
 }  // namespace
@@ -504,7 +525,8 @@ size_t latent_decode_layout(LatentDecodeArgs* a, void* ws) {
     a->rt = tiles >= 3 ? 4 : tiles;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
     a->split.units = a->row_tiles;
-    a->n_wg = device_cu_count();
+    a->n_wg = min(device_cu_count(), JOIN_MAX_WG);
+    a->n_join = 4 * device_cu_count();
     const size_t part = (size_t)2 * a->n_wg * 16 * a->rt;
     const size_t lat = (size_t)a->split.batch * a->rows * a->rank;  // bf16 elements
     size_t off = 0;
@@ -516,7 +538,7 @@ size_t latent_decode_layout(LatentDecodeArgs* a, void* ws) {
     a->part_o = reinterpret_cast<float*>(take(part * a->rank * sizeof(float)));
     a->part_ml = reinterpret_cast<float*>(take(part * 2 * sizeof(float)));
     a->q_lat = take(lat * 2);
-    a->o_lat = take(lat * 2);
+    a->o_lat = reinterpret_cast<float*>(take(lat * sizeof(float)));
     return off;
 }
 
@@ -526,7 +548,7 @@ hipError_t launch_latent_decode(const LatentDecodeArgs& a, hipStream_t s) {
     else run_absorb<64>(a, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return a.rank == 512 ? run_core<512>(a, s) : run_core<256>(a, s);
+    return a.rank == 512 ? run_rank<512>(a, s) : run_rank<256>(a, s);
 }
 
 }  // namespace gdn

@@ -20,6 +20,7 @@
 #include "attn_launch.h"
 #include "gdn_common.h"
 #include "gdn_launch.h"
+#include "key_join.h"
 
 namespace gdn {
 
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
     constexpr int NV = KW * CPR / WAVE;  // 16-byte pieces of V per lane
     __shared__ __align__(16) char smem[L::BYTES];
     __shared__ float ml[PD_WAVES][16][2];
-    const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+    const int tid = threadIdx.x, lane = lane_id(), wave = uniform(wave_id());
     const int col = lane & 15, grp = lane >> 4;
     SplitRun run = split_run<KB, PD_THREADS>(a.split, blockIdx.x, a.n_wg);
     const int64_t run_start = run.pos;
@@ -145,14 +146,14 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
 
     while (run.pos < run.end) {
         const int b = run.b;
-        const int nkeys = split_keys(a.split, b);
+        const int nkeys = uniform(split_keys(a.split, b));
         const int nch = (nkeys + KB - 1) / KB;
-        const int unit = (int)((run.pos - run.base) / nch);
+        const int unit = uniform((int)((run.pos - run.base) / nch));
         const int c0 = (int)(run.pos - run.base - (int64_t)unit * nch);
         const int c1 = (int)min((int64_t)nch, c0 + (run.end - run.pos));
         const int kvh = unit / a.row_tiles, row0 = (unit - kvh * a.row_tiles) * 16 * RT;
         const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
-        const int seen0 = a.split.seq_lens[b] - a.n_pos + 1;  // keys that position 0 sees
+        const int seen0 = uniform(a.split.seq_lens[b]) - a.n_pos + 1;  // keys that position 0 sees
 
         frag q[RT][NF];
         int lim[RT];
@@ -377,64 +378,32 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
         if (run.pos < run.end && run.pos == run.base + (int64_t)nch * a.split.units) {
             run.base = run.pos;
             do run.b++;
-            while (run.b + 1 < a.split.batch && split_chunks<KB>(a.split, run.b) == 0);
+            while (run.b + 1 < a.split.batch && uniform(split_keys(a.split, run.b)) == 0);
         }
     }
 }
 
-// Joins the partial results of the units that were cut: one wave per query row. Rows of units
-// that a single workgroup finished are left alone; a request without keys gets zeros.
+// Results of the units that were cut, and zeros for requests without keys.
 template <typename T, int D>
-__global__ __launch_bounds__(PD_THREADS) void paged_join_kernel(PagedDecodeArgs a) {
+__global__ __launch_bounds__(JOIN_THREADS) void paged_join_kernel(PagedDecodeArgs a) {
     constexpr int KB = PdTile<T, D>::KW * PD_WAVES;
-    constexpr int PER = D / WAVE;
     const int tile = 16 * a.rt;
-    const int lane = lane_id();
-    const int64_t idx = (int64_t)blockIdx.x * PD_WAVES + wave_id();
-    const int b = (int)(idx / (a.kv_heads * a.rows));
-    if (b >= a.split.batch) return;
-    const int rest = (int)(idx - (int64_t)b * a.kv_heads * a.rows);
-    const int kvh = rest / a.rows, rr = rest - kvh * a.rows;
-    const int unit = kvh * a.row_tiles + rr / tile, r = rr % tile;
-    const int p = rr / a.group, h = rr - p * a.group;
-    T* dst = reinterpret_cast<T*>(a.o) +
-             (((size_t)b * a.n_pos + p) * a.H + (size_t)kvh * a.group + h) * D + lane * PER;
-    const int nch = split_chunks<KB>(a.split, b);
-    float x[PER];
-#pragma unroll
-    for (int i = 0; i < PER; i++) x[i] = 0.f;
-    if (nch > 0) {
-        int64_t base, total;
-        split_base<KB>(a.split, b, &base, &total);
-        const int64_t u0 = base + (int64_t)unit * nch;
-        const int n = split_wgs(total, a.n_wg);
-        const int w0 = split_owner(u0, total, n), w1 = split_owner(u0 + nch - 1, total, n);
-        if (w0 == w1) return;
-        // part of workgroup w: its first unit is this one unless it started before it (w0 only)
-        const int late = split_start(w0, total, n) < u0 ? 1 : 0;
-        auto at = [&](int w) {
-            return ((size_t)(2 * w + (w == w0 ? late : 0)) * tile + r);
-        };
-        float top = -INFINITY;
-        for (int w = w0 + lane; w <= w1; w += WAVE) top = fmaxf(top, a.part_ml[at(w) * 2]);
-#pragma unroll
-        for (int off = WAVE / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, WAVE));
-        const float ref = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-#pragma unroll 8
-        for (int w = w0; w <= w1; w++) {
-            const size_t e = at(w);
-            const float wt = __builtin_amdgcn_exp2f(a.part_ml[e * 2] - ref);
-            sum = fmaf(wt, a.part_ml[e * 2 + 1], sum);
-#pragma unroll
-            for (int i = 0; i < PER; i++) x[i] = fmaf(wt, a.part_o[e * D + lane * PER + i], x[i]);
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-        for (int i = 0; i < PER; i++) x[i] *= inv;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; i++) dst[i] = from_f32<T>(x[i]);
+    const JoinShape s = {a.split, a.n_wg, tile, min(tile, a.rows), D, a.part_o, a.part_ml};
+    join_parts<KB>(
+        s, [&](int unit) { return min(tile, a.rows - (unit % a.row_tiles) * tile); },
+        [&](int b, int unit, int row, int col, const float x[4]) {
+            const int kvh = unit / a.row_tiles, r = (unit - kvh * a.row_tiles) * tile + row;
+            const int p = r / a.group, h = r - p * a.group;
+            store4<T>(reinterpret_cast<T*>(a.o) +
+                          (((size_t)b * a.n_pos + p) * a.H + (size_t)kvh * a.group + h) * D + col,
+                      x);
+        },
+        [&](int b) {
+            const size_t n = (size_t)a.n_pos * a.H * D;
+            const float z[4] = {0.f, 0.f, 0.f, 0.f};
+            for (size_t i = threadIdx.x * 4; i < n; i += JOIN_THREADS * 4)
+                store4<T>(reinterpret_cast<T*>(a.o) + (size_t)b * n + i, z);
+        });
 }
 
 template <typename T, int D, int RT>
@@ -443,9 +412,8 @@ hipError_t run_decode(const PagedDecodeArgs& a, hipStream_t s) {
                        0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t rows = (int64_t)a.split.batch * a.kv_heads * a.rows;
-    hipLaunchKernelGGL((paged_join_kernel<T, D>), dim3((unsigned)((rows + PD_WAVES - 1) / PD_WAVES)),
-                       dim3(PD_THREADS), 0, s, a);
+    hipLaunchKernelGGL((paged_join_kernel<T, D>), dim3((unsigned)a.n_join), dim3(JOIN_THREADS), 0, s,
+                       a);
     return hipGetLastError();
 }
 
@@ -484,7 +452,8 @@ size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
     a->rt = tiles >= 4 && most >= 4 ? 4 : tiles >= 2 && most >= 2 ? 2 : 1;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
     a->split.units = a->kv_heads * a->row_tiles;
-    a->n_wg = 2 * device_cu_count();
+    a->n_wg = min(2 * device_cu_count(), JOIN_MAX_WG);
+    a->n_join = 4 * device_cu_count();
     const size_t rows = (size_t)2 * a->n_wg * 16 * a->rt;
     a->part_o = static_cast<float*>(ws);
     a->part_ml = a->part_o == nullptr ? nullptr : a->part_o + rows * a->d;
