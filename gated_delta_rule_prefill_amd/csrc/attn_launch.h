@@ -46,13 +46,13 @@ struct PagedDecodeArgs {
     const void *q, *k_cache, *v_cache;
     const int32_t* block_table;
     FastDiv block;       // by the page size
-    SplitShape split;    // units = kv_heads * row_tiles
-    int group, rows, rt, row_tiles, n_wg, n_join;
+    SplitShape split;    // units = kv_heads
+    int group, rows, rt, row_tiles, workers, n_join;
     void* o;
-    float* part_o;       // [2 n_wg][16 rt][d]
-    float* part_ml;      // [2 n_wg][16 rt][2]
+    float* part_o;       // [2 workers][row_tiles][16 rt][d]
+    float* part_ml;      // [2 workers][row_tiles][16 rt][2]
 };
-// Row tiles, workgroups and workspace bytes of a call (fills rt, row_tiles, n_wg, split.units).
+// Row tiles, workers and workspace bytes of a call (fills what lies between q and o).
 size_t paged_decode_layout(PagedDecodeArgs* a, void* ws);
 hipError_t launch_paged_decode(const PagedDecodeArgs& a, hipStream_t stream);
 
@@ -64,13 +64,13 @@ struct LatentDecodeArgs {
     const void *q_nope, *q_pe, *w_kv, *cache;
     const int32_t* block_table;
     FastDiv block;       // by the page size
-    SplitShape split;    // units = row_tiles
-    int rows, rt, row_tiles, n_wg, n_join;
+    SplitShape split;    // units = 1
+    int rows, rt, row_tiles, workers, n_join;
     void* o;
     void* q_lat;         // [batch n_pos][H][rank] bf16: queries in the latent space
     float* o_lat;        // [batch n_pos][H][rank]: outputs there
-    float* part_o;       // [2 n_wg][16 rt][rank]
-    float* part_ml;      // [2 n_wg][16 rt][2]
+    float* part_o;       // [2 workers][row_tiles][16 rt][rank]
+    float* part_ml;      // [2 workers][row_tiles][16 rt][2]
 };
 size_t latent_decode_layout(LatentDecodeArgs* a, void* ws);
 hipError_t launch_latent_decode(const LatentDecodeArgs& a, hipStream_t stream);

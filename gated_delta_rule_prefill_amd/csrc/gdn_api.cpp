@@ -360,6 +360,16 @@ int check_table(int32_t max_blocks, int32_t block_size) {
     return GDN_OK;
 }
 
+// The split of a decode call counts its key chunks (64 keys at least) in 32 bits.
+int check_chunks(int32_t batch, int32_t units, int32_t max_blocks, int32_t block_size) {
+    const int64_t chunks = ((int64_t)max_blocks * block_size + 63) / 64;
+    if (chunks * units > 0x3fffffffll / (batch > 0 ? batch : 1))
+        return fail(GDN_ERR_UNSUPPORTED, "batch x heads x table row are too many key chunks (%d x "
+                                         "%d x %lld): split the batch", batch, units,
+                    (long long)chunks);
+    return GDN_OK;
+}
+
 // Source rows of an append: `width` elements each, `stride` elements apart, 16-byte aligned.
 int check_rows(int32_t dtype, int32_t tokens, int64_t stride, int64_t width, const char* name) {
     if (tokens < 0) return fail(GDN_ERR_SHAPE, "tokens must be >= 0 (got %d)", tokens);
@@ -903,6 +913,7 @@ int gdn_paged_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_
     int st = check_paged_dims(dims, batch, n_pos);
     if (!st) st = check_cache(dims->dtype, dims->num_kv_heads, n_blocks, block_size);
     if (!st) st = check_table(max_blocks, block_size);
+    if (!st) st = check_chunks(batch, dims->num_kv_heads, max_blocks, block_size);
     if (st) return st;
     if (batch == 0) return ok();
     REQUIRE_PTR(q);
@@ -952,6 +963,7 @@ int gdn_latent_decode(const gdn_latent_dims_t* dims, const void* q_nope, const v
     if (!st) st = check_latent_rows(dims, (int64_t)batch * n_pos);
     if (!st) st = check_cache(dims->dtype, 1, n_blocks, block_size);
     if (!st) st = check_table(max_blocks, block_size);
+    if (!st) st = check_chunks(batch, 1, max_blocks, block_size);
     if (st) return st;
     if (batch == 0) return ok();
     REQUIRE_PTR(q_nope);

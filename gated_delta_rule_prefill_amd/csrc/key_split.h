@@ -1,13 +1,18 @@
 // Work split of the paged decode kernels: the keys of all (request, head group) units laid end
-// to end in chunks of KB keys, and cut into equal runs of chunks, one per workgroup. Lengths
-// are device data, so every workgroup derives the cut from them; nothing is read on the host.
+// to end in chunks of KB keys, and cut into equal runs of chunks, one per worker. Lengths are
+// device data, so every workgroup derives the cut from them; nothing is read on the host.
 //
-// A unit that one workgroup covers whole is finished by it. A unit cut between workgroups
-// leaves one partial result (unnormalised output, running maximum and sum, per row) per
-// workgroup that touched it, and a second kernel joins them (key_join.h). A workgroup can touch at most two
-// cut units (its first and its last), so it owns two partial slots: 2 w for the unit it starts
-// with, 2 w + 1 for a later one. Work is even to one chunk whatever the lengths, the slots are
-// as many as the grid is wide, and the sums run in a fixed order.
+// A unit that one worker covers whole is finished by it. A unit cut between workers leaves one
+// partial result (unnormalised output, running maximum and sum, per row) per worker that touched
+// it, and a second kernel joins them (key_join.h). A worker can touch at most two cut units (its
+// first and its last), so it owns two partial slots: 2 w for the unit it starts with, 2 w + 1
+// for a later one. Work is even to one chunk whatever the lengths, the slots are as many as the
+// workers, and the sums run in a fixed order. With fewer chunks than workers each chunk gets one
+// worker and the rest have nothing to do, so every worker between the first and the last of a
+// unit holds a part of it.
+//
+// Query rows beyond one row tile: a worker is then one workgroup per row tile, side by side on
+// the same XCD at the same time, so that the tiles after the first find the keys in its L2.
 #pragma once
 #include "gdn_common.h"
 
@@ -30,7 +35,7 @@ struct FastDiv {
 struct SplitShape {
     const int32_t* seq_lens;
     int batch;
-    int units;      // per request: head groups x row tiles
+    int units;      // head groups of a request
     int max_keys;   // keys a table row can address
 };
 
@@ -43,65 +48,76 @@ __device__ __forceinline__ int split_chunks(const SplitShape& s, int b) {
     return (split_keys(s, b) + KB - 1) / KB;
 }
 
-// Workgroups that get work, the first chunk of workgroup w, and the owner of chunk x.
-__device__ __forceinline__ int split_wgs(int64_t total, int n_wg) {
-    return total < n_wg ? (int)total : n_wg;
+// Which worker and row tile a workgroup is. Workgroups are dealt to the 8 XCDs in turn; n is a
+// multiple of 8.
+struct SplitPlace {
+    int worker, row_tile;
+};
+__device__ __forceinline__ SplitPlace split_place(int block, int row_tiles) {
+    const int round = block / (8 * row_tiles), rest = block - round * 8 * row_tiles;
+    return {round * 8 + (rest & 7), rest >> 3};
 }
-__device__ __forceinline__ int64_t split_start(int w, int64_t total, int n) {
-    return (int64_t)((uint64_t)w * (uint64_t)total / (uint32_t)n);
+inline int split_workers(int workgroups, int row_tiles) {
+    const int n = workgroups / row_tiles / 8 * 8;
+    return n < 8 ? 8 : n;
 }
-__device__ __forceinline__ int split_owner(int64_t x, int64_t total, int n) {
-    return (int)(((uint64_t)(x + 1) * (uint32_t)n - 1) / (uint64_t)total);
-}
+
+// `total` chunks over at most n workers: the first `more` take each + 1, the others `each`.
+struct SplitCut {
+    int total, n, each, more;
+    __device__ __forceinline__ static SplitCut of(int total, int workers) {
+        const int n = total < workers ? total : workers;
+        if (n == 0) return {0, 0, 0, 0};
+        return {total, n, total / n, total % n};
+    }
+    __device__ __forceinline__ int start(int w) const { return w * each + min(w, more); }
+    __device__ __forceinline__ int owner(int x) const {
+        const int big = more * (each + 1);
+        return x < big ? x / (each + 1) : more + (x - big) / each;
+    }
+};
 
 // Workgroup-uniform values moved to scalar registers.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
-    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 | lo);
-}
-
-// This workgroup's run of chunks [pos, end), and the request that chunk `pos` lies in, whose
-// first chunk is `base`. All threads of the workgroup call it.
+// A worker's run of chunks [pos, end), and the request that chunk `pos` lies in, whose first
+// chunk is `base`. All threads of the workgroup call it.
 struct SplitRun {
-    int64_t pos, end, base;
-    int b;
+    int pos, end, base, b;
 };
 template <int KB, int THREADS>
-__device__ SplitRun split_run(const SplitShape& s, int w, int n_wg) {
-    __shared__ int64_t wave_tot[THREADS / WAVE];
-    __shared__ int64_t found_base;
-    __shared__ int found_b;
+__device__ SplitRun split_run(const SplitShape& s, int w, int workers) {
+    __shared__ int wave_tot[THREADS / WAVE];
+    __shared__ int found_base, found_b;
     const int tid = threadIdx.x;
     const int per = (s.batch + THREADS - 1) / THREADS;
     const int b0 = min(tid * per, s.batch), b1 = min(b0 + per, s.batch);
-    int64_t mine = 0;
+    int mine = 0;
     for (int b = b0; b < b1; b++) mine += split_chunks<KB>(s, b);
     mine *= s.units;
-    int64_t upto = mine;
+    int upto = mine;
 #pragma unroll
     for (int off = 1; off < WAVE; off <<= 1) {
-        const int64_t t = __shfl_up(upto, off, WAVE);
+        const int t = __shfl_up(upto, off, WAVE);
         if (lane_id() >= off) upto += t;
     }
     if (lane_id() == WAVE - 1) wave_tot[wave_id()] = upto;
     __syncthreads();
-    int64_t total = 0;
+    int total = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / WAVE; i++) {
         if (i < wave_id()) upto += wave_tot[i];
         total += wave_tot[i];
     }
-    SplitRun r;
-    const int n = split_wgs(total, n_wg);
-    r.pos = w < n ? split_start(w, total, n) : 0;
-    r.end = w < n ? split_start(w + 1, total, n) : 0;
-    const int64_t before = upto - mine;
-    if (before <= r.pos && r.pos < upto) {  // exactly one thread when pos < total
-        int64_t at = before;
-        int b = b0;
+    const SplitCut cut = SplitCut::of(uniform(total), workers);
+    SplitRun r = {0, 0, 0, 0};
+    if (w >= cut.n) return r;
+    r.pos = cut.start(w);
+    r.end = cut.start(w + 1);
+    const int before = upto - mine;
+    if (before <= r.pos && r.pos < upto) {  // exactly one thread
+        int at = before, b = b0;
         for (; b + 1 < b1; b++) {
-            const int64_t c = (int64_t)split_chunks<KB>(s, b) * s.units;
+            const int c = split_chunks<KB>(s, b) * s.units;
             if (r.pos < at + c) break;
             at += c;
         }
@@ -109,12 +125,8 @@ __device__ SplitRun split_run(const SplitShape& s, int w, int n_wg) {
         found_b = b;
     }
     __syncthreads();
-    // (found_* are unset when there is nothing to do)
-    const bool any = r.pos < r.end;
-    r.base = uniform(any ? found_base : 0);
-    r.b = uniform(any ? found_b : 0);
-    r.pos = uniform(r.pos);
-    r.end = uniform(r.end);
+    r.base = uniform(found_base);
+    r.b = uniform(found_b);
     return r;
 }
 

@@ -155,8 +155,10 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
     const int col = lane & 15, grp = lane >> 4;
     const int kg = wave / RH, part = wave % RH;  // key group and 16-row part of the scores
     const int key_row = kg * KEYS;               // first tile row of this wave's keys
-    SplitRun run = split_run<LD_KB, WAVES * WAVE>(a.split, blockIdx.x, a.n_wg);
-    const int64_t run_start = run.pos;
+    const SplitPlace me = split_place(blockIdx.x, a.row_tiles);
+    SplitRun run = split_run<LD_KB, WAVES * WAVE>(a.split, me.worker, a.workers);
+    const int run_start = run.pos;
+    const int row0 = me.row_tile * ROWS;
     const float cs = a.scale * LOG2E;
     const char* cache = reinterpret_cast<const char*>(a.cache);
 
@@ -178,10 +180,8 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
         const int b = run.b;
         const int nkeys = uniform(split_keys(a.split, b));
         const int nch = (nkeys + LD_KB - 1) / LD_KB;
-        const int unit = uniform((int)((run.pos - run.base) / nch));
-        const int c0 = (int)(run.pos - run.base - (int64_t)unit * nch);
-        const int c1 = (int)min((int64_t)nch, c0 + (run.end - run.pos));
-        const int row0 = unit * ROWS;
+        const int c0 = run.pos - run.base;
+        const int c1 = min(nch, c0 + (run.end - run.pos));
         const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
         const int seen0 = uniform(a.split.seq_lens[b]) - a.n_pos + 1;  // keys that position 0 sees
 
@@ -357,7 +357,8 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
 
         // total of the running sums over lanes and waves
         const bool whole = c0 == 0 && c1 == nch;
-        const int slot = 2 * (int)blockIdx.x + (run.pos == run_start ? 0 : 1);
+        const int slot = 2 * me.worker + (run.pos == run_start ? 0 : 1);
+        const size_t part_row = ((size_t)slot * a.row_tiles + me.row_tile) * ROWS;
         lds_barrier();
         l += __shfl_xor(l, 16, WAVE);
         l += __shfl_xor(l, 32, WAVE);
@@ -372,7 +373,7 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
                 for (int g = 0; g < Y::GROUPS; g++) sum += tops[g][rr];
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
                 float* out = whole ? a.o_lat + ((size_t)b * a.rows + r) * R
-                                   : a.part_o + ((size_t)slot * ROWS + rr) * R;
+                                   : a.part_o + (part_row + rr) * R;
 #pragma unroll
                 for (int j = 0; j < NT; j++) {
                     const int d = (wave * NT + j) * 16 + grp * 4;
@@ -382,7 +383,7 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
                     store4<float>(out + d, x);
                 }
                 if (!whole && wave == 0 && grp == 0) {
-                    float* pm = a.part_ml + ((size_t)slot * ROWS + rr) * 2;
+                    float* pm = a.part_ml + (part_row + rr) * 2;
                     pm[0] = m[t];
                     pm[1] = sum;
                 }
@@ -391,7 +392,7 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
         lds_barrier();  // the next unit writes tops and the tiles
 
         run.pos += c1 - c0;
-        if (run.pos < run.end && run.pos == run.base + (int64_t)nch * a.split.units) {
+        if (run.pos < run.end && run.pos == run.base + nch) {
             run.base = run.pos;
             do run.b++;
             while (run.b + 1 < a.split.batch && uniform(split_keys(a.split, run.b)) == 0);
@@ -401,16 +402,16 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
 
 // ------------------------------------------------------------------------------------ join
 // Weighted latents of the units that were cut, and zeros for requests without keys.
+template <int R>
 __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentDecodeArgs a) {
-    const int tile = 16 * a.rt;
-    const JoinShape s = {a.split, a.n_wg, tile, min(tile, a.rows), a.rank, a.part_o, a.part_ml};
-    join_parts<LD_KB>(
-        s, [&](int unit) { return min(tile, a.rows - unit * tile); },
-        [&](int b, int unit, int row, int col, const float x[4]) {
-            store4<float>(a.o_lat + ((size_t)b * a.rows + unit * tile + row) * a.rank + col, x);
+    const JoinShape s = {a.split, a.workers, a.row_tiles, 16 * a.rt, a.rows, a.part_o, a.part_ml};
+    join_parts<LD_KB, R>(
+        s,
+        [&](int b, int, int row, int col, const float x[4]) {
+            store4<float>(a.o_lat + ((size_t)b * a.rows + row) * R + col, x);
         },
         [&](int b) {
-            const size_t n = (size_t)a.rows * a.rank;
+            const size_t n = (size_t)a.rows * R;
             const float z[4] = {0.f, 0.f, 0.f, 0.f};
             for (size_t i = threadIdx.x * 4; i < n; i += JOIN_THREADS * 4)
                 store4<float>(a.o_lat + (size_t)b * n + i, z);
@@ -418,19 +419,29 @@ __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentDecodeA
 }
 
 // -------------------------------------------------------------------------------------- up
-// o = W_uv u, one head per workgroup: its rows of W_uv stay in registers as the MFMA's A
-// operand while the (request, position) rows pass, 16 at a time. u is taken as the sum of two
-// bf16 numbers, its rounding and the rounding of what that leaves (2^-17 of it together): one
-// more MFMA each, in a pass that waits for memory, for an output error that is a third smaller.
+// o = W_uv u for one head and 16 (request, position) rows. u is taken as the sum of two bf16
+// numbers, its rounding and the rounding of what that leaves (2^-17 of it together): one more
+// MFMA each, in a kernel that waits for memory, for an output error that is a third smaller.
+// Everything is requested at once (the weights as the MFMA's A operand into registers, the rows
+// of u into LDS), so a workgroup pays one trip to memory.
 template <int R, int DV>
-__global__ __launch_bounds__(LD_THREADS) void latent_up_kernel(LatentDecodeArgs a,
-                                                               int tiles_per_wg) {
+__global__ __launch_bounds__(LD_THREADS) void latent_up_kernel(LatentDecodeArgs a) {
     constexpr int NJ = DV / 16 / LD_WAVES;
+    constexpr int PITCH = R * 2 + 16;                    // LDS row: 16-byte pieces on all banks
+    constexpr int PER = 16 * R / 4 / LD_THREADS;         // 4-column pieces of u per thread
+    __shared__ __align__(16) char lds[2][16 * PITCH];    // the two parts of u
     const int h = blockIdx.x, lane = lane_id(), wave = wave_id();
     const int col = lane & 15, grp = lane >> 4;
-    const int rows = a.split.batch * a.n_pos;
+    const int rows = a.split.batch * a.n_pos, row0 = blockIdx.y * 16;
     const bf16* W = reinterpret_cast<const bf16*>(a.w_kv) +
                     ((size_t)h * (a.d_nope + DV) + a.d_nope) * R;
+    f32x4 u[PER];
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        const int x = i * LD_THREADS + threadIdx.x, r = x / (R / 4), c = x % (R / 4);
+        u[i] = *reinterpret_cast<const f32x4*>(
+            a.o_lat + ((size_t)min(row0 + r, rows - 1) * a.H + h) * R + c * 4);
+    }
     bf16x8 w[NJ][R / 32];
 #pragma unroll
     for (int j = 0; j < NJ; j++)
@@ -438,42 +449,45 @@ __global__ __launch_bounds__(LD_THREADS) void latent_up_kernel(LatentDecodeArgs 
         for (int k = 0; k < R / 32; k++)
             w[j][k] = Mma<bf16>::load(W + (size_t)((wave * NJ + j) * 16 + col) * R + k * 32 +
                                       grp * 8);
-    const int t0 = blockIdx.y * tiles_per_wg;
-    for (int t = t0; t < t0 + tiles_per_wg && t * 16 < rows; t++) {
-        const int row = t * 16 + col;
-        const float* u = a.o_lat + ((size_t)min(row, rows - 1) * a.H + h) * R + grp * 8;
-        f32x4 d[NJ];
+    sched_fence();
 #pragma unroll
-        for (int j = 0; j < NJ; j++) d[j] = zero4();
+    for (int i = 0; i < PER; i++) {
+        const int x = i * LD_THREADS + threadIdx.x, r = x / (R / 4), c = x % (R / 4);
+        float hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < R / 32; k++) {
-            float x[8];
-            load8<float>(u + k * 32, x);
-            bf16x8 hi, lo;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                hi[i] = (bf16)x[i];
-                lo[i] = (bf16)(x[i] - (float)hi[i]);
-            }
-#pragma unroll
-            for (int j = 0; j < NJ; j++) {
-                d[j] = Mma<bf16>::mma(w[j][k], hi, d[j]);
-                d[j] = Mma<bf16>::mma(w[j][k], lo, d[j]);
-            }
+        for (int e = 0; e < 4; e++) {
+            hi[e] = (float)(bf16)u[i][e];
+            lo[e] = u[i][e] - hi[e];
         }
-        bf16* out = reinterpret_cast<bf16*>(a.o) + ((size_t)row * a.H + h) * DV;
+        *reinterpret_cast<uint64_t*>(lds[0] + r * PITCH + c * 8) = bits4(hi);
+        *reinterpret_cast<uint64_t*>(lds[1] + r * PITCH + c * 8) = bits4(lo);
+    }
+    __syncthreads();
+    f32x4 d[NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; j++) {
-            const float y[4] = {d[j][0], d[j][1], d[j][2], d[j][3]};
-            if (row < rows) store4<bf16>(out + (wave * NJ + j) * 16 + grp * 4, y);
+    for (int j = 0; j < NJ; j++) d[j] = zero4();
+#pragma unroll
+    for (int k = 0; k < R / 32; k++)
+#pragma unroll
+        for (int part = 0; part < 2; part++) {
+            const bf16x8 x = *reinterpret_cast<const bf16x8*>(lds[part] + col * PITCH + k * 64 +
+                                                              grp * 16);
+#pragma unroll
+            for (int j = 0; j < NJ; j++) d[j] = Mma<bf16>::mma(w[j][k], x, d[j]);
         }
+    const int row = row0 + col;
+    bf16* out = reinterpret_cast<bf16*>(a.o) + ((size_t)row * a.H + h) * DV;
+#pragma unroll
+    for (int j = 0; j < NJ; j++) {
+        const float y[4] = {d[j][0], d[j][1], d[j][2], d[j][3]};
+        if (row < rows) store4<bf16>(out + (wave * NJ + j) * 16 + grp * 4, y);
     }
 }
 
 template <int DN>
 void run_absorb(const LatentDecodeArgs& a, hipStream_t s) {
     const int tiles = (a.split.batch * a.n_pos + 15) / 16;
-    const int per = tiles < 8 ? tiles : 8;
+    const int per = tiles < 2 ? tiles : 2;  // each row tile is one more trip to memory in turn
     hipLaunchKernelGGL(latent_absorb_kernel<DN>,
                        dim3((unsigned)a.H, (unsigned)(a.rank / AB_COLS),
                             (unsigned)((tiles + per - 1) / per)),
@@ -482,7 +496,7 @@ void run_absorb(const LatentDecodeArgs& a, hipStream_t s) {
 
 template <int R, int RH, int KS>
 void core_launch(const LatentDecodeArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((latent_core_kernel<R, RH, KS>), dim3((unsigned)a.n_wg),
+    hipLaunchKernelGGL((latent_core_kernel<R, RH, KS>), dim3((unsigned)(a.workers * a.row_tiles)),
                        dim3(LdWaves<RH, KS>::WAVES * WAVE), 0, s, a);
 }
 
@@ -500,10 +514,8 @@ hipError_t run_core(const LatentDecodeArgs& a, hipStream_t s) {
 template <int R, int DV>
 hipError_t run_up(const LatentDecodeArgs& a, hipStream_t s) {
     const int tiles = (a.split.batch * a.n_pos + 15) / 16;
-    const int per = tiles < 4 ? tiles : 4;
-    hipLaunchKernelGGL((latent_up_kernel<R, DV>),
-                       dim3((unsigned)a.H, (unsigned)((tiles + per - 1) / per)), dim3(LD_THREADS),
-                       0, s, a, per);
+    hipLaunchKernelGGL((latent_up_kernel<R, DV>), dim3((unsigned)a.H, (unsigned)tiles),
+                       dim3(LD_THREADS), 0, s, a);
     return hipGetLastError();
 }
 
@@ -511,7 +523,7 @@ template <int R>
 hipError_t run_rank(const LatentDecodeArgs& a, hipStream_t s) {
     hipError_t e = run_core<R>(a, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)a.n_join), dim3(JOIN_THREADS), 0, s, a);
+    hipLaunchKernelGGL(latent_join_kernel<R>, dim3((unsigned)a.n_join), dim3(JOIN_THREADS), 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     return a.d_v == 128 ? run_up<R, 128>(a, s) : run_up<R, 64>(a, s);
@@ -524,10 +536,10 @@ size_t latent_decode_layout(LatentDecodeArgs* a, void* ws) {
     const int tiles = (a->rows + 15) / 16;
     a->rt = tiles >= 3 ? 4 : tiles;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
-    a->split.units = a->row_tiles;
-    a->n_wg = min(device_cu_count(), JOIN_MAX_WG);
+    a->split.units = 1;
+    a->workers = split_workers(min(device_cu_count(), JOIN_MAX_WORKERS), a->row_tiles);
     a->n_join = 4 * device_cu_count();
-    const size_t part = (size_t)2 * a->n_wg * 16 * a->rt;
+    const size_t part = (size_t)2 * a->workers * a->row_tiles * 16 * a->rt;
     const size_t lat = (size_t)a->split.batch * a->rows * a->rank;  // bf16 elements
     size_t off = 0;
     auto take = [&](size_t bytes) {

@@ -139,8 +139,10 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
     __shared__ float ml[PD_WAVES][16][2];
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform(wave_id());
     const int col = lane & 15, grp = lane >> 4;
-    SplitRun run = split_run<KB, PD_THREADS>(a.split, blockIdx.x, a.n_wg);
-    const int64_t run_start = run.pos;
+    const SplitPlace me = split_place(blockIdx.x, a.row_tiles);
+    SplitRun run = split_run<KB, PD_THREADS>(a.split, me.worker, a.workers);
+    const int run_start = run.pos;
+    const int row0 = me.row_tile * 16 * RT;
     char* vlds = smem + wave * L::VTILE;
     const float cs = a.scale * LOG2E;
 
@@ -148,10 +150,9 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
         const int b = run.b;
         const int nkeys = uniform(split_keys(a.split, b));
         const int nch = (nkeys + KB - 1) / KB;
-        const int unit = uniform((int)((run.pos - run.base) / nch));
-        const int c0 = (int)(run.pos - run.base - (int64_t)unit * nch);
-        const int c1 = (int)min((int64_t)nch, c0 + (run.end - run.pos));
-        const int kvh = unit / a.row_tiles, row0 = (unit - kvh * a.row_tiles) * 16 * RT;
+        const int kvh = (run.pos - run.base) / nch;
+        const int c0 = run.pos - run.base - kvh * nch;
+        const int c1 = min(nch, c0 + (run.end - run.pos));
         const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
         const int seen0 = uniform(a.split.seq_lens[b]) - a.n_pos + 1;  // keys that position 0 sees
 
@@ -312,7 +313,8 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
 
         // merge the four waves, one 16-row tile at a time
         const bool whole = c0 == 0 && c1 == nch;
-        const int slot = 2 * (int)blockIdx.x + (run.pos == run_start ? 0 : 1);
+        const int slot = 2 * me.worker + (run.pos == run_start ? 0 : 1);
+        const size_t part_row = ((size_t)slot * a.row_tiles + me.row_tile) * (16 * RT);
         float* mrow = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int rt = 0; rt < RT; rt++) {
@@ -345,7 +347,7 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
                 const int p = rr / a.group, h = rr - p * a.group;
                 T* dst = reinterpret_cast<T*>(a.o) +
                          (((size_t)b * a.n_pos + p) * a.H + (size_t)kvh * a.group + h) * D;
-                float* part = a.part_o + ((size_t)slot * RT * 16 + rt * 16 + r) * D;
+                float* part = a.part_o + (part_row + rt * 16 + r) * D;
 #pragma unroll
                 for (int j = 0; j < D / 64; j++) {
                     const int d = j * 64 + (tid & 15) * 4;
@@ -366,7 +368,7 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
                     }
                 }
                 if (!whole && (tid & 15) == 0) {
-                    float* pm = a.part_ml + ((size_t)slot * RT * 16 + rt * 16 + r) * 2;
+                    float* pm = a.part_ml + (part_row + rt * 16 + r) * 2;
                     pm[0] = top;
                     pm[1] = sum;
                 }
@@ -375,7 +377,7 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
         __syncthreads();  // the merge rows are the next unit's V tiles
 
         run.pos += c1 - c0;
-        if (run.pos < run.end && run.pos == run.base + (int64_t)nch * a.split.units) {
+        if (run.pos < run.end && run.pos == run.base + nch * a.split.units) {
             run.base = run.pos;
             do run.b++;
             while (run.b + 1 < a.split.batch && uniform(split_keys(a.split, run.b)) == 0);
@@ -387,13 +389,11 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
 template <typename T, int D>
 __global__ __launch_bounds__(JOIN_THREADS) void paged_join_kernel(PagedDecodeArgs a) {
     constexpr int KB = PdTile<T, D>::KW * PD_WAVES;
-    const int tile = 16 * a.rt;
-    const JoinShape s = {a.split, a.n_wg, tile, min(tile, a.rows), D, a.part_o, a.part_ml};
-    join_parts<KB>(
-        s, [&](int unit) { return min(tile, a.rows - (unit % a.row_tiles) * tile); },
-        [&](int b, int unit, int row, int col, const float x[4]) {
-            const int kvh = unit / a.row_tiles, r = (unit - kvh * a.row_tiles) * tile + row;
-            const int p = r / a.group, h = r - p * a.group;
+    const JoinShape s = {a.split, a.workers, a.row_tiles, 16 * a.rt, a.rows, a.part_o, a.part_ml};
+    join_parts<KB, D>(
+        s,
+        [&](int b, int kvh, int row, int col, const float x[4]) {
+            const int p = row / a.group, h = row - p * a.group;
             store4<T>(reinterpret_cast<T*>(a.o) +
                           (((size_t)b * a.n_pos + p) * a.H + (size_t)kvh * a.group + h) * D + col,
                       x);
@@ -408,8 +408,8 @@ __global__ __launch_bounds__(JOIN_THREADS) void paged_join_kernel(PagedDecodeArg
 
 template <typename T, int D, int RT>
 hipError_t run_decode(const PagedDecodeArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((paged_decode_kernel<T, D, RT>), dim3((unsigned)a.n_wg), dim3(PD_THREADS),
-                       0, s, a);
+    hipLaunchKernelGGL((paged_decode_kernel<T, D, RT>), dim3((unsigned)(a.workers * a.row_tiles)),
+                       dim3(PD_THREADS), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((paged_join_kernel<T, D>), dim3((unsigned)a.n_join), dim3(JOIN_THREADS), 0, s,
@@ -451,10 +451,10 @@ size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
     const int tiles = (a->rows + 15) / 16;
     a->rt = tiles >= 4 && most >= 4 ? 4 : tiles >= 2 && most >= 2 ? 2 : 1;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
-    a->split.units = a->kv_heads * a->row_tiles;
-    a->n_wg = min(2 * device_cu_count(), JOIN_MAX_WG);
+    a->split.units = a->kv_heads;
+    a->workers = split_workers(min(2 * device_cu_count(), JOIN_MAX_WORKERS), a->row_tiles);
     a->n_join = 4 * device_cu_count();
-    const size_t rows = (size_t)2 * a->n_wg * 16 * a->rt;
+    const size_t rows = (size_t)2 * a->workers * a->row_tiles * 16 * a->rt;
     a->part_o = static_cast<float*>(ws);
     a->part_ml = a->part_o == nullptr ? nullptr : a->part_o + rows * a->d;
     return rows * (a->d + 2) * sizeof(float);
