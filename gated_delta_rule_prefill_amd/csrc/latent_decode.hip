@@ -144,13 +144,14 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
     using X = LdTile<R>;
     using Y = LdWaves<RH, KS>;
     constexpr int WAVES = Y::WAVES, KEYS = Y::KEYS, OWN = Y::OWN;
-    constexpr uint32_t ALL = (uint32_t)((1ull << KEYS) - 1);
+    constexpr uint64_t ALL = (1ull << KEYS) - 1;
     constexpr int ROWS = 16 * RH;
     constexpr int NL = R / 32, NF = NL + LD_ROPE / 32;  // key fragments: latent, then rotary
     constexpr int NT = R / 16 / WAVES;                  // 16-column output tiles per wave
-    __shared__ __align__(16) char tile[2 * X::BYTES];
-    __shared__ __align__(16) char wt[ROWS * LD_KB * 2];
-    __shared__ float tops[Y::GROUPS][ROWS];
+    __shared__ __align__(1024) char tile[2 * X::BYTES];
+    __shared__ __align__(1024) char wt[ROWS * LD_KB * 2];
+    __shared__ float tops[Y::GROUPS][ROWS];  // row maxima of a tile per key group; then row sums
+    __shared__ float shrinks[ROWS];          // what a tile's new maxima scale older sums by
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int col = lane & 15, grp = lane >> 4;
     const int kg = wave / RH, part = wave % RH;  // key group and 16-row part of the scores
@@ -162,19 +163,14 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
     const float cs = a.scale * LOG2E;
     const char* cache = reinterpret_cast<const char*>(a.cache);
 
-    // LDS byte offsets of this lane's reads (the piece index is xored with a function of the
-    // row, so most of it folds into an immediate: four offsets for the key fragments, one for
-    // the transposing reads, whose second half lies 4 rows on with the lowest piece bit turned)
-    int k_at[4], pe_at[2], p_at[2];
-#pragma unroll
-    for (int f = 0; f < 4; f++) k_at[f] = X::lat(key_row + col, f * 4 + grp);
-#pragma unroll
-    for (int f = 0; f < 2; f++) {
-        pe_at[f] = X::rope(key_row + col, f * 4 + grp);
-        p_at[f] = ld_weight(col, f * 4 + grp);
-    }
-    const int v_at = X::lat(grp * 8 + ((lane >> 2) & 3), wave * NT * 2 + ((lane & 3) >> 1)) +
-                     (lane & 1) * 8;
+    // LDS byte offsets of this lane's reads and writes within a tile or the weights. A piece
+    // index is xored with a function of the row, so its constant part can be xored in last, and
+    // one offset serves all pieces of a kind.
+    const uint32_t k_at = X::lat(key_row + col, grp), pe_at = X::rope(key_row + col, grp);
+    const uint32_t p_at = ld_weight(col, grp);
+    const uint32_t p_put = ld_weight(col, kg * KS * 2 + (grp >> 1)) + (grp & 1) * 8;
+    const uint32_t v_at = X::lat(grp * 8 + ((lane >> 2) & 3), wave * NT * 2 + ((lane & 3) >> 1)) +
+                          (lane & 1) * 8;
 
     while (run.pos < run.end) {
         const int b = run.b;
@@ -185,19 +181,24 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
         const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
         const int seen0 = uniform(a.split.seq_lens[b]) - a.n_pos + 1;  // keys that position 0 sees
 
-        // the page of lane's key among this wave's keys of a chunk (KEYS lanes, repeated)
+        // the table entry of lane's key among this wave's keys of a chunk (KEYS lanes, repeated);
+        // keys past the end read the table's last entry, and load_tile() drops them
         int page;
         auto load_pages = [&](int c) {
-            const int key = c * LD_KB + key_row + lane % KEYS;
-            page = key < nkeys ? table[a.block((uint32_t)key)] : -1;
+            const uint32_t key = (uint32_t)(c * LD_KB + key_row + lane % KEYS);
+            page = table[min(a.block(key), (uint32_t)a.max_blocks - 1)];
         };
-        uint32_t exist, exist_next = 0;
-        auto load_tile = [&](int c, int buf) {
+        uint64_t exist, exist_next = 0;
+        // Tile c into a buffer, its pages being in `page`, which then takes those of chunk `next`.
+        // (That load goes first: the compiler's wait for it must not be behind the tile's.)
+        auto load_tile = [&](int c, int buf, int next) {
             const uint32_t key = (uint32_t)(c * LD_KB + key_row + lane % KEYS);
             const uint32_t off = key - a.block(key) * a.block.div;
-            const bool ok = page >= 0 && page < a.n_blocks;
+            const bool ok = (int)key < nkeys && page >= 0 && page < a.n_blocks;
             const uint32_t slot = ok ? (uint32_t)page * a.block.div + off : 0u;
-            exist_next = (uint32_t)__ballot(ok) & ALL;
+            exist_next = __ballot(ok) & ALL;
+            load_pages(next);
+            sched_fence();
             const uint32_t at = lds_offset(tile) + buf * X::BYTES;
             const int first = part * OWN;
             if constexpr (X::PIECES == 64) {
@@ -231,8 +232,7 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
             }
         };
         load_pages(c0);
-        load_tile(c0, 0);
-        load_pages(c0 + 1 < c1 ? c0 + 1 : c0);
+        load_tile(c0, 0, c0 + 1);
 
         bf16x8 q[NF];
         const int q_row = row0 + part * 16 + col;
@@ -247,110 +247,140 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
                 q[f] = Mma<bf16>::load(f < NL ? ql + f * 32 + grp * 8
                                               : qp + (f - NL) * 32 + grp * 8);
         }
+        arrived(q);
         f32x4 acc[RH][NT];
-        float m[RH], l = 0.f;  // running maxima of all rows; this lane's share of its row's sum
+        float m = -INFINITY, l = 0.f;  // this lane's row: running maximum, share of the sum
 #pragma unroll
-        for (int t = 0; t < RH; t++) {
-            m[t] = -INFINITY;
+        for (int t = 0; t < RH; t++)
 #pragma unroll
             for (int j = 0; j < NT; j++) acc[t][j] = zero4();
-        }
 
         for (int c = c0; c < c1; c++) {
             const int buf = (c - c0) & 1;
-            const char* kt = tile + buf * X::BYTES;
+            const uint32_t kt = lds_offset(tile) + buf * X::BYTES;
+            // (copies that the compiler cannot take for constant over the key loop: it would keep
+            // every sum below in a register of its own and spill for it)
+            uint32_t k_here = kt + k_at, pe_here = kt + pe_at, v_here = kt + v_at;
+            uint32_t p_here = p_at, put_here = p_put;
+            asm volatile("" : "+v"(k_here), "+v"(pe_here), "+v"(v_here), "+v"(p_here),
+                              "+v"(put_here));
+            auto weights = [&](int t) {  // of the 16 rows of row tile t
+                return lds_offset(wt) + t * (16 * LD_KB * 2);
+            };
             exist = exist_next;
             lds_loads_done();
             if (exist != ALL) {
                 // latents of absent keys as zeros: a zero weight does not cancel what they hold
+#pragma unroll 1
                 for (int r = part * OWN; r < part * OWN + OWN; r++)
                     if (!((exist >> r) & 1) && lane < X::PIECES)
-                        *reinterpret_cast<f32x4*>(tile + buf * X::BYTES + (key_row + r) * X::LAT +
-                                                  lane * 16) = zero4();
+                        lds_put(kt + (key_row + r) * X::LAT + lane * 16, zero4());
             }
             lds_barrier();  // tile c is whole; all waves are done with the other buffer
-            if (c + 1 < c1) {
-                load_tile(c + 1, buf ^ 1);
-                load_pages(c + 2 < c1 ? c + 2 : c + 1);
-            }
+            if (c + 1 < c1) load_tile(c + 1, buf ^ 1, c + 2);
             f32x4 s[KS];
 #pragma unroll
             for (int x = 0; x < KS; x++) s[x] = zero4();
+            // key fragments two steps of the contraction at a time, the next two on their way
+            bf16x8 k[2][2][KS];
+            auto load_k = [&](int f, bf16x8 (&to)[KS]) {
 #pragma unroll
-            for (int f = 0; f < NF; f++)
+                for (int x = 0; x < KS; x++)  // (16 rows on, the pieces are turned alike)
+                    to[x] = lds_get<bf16x8>(
+                        f < NL ? (k_here ^ (f & 3) << 6) + (f >> 2) * 256 + x * (16 * X::LAT)
+                               : (pe_here ^ (f - NL) << 6) + x * (16 * LD_ROPE * 2));
+            };
+            load_k(0, k[0][0]);
+            load_k(1, k[0][1]);
 #pragma unroll
-                for (int x = 0; x < KS; x++) {
-                    // (16 rows on, the pieces are turned alike)
-                    const char* at = f < NL
-                        ? kt + k_at[f & 3] + (f >> 2) * 256 + x * (16 * X::LAT)
-                        : kt + pe_at[f - NL] + x * (16 * LD_ROPE * 2);
-                    s[x] = Mma<bf16>::mma(*reinterpret_cast<const bf16x8*>(at), q[f], s[x]);
+            for (int f = 0; f < NF; f += 2) {
+                const int now = (f >> 1) & 1;
+                if (f + 2 < NF) {
+                    load_k(f + 2, k[now ^ 1][0]);
+                    load_k(f + 3, k[now ^ 1][1]);
                 }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+#pragma unroll
+                    for (int x = 0; x < KS; x++) s[x] = Mma<bf16>::mma(k[now][e][x], q[f + e], s[x]);
+            }
             const int key0 = c * LD_KB + key_row;
-            const bool mask = exist != ALL || key0 + KEYS > seen0;
-            float top = -INFINITY;
+            if (exist != ALL || key0 + KEYS > seen0) {
+                // this lane's keys are key0 + first + 16 x + i (hidden from the compiler, which
+                // would keep what depends on it in registers across the key loop)
+                int first = grp * 4;
+                asm volatile("" : "+v"(first));
+                const uint64_t here = exist >> first;
+                const int left = lim - key0 - first;
+#pragma unroll
+                for (int x = 0; x < KS; x++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const bool keep = ((here >> (x * 16 + i)) & 1) && x * 16 + i < left;
+                        s[x][i] = keep ? s[x][i] * cs : -INFINITY;
+                    }
+            } else {
+#pragma unroll
+                for (int x = 0; x < KS; x++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) s[x][i] *= cs;
+            }
+            float top = s[0][0];
 #pragma unroll
             for (int x = 0; x < KS; x++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    s[x][i] *= cs;
-                    if (mask) {
-                        const int k = x * 16 + grp * 4 + i;
-                        const bool keep = ((exist >> k) & 1) && key0 + k < lim;
-                        s[x][i] = keep ? s[x][i] : -INFINITY;
-                    }
-                    top = fmaxf(top, s[x][i]);
-                }
+                for (int i = 0; i < 4; i++) top = fmaxf(top, s[x][i]);
             top = fmaxf(top, __shfl_xor(top, 16, WAVE));
             top = fmaxf(top, __shfl_xor(top, 32, WAVE));
             if (grp == 0) tops[kg][part * 16 + col] = top;
             lds_barrier();
-            // all waves follow the maxima of all rows, their outputs' columns hold them all
-            float own_ref = 0.f;
+            float m1 = m;
 #pragma unroll
-            for (int t = 0; t < RH; t++) {
-                float m1 = m[t];
-#pragma unroll
-                for (int g = 0; g < Y::GROUPS; g++) m1 = fmaxf(m1, tops[g][t * 16 + col]);
-                const float ref = m1 == -INFINITY ? 0.f : m1;  // a row with no key so far
-                if (t == part) own_ref = ref;
-                if (__any(m1 > m[t])) {
-                    const float shrink = __builtin_amdgcn_exp2f(m[t] - ref);
-                    if (t == part) l *= shrink;
-#pragma unroll
-                    for (int j = 0; j < NT; j++)
-#pragma unroll
-                        for (int i = 0; i < 4; i++) acc[t][j][i] *= shrink;
-                    m[t] = m1;
-                }
-            }
+            for (int g = 0; g < Y::GROUPS; g++) m1 = fmaxf(m1, tops[g][part * 16 + col]);
+            const float ref = m1 == -INFINITY ? 0.f : m1;  // a row with no key so far
+            const float shrink = __builtin_amdgcn_exp2f(m - ref);
+            // (the exponential is 1 when the maximum stays; a row still without a key has sums
+            // of zero, which its exp2(-inf - 0) = 0 leaves)
+            l *= shrink;
+            if (kg == 0 && grp == 0) shrinks[part * 16 + col] = shrink;
+            m = m1;
 #pragma unroll
             for (int x = 0; x < KS; x++) {
                 float p[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    p[i] = __builtin_amdgcn_exp2f(s[x][i] - own_ref);
+                    p[i] = __builtin_amdgcn_exp2f(s[x][i] - ref);
                     l += p[i];
                 }
-                *reinterpret_cast<uint64_t*>(
-                    wt + ld_weight(part * 16 + col, (kg * KS + x) * 2 + (grp >> 1)) +
-                    (grp & 1) * 8) = bits4(p);
+                lds_put((weights(part) + put_here) ^ x << 5, bits4(p));
             }
             lds_barrier();
 #pragma unroll
-            for (int ks = 0; ks < LD_KB / 32; ks++) {
-                bf16x8 pb[RH];
+            for (int t = 0; t < RH; t++) {
+                const float f = shrinks[t * 16 + col];
+                if (__any(f != 1.f)) {
 #pragma unroll
-                for (int t = 0; t < RH; t++)
-                    pb[t] = *reinterpret_cast<const bf16x8*>(wt + p_at[ks] + t * (16 * LD_KB * 2));
+                    for (int j = 0; j < NT; j++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) acc[t][j][i] *= f;
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < LD_KB / 32; ks++) {
+                bf16x8 v[NT];
 #pragma unroll
                 for (int j = 0; j < NT; j++) {
-                    const char* v0 = kt + (v_at ^ (j << 5)) + ks * (32 * X::LAT);
-                    const char* v1 = kt + (v_at ^ (j << 5) ^ 16) + ks * (32 * X::LAT) + 4 * X::LAT;
-                    const bf16x8 v = join(lds_read_tr(v0), lds_read_tr(v1));
+                    // the second half lies 4 rows on, where the lowest piece bit is turned
+                    const uint32_t at = v_here ^ j << 5;
+                    v[j] = join(lds_read_tr(at + ks * (32 * X::LAT)),
+                                lds_read_tr((at ^ 16) + ks * (32 * X::LAT) + 4 * X::LAT));
+                }
 #pragma unroll
-                    for (int t = 0; t < RH; t++)
-                        acc[t][j] = Mma<bf16>::mma(v, pb[t], acc[t][j]);
+                for (int t = 0; t < RH; t++) {
+                    const bf16x8 p = lds_get<bf16x8>((weights(t) + p_here) ^ ks << 6);
+#pragma unroll
+                    for (int j = 0; j < NT; j++) acc[t][j] = Mma<bf16>::mma(v[j], p, acc[t][j]);
                 }
             }
         }
@@ -382,13 +412,11 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
                     for (int i = 0; i < 4; i++) x[i] = whole ? acc[t][j][i] * inv : acc[t][j][i];
                     store4<float>(out + d, x);
                 }
-                if (!whole && wave == 0 && grp == 0) {
-                    float* pm = a.part_ml + (part_row + rr) * 2;
-                    pm[0] = m[t];
-                    pm[1] = sum;
-                }
+                if (!whole && wave == 0 && grp == 0) a.part_ml[(part_row + rr) * 2 + 1] = sum;
             }
         }
+        if (!whole && kg == 0 && grp == 0 && live)
+            a.part_ml[(part_row + part * 16 + col) * 2] = m;
         lds_barrier();  // the next unit writes tops and the tiles
 
         run.pos += c1 - c0;
@@ -534,7 +562,7 @@ hipError_t run_rank(const LatentDecodeArgs& a, hipStream_t s) {
 size_t latent_decode_layout(LatentDecodeArgs* a, void* ws) {
     a->rows = a->H * a->n_pos;
     const int tiles = (a->rows + 15) / 16;
-    a->rt = tiles >= 3 ? 4 : tiles;
+    a->rt = tiles > 2 ? 4 : tiles;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
     a->split.units = 1;
     a->workers = split_workers(min(device_cu_count(), JOIN_MAX_WORKERS), a->row_tiles);

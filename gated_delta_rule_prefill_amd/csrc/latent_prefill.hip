@@ -301,6 +301,7 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
 #pragma unroll
         for (int f = 0; f < NR; f++) q[NK + f] = Mma<bf16>::load(qp + f * 16 + half * 8);
     }
+    arrived(q);
     const char* ksrc = reinterpret_cast<const char*>(a.k) +
                        ((size_t)h * a.key_tiles + kt0) * (LP_KB * D * 2);
     const char* vsrc = reinterpret_cast<const char*>(a.vt) +

@@ -11,6 +11,18 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
 
+// LDS by 32-bit byte offset: the compiler otherwise carries some addresses as 64-bit generic
+// pointers, two registers each.
+typedef __attribute__((address_space(3))) char lds_char;
+template <typename V>
+__device__ __forceinline__ V lds_get(uint32_t at) {
+    return *(const __attribute__((address_space(3))) V*)(lds_char*)(uintptr_t)at;
+}
+template <typename V>
+__device__ __forceinline__ void lds_put(uint32_t at, V v) {
+    *(__attribute__((address_space(3))) V*)(lds_char*)(uintptr_t)at = v;
+}
+
 // 64 lanes x 16 bytes from `base` + each lane's `offset` to the 1 KiB of LDS at `lds` (wave
 // uniform, lane l's piece at 16 l). No register receives data, and the compiler does not count
 // the load: lds_loads_done() has to come before the barrier behind which the data is read.
@@ -30,6 +42,13 @@ __device__ __forceinline__ void load_to_lds(const void* lane_address, uint32_t l
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(lane_address)
                  : "memory");
 }
+// Makes the compiler wait for these registers' loads here. Left to their first use inside a loop,
+// the wait would be repeated in every pass and take the tile loads behind them along.
+template <int N>
+__device__ __forceinline__ void arrived(bf16x8 (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i++) asm volatile("" : "+v"(x[i]));
+}
 __device__ __forceinline__ void lds_loads_done() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
@@ -40,6 +59,10 @@ __device__ __forceinline__ void lds_loads_done() {
 __device__ __forceinline__ bf16x4 lds_read_tr(const char* p) {
     typedef __attribute__((address_space(3))) s16x4* lptr;
     return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(p)));
+}
+__device__ __forceinline__ bf16x4 lds_read_tr(uint32_t at) {
+    typedef __attribute__((address_space(3))) s16x4* lptr;
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(uintptr_t)at));
 }
 __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
     bf16x8 r;

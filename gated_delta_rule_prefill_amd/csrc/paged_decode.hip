@@ -181,13 +181,14 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
             for (int j = 0; j < D / 16; j++) acc[rt][j] = zero4();
         }
 
-        // page of this lane's key of each 16-key group of wave step c (lanes 16.. repeat 0..15)
+        // table entry of this lane's key of each 16-key group of wave step c (lanes 16.. repeat
+        // 0..15); keys past the end read the table's last entry, and find_rows() drops them
         int page[NSUB];
         auto load_pages = [&](int c) {
 #pragma unroll
             for (int t = 0; t < NSUB; t++) {
-                const int key = c * KB + wave * KW + t * 16 + col;
-                page[t] = key < nkeys ? table[a.block((uint32_t)key)] : -1;
+                const uint32_t key = (uint32_t)(c * KB + wave * KW + t * 16 + col);
+                page[t] = table[min(a.block(key), (uint32_t)a.max_blocks - 1)];
             }
         };
         uint32_t row[NSUB];
@@ -196,7 +197,7 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
             for (int t = 0; t < NSUB; t++) {
                 const uint32_t key = (uint32_t)(c * KB + wave * KW + t * 16 + col);
                 const uint32_t off = key - a.block(key) * a.block.div;
-                const bool ok = page[t] >= 0 && page[t] < a.n_blocks;
+                const bool ok = (int)key < nkeys && page[t] >= 0 && page[t] < a.n_blocks;
                 row[t] = ok ? ((uint32_t)page[t] * a.kv_heads + kvh) * a.block.div + off : NO_ROW;
             }
         };
@@ -228,9 +229,9 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
         };
         load_pages(c0);
         find_rows(c0);
+        load_pages(c0 + 1);
         load_k();
         load_v();
-        load_pages(c0 + 1 < c1 ? c0 + 1 : c0);
 
         for (int c = c0; c < c1; c++) {
             float s[RT][NSUB][4];
@@ -276,9 +277,9 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
             }
             if (c + 1 < c1) {
                 find_rows(c + 1);
+                load_pages(c + 2);  // first: the wait for it must not be behind the others
                 load_k();
                 load_v();
-                load_pages(c + 2 < c1 ? c + 2 : c + 1);
             }
 #pragma unroll
             for (int rt = 0; rt < RT; rt++) {
