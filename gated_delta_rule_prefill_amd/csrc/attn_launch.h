@@ -6,7 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "key_split.h"
+#include "key_join.h"
 
 namespace gdn {
 
@@ -47,10 +47,9 @@ struct PagedDecodeArgs {
     const int32_t* block_table;
     FastDiv block;       // by the page size
     SplitShape split;    // units = kv_heads
-    int group, rows, rt, row_tiles, workers, n_join;
+    int group, rows, rt, row_tiles, workers;
+    JoinShape join;
     void* o;
-    float* part_o;       // [2 workers][row_tiles][16 rt][d]
-    float* part_ml;      // [2 workers][row_tiles][16 rt][2]
 };
 // Row tiles, workers and workspace bytes of a call (fills what lies between q and o).
 size_t paged_decode_layout(PagedDecodeArgs* a, void* ws);
@@ -65,12 +64,11 @@ struct LatentDecodeArgs {
     const int32_t* block_table;
     FastDiv block;       // by the page size
     SplitShape split;    // units = 1
-    int rows, rt, row_tiles, workers, n_join;
+    int rows, rt, row_tiles, workers;
+    JoinShape join;
     void* o;
     void* q_lat;         // [batch n_pos][H][rank] bf16: queries in the latent space
     float* o_lat;        // [batch n_pos][H][rank]: outputs there
-    float* part_o;       // [2 workers][row_tiles][16 rt][rank]
-    float* part_ml;      // [2 workers][row_tiles][16 rt][2]
 };
 size_t latent_decode_layout(LatentDecodeArgs* a, void* ws);
 hipError_t launch_latent_decode(const LatentDecodeArgs& a, hipStream_t stream);

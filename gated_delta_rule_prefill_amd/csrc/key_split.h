@@ -83,6 +83,7 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 // chunk is `base`. All threads of the workgroup call it.
 struct SplitRun {
     int pos, end, base, b;
+    SplitCut cut;
 };
 template <int KB, int THREADS>
 __device__ SplitRun split_run(const SplitShape& s, int w, int workers) {
@@ -109,7 +110,7 @@ __device__ SplitRun split_run(const SplitShape& s, int w, int workers) {
         total += wave_tot[i];
     }
     const SplitCut cut = SplitCut::of(uniform(total), workers);
-    SplitRun r = {0, 0, 0, 0};
+    SplitRun r = {0, 0, 0, 0, cut};
     if (w >= cut.n) return r;
     r.pos = cut.start(w);
     r.end = cut.start(w + 1);

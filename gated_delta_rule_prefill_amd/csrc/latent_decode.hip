@@ -33,10 +33,10 @@ __device__ __forceinline__ uint64_t bits4(const float x[4]) {
 
 // ---------------------------------------------------------------------------------- absorb
 // q'^T (rank x rows) = W_uk^T q_nope^T per head: a workgroup takes 128 rank columns of one
-// head's W_uk (LDS, read back transposed into the MFMA's A operand and kept in registers) and
-// runs over its share of the (request, position) rows, 16 at a time. Bound by reading the
-// weights once. q' is rounded to bf16 as the core's MFMA operand.
-constexpr int AB_COLS = 128;
+// head's W_uk (through LDS, read back transposed as the MFMA's A operand) and 32 (request,
+// position) rows, all loads issued at once: one trip to memory. q' is rounded to bf16 as the
+// core's MFMA operand.
+constexpr int AB_COLS = 128, AB_TILES = 2;
 
 // LDS position of the 16-byte piece c of row n (rows of AB_COLS elements = 16 pieces): the 16
 // rows of a transposing read are 8 g + (0..3), so pairs of pieces turn by those bits
@@ -46,48 +46,55 @@ __device__ __forceinline__ int ab_place(int n, int c) {
 }
 
 template <int DN>
-__global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeArgs a,
-                                                                   int tiles_per_wg) {
+__global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeArgs a) {
     __shared__ __align__(16) char w[DN * AB_COLS * 2];
     const int h = blockIdx.x, r0 = blockIdx.y * AB_COLS;
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+    const int col = lane & 15, grp = lane >> 4;
+    const int rows = a.split.batch * a.n_pos, row0 = blockIdx.z * (AB_TILES * 16);
     const bf16* W = reinterpret_cast<const bf16*>(a.w_kv) +
                     (size_t)h * (a.d_nope + a.d_v) * a.rank + r0;
+    f32x4 in[DN * 16 / LD_THREADS];
 #pragma unroll
     for (int i = 0; i < DN * 16 / LD_THREADS; i++) {
-        const int x = i * LD_THREADS + tid, n = x >> 4, c = x & 15;
-        *reinterpret_cast<f32x4*>(w + ab_place(n, c)) =
-            *reinterpret_cast<const f32x4*>(W + (size_t)n * a.rank + c * 8);
+        const int x = i * LD_THREADS + tid;
+        in[i] = *reinterpret_cast<const f32x4*>(W + (size_t)(x >> 4) * a.rank + (x & 15) * 8);
+    }
+    bf16x8 B[AB_TILES][DN / 32];
+#pragma unroll
+    for (int t = 0; t < AB_TILES; t++) {
+        const bf16* q = reinterpret_cast<const bf16*>(a.q_nope) +
+                        ((size_t)min(row0 + t * 16 + col, rows - 1) * a.H + h) * DN;
+#pragma unroll
+        for (int k = 0; k < DN / 32; k++) B[t][k] = Mma<bf16>::load(q + k * 32 + grp * 8);
+    }
+    sched_fence();
+#pragma unroll
+    for (int i = 0; i < DN * 16 / LD_THREADS; i++) {
+        const int x = i * LD_THREADS + tid;
+        *reinterpret_cast<f32x4*>(w + ab_place(x >> 4, x & 15)) = in[i];
     }
     __syncthreads();
-    const int col = lane & 15, grp = lane >> 4;
-    bf16x8 A[2][DN / 32];  // 2 x 16 rank columns of this wave
 #pragma unroll
-    for (int t = 0; t < 2; t++)
+    for (int x = 0; x < 2; x++) {  // 2 x 16 rank columns of this wave
+        bf16x8 A[DN / 32];
 #pragma unroll
         for (int k = 0; k < DN / 32; k++) {
             const int n = k * 32 + grp * 8 + ((lane >> 2) & 3);
-            const int c = (wave * 2 + t) * 2 + ((lane & 3) >> 1);
-            A[t][k] = join(lds_read_tr(w + ab_place(n, c) + (lane & 1) * 8),
-                           lds_read_tr(w + ab_place(n + 4, c) + (lane & 1) * 8));
+            const int c = (wave * 2 + x) * 2 + ((lane & 3) >> 1);
+            A[k] = join(lds_read_tr(w + ab_place(n, c) + (lane & 1) * 8),
+                        lds_read_tr(w + ab_place(n + 4, c) + (lane & 1) * 8));
         }
-    const int rows = a.split.batch * a.n_pos;
-    const int t0 = blockIdx.z * tiles_per_wg;
-    for (int t = t0; t < t0 + tiles_per_wg && t * 16 < rows; t++) {
-        const int row = t * 16 + col;
-        const bf16* q = reinterpret_cast<const bf16*>(a.q_nope) +
-                        ((size_t)min(row, rows - 1) * a.H + h) * DN;
-        bf16x8 B[DN / 32];
 #pragma unroll
-        for (int k = 0; k < DN / 32; k++) B[k] = Mma<bf16>::load(q + k * 32 + grp * 8);
-        bf16* out = reinterpret_cast<bf16*>(a.q_lat) + ((size_t)row * a.H + h) * a.rank + r0;
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
+        for (int t = 0; t < AB_TILES; t++) {
+            const int row = row0 + t * 16 + col;
             f32x4 d = zero4();
 #pragma unroll
-            for (int k = 0; k < DN / 32; k++) d = Mma<bf16>::mma(A[x][k], B[k], d);
-            float y[4] = {d[0], d[1], d[2], d[3]};
-            if (row < rows) store4<bf16>(out + (wave * 2 + x) * 16 + grp * 4, y);
+            for (int k = 0; k < DN / 32; k++) d = Mma<bf16>::mma(A[k], B[t][k], d);
+            const float y[4] = {d[0], d[1], d[2], d[3]};
+            if (row < rows)
+                store4<bf16>(reinterpret_cast<bf16*>(a.q_lat) + ((size_t)row * a.H + h) * a.rank +
+                                 r0 + (wave * 2 + x) * 16 + grp * 4, y);
         }
     }
 }
@@ -157,9 +164,23 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
     const int kg = wave / RH, part = wave % RH;  // key group and 16-row part of the scores
     const int key_row = kg * KEYS;               // first tile row of this wave's keys
     const SplitPlace me = split_place(blockIdx.x, a.row_tiles);
+    int own_keys = me.worker < a.split.batch ? split_keys(a.split, me.worker) : 1;
     SplitRun run = split_run<LD_KB, WAVES * WAVE>(a.split, me.worker, a.workers);
     const int run_start = run.pos;
     const int row0 = me.row_tile * ROWS;
+    if (me.row_tile == 0) {
+        // requests without keys: zeros, and nothing to join
+        for (int b = me.worker; b < a.split.batch; b += a.workers) {
+            if (b != me.worker) own_keys = split_keys(a.split, b);
+            if (uniform(own_keys) != 0) continue;
+            const size_t n = (size_t)a.rows * R;
+            const float z[4] = {0.f, 0.f, 0.f, 0.f};
+            for (size_t i = threadIdx.x * 4; i < n; i += WAVES * WAVE * 4)
+                store4<float>(a.o_lat + (size_t)b * n + i, z);
+            if (a.join.per_unit && threadIdx.x == 0) join_none(a.join, b);
+        }
+        if (!a.join.per_unit && threadIdx.x == 0) join_none(a.join, me.worker);
+    }
     const float cs = a.scale * LOG2E;
     const char* cache = reinterpret_cast<const char*>(a.cache);
 
@@ -387,6 +408,8 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
 
         // total of the running sums over lanes and waves
         const bool whole = c0 == 0 && c1 == nch;
+        if (c0 == 0 && me.row_tile == 0 && threadIdx.x == 0)
+            join_note(a.join, a.split, run, me.worker, b, 0, c1, nch, run.pos != run_start);
         const int slot = 2 * me.worker + (run.pos == run_start ? 0 : 1);
         const size_t part_row = ((size_t)slot * a.row_tiles + me.row_tile) * ROWS;
         lds_barrier();
@@ -403,7 +426,7 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
                 for (int g = 0; g < Y::GROUPS; g++) sum += tops[g][rr];
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
                 float* out = whole ? a.o_lat + ((size_t)b * a.rows + r) * R
-                                   : a.part_o + (part_row + rr) * R;
+                                   : a.join.part_o + (part_row + rr) * R;
 #pragma unroll
                 for (int j = 0; j < NT; j++) {
                     const int d = (wave * NT + j) * 16 + grp * 4;
@@ -412,11 +435,11 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
                     for (int i = 0; i < 4; i++) x[i] = whole ? acc[t][j][i] * inv : acc[t][j][i];
                     store4<float>(out + d, x);
                 }
-                if (!whole && wave == 0 && grp == 0) a.part_ml[(part_row + rr) * 2 + 1] = sum;
+                if (!whole && wave == 0 && grp == 0) a.join.part_ml[(part_row + rr) * 2 + 1] = sum;
             }
         }
         if (!whole && kg == 0 && grp == 0 && live)
-            a.part_ml[(part_row + part * 16 + col) * 2] = m;
+            a.join.part_ml[(part_row + part * 16 + col) * 2] = m;
         lds_barrier();  // the next unit writes tops and the tiles
 
         run.pos += c1 - c0;
@@ -429,21 +452,12 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
 }
 
 // ------------------------------------------------------------------------------------ join
-// Weighted latents of the units that were cut, and zeros for requests without keys.
+// Weighted latents of the units that were cut.
 template <int R>
 __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentDecodeArgs a) {
-    const JoinShape s = {a.split, a.workers, a.row_tiles, 16 * a.rt, a.rows, a.part_o, a.part_ml};
-    join_parts<LD_KB, R>(
-        s,
-        [&](int b, int, int row, int col, const float x[4]) {
-            store4<float>(a.o_lat + ((size_t)b * a.rows + row) * R + col, x);
-        },
-        [&](int b) {
-            const size_t n = (size_t)a.rows * R;
-            const float z[4] = {0.f, 0.f, 0.f, 0.f};
-            for (size_t i = threadIdx.x * 4; i < n; i += JOIN_THREADS * 4)
-                store4<float>(a.o_lat + (size_t)b * n + i, z);
-        });
+    join_parts<R>(a.join, [&](int b, int, int row, int col, const float x[4]) {
+        store4<float>(a.o_lat + ((size_t)b * a.rows + row) * R + col, x);
+    });
 }
 
 // -------------------------------------------------------------------------------------- up
@@ -514,12 +528,10 @@ __global__ __launch_bounds__(LD_THREADS) void latent_up_kernel(LatentDecodeArgs 
 
 template <int DN>
 void run_absorb(const LatentDecodeArgs& a, hipStream_t s) {
-    const int tiles = (a.split.batch * a.n_pos + 15) / 16;
-    const int per = tiles < 2 ? tiles : 2;  // each row tile is one more trip to memory in turn
+    const int tiles = (a.split.batch * a.n_pos + 16 * AB_TILES - 1) / (16 * AB_TILES);
     hipLaunchKernelGGL(latent_absorb_kernel<DN>,
-                       dim3((unsigned)a.H, (unsigned)(a.rank / AB_COLS),
-                            (unsigned)((tiles + per - 1) / per)),
-                       dim3(LD_THREADS), 0, s, a, per);
+                       dim3((unsigned)a.H, (unsigned)(a.rank / AB_COLS), (unsigned)tiles),
+                       dim3(LD_THREADS), 0, s, a);
 }
 
 template <int R, int RH, int KS>
@@ -551,7 +563,8 @@ template <int R>
 hipError_t run_rank(const LatentDecodeArgs& a, hipStream_t s) {
     hipError_t e = run_core<R>(a, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(latent_join_kernel<R>, dim3((unsigned)a.n_join), dim3(JOIN_THREADS), 0, s, a);
+    hipLaunchKernelGGL(latent_join_kernel<R>, dim3((unsigned)(a.join.count * a.join.share)),
+                       dim3(JOIN_THREADS), 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     return a.d_v == 128 ? run_up<R, 128>(a, s) : run_up<R, 64>(a, s);
@@ -565,9 +578,14 @@ size_t latent_decode_layout(LatentDecodeArgs* a, void* ws) {
     a->rt = tiles > 2 ? 4 : tiles;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
     a->split.units = 1;
-    a->workers = split_workers(min(device_cu_count(), JOIN_MAX_WORKERS), a->row_tiles);
-    a->n_join = 4 * device_cu_count();
-    const size_t part = (size_t)2 * a->workers * a->row_tiles * 16 * a->rt;
+    const int cus = device_cu_count();
+    a->workers = split_workers(cus, a->row_tiles);
+    JoinShape& j = a->join;
+    j.row_tiles = a->row_tiles;
+    j.tile = 16 * a->rt;
+    j.rows = a->rows;
+    join_layout(&j, a->split.batch, a->workers, cus);
+    const size_t part = (size_t)2 * a->workers * a->row_tiles * j.tile;
     const size_t lat = (size_t)a->split.batch * a->rows * a->rank;  // bf16 elements
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -575,8 +593,9 @@ size_t latent_decode_layout(LatentDecodeArgs* a, void* ws) {
         off += (bytes + 255) & ~(size_t)255;
         return p;
     };
-    a->part_o = reinterpret_cast<float*>(take(part * a->rank * sizeof(float)));
-    a->part_ml = reinterpret_cast<float*>(take(part * 2 * sizeof(float)));
+    j.part_o = reinterpret_cast<float*>(take(part * a->rank * sizeof(float)));
+    j.part_ml = reinterpret_cast<float*>(take(part * 2 * sizeof(float)));
+    j.notes = reinterpret_cast<int4*>(take((size_t)j.count * sizeof(int4)));
     a->q_lat = take(lat * 2);
     a->o_lat = reinterpret_cast<float*>(take(lat * sizeof(float)));
     return off;

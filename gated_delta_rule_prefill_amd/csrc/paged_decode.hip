@@ -140,9 +140,24 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform(wave_id());
     const int col = lane & 15, grp = lane >> 4;
     const SplitPlace me = split_place(blockIdx.x, a.row_tiles);
+    int own_keys = me.worker < a.split.batch ? split_keys(a.split, me.worker) : 1;
     SplitRun run = split_run<KB, PD_THREADS>(a.split, me.worker, a.workers);
     const int run_start = run.pos;
     const int row0 = me.row_tile * 16 * RT;
+    if (me.row_tile == 0) {
+        // requests without keys: zeros, and nothing to join
+        for (int b = me.worker; b < a.split.batch; b += a.workers) {
+            if (b != me.worker) own_keys = split_keys(a.split, b);
+            if (uniform(own_keys) != 0) continue;
+            const size_t n = (size_t)a.n_pos * a.H * D;
+            const float z[4] = {0.f, 0.f, 0.f, 0.f};
+            for (size_t i = tid * 4; i < n; i += PD_THREADS * 4)
+                store4<T>(reinterpret_cast<T*>(a.o) + (size_t)b * n + i, z);
+            if (a.join.per_unit)
+                for (int u = tid; u < a.kv_heads; u += PD_THREADS) join_none(a.join, b * a.kv_heads + u);
+        }
+        if (!a.join.per_unit && tid == 0) join_none(a.join, me.worker);
+    }
     char* vlds = smem + wave * L::VTILE;
     const float cs = a.scale * LOG2E;
 
@@ -314,6 +329,8 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
 
         // merge the four waves, one 16-row tile at a time
         const bool whole = c0 == 0 && c1 == nch;
+        if (c0 == 0 && me.row_tile == 0 && tid == 0)
+            join_note(a.join, a.split, run, me.worker, b, kvh, c1, nch, run.pos != run_start);
         const int slot = 2 * me.worker + (run.pos == run_start ? 0 : 1);
         const size_t part_row = ((size_t)slot * a.row_tiles + me.row_tile) * (16 * RT);
         float* mrow = reinterpret_cast<float*>(smem);
@@ -348,7 +365,7 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
                 const int p = rr / a.group, h = rr - p * a.group;
                 T* dst = reinterpret_cast<T*>(a.o) +
                          (((size_t)b * a.n_pos + p) * a.H + (size_t)kvh * a.group + h) * D;
-                float* part = a.part_o + (part_row + rt * 16 + r) * D;
+                float* part = a.join.part_o + (part_row + rt * 16 + r) * D;
 #pragma unroll
                 for (int j = 0; j < D / 64; j++) {
                     const int d = j * 64 + (tid & 15) * 4;
@@ -369,7 +386,7 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
                     }
                 }
                 if (!whole && (tid & 15) == 0) {
-                    float* pm = a.part_ml + (part_row + rt * 16 + r) * 2;
+                    float* pm = a.join.part_ml + (part_row + rt * 16 + r) * 2;
                     pm[0] = top;
                     pm[1] = sum;
                 }
@@ -386,25 +403,15 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
     }
 }
 
-// Results of the units that were cut, and zeros for requests without keys.
+// Results of the units that were cut.
 template <typename T, int D>
 __global__ __launch_bounds__(JOIN_THREADS) void paged_join_kernel(PagedDecodeArgs a) {
-    constexpr int KB = PdTile<T, D>::KW * PD_WAVES;
-    const JoinShape s = {a.split, a.workers, a.row_tiles, 16 * a.rt, a.rows, a.part_o, a.part_ml};
-    join_parts<KB, D>(
-        s,
-        [&](int b, int kvh, int row, int col, const float x[4]) {
-            const int p = row / a.group, h = row - p * a.group;
-            store4<T>(reinterpret_cast<T*>(a.o) +
-                          (((size_t)b * a.n_pos + p) * a.H + (size_t)kvh * a.group + h) * D + col,
-                      x);
-        },
-        [&](int b) {
-            const size_t n = (size_t)a.n_pos * a.H * D;
-            const float z[4] = {0.f, 0.f, 0.f, 0.f};
-            for (size_t i = threadIdx.x * 4; i < n; i += JOIN_THREADS * 4)
-                store4<T>(reinterpret_cast<T*>(a.o) + (size_t)b * n + i, z);
-        });
+    join_parts<D>(a.join, [&](int b, int kvh, int row, int col, const float x[4]) {
+        const int p = row / a.group, h = row - p * a.group;
+        store4<T>(reinterpret_cast<T*>(a.o) +
+                      (((size_t)b * a.n_pos + p) * a.H + (size_t)kvh * a.group + h) * D + col,
+                  x);
+    });
 }
 
 template <typename T, int D, int RT>
@@ -413,8 +420,8 @@ hipError_t run_decode(const PagedDecodeArgs& a, hipStream_t s) {
                        dim3(PD_THREADS), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((paged_join_kernel<T, D>), dim3((unsigned)a.n_join), dim3(JOIN_THREADS), 0, s,
-                       a);
+    hipLaunchKernelGGL((paged_join_kernel<T, D>), dim3((unsigned)(a.join.count * a.join.share)),
+                       dim3(JOIN_THREADS), 0, s, a);
     return hipGetLastError();
 }
 
@@ -453,12 +460,18 @@ size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
     a->rt = tiles >= 4 && most >= 4 ? 4 : tiles >= 2 && most >= 2 ? 2 : 1;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
     a->split.units = a->kv_heads;
-    a->workers = split_workers(min(2 * device_cu_count(), JOIN_MAX_WORKERS), a->row_tiles);
-    a->n_join = 4 * device_cu_count();
-    const size_t rows = (size_t)2 * a->workers * a->row_tiles * 16 * a->rt;
-    a->part_o = static_cast<float*>(ws);
-    a->part_ml = a->part_o == nullptr ? nullptr : a->part_o + rows * a->d;
-    return rows * (a->d + 2) * sizeof(float);
+    const int cus = device_cu_count();
+    a->workers = split_workers(2 * cus, a->row_tiles);
+    JoinShape& j = a->join;
+    j.row_tiles = a->row_tiles;
+    j.tile = 16 * a->rt;
+    j.rows = a->rows;
+    join_layout(&j, (int64_t)a->split.batch * a->split.units, a->workers, cus);
+    const size_t rows = (size_t)2 * a->workers * a->row_tiles * j.tile;
+    j.part_o = static_cast<float*>(ws);
+    j.part_ml = ws == nullptr ? nullptr : j.part_o + rows * a->d;
+    j.notes = ws == nullptr ? nullptr : reinterpret_cast<int4*>(j.part_ml + rows * 2);
+    return rows * (a->d + 2) * sizeof(float) + (size_t)j.count * sizeof(int4);
 }
 
 hipError_t launch_paged_decode(const PagedDecodeArgs& a, hipStream_t s) {

@@ -418,65 +418,91 @@ def gdn_conv1d_silu(x, w, cu_seqlens, planes=1, y=None, stream=None):
 
 
 # ------------------------------------------------- paged softmax attention (hybrid models)
-class _Call:
-    """One launch on the tensors' own device: that device is made current, and the stream is
-    its current stream unless one is given. Buffers that the binding allocates for a call on
-    another stream are marked as used there, so the allocator does not hand them out early."""
-
-    def __init__(self, like, stream):
-        self.device = like.device
-        self.given = stream
-
-    def __enter__(self):
-        self.guard = torch.cuda.device(self.device)
-        self.guard.__enter__()
-        cur = torch.cuda.current_stream()
-        if self.given is None:
-            self.stream, self.other = cur, False
-        else:
-            self.stream = (self.given if hasattr(self.given, "cuda_stream")
-                           else torch.cuda.ExternalStream(int(self.given)))
-            self.other = self.stream.cuda_stream != cur.cuda_stream
-        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
-        return self
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
-
-    def new(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other:
-            t.record_stream(self.stream)
-        return t
+# These calls are short (a decode step's bookkeeping runs 4 us on the GPU), so the checks are
+# kept to a few attribute reads per tensor; a failed one works out its message afterwards.
+_raw_stream = torch._C._cuda_getCurrentRawStream  # handle of a device's current stream
+_I32, _I64, _BF16 = torch.int32, torch.int64, torch.bfloat16
 
 
-def _same_device(*ts):
-    _dev(*ts)
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"all tensors must be on one GPU, got {sorted(map(str, devs))}")
-
-
-def _want(name, t, shape, dtype):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-
-
-def _table(block_table, n):
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [requests, max_blocks]")
-    _want("block_table", block_table, (n, block_table.shape[1]), torch.int32)
-
-
-def _rows(name, t, width):
-    """A token-major source whose rows may lie apart (a part of a fused projection): returns
-    the row stride in elements."""
+def _bad(name, t, shape, dtype):
     if not t.is_cuda:
+        raise ValueError(f"all tensors must be on the GPU ({name} is on {t.device})")
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"all tensors must be contiguous ({name} is not)")
+    raise ValueError(f"all tensors must be on one GPU ({name} is on {t.device})")
+
+
+def _arg(name, t, shape, dtype, dev):
+    """Address of a contiguous tensor of this shape and type on GPU `dev`."""
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != dev
+            or not t.is_contiguous()):
+        _bad(name, t, shape, dtype)
+    return t.data_ptr()
+
+
+def _table_arg(t, n, dev):
+    if t.dim() != 2:
+        raise ValueError("block_table must be [requests, max_blocks]")
+    return _arg("block_table", t, (n, t.shape[1]), _I32, dev)
+
+
+def _rows_arg(name, t, shape, dtype, dev):
+    """Address and row stride (elements) of a token-major source whose rows may lie apart, as
+    parts of a fused projection's output do."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _bad(name, t, shape, dtype)
+    row = shape[1] * shape[2] if len(shape) == 3 else shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    stride = t.stride()
+    if stride[-1] != 1 or (len(shape) == 3 and shape[1] > 1 and stride[1] != shape[2]):
+        raise ValueError(f"{name}: each token's row must be contiguous")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else row
+
+
+def _space(workspace, need, like, stream, dev):
+    """Address and size of the workspace; one is allocated unless given."""
+    if workspace is None:
+        workspace = _new((max(need(), 1),), torch.uint8, like, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _bad("workspace", workspace, workspace.shape, workspace.dtype)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _new(shape, dtype, like, stream):
+    """A buffer on the tensors' GPU. On another stream than the current one it is marked as
+    used there, so that the allocator does not hand it out before that stream is done."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        t.record_stream(stream)
+    return t
+
+
+def _gpu(t):
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("all tensors must be on the GPU")
-    inner = t[0] if t.shape[0] else t
-    if t.shape[0] and (not inner.is_contiguous() or inner.numel() != width):
-        raise ValueError(f"{name}: rows must be contiguous with {width} elements")
-    return int(t.stride(0)) if t.shape[0] > 1 else width
+    return dev
+
+
+def _run(name, dev, stream, *args):
+    """One call with the tensors' GPU current, on its current stream unless one is given."""
+    if stream is None:
+        handle = _raw_stream(dev)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status:
+        _check(name, status)
 
 
 def gdn_paged_plan(ctx_lens, new_lens, block_table, free_blocks, block_size, max_tokens,
@@ -487,32 +513,24 @@ def gdn_paged_plan(ctx_lens, new_lens, block_table, free_blocks, block_size, max
     is the length of the token buffers. Returns (cu_seqlens [n + 1] int32, seq_lens [n] int32,
     slot_map [max_tokens] int64, positions [max_tokens] int32, counts [2] int32: tokens, pages
     asked for)."""
-    n, T = int(ctx_lens.numel()), int(max_tokens)
-    i32 = torch.int32
-    _want("ctx_lens", ctx_lens, (n,), i32)
-    _want("new_lens", new_lens, (n,), i32)
-    _table(block_table, n)
-    _want("free_blocks", free_blocks, (free_blocks.numel(),), i32)
+    n, T = ctx_lens.numel(), int(max_tokens)
+    n_free = free_blocks.numel()
     if T < 0:
         raise ValueError("max_tokens must be >= 0")
-    with _Call(ctx_lens, stream) as c:
-        cu_seqlens = c.new((n + 1,), i32) if cu_seqlens is None else cu_seqlens
-        seq_lens = c.new((n,), i32) if seq_lens is None else seq_lens
-        slot_map = c.new((T,), torch.int64) if slot_map is None else slot_map
-        positions = c.new((T,), i32) if positions is None else positions
-        counts = c.new((2,), i32) if counts is None else counts
-        _want("cu_seqlens", cu_seqlens, (n + 1,), i32)
-        _want("seq_lens", seq_lens, (n,), i32)
-        _want("slot_map", slot_map, (T,), torch.int64)
-        _want("positions", positions, (T,), i32)
-        _want("counts", counts, (2,), i32)
-        _same_device(ctx_lens, new_lens, block_table, free_blocks, cu_seqlens, seq_lens, slot_map,
-                     positions, counts)
-        _check("gdn_paged_plan", lib().gdn_paged_plan(
-            _ptr(ctx_lens), _ptr(new_lens), n, int(block_size), _ptr(block_table),
-            int(block_table.shape[1]), _ptr(free_blocks), int(free_blocks.numel()), T,
-            _ptr(cu_seqlens), _ptr(seq_lens), _ptr(slot_map), _ptr(positions), _ptr(counts),
-            c.ptr))
+    dev = _gpu(ctx_lens)
+    like = ctx_lens
+    cu_seqlens = _new((n + 1,), _I32, like, stream) if cu_seqlens is None else cu_seqlens
+    seq_lens = _new((n,), _I32, like, stream) if seq_lens is None else seq_lens
+    slot_map = _new((T,), _I64, like, stream) if slot_map is None else slot_map
+    positions = _new((T,), _I32, like, stream) if positions is None else positions
+    counts = _new((2,), _I32, like, stream) if counts is None else counts
+    _run("gdn_paged_plan", dev, stream, _arg("ctx_lens", ctx_lens, (n,), _I32, dev),
+         _arg("new_lens", new_lens, (n,), _I32, dev), n, int(block_size),
+         _table_arg(block_table, n, dev), block_table.shape[1],
+         _arg("free_blocks", free_blocks, (n_free,), _I32, dev), n_free, T,
+         _arg("cu_seqlens", cu_seqlens, (n + 1,), _I32, dev),
+         _arg("seq_lens", seq_lens, (n,), _I32, dev), _arg("slot_map", slot_map, (T,), _I64, dev),
+         _arg("positions", positions, (T,), _I32, dev), _arg("counts", counts, (2,), _I32, dev))
     return cu_seqlens, seq_lens, slot_map, positions, counts
 
 
@@ -522,18 +540,13 @@ def gdn_paged_append(k, v, slot_map, k_cache, v_cache, stream=None):
     block_size, d], updated in place."""
     T, h, d = k.shape
     n_blocks, _, bs, _ = k_cache.shape
-    _want("v", v, k.shape, k.dtype)
-    _want("slot_map", slot_map, (T,), torch.int64)
-    _want("k_cache", k_cache, (n_blocks, h, bs, d), k.dtype)
-    _want("v_cache", v_cache, k_cache.shape, k.dtype)
-    _same_device(slot_map, k_cache, v_cache)
-    ks, vs = _rows("k", k, h * d), _rows("v", v, h * d)
-    if k.device != k_cache.device or v.device != k_cache.device:
-        raise ValueError("all tensors must be on one GPU")
-    with _Call(k_cache, stream) as c:
-        _check("gdn_paged_append", lib().gdn_paged_append(
-            _dtype_code(k), _ptr(k), ks, _ptr(v), vs, _ptr(slot_map), int(T), int(h), int(d),
-            _ptr(k_cache), _ptr(v_cache), int(n_blocks), int(bs), c.ptr))
+    dt, dev = k.dtype, _gpu(k_cache)
+    ka, ks = _rows_arg("k", k, (T, h, d), dt, dev)
+    va, vs = _rows_arg("v", v, (T, h, d), dt, dev)
+    _run("gdn_paged_append", dev, stream, _dtype_code(k), ka, ks, va, vs,
+         _arg("slot_map", slot_map, (T,), _I64, dev), T, h, d,
+         _arg("k_cache", k_cache, (n_blocks, h, bs, d), dt, dev),
+         _arg("v_cache", v_cache, (n_blocks, h, bs, d), dt, dev), n_blocks, bs)
 
 
 def gdn_latent_append(c_kv, k_pe, slot_map, cache, stream=None):
@@ -543,17 +556,12 @@ def gdn_latent_append(c_kv, k_pe, slot_map, cache, stream=None):
     T, rank = c_kv.shape
     rope = k_pe.shape[1]
     n_blocks, bs, _ = cache.shape
-    _want("k_pe", k_pe, (T, rope), c_kv.dtype)
-    _want("slot_map", slot_map, (T,), torch.int64)
-    _want("cache", cache, (n_blocks, bs, rank + rope), c_kv.dtype)
-    _same_device(slot_map, cache)
-    cs, ps = _rows("c_kv", c_kv, rank), _rows("k_pe", k_pe, rope)
-    if c_kv.device != cache.device or k_pe.device != cache.device:
-        raise ValueError("all tensors must be on one GPU")
-    with _Call(cache, stream) as c:
-        _check("gdn_latent_append", lib().gdn_latent_append(
-            _dtype_code(c_kv), _ptr(c_kv), cs, _ptr(k_pe), ps, _ptr(slot_map), int(T), int(rank),
-            int(rope), _ptr(cache), int(n_blocks), int(bs), c.ptr))
+    dt, dev = c_kv.dtype, _gpu(cache)
+    ca, cs = _rows_arg("c_kv", c_kv, (T, rank), dt, dev)
+    pa, ps = _rows_arg("k_pe", k_pe, (T, rope), dt, dev)
+    _run("gdn_latent_append", dev, stream, _dtype_code(c_kv), ca, cs, pa, ps,
+         _arg("slot_map", slot_map, (T,), _I64, dev), T, rank, rope,
+         _arg("cache", cache, (n_blocks, bs, rank + rope), dt, dev), n_blocks, bs)
 
 
 def _code(dtype):
@@ -570,46 +578,38 @@ def gdn_paged_decode_workspace_bytes(H, kv_heads, d, dtype, batch, n_pos=1):
     return int(out.value)
 
 
-def _positions(q):
-    """[B, H, d] is one position per request."""
-    return q[:, None] if q.dim() == 3 else q
-
-
 def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=1.0, o=None,
                      workspace=None, stream=None):
     """Attention of the newest tokens over a paged cache. q [B, H, d] (a decode step) or
     [B, P, H, d] (a verify step: the request's newest P tokens, all of them in the cache);
     k_cache, v_cache [n_blocks, kv_heads, block_size, d]; block_table [B, max_blocks] int32;
     seq_lens [B] int32. Returns o, shaped as q."""
-    q4 = _positions(q)
-    B, P, H, d = q4.shape
+    shape, dt = q.shape, q.dtype
+    if len(shape) == 3:  # one position per request
+        (B, H, d), P = shape, 1
+    else:
+        B, P, H, d = shape
     n_blocks, kv, bs, _ = k_cache.shape
-    _want("k_cache", k_cache, (n_blocks, kv, bs, d), q.dtype)
-    _want("v_cache", v_cache, k_cache.shape, q.dtype)
-    _table(block_table, B)
-    _want("seq_lens", seq_lens, (B,), torch.int32)
-    with _Call(q, stream) as c:
-        o = c.new(q.shape, q.dtype) if o is None else o
-        _want("o", o, q.shape, q.dtype)
-        dims = gdn_paged_dims_t(int(H), int(kv), int(d), _dtype_code(q), float(scale))
-        if workspace is None:
-            workspace = c.new((max(1, gdn_paged_decode_workspace_bytes(
-                H, kv, d, _dtype_code(q), B, P)),), torch.uint8)
-        _same_device(q, k_cache, v_cache, block_table, seq_lens, o, workspace)
-        _check("gdn_paged_decode", lib().gdn_paged_decode(
-            ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), int(n_blocks), int(bs),
-            _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(B), int(P), _ptr(o),
-            _ptr(workspace), int(workspace.numel() * workspace.element_size()), c.ptr))
+    dev = _gpu(q)
+    code = _dtype_code(q)
+    o = _new(shape, dt, q, stream) if o is None else o
+    ws, ws_bytes = _space(workspace, lambda: gdn_paged_decode_workspace_bytes(
+        H, kv, d, code, B, P), q, stream, dev)
+    _run("gdn_paged_decode", dev, stream, gdn_paged_dims_t(H, kv, d, code, scale),
+         _arg("q", q, shape, dt, dev), _arg("k_cache", k_cache, (n_blocks, kv, bs, d), dt, dev),
+         _arg("v_cache", v_cache, (n_blocks, kv, bs, d), dt, dev), n_blocks, bs,
+         _table_arg(block_table, B, dev), block_table.shape[1],
+         _arg("seq_lens", seq_lens, (B,), _I32, dev), B, P, _arg("o", o, shape, dt, dev), ws,
+         ws_bytes)
     return o
 
 
 def _latent_dims(H, rank, d_rope, d_nope, d_v, scale):
-    return gdn_latent_dims_t(int(H), int(rank), int(d_rope), int(d_nope), int(d_v),
-                             GDN_DTYPE_BF16, float(scale))
+    return gdn_latent_dims_t(H, rank, d_rope, d_nope, d_v, GDN_DTYPE_BF16, scale)
 
 
 def gdn_latent_decode_workspace_bytes(H, rank, d_rope, d_nope, d_v, batch, n_pos=1):
-    dims = _latent_dims(H, rank, d_rope, d_nope, d_v, 1.0)
+    dims = _latent_dims(int(H), int(rank), int(d_rope), int(d_nope), int(d_v), 1.0)
     out = _SZ(0)
     _check("gdn_latent_decode_workspace_bytes", lib().gdn_latent_decode_workspace_bytes(
         ctypes.byref(dims), int(batch), int(n_pos), ctypes.byref(out)))
@@ -623,37 +623,33 @@ def gdn_latent_decode(q_nope, q_pe, w_kv, cache, block_table, seq_lens, scale=1.
     up projection, then of the value's; d_nope == d_v); cache [n_blocks, block_size, rank +
     d_rope]; block_table [B, max_blocks] int32; seq_lens [B] int32. Returns o, shaped as
     q_nope."""
-    qn = _positions(q_nope)
-    B, P, H, dn = qn.shape
+    shape = q_nope.shape
+    if len(shape) == 3:  # one position per request
+        (B, H, dn), P = shape, 1
+    else:
+        B, P, H, dn = shape
     rank, rope = w_kv.shape[2], q_pe.shape[-1]
     dv = w_kv.shape[1] - dn
     n_blocks, bs, _ = cache.shape
-    bf = torch.bfloat16
-    _want("q_nope", q_nope, q_nope.shape, bf)
-    _want("q_pe", q_pe, (*q_nope.shape[:-1], rope), bf)
-    _want("w_kv", w_kv, (H, dn + dv, rank), bf)
-    _want("cache", cache, (n_blocks, bs, rank + rope), bf)
-    _table(block_table, B)
-    _want("seq_lens", seq_lens, (B,), torch.int32)
-    with _Call(q_nope, stream) as c:
-        shape = (*q_nope.shape[:-1], dv)
-        o = c.new(shape, bf) if o is None else o
-        _want("o", o, shape, bf)
-        dims = _latent_dims(H, rank, rope, dn, dv, scale)
-        if workspace is None:
-            workspace = c.new((max(1, gdn_latent_decode_workspace_bytes(
-                H, rank, rope, dn, dv, B, P)),), torch.uint8)
-        _same_device(q_nope, q_pe, w_kv, cache, block_table, seq_lens, o, workspace)
-        _check("gdn_latent_decode", lib().gdn_latent_decode(
-            ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(w_kv), _ptr(cache), int(n_blocks),
-            int(bs), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(B), int(P),
-            _ptr(o), _ptr(workspace), int(workspace.numel() * workspace.element_size()), c.ptr))
+    dev = _gpu(q_nope)
+    o_shape = (*shape[:-1], dv)
+    o = _new(o_shape, _BF16, q_nope, stream) if o is None else o
+    ws, ws_bytes = _space(workspace, lambda: gdn_latent_decode_workspace_bytes(
+        H, rank, rope, dn, dv, B, P), q_nope, stream, dev)
+    _run("gdn_latent_decode", dev, stream, _latent_dims(H, rank, rope, dn, dv, scale),
+         _arg("q_nope", q_nope, shape, _BF16, dev),
+         _arg("q_pe", q_pe, (*shape[:-1], rope), _BF16, dev),
+         _arg("w_kv", w_kv, (H, dn + dv, rank), _BF16, dev),
+         _arg("cache", cache, (n_blocks, bs, rank + rope), _BF16, dev), n_blocks, bs,
+         _table_arg(block_table, B, dev), block_table.shape[1],
+         _arg("seq_lens", seq_lens, (B,), _I32, dev), B, P, _arg("o", o, o_shape, _BF16, dev), ws,
+         ws_bytes)
     return o
 
 
 def gdn_latent_prefill_workspace_bytes(H, rank, d_rope, d_nope, d_v, n_seqs, total_tokens,
                                        total_keys):
-    dims = _latent_dims(H, rank, d_rope, d_nope, d_v, 1.0)
+    dims = _latent_dims(int(H), int(rank), int(d_rope), int(d_nope), int(d_v), 1.0)
     out = _SZ(0)
     _check("gdn_latent_prefill_workspace_bytes", lib().gdn_latent_prefill_workspace_bytes(
         ctypes.byref(dims), int(n_seqs), int(total_tokens), int(total_keys), ctypes.byref(out)))
@@ -667,29 +663,21 @@ def gdn_latent_prefill(q_nope, q_pe, w_kv, cache, block_table, cu_seqlens, seq_l
     int32; seq_lens [n] int32, the new tokens included; total_keys >= the sum of seq_lens.
     Returns o [T, H, d]."""
     T, H, dn = q_nope.shape
-    n = int(seq_lens.numel())
+    n = seq_lens.numel()
     rank, rope = w_kv.shape[2], q_pe.shape[2]
     dv = w_kv.shape[1] - dn
     n_blocks, bs, _ = cache.shape
-    bf = torch.bfloat16
-    _want("q_nope", q_nope, (T, H, dn), bf)
-    _want("q_pe", q_pe, (T, H, rope), bf)
-    _want("w_kv", w_kv, (H, dn + dv, rank), bf)
-    _want("cache", cache, (n_blocks, bs, rank + rope), bf)
-    _table(block_table, n)
-    _want("cu_seqlens", cu_seqlens, (n + 1,), torch.int32)
-    _want("seq_lens", seq_lens, (n,), torch.int32)
-    with _Call(q_nope, stream) as c:
-        o = c.new((T, H, dv), bf) if o is None else o
-        _want("o", o, (T, H, dv), bf)
-        dims = _latent_dims(H, rank, rope, dn, dv, scale)
-        if workspace is None:
-            workspace = c.new((max(1, gdn_latent_prefill_workspace_bytes(
-                H, rank, rope, dn, dv, n, T, total_keys)),), torch.uint8)
-        _same_device(q_nope, q_pe, w_kv, cache, block_table, cu_seqlens, seq_lens, o, workspace)
-        _check("gdn_latent_prefill", lib().gdn_latent_prefill(
-            ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(w_kv), _ptr(cache), int(n_blocks),
-            int(bs), _ptr(block_table), int(block_table.shape[1]), _ptr(cu_seqlens),
-            _ptr(seq_lens), n, int(T), int(total_keys), _ptr(o), _ptr(workspace),
-            int(workspace.numel() * workspace.element_size()), c.ptr))
+    dev = _gpu(q_nope)
+    o = _new((T, H, dv), _BF16, q_nope, stream) if o is None else o
+    ws, ws_bytes = _space(workspace, lambda: gdn_latent_prefill_workspace_bytes(
+        H, rank, rope, dn, dv, n, T, total_keys), q_nope, stream, dev)
+    _run("gdn_latent_prefill", dev, stream, _latent_dims(H, rank, rope, dn, dv, scale),
+         _arg("q_nope", q_nope, (T, H, dn), _BF16, dev),
+         _arg("q_pe", q_pe, (T, H, rope), _BF16, dev),
+         _arg("w_kv", w_kv, (H, dn + dv, rank), _BF16, dev),
+         _arg("cache", cache, (n_blocks, bs, rank + rope), _BF16, dev), n_blocks, bs,
+         _table_arg(block_table, n, dev), block_table.shape[1],
+         _arg("cu_seqlens", cu_seqlens, (n + 1,), _I32, dev),
+         _arg("seq_lens", seq_lens, (n,), _I32, dev), n, T, int(total_keys),
+         _arg("o", o, (T, H, dv), _BF16, dev), ws, ws_bytes)
     return o
