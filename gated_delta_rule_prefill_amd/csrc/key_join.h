@@ -20,20 +20,25 @@ constexpr int JOIN_GROUPS = JOIN_THREADS / 32;
 
 struct JoinShape {
     int4* notes;          // [count]
-    int count, share;
+    int count, share;     // share workgroups per note (and column slice)
+    int slices;           // workgroups side by side along a row's columns
     int per_unit;         // notes are kept per unit (else per worker)
     int row_tiles, tile;  // row tiles of a worker, rows of a tile
     int rows;             // live rows of a unit, over its row tiles
     float* part_o;        // [2 workers][row_tiles][tile][COLS]
     float* part_ml;       // [2 workers][row_tiles][tile][2]
 };
-// Notes of a call and their workgroups: about 4 per CU, no more than a note has rows.
-inline void join_layout(JoinShape* j, int64_t units, int workers, int cus) {
+// Notes of a call and their workgroups: about 4 per CU, no more for a note than it has rows,
+// and the columns split up too where that leaves CUs idle (one long request).
+inline void join_layout(JoinShape* j, int64_t units, int workers, int cus, int cols) {
     j->per_unit = units <= workers;
     j->count = j->per_unit ? (int)units : workers;
     const int share = j->count > 0 ? 4 * cus / j->count : 1;
     j->share = share < 1 ? 1 : share < j->rows ? share : j->rows;
+    const int slices = (cols + 127) / 128;
+    j->slices = share >= j->rows * slices ? slices : 1;
 }
+inline unsigned join_grid(const JoinShape& j) { return (unsigned)(j.count * j.share * j.slices); }
 
 // A note: request, unit, 2 (first worker) + (its part is in the late slot), last worker; -1 for
 // the last worker of a unit that needs no joining.
@@ -52,21 +57,20 @@ __device__ __forceinline__ void join_note(const JoinShape& j, const SplitShape& 
         join_none(j, b * s.units + unit);
 }
 
-// store(b, unit, row, col, x[4]) takes 4 columns of a row of request b's unit.
-template <int COLS, typename Store>
-__device__ __forceinline__ void join_parts(const JoinShape& s, Store store) {
-    constexpr int NC = (COLS + 127) / 128;  // 16-byte pieces of a row per lane
+// One workgroup's share of a note's rows, NC pieces of 128 columns from column `first` on, U
+// parts on their way at a time.
+template <int COLS, int NC, int U, typename Store>
+__device__ __forceinline__ void join_rows(const JoinShape& s, int4 note, int step0, int first,
+                                          Store store) {
     __shared__ float red[JOIN_GROUPS][NC * 128 + 4];
-    const int4 note = s.notes[blockIdx.x / s.share];
     const int b = note.x, unit = note.y, w0 = note.z >> 1, late = note.z & 1, w1 = note.w;
-    if (w1 < 0) return;
     const int tid = threadIdx.x, group = tid >> 5, lane = tid & 31;
     const size_t rows_per_part = (size_t)s.row_tiles * s.tile;
     const int parts = w1 - w0 + 1;
-    int gpr = 1;  // groups per row
-    while (gpr < JOIN_GROUPS && gpr < parts) gpr *= 2;
+    int gpr = 1;  // groups per row: U parts each, if there are groups enough
+    while (gpr < JOIN_GROUPS && gpr * U < parts) gpr *= 2;
     const int rows_here = JOIN_GROUPS / gpr, turn = group & (gpr - 1);
-    for (int step = blockIdx.x % s.share; step * rows_here < s.rows; step += s.share) {
+    for (int step = step0; step * rows_here < s.rows; step += s.share) {
         const int row = step * rows_here + group / gpr;
         const bool live = row < s.rows;
         const int r = live ? row : 0;
@@ -92,25 +96,25 @@ __device__ __forceinline__ void join_parts(const JoinShape& s, Store store) {
                 if (turn == 0) sum = fmaf(f, s.part_ml[e * 2 + 1], sum);
             }
             const int n = min(32, w1 - base + 1);
-            for (int i0 = turn; i0 < n; i0 += 4 * gpr) {
-                // four parts on their way at a time (the surplus ones weigh nothing)
-                f32x4 y[4][NC];
-                float g[4];
+            for (int i0 = turn; i0 < n; i0 += U * gpr) {
+                // (the surplus ones weigh nothing)
+                f32x4 y[U][NC];
+                float g[U];
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
+                for (int k = 0; k < U; k++) {
                     const int i = i0 + k * gpr;
                     g[k] = __shfl(f, i & 31, 32);
                     if (i >= n) g[k] = 0.f;
                     const float* src = s.part_o + at(base + min(i, n - 1)) * COLS;
 #pragma unroll
                     for (int c = 0; c < NC; c++) {
-                        const int col = c * 128 + lane * 4;
+                        const int col = first + c * 128 + lane * 4;
                         y[k][c] = COLS % 128 == 0 || col < COLS
                                       ? *reinterpret_cast<const f32x4*>(src + col) : zero4();
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < 4; k++)
+                for (int k = 0; k < U; k++)
 #pragma unroll
                     for (int c = 0; c < NC; c++)
 #pragma unroll
@@ -139,12 +143,27 @@ __device__ __forceinline__ void join_parts(const JoinShape& s, Store store) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
 #pragma unroll
             for (int c = 0; c < NC; c++) {
-                const int col = c * 128 + lane * 4;
+                const int col = first + c * 128 + lane * 4;
                 if (COLS % 128 != 0 && col >= COLS) continue;
                 const float y[4] = {x[c][0] * inv, x[c][1] * inv, x[c][2] * inv, x[c][3] * inv};
                 store(b, unit, row, col, y);
             }
         }
+    }
+}
+
+// store(b, unit, row, col, x[4]) takes 4 columns of a row of request b's unit.
+template <int COLS, typename Store>
+__device__ __forceinline__ void join_parts(const JoinShape& s, Store store) {
+    constexpr int NC = (COLS + 127) / 128;
+    const int per_note = s.share * s.slices;
+    const int4 note = s.notes[blockIdx.x / per_note];
+    if (note.w < 0) return;
+    const int rest = blockIdx.x % per_note;
+    if (s.slices == 1) {
+        join_rows<COLS, NC, 4>(s, note, rest, 0, store);
+    } else if constexpr (NC > 1) {
+        join_rows<COLS, 1, 8>(s, note, rest / s.slices, rest % s.slices * 128, store);
     }
 }
 

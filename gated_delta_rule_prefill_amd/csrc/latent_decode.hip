@@ -33,10 +33,10 @@ __device__ __forceinline__ uint64_t bits4(const float x[4]) {
 
 // ---------------------------------------------------------------------------------- absorb
 // q'^T (rank x rows) = W_uk^T q_nope^T per head: a workgroup takes 128 rank columns of one
-// head's W_uk (through LDS, read back transposed as the MFMA's A operand) and 32 (request,
+// head's W_uk (through LDS, read back transposed as the MFMA's A operand) and 64 (request,
 // position) rows, all loads issued at once: one trip to memory. q' is rounded to bf16 as the
 // core's MFMA operand.
-constexpr int AB_COLS = 128, AB_TILES = 2;
+constexpr int AB_COLS = 128, AB_TILES = 4;
 
 // LDS position of the 16-byte piece c of row n (rows of AB_COLS elements = 16 pieces): the 16
 // rows of a transposing read are 8 g + (0..3), so pairs of pieces turn by those bits
@@ -213,6 +213,7 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
         // Tile c into a buffer, its pages being in `page`, which then takes those of chunk `next`.
         // (That load goes first: the compiler's wait for it must not be behind the tile's.)
         auto load_tile = [&](int c, int buf, int next) {
+            arrived(page);
             const uint32_t key = (uint32_t)(c * LD_KB + key_row + lane % KEYS);
             const uint32_t off = key - a.block(key) * a.block.div;
             const bool ok = (int)key < nkeys && page >= 0 && page < a.n_blocks;
@@ -461,29 +462,33 @@ __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentDecodeA
 }
 
 // -------------------------------------------------------------------------------------- up
-// o = W_uv u for one head and 16 (request, position) rows. u is taken as the sum of two bf16
+// o = W_uv u for one head and 32 (request, position) rows. u is taken as the sum of two bf16
 // numbers, its rounding and the rounding of what that leaves (2^-17 of it together): one more
 // MFMA each, in a kernel that waits for memory, for an output error that is a third smaller.
 // Everything is requested at once (the weights as the MFMA's A operand into registers, the rows
 // of u into LDS), so a workgroup pays one trip to memory.
+constexpr int UP_TILES = 2;
+
 template <int R, int DV>
-__global__ __launch_bounds__(LD_THREADS) void latent_up_kernel(LatentDecodeArgs a) {
+__global__ __launch_bounds__(LD_THREADS, 2) void latent_up_kernel(LatentDecodeArgs a) {
     constexpr int NJ = DV / 16 / LD_WAVES;
     constexpr int PITCH = R * 2 + 16;                    // LDS row: 16-byte pieces on all banks
-    constexpr int PER = 16 * R / 4 / LD_THREADS;         // 4-column pieces of u per thread
-    __shared__ __align__(16) char lds[2][16 * PITCH];    // the two parts of u
+    constexpr int PER = 16 * R / 4 / LD_THREADS;         // 4-column pieces of a tile per thread
+    __shared__ __align__(16) char lds[UP_TILES][2][16 * PITCH];  // the two parts of u
     const int h = blockIdx.x, lane = lane_id(), wave = wave_id();
     const int col = lane & 15, grp = lane >> 4;
-    const int rows = a.split.batch * a.n_pos, row0 = blockIdx.y * 16;
+    const int rows = a.split.batch * a.n_pos, row0 = blockIdx.y * (UP_TILES * 16);
     const bf16* W = reinterpret_cast<const bf16*>(a.w_kv) +
                     ((size_t)h * (a.d_nope + DV) + a.d_nope) * R;
-    f32x4 u[PER];
+    f32x4 u[UP_TILES][PER];
 #pragma unroll
-    for (int i = 0; i < PER; i++) {
-        const int x = i * LD_THREADS + threadIdx.x, r = x / (R / 4), c = x % (R / 4);
-        u[i] = *reinterpret_cast<const f32x4*>(
-            a.o_lat + ((size_t)min(row0 + r, rows - 1) * a.H + h) * R + c * 4);
-    }
+    for (int t = 0; t < UP_TILES; t++)
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const int x = i * LD_THREADS + threadIdx.x, r = x / (R / 4), c = x % (R / 4);
+            u[t][i] = *reinterpret_cast<const f32x4*>(
+                a.o_lat + ((size_t)min(row0 + t * 16 + r, rows - 1) * a.H + h) * R + c * 4);
+        }
     bf16x8 w[NJ][R / 32];
 #pragma unroll
     for (int j = 0; j < NJ; j++)
@@ -493,36 +498,41 @@ __global__ __launch_bounds__(LD_THREADS) void latent_up_kernel(LatentDecodeArgs 
                                       grp * 8);
     sched_fence();
 #pragma unroll
-    for (int i = 0; i < PER; i++) {
-        const int x = i * LD_THREADS + threadIdx.x, r = x / (R / 4), c = x % (R / 4);
-        float hi[4], lo[4];
+    for (int t = 0; t < UP_TILES; t++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            hi[e] = (float)(bf16)u[i][e];
-            lo[e] = u[i][e] - hi[e];
+        for (int i = 0; i < PER; i++) {
+            const int x = i * LD_THREADS + threadIdx.x, r = x / (R / 4), c = x % (R / 4);
+            float hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                hi[e] = (float)(bf16)u[t][i][e];
+                lo[e] = u[t][i][e] - hi[e];
+            }
+            *reinterpret_cast<uint64_t*>(lds[t][0] + r * PITCH + c * 8) = bits4(hi);
+            *reinterpret_cast<uint64_t*>(lds[t][1] + r * PITCH + c * 8) = bits4(lo);
         }
-        *reinterpret_cast<uint64_t*>(lds[0] + r * PITCH + c * 8) = bits4(hi);
-        *reinterpret_cast<uint64_t*>(lds[1] + r * PITCH + c * 8) = bits4(lo);
-    }
     __syncthreads();
-    f32x4 d[NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; j++) d[j] = zero4();
+    for (int t = 0; t < UP_TILES; t++) {
+        f32x4 d[NJ];
 #pragma unroll
-    for (int k = 0; k < R / 32; k++)
+        for (int j = 0; j < NJ; j++) d[j] = zero4();
 #pragma unroll
-        for (int part = 0; part < 2; part++) {
-            const bf16x8 x = *reinterpret_cast<const bf16x8*>(lds[part] + col * PITCH + k * 64 +
-                                                              grp * 16);
+        for (int k = 0; k < R / 32; k++)
 #pragma unroll
-            for (int j = 0; j < NJ; j++) d[j] = Mma<bf16>::mma(w[j][k], x, d[j]);
+            for (int part = 0; part < 2; part++) {
+                const bf16x8 x = *reinterpret_cast<const bf16x8*>(lds[t][part] + col * PITCH +
+                                                                  k * 64 + grp * 16);
+#pragma unroll
+                for (int j = 0; j < NJ; j++) d[j] = Mma<bf16>::mma(w[j][k], x, d[j]);
+            }
+        const int row = row0 + t * 16 + col;
+        bf16* out = reinterpret_cast<bf16*>(a.o) + ((size_t)row * a.H + h) * DV;
+#pragma unroll
+        for (int j = 0; j < NJ; j++) {
+            const float y[4] = {d[j][0], d[j][1], d[j][2], d[j][3]};
+            if (row < rows) store4<bf16>(out + (wave * NJ + j) * 16 + grp * 4, y);
         }
-    const int row = row0 + col;
-    bf16* out = reinterpret_cast<bf16*>(a.o) + ((size_t)row * a.H + h) * DV;
-#pragma unroll
-    for (int j = 0; j < NJ; j++) {
-        const float y[4] = {d[j][0], d[j][1], d[j][2], d[j][3]};
-        if (row < rows) store4<bf16>(out + (wave * NJ + j) * 16 + grp * 4, y);
     }
 }
 
@@ -553,7 +563,7 @@ hipError_t run_core(const LatentDecodeArgs& a, hipStream_t s) {
 
 template <int R, int DV>
 hipError_t run_up(const LatentDecodeArgs& a, hipStream_t s) {
-    const int tiles = (a.split.batch * a.n_pos + 15) / 16;
+    const int tiles = (a.split.batch * a.n_pos + 16 * UP_TILES - 1) / (16 * UP_TILES);
     hipLaunchKernelGGL((latent_up_kernel<R, DV>), dim3((unsigned)a.H, (unsigned)tiles),
                        dim3(LD_THREADS), 0, s, a);
     return hipGetLastError();
@@ -563,8 +573,8 @@ template <int R>
 hipError_t run_rank(const LatentDecodeArgs& a, hipStream_t s) {
     hipError_t e = run_core<R>(a, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(latent_join_kernel<R>, dim3((unsigned)(a.join.count * a.join.share)),
-                       dim3(JOIN_THREADS), 0, s, a);
+    hipLaunchKernelGGL(latent_join_kernel<R>, dim3(join_grid(a.join)), dim3(JOIN_THREADS),
+                       0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     return a.d_v == 128 ? run_up<R, 128>(a, s) : run_up<R, 64>(a, s);
@@ -584,7 +594,7 @@ size_t latent_decode_layout(LatentDecodeArgs* a, void* ws) {
     j.row_tiles = a->row_tiles;
     j.tile = 16 * a->rt;
     j.rows = a->rows;
-    join_layout(&j, a->split.batch, a->workers, cus);
+    join_layout(&j, a->split.batch, a->workers, cus, a->rank);
     const size_t part = (size_t)2 * a->workers * a->row_tiles * j.tile;
     const size_t lat = (size_t)a->split.batch * a->rows * a->rank;  // bf16 elements
     size_t off = 0;

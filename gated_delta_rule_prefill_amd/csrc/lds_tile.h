@@ -42,6 +42,8 @@ __device__ __forceinline__ void load_to_lds(const void* lane_address, uint32_t l
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(lane_address)
                  : "memory");
 }
+// A loaded value is first looked at here: nothing that depends on it moves up to its load.
+__device__ __forceinline__ void arrived(int& x) { asm volatile("" : "+v"(x)); }
 // Makes the compiler wait for these registers' loads here. Left to their first use inside a loop,
 // the wait would be repeated in every pass and take the tile loads behind them along.
 template <int N>

@@ -21,6 +21,7 @@
 #include "gdn_common.h"
 #include "gdn_launch.h"
 #include "key_join.h"
+#include "lds_tile.h"
 
 namespace gdn {
 
@@ -30,19 +31,13 @@ constexpr int PD_THREADS = 256;
 constexpr int PD_WAVES = PD_THREADS / WAVE;
 constexpr float LOG2E = 1.4426950408889634f;
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ bf16x4 lds_read_tr(const char* p) {
-    typedef __attribute__((address_space(3))) s16x4* lptr;
-    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(p)));
-}
-
 // Per element type: keys per wave step, fragments, and the two products.
 template <typename T, int D> struct PdTile;
 
 template <int D> struct PdTile<bf16, D> {
-    static constexpr int KW = 32;            // keys of a wave step: one MFMA contraction of P V
+    // Keys of a wave step: a contraction of P V. With 32 at d = 256 the step's keys and values
+    // alone take 128 registers beside 96 for queries and outputs, one wave fits a SIMD and spills.
+    static constexpr int KW = D == 256 ? 16 : 32;
     static constexpr int NSUB = KW / 16;
     static constexpr int NF = D / 32;        // 16-byte pieces per lane of a key or query row
     static constexpr int ROW = D * 2;        // bytes of an LDS row
@@ -65,25 +60,24 @@ template <int D> struct PdTile<bf16, D> {
     template <int NS>
     __device__ __forceinline__ static void pv(f32x4* o, const char* v, const float (*p)[4],
                                               int lane) {
-        bf16x8 pb;
-#pragma unroll
-        for (int t = 0; t < 2; t++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) pb[t * 4 + i] = (bf16)p[t][i];
         const int r = (lane >> 4) * 4 + ((lane >> 2) & 3);
         const char* row = v + r * ROW + (lane & 3) * 8;
         const int turned = turn(r) << 5;
+        bf16x4 pb[NSUB];
+#pragma unroll
+        for (int t = 0; t < NSUB; t++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) pb[t][i] = (bf16)p[t][i];
 #pragma unroll
         for (int j = 0; j < D / 16; j++) {
             const char* at = row + ((j << 5) ^ turned);
-            const bf16x4 a0 = lds_read_tr(at), a1 = lds_read_tr(at + 16 * ROW);
-            bf16x8 a;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                a[i] = a0[i];
-                a[4 + i] = a1[i];
-            }
-            o[j] = Mma<bf16>::mma(a, pb, o[j]);
+            if constexpr (NSUB == 2)
+                o[j] = Mma<bf16>::mma(join(lds_read_tr(at), lds_read_tr(at + 16 * ROW)),
+                                      join(pb[0], pb[1]), o[j]);
+            else
+                o[j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
+                    __builtin_bit_cast(s16x4, lds_read_tr(at)), __builtin_bit_cast(s16x4, pb[0]),
+                    o[j], 0, 0, 0);
         }
     }
 };
@@ -127,8 +121,13 @@ struct PdLds {
 
 constexpr uint32_t NO_ROW = 0xffffffffu;
 
+// Two waves per SIMD (256 registers each) where one row tile fits beside a step's keys and
+// values: the loads of one wave then fill the time the other computes.
 template <typename T, int D, int RT>
-__global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArgs a) {
+constexpr int PD_WAVES_PER_SIMD = RT == 1 && (sizeof(T) == 2 || D <= 128) ? 2 : 1;
+
+template <typename T, int D, int RT>
+__global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void paged_decode_kernel(PagedDecodeArgs a) {
     using X = PdTile<T, D>;
     using L = PdLds<T, D, RT>;
     typedef typename X::frag frag;
@@ -210,6 +209,7 @@ __global__ __launch_bounds__(PD_THREADS) void paged_decode_kernel(PagedDecodeArg
         auto find_rows = [&](int c) {
 #pragma unroll
             for (int t = 0; t < NSUB; t++) {
+                arrived(page[t]);
                 const uint32_t key = (uint32_t)(c * KB + wave * KW + t * 16 + col);
                 const uint32_t off = key - a.block(key) * a.block.div;
                 const bool ok = (int)key < nkeys && page[t] >= 0 && page[t] < a.n_blocks;
@@ -420,8 +420,8 @@ hipError_t run_decode(const PagedDecodeArgs& a, hipStream_t s) {
                        dim3(PD_THREADS), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((paged_join_kernel<T, D>), dim3((unsigned)(a.join.count * a.join.share)),
-                       dim3(JOIN_THREADS), 0, s, a);
+    hipLaunchKernelGGL((paged_join_kernel<T, D>), dim3(join_grid(a.join)), dim3(JOIN_THREADS),
+                       0, s, a);
     return hipGetLastError();
 }
 
@@ -430,10 +430,10 @@ hipError_t pick_rows(const PagedDecodeArgs& a, hipStream_t s) {
     switch (a.rt) {
         case 1: return run_decode<T, D, 1>(a, s);
         case 2:
-            if constexpr (sizeof(T) == 2) return run_decode<T, D, 2>(a, s);
+            if constexpr (sizeof(T) == 2 && D <= 128) return run_decode<T, D, 2>(a, s);
             break;
         case 4:
-            if constexpr (sizeof(T) == 2 && D <= 128) return run_decode<T, D, 4>(a, s);
+            if constexpr (sizeof(T) == 2 && D == 64) return run_decode<T, D, 4>(a, s);
             break;
     }
     return hipErrorInvalidValue;
@@ -455,7 +455,7 @@ size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
     a->group = a->H / a->kv_heads;
     a->rows = a->group * a->n_pos;
     // rows of a tile: as many as the registers hold beside the head dim
-    const int most = a->dtype == 0 ? 1 : a->d <= 128 ? 4 : 2;
+    const int most = a->dtype == 0 || a->d == 256 ? 1 : a->d == 128 ? 2 : 4;
     const int tiles = (a->rows + 15) / 16;
     a->rt = tiles >= 4 && most >= 4 ? 4 : tiles >= 2 && most >= 2 ? 2 : 1;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
@@ -466,7 +466,7 @@ size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
     j.row_tiles = a->row_tiles;
     j.tile = 16 * a->rt;
     j.rows = a->rows;
-    join_layout(&j, (int64_t)a->split.batch * a->split.units, a->workers, cus);
+    join_layout(&j, (int64_t)a->split.batch * a->split.units, a->workers, cus, a->d);
     const size_t rows = (size_t)2 * a->workers * a->row_tiles * j.tile;
     j.part_o = static_cast<float*>(ws);
     j.part_ml = ws == nullptr ? nullptr : j.part_o + rows * a->d;
