@@ -17,6 +17,7 @@ namespace gdn {
 
 constexpr int JOIN_THREADS = 256;
 constexpr int JOIN_GROUPS = JOIN_THREADS / 32;
+constexpr int JOIN_MAX_WORKERS = 1024;  // most parts of a unit
 
 struct JoinShape {
     int4* notes;          // [count]
@@ -58,11 +59,13 @@ __device__ __forceinline__ void join_note(const JoinShape& j, const SplitShape& 
 }
 
 // One workgroup's share of a note's rows, NC pieces of 128 columns from column `first` on, U
-// parts on their way at a time.
+// parts on their way at a time per group.
 template <int COLS, int NC, int U, typename Store>
 __device__ __forceinline__ void join_rows(const JoinShape& s, int4 note, int step0, int first,
                                           Store store) {
     __shared__ float red[JOIN_GROUPS][NC * 128 + 4];
+    __shared__ float weight[JOIN_MAX_WORKERS];
+    __shared__ float wave_part[JOIN_THREADS / WAVE];
     const int b = note.x, unit = note.y, w0 = note.z >> 1, late = note.z & 1, w1 = note.w;
     const int tid = threadIdx.x, group = tid >> 5, lane = tid & 31;
     const size_t rows_per_part = (size_t)s.row_tiles * s.tile;
@@ -74,55 +77,85 @@ __device__ __forceinline__ void join_rows(const JoinShape& s, int4 note, int ste
         const int row = step * rows_here + group / gpr;
         const bool live = row < s.rows;
         const int r = live ? row : 0;
-        auto at = [&](int w) {
-            return (size_t)(2 * w + (w == w0 ? late : 0)) * rows_per_part + r;
+        auto at = [&](int i) {  // part i of the unit
+            return (size_t)(2 * (w0 + i) + (i == 0 ? late : 0)) * rows_per_part + r;
         };
-        float top = -INFINITY;
-        for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, s.part_ml[at(w) * 2]);
+        // the parts' weights: lane i's is part i's, or all of them in LDS where a row has so
+        // many that the whole workgroup shares it
+        float f = 0.f, sum = 0.f;
+        if (gpr < JOIN_GROUPS) {  // at most JOIN_GROUPS / 2 x U <= 32 parts
+            float m = -INFINITY, l = 0.f;
+            if (lane < parts) {
+                m = s.part_ml[at(lane) * 2];
+                l = s.part_ml[at(lane) * 2 + 1];
+            }
+            float top = m;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 32));
-        const float ref = top == -INFINITY ? 0.f : top;
+            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 32));
+            f = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.f : top));
+            sum = f * l;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 32);
+        } else {
+            constexpr int PER = JOIN_MAX_WORKERS / JOIN_THREADS;
+            float m[PER], l[PER], top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < PER; k++) {
+                const int i = k * JOIN_THREADS + tid;
+                m[k] = i < parts ? s.part_ml[at(i) * 2] : -INFINITY;
+                l[k] = i < parts ? s.part_ml[at(i) * 2 + 1] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < PER; k++) top = fmaxf(top, m[k]);
+#pragma unroll
+            for (int off = WAVE / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, WAVE));
+            if (lane_id() == 0) wave_part[wave_id()] = top;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < JOIN_THREADS / WAVE; i++) top = fmaxf(top, wave_part[i]);
+            const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int k = 0; k < PER; k++) {
+                const float w = __builtin_amdgcn_exp2f(m[k] - ref);
+                weight[k * JOIN_THREADS + tid] = w;
+                sum = fmaf(w, l[k], sum);
+            }
+#pragma unroll
+            for (int off = WAVE / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, WAVE);
+            __syncthreads();
+            if (lane_id() == 0) wave_part[wave_id()] = sum;
+            __syncthreads();
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < JOIN_THREADS / WAVE; i++) sum += wave_part[i];
+        }
         f32x4 x[NC];
 #pragma unroll
         for (int c = 0; c < NC; c++) x[c] = zero4();
-        float sum = 0.f;  // this lane's share
-        for (int base = w0; base <= w1; base += 32) {
-            // lane i weighs part base + i; each group then adds up every gpr-th of the 32
-            const int mine = base + lane;
-            float f = 0.f;
-            if (mine <= w1) {
-                const size_t e = at(mine);
-                f = __builtin_amdgcn_exp2f(s.part_ml[e * 2] - ref);
-                if (turn == 0) sum = fmaf(f, s.part_ml[e * 2 + 1], sum);
-            }
-            const int n = min(32, w1 - base + 1);
-            for (int i0 = turn; i0 < n; i0 += U * gpr) {
-                // (the surplus ones weigh nothing)
-                f32x4 y[U][NC];
-                float g[U];
+        for (int i0 = turn; i0 < parts; i0 += U * gpr) {
+            f32x4 y[U][NC];
+            float g[U];
 #pragma unroll
-                for (int k = 0; k < U; k++) {
-                    const int i = i0 + k * gpr;
-                    g[k] = __shfl(f, i & 31, 32);
-                    if (i >= n) g[k] = 0.f;
-                    const float* src = s.part_o + at(base + min(i, n - 1)) * COLS;
+            for (int k = 0; k < U; k++) {  // (the surplus ones weigh nothing)
+                const int i = i0 + k * gpr;
+                g[k] = gpr < JOIN_GROUPS ? __shfl(f, i & 31, 32)
+                                         : weight[min(i, JOIN_MAX_WORKERS - 1)];
+                if (i >= parts) g[k] = 0.f;
+                const float* src = s.part_o + at(min(i, parts - 1)) * COLS;
 #pragma unroll
-                    for (int c = 0; c < NC; c++) {
-                        const int col = first + c * 128 + lane * 4;
-                        y[k][c] = COLS % 128 == 0 || col < COLS
-                                      ? *reinterpret_cast<const f32x4*>(src + col) : zero4();
-                    }
+                for (int c = 0; c < NC; c++) {
+                    const int col = first + c * 128 + lane * 4;
+                    y[k][c] = COLS % 128 == 0 || col < COLS
+                                  ? *reinterpret_cast<const f32x4*>(src + col) : zero4();
                 }
-#pragma unroll
-                for (int k = 0; k < U; k++)
-#pragma unroll
-                    for (int c = 0; c < NC; c++)
-#pragma unroll
-                        for (int e = 0; e < 4; e++) x[c][e] = fmaf(g[k], y[k][c][e], x[c][e]);
             }
-        }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 32);
+            for (int k = 0; k < U; k++)
+#pragma unroll
+                for (int c = 0; c < NC; c++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) x[c][e] = fmaf(g[k], y[k][c][e], x[c][e]);
+        }
         if (gpr > 1) {  // uniform over the workgroup
 #pragma unroll
             for (int c = 0; c < NC; c++)

@@ -59,7 +59,7 @@ __device__ __forceinline__ SplitPlace split_place(int block, int row_tiles) {
 }
 inline int split_workers(int workgroups, int row_tiles) {
     const int n = workgroups / row_tiles / 8 * 8;
-    return n < 8 ? 8 : n;
+    return n < 8 ? 8 : n > 1024 ? 1024 : n;
 }
 
 // `total` chunks over at most n workers: the first `more` take each + 1, the others `each`.
