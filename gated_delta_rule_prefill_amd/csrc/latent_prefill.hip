@@ -244,18 +244,19 @@ __global__ __launch_bounds__(LP_THREADS) void latent_expand_kernel(LatentPrefill
 
 // ---------------------------------------------------------------------------------- attend
 // A workgroup takes 128 query rows of one head, 32 a wave; all four waves walk the same key
-// tiles, loaded straight into LDS, two buffers, one barrier a tile. With 32 x 32 x 16 MFMAs:
+// tiles, loaded straight into LDS, one barrier a tile. With 32 x 32 x 16 MFMAs:
 //   S^T = K Q^T     queries in registers as the B operand, so a query is an accumulator column:
 //                   its scores lie in two lanes, and its statistics need one exchange a tile;
 //   O^T += V^T P^T  the accumulator layout of S^T is the B operand's with the keys of each 16
 //                   renumbered, and V^T was written out in that order: weights never leave the
 //                   registers.
+// A tile's scores (matrix pipe) are formed beside the previous tile's softmax (vector pipe): keys
+// and values have two LDS buffers each, and the keys run one tile ahead of the values.
 template <int D>
 struct LpTile {
-    static constexpr int K_AT = 0;                                // [64][D] keys
-    static constexpr int PE_AT = LP_KB * D * 2;                   // [64][64] rotary keys
-    static constexpr int V_AT = PE_AT + LP_KB * LP_ROPE * 2;      // [D][64] values
-    static constexpr int BYTES = V_AT + D * LP_KB * 2;
+    static constexpr int K_BYTES = LP_KB * (D + LP_ROPE) * 2;     // [64][D] keys, [64][64] rotary
+    static constexpr int PE_AT = LP_KB * D * 2;
+    static constexpr int V_BYTES = D * LP_KB * 2;                 // [D][64] values
     // pieces of a key row turned by the row (256-byte rows: 16 pieces)
     __device__ __forceinline__ static int turn(int r) { return D == 128 ? r & 15 : (r >> 1) & 7; }
     __device__ __forceinline__ static int key(int r, int c) {
@@ -268,7 +269,8 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
     using X = LpTile<D>;
     constexpr int NK = D / 16, NR = LP_ROPE / 16;  // contraction steps of a score
     constexpr int NO = D / 32;                     // 32-column output tiles
-    __shared__ __align__(16) char tile[2][X::BYTES];
+    __shared__ __align__(1024) char k_tile[2][X::K_BYTES];
+    __shared__ __align__(1024) char v_tile[2][X::V_BYTES];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int h = blockIdx.x % a.H;
@@ -283,15 +285,20 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
     const int keys = min(lp_keys(a, seq), (a.key_tile[seq + 1] - kt0) * LP_KB);
     const int last_row = min(q0 + LP_QB, fresh) - 1;
     const int reach = min(keys, first_pos + last_row + 1);  // keys that the tile's last row sees
-    const int nt = reach > 0 ? (reach + LP_KB - 1) / LP_KB : 0;
+    const int nt = uniform(reach > 0 ? (reach + LP_KB - 1) / LP_KB : 0);
 
     const int col = lane & 31, half = lane >> 5;
     const int row = q0 + wave * 32 + col;               // this lane's query row
     const bool live = row < fresh;
     const int pos = first_pos + row;
-    const int wave_first = first_pos + q0 + wave * 32;  // position of the wave's first row
+    const int wave_first = uniform(first_pos + q0 + wave * 32);  // position of the wave's first row
+    // tiles that this wave's rows see
+    const int mine = wave_first + 31 < 0 ? 0 : min(nt, (wave_first + 31) / LP_KB + 1);
     const size_t token = (size_t)min(max(a.cu_seqlens[seq], 0), a.total_tokens) +
                          (live ? row : q0);
+    // The scale enters the exponent's multiplication; a negative one is moved into the queries,
+    // so that the largest score is the largest weight (and zero makes the queries zero).
+    const float cs = a.scale == 0.f ? 1.f : fabsf(a.scale) * LOG2E;
     bf16x8 q[NK + NR];
     {
         const bf16* qn = reinterpret_cast<const bf16*>(a.q_nope) + (token * a.H + h) * D;
@@ -301,34 +308,47 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
 #pragma unroll
         for (int f = 0; f < NR; f++) q[NK + f] = Mma<bf16>::load(qp + f * 16 + half * 8);
     }
+    if (a.scale <= 0.f) {
+#pragma unroll
+        for (int f = 0; f < NK + NR; f++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) q[f][i] = a.scale < 0.f ? -q[f][i] : (bf16)0.f;
+    }
     arrived(q);
     const char* ksrc = reinterpret_cast<const char*>(a.k) +
                        ((size_t)h * a.key_tiles + kt0) * (LP_KB * D * 2);
     const char* vsrc = reinterpret_cast<const char*>(a.vt) +
                        ((size_t)h * a.key_tiles + kt0) * (LP_KB * D * 2);
     const char* psrc = reinterpret_cast<const char*>(a.k_pe) + (size_t)kt0 * (LP_KB * LP_ROPE * 2);
-    auto load = [&](int t, int buf) {
-        const uint32_t at = lds_offset(tile[buf]);
-        constexpr int KI = LP_KB * D * 2 / 1024 / LP_WAVES;  // 1 KiB loads per wave
+    // Byte offsets of this lane within a tile. Pieces are xored with a function of their row, so
+    // the constant part of a piece index is xored in last and one offset serves all of them;
+    // fixed() hides it from the compiler, which would keep every result of that across the loop.
+    auto fixed = [](uint32_t x) {
+        asm volatile("" : "+v"(x));
+        return x;
+    };
+    const uint32_t k_at = X::key(col, half), r_at = row128(col, half);
+    const uint32_t load128 = row128(lane >> 3, lane & 7);       // 8 rows of 128 bytes per load
+    const uint32_t load_k = D == 128 ? X::key(lane >> 4, lane & 15) : load128;
+    constexpr int KI = LP_KB * D * 2 / 1024 / LP_WAVES;         // 1 KiB loads per wave
+    auto load_keys = [&](int t) {
+        const uint32_t at = lds_offset(k_tile[t & 1]), off = fixed(load_k), pe = fixed(load128);
+        const char* src = ksrc + ((size_t)t * LP_WAVES + wave) * (KI * 1024);
 #pragma unroll
-        for (int i = 0; i < KI; i++) {
-            const int x = (wave * KI + i) * 64 + lane;       // 16-byte piece of the key tile
-            const int r = x / (D / 8), c = x % (D / 8);
-            load_to_lds(ksrc + (size_t)t * (LP_KB * D * 2),
-                        (uint32_t)(r * (D * 2) + ((c ^ X::turn(r)) << 4)),
-                        at + X::K_AT + (wave * KI + i) * 1024);
-            const int vr = x >> 3, vc = x & 7;
-            load_to_lds(vsrc + (size_t)t * (LP_KB * D * 2),
-                        (uint32_t)(vr * 128 + ((vc ^ ((vr >> 1) & 7)) << 4)),
-                        at + X::V_AT + (wave * KI + i) * 1024);
-        }
+        for (int i = 0; i < KI; i++)  // 1 KiB on, the rows' turn is off by 4 i (128-byte rows: 4)
+            load_to_lds(src + i * 1024, off ^ (D == 128 ? i << 6 : (i & 1) << 6),
+                        at + (wave * KI + i) * 1024);
+        const char* psrc_t = psrc + ((size_t)t * LP_WAVES + wave) * 2048;
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const int r = (wave * 2 + i) * 8 + (lane >> 3), c = lane & 7;
-            load_to_lds(psrc + (size_t)t * (LP_KB * LP_ROPE * 2),
-                        (uint32_t)(r * 128 + ((c ^ ((r >> 1) & 7)) << 4)),
-                        at + X::PE_AT + (wave * 2 + i) * 1024);
-        }
+        for (int i = 0; i < 2; i++)
+            load_to_lds(psrc_t + i * 1024, pe ^ i << 6, at + X::PE_AT + (wave * 2 + i) * 1024);
+    };
+    auto load_values = [&](int t) {
+        const uint32_t at = lds_offset(v_tile[t & 1]), off = fixed(load128);
+        const char* src = vsrc + ((size_t)t * LP_WAVES + wave) * (KI * 1024);
+#pragma unroll
+        for (int i = 0; i < KI; i++)
+            load_to_lds(src + i * 1024, off ^ (i & 1) << 6, at + (wave * KI + i) * 1024);
     };
     f32x16 acc[NO];
 #pragma unroll
@@ -336,28 +356,11 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
 #pragma unroll
         for (int i = 0; i < 16; i++) acc[j][i] = 0.f;
     float m = -INFINITY, l = 0.f;
-    const float cs = a.scale * LOG2E;
-    uint64_t exist_next = 0;
-    if (nt > 0) {
-        exist_next = a.exist[kt0];
-        load(0, 0);
-    }
-    for (int t = 0; t < nt; t++) {
-        const char* kt = tile[t & 1];
-        lds_loads_done();
-        // (moved to scalar registers here, where nothing is in flight: a wait for the ordinary
-        // load further down would also wait for the tile loads issued behind it)
-        const uint64_t exist =
-            (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(exist_next >> 32)) << 32 |
-            (uint32_t)__builtin_amdgcn_readfirstlane((int)exist_next);
-        lds_barrier();  // tile t is whole; all waves are done with the other buffer
-        if (t + 1 < nt) {
-            exist_next = a.exist[kt0 + t + 1];
-            load(t + 1, (t + 1) & 1);
-        }
-        const int key0 = t * LP_KB;
-        if (key0 > wave_first + 31) continue;  // beyond all of this wave's rows
-        f32x16 s[2];
+
+    // scores of tile t, unscaled
+    auto scores = [&](int t, f32x16 (&s)[2]) {
+        const uint32_t kt = lds_offset(k_tile[t & 1]);
+        const uint32_t key = fixed(kt + k_at), pe = fixed(kt + X::PE_AT + r_at);
 #pragma unroll
         for (int x = 0; x < 2; x++)
 #pragma unroll
@@ -365,28 +368,48 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
 #pragma unroll
         for (int f = 0; f < NK + NR; f++)
 #pragma unroll
-            for (int x = 0; x < 2; x++) {
-                const int r = x * 32 + col;
-                const bf16x8 k = *reinterpret_cast<const bf16x8*>(
-                    kt + (f < NK ? X::K_AT + X::key(r, f * 2 + half)
-                                 : X::PE_AT + row128(r, (f - NK) * 2 + half)));
-                s[x] = mma32(k, q[f], s[x]);
+            for (int x = 0; x < 2; x++)  // (32 rows on, the pieces are turned alike)
+                s[x] = mma32(lds_get<bf16x8>(f < NK ? (key ^ f << 5) + x * (32 * D * 2)
+                                                    : (pe ^ (f - NK) << 5) + x * (32 * 128)),
+                             q[f], s[x]);
+    };
+    auto mask = [&](int t, uint64_t exist, f32x16 (&s)[2]) {
+        const int key0 = t * LP_KB;
+        if (exist == ~0ull && key0 + LP_KB - 1 <= wave_first) return;
+        // this lane's keys are key0 + first + ..: hidden from the compiler, which would keep
+        // what depends on it in registers across the key loop
+        int first = half * 4;
+        asm volatile("" : "+v"(first));
+        const uint64_t here = exist >> first;
+        const int left = pos - key0 - first;
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const int k = x * 32 + (i >> 2) * 8 + (i & 3);
+                s[x][i] = ((here >> k) & 1) && k <= left ? s[x][i] : -INFINITY;
             }
-        if (exist != ~0ull || key0 + LP_KB - 1 > wave_first) {
-#pragma unroll
-            for (int x = 0; x < 2; x++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const int k = x * 32 + (i >> 2) * 8 + half * 4 + (i & 3);
-                    const bool keep = ((exist >> k) & 1) && key0 + k <= pos;
-                    s[x][i] = keep ? s[x][i] * cs : -INFINITY;
-                }
-        } else {
-#pragma unroll
-            for (int x = 0; x < 2; x++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) s[x][i] *= cs;
+    };
+    uint64_t exist_next = 0;
+    auto take_exist = [&]() {
+        // moved to scalar registers where nothing else is in flight: a wait for the ordinary
+        // load further down would also wait for the tile loads issued behind it
+        return (uint64_t)(uint32_t)uniform((int)(exist_next >> 32)) << 32 |
+               (uint32_t)uniform((int)exist_next);
+    };
+    // One tile: its weights from s (masked), its values added; meanwhile the next tile's scores.
+    auto step = [&](int t, f32x16 (&s)[2], f32x16 (&next)[2]) {
+        lds_loads_done();
+        const uint64_t exist = take_exist();  // of tile t + 1
+        lds_barrier();  // keys t + 1 and values t are whole; all are done with what they replace
+        if (t + 2 < nt) {
+            exist_next = a.exist[kt0 + t + 2];
+            sched_fence();
+            load_keys(t + 2);
         }
+        if (t + 1 < nt) load_values(t + 1);
+        if (t >= mine) return;
+        scores(t + 1 < mine ? t + 1 : t, next);
         float top = s[0][0];
 #pragma unroll
         for (int x = 0; x < 2; x++)
@@ -394,34 +417,55 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
             for (int i = 0; i < 16; i++) top = fmaxf(top, s[x][i]);
         top = fmaxf(top, __shfl_xor(top, 32, WAVE));
         const float m1 = fmaxf(m, top);
-        const float ref = m1 == -INFINITY ? 0.f : m1;  // a row with no key so far
-        if (__any(m1 > m)) {
-            const float shrink = __builtin_amdgcn_exp2f(m - ref);
-            l *= shrink;
-#pragma unroll
-            for (int j = 0; j < NO; j++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) acc[j][i] *= shrink;
-            m = m1;
-        }
+        const float ref = m1 == -INFINITY ? 0.f : m1 * cs;  // a row with no key so far
+        const float shrink = __builtin_amdgcn_exp2f(fmaf(m, cs, -ref));
+        const bool grown = m1 > m;
+        m = m1;
+        l *= shrink;
+        bf16x8 p[LP_KB / 16];
 #pragma unroll
         for (int x = 0; x < 2; x++)
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-                s[x][i] = __builtin_amdgcn_exp2f(s[x][i] - ref);
-                l += s[x][i];
+                const float w = __builtin_amdgcn_exp2f(fmaf(s[x][i], cs, -ref));
+                l += w;
+                p[x * 2 + (i >> 3)][i & 7] = (bf16)w;
             }
+        if (__any(grown)) {
 #pragma unroll
-        for (int st = 0; st < LP_KB / 16; st++) {
-            bf16x8 p;
+            for (int j = 0; j < NO; j++)
 #pragma unroll
-            for (int i = 0; i < 8; i++) p[i] = (bf16)s[st >> 1][(st & 1) * 8 + i];
+                for (int i = 0; i < 16; i++) acc[j][i] *= shrink;
+        }
+        const uint32_t value = fixed(lds_offset(v_tile[t & 1]) + r_at);
 #pragma unroll
-            for (int j = 0; j < NO; j++) {
-                const bf16x8 v = *reinterpret_cast<const bf16x8*>(
-                    kt + X::V_AT + row128(j * 32 + col, st * 2 + half));
-                acc[j] = mma32(v, p, acc[j]);
-            }
+        for (int st = 0; st < LP_KB / 16; st++)
+#pragma unroll
+            for (int j = 0; j < NO; j++)
+                acc[j] = mma32(lds_get<bf16x8>((value ^ st << 5) + j * (32 * 128)), p[st], acc[j]);
+        if (t + 1 < mine) mask(t + 1, exist, next);
+    };
+    if (nt > 0) {
+        f32x16 s0[2], s1[2];
+        exist_next = a.exist[kt0];
+        sched_fence();
+        load_keys(0);
+        lds_loads_done();
+        const uint64_t exist = take_exist();
+        lds_barrier();
+        if (nt > 1) {
+            exist_next = a.exist[kt0 + 1];
+            sched_fence();
+            load_keys(1);
+        }
+        load_values(0);
+        if (mine > 0) {
+            scores(0, s0);
+            mask(0, exist, s0);
+        }
+        for (int t = 0; t < nt; t += 2) {
+            step(t, s0, s1);
+            if (t + 1 < nt) step(t + 1, s1, s0);
         }
     }
     l += __shfl_xor(l, 32, WAVE);
