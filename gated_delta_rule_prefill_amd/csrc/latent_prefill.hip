@@ -355,23 +355,42 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
     for (int j = 0; j < NO; j++)
 #pragma unroll
         for (int i = 0; i < 16; i++) acc[j][i] = 0.f;
-    float m = -INFINITY, l = 0.f;
+    // The exponents' reference (scaled) and the sum. The reference follows the maximum only once
+    // that is more than 2^LAG above it: weights then reach 2^LAG, which neither fp32 sums nor
+    // bf16 weights mind, and the outputs are rescaled a few times in all instead of at every
+    // tile in which one of 32 rows finds a new maximum.
+    constexpr float LAG = 8.f;
+    float ref = -INFINITY, l = 0.f;
 
-    // scores of tile t, unscaled
-    auto scores = [&](int t, f32x16 (&s)[2]) {
+    // Scores of tile t, unscaled, and beside each pair of MFMAs a slice of other work: the
+    // matrix pipe takes 32 cycles for one MFMA, in which the wave can issue eight vector
+    // instructions. The fences keep the compiler from taking the two apart again.
+    constexpr int NF = NK + NR, AHEAD = 3;
+    auto scores = [&](int t, f32x16 (&s)[2], auto beside) {
         const uint32_t kt = lds_offset(k_tile[t & 1]);
         const uint32_t key = fixed(kt + k_at), pe = fixed(kt + X::PE_AT + r_at);
+        bf16x8 k[AHEAD + 1][2];
+        auto load = [&](int f) {
+#pragma unroll
+            for (int x = 0; x < 2; x++)  // (32 rows on, the pieces are turned alike)
+                k[f % (AHEAD + 1)][x] = lds_get<bf16x8>(
+                    f < NK ? (key ^ f << 5) + x * (32 * D * 2)
+                           : (pe ^ (f - NK) << 5) + x * (32 * 128));
+        };
+#pragma unroll
+        for (int f = 0; f < AHEAD; f++) load(f);
 #pragma unroll
         for (int x = 0; x < 2; x++)
 #pragma unroll
             for (int i = 0; i < 16; i++) s[x][i] = 0.f;
 #pragma unroll
-        for (int f = 0; f < NK + NR; f++)
+        for (int f = 0; f < NF; f++) {
+            if (f + AHEAD < NF) load(f + AHEAD);
 #pragma unroll
-            for (int x = 0; x < 2; x++)  // (32 rows on, the pieces are turned alike)
-                s[x] = mma32(lds_get<bf16x8>(f < NK ? (key ^ f << 5) + x * (32 * D * 2)
-                                                    : (pe ^ (f - NK) << 5) + x * (32 * 128)),
-                             q[f], s[x]);
+            for (int x = 0; x < 2; x++) s[x] = mma32(k[f % (AHEAD + 1)][x], q[f], s[x]);
+            beside(f);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     auto mask = [&](int t, uint64_t exist, f32x16 (&s)[2]) {
         const int key0 = t * LP_KB;
@@ -409,40 +428,56 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
         }
         if (t + 1 < nt) load_values(t + 1);
         if (t >= mine) return;
-        scores(t + 1 < mine ? t + 1 : t, next);
-        float top = s[0][0];
-#pragma unroll
-        for (int x = 0; x < 2; x++)
-#pragma unroll
-            for (int i = 0; i < 16; i++) top = fmaxf(top, s[x][i]);
-        top = fmaxf(top, __shfl_xor(top, 32, WAVE));
-        const float m1 = fmaxf(m, top);
-        const float ref = m1 == -INFINITY ? 0.f : m1 * cs;  // a row with no key so far
-        const float shrink = __builtin_amdgcn_exp2f(fmaf(m, cs, -ref));
-        const bool grown = m1 > m;
-        m = m1;
-        l *= shrink;
+        float top = -INFINITY, shift = 0.f;
+        bool grown = false;
         bf16x8 p[LP_KB / 16];
+        // slices 0 and 1: the tile's maximum; 2: over both halves; from 3 on: the weights
+        constexpr int PER = (32 + NF - 4) / (NF - 3);
+        scores(t + 1 < mine ? t + 1 : t, next, [&](int f) {
+            if (f < 2) {
 #pragma unroll
-        for (int x = 0; x < 2; x++)
+                for (int i = 0; i < 16; i++) top = fmaxf(top, s[f][i]);
+            } else if (f == 2) {
+                top = max_halves(top) * cs;
+                grown = top > ref + LAG;
+                const float to = grown ? top : ref;
+                shift = to == -INFINITY ? 0.f : to;  // a row with no key so far
+            } else {
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-                const float w = __builtin_amdgcn_exp2f(fmaf(s[x][i], cs, -ref));
-                l += w;
-                p[x * 2 + (i >> 3)][i & 7] = (bf16)w;
+                for (int i = (f - 3) * PER; i < (f - 2) * PER && i < 32; i++) {
+                    float w = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], cs, -shift));
+                    asm volatile("" : "+v"(w));  // formed here, not where it is used
+                    s[i >> 4][i & 15] = w;
+                    p[i >> 3][i & 7] = (bf16)w;
+                }
             }
+        });
         if (__any(grown)) {
+            // (a row without a reference so far has sums of zero)
+            const float shrink = grown ? __builtin_amdgcn_exp2f(ref - shift) : 1.f;
+            ref = grown ? shift : ref;
+            l *= shrink;
 #pragma unroll
             for (int j = 0; j < NO; j++)
 #pragma unroll
                 for (int i = 0; i < 16; i++) acc[j][i] *= shrink;
         }
         const uint32_t value = fixed(lds_offset(v_tile[t & 1]) + r_at);
+        bf16x8 v[AHEAD + 1];
+        constexpr int NV = LP_KB / 16 * NO;
+        auto load = [&](int n) {
+            v[n % (AHEAD + 1)] = lds_get<bf16x8>((value ^ (n / NO) << 5) + n % NO * (32 * 128));
+        };
 #pragma unroll
-        for (int st = 0; st < LP_KB / 16; st++)
+        for (int n = 0; n < AHEAD; n++) load(n);
 #pragma unroll
-            for (int j = 0; j < NO; j++)
-                acc[j] = mma32(lds_get<bf16x8>((value ^ st << 5) + j * (32 * 128)), p[st], acc[j]);
+        for (int n = 0; n < NV; n++) {
+            if (n + AHEAD < NV) load(n + AHEAD);
+            acc[n % NO] = mma32(v[n % (AHEAD + 1)], p[n / NO], acc[n % NO]);
+#pragma unroll
+            for (int i = n * 32 / NV; i < (n + 1) * 32 / NV; i++) l += s[i >> 4][i & 15];
+            __builtin_amdgcn_sched_barrier(0);
+        }
         if (t + 1 < mine) mask(t + 1, exist, next);
     };
     if (nt > 0) {
@@ -460,7 +495,7 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
         }
         load_values(0);
         if (mine > 0) {
-            scores(0, s0);
+            scores(0, s0, [](int) {});
             mask(0, exist, s0);
         }
         for (int t = 0; t < nt; t += 2) {

@@ -76,4 +76,13 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
     return r;
 }
 
+// Maximum over a lane and its partner 32 lanes on, in the vector pipe: the exchange leaves the
+// lower halves in one register and the upper halves in the other.
+__device__ __forceinline__ float max_halves(float x) {
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    const uint32_t b = __float_as_uint(x);
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 }  // namespace gdn
