@@ -7,8 +7,11 @@
 // form needs 2 (2 rank + 64).
 //
 // Three launches: the tile tables (prefix sums of the device-resident lengths), expand, attend.
+#include <type_traits>
+
 #include "attn_launch.h"
 #include "gdn_common.h"
+#include "gdn_launch.h"
 #include "lds_tile.h"
 
 namespace gdn {
@@ -93,26 +96,34 @@ __global__ __launch_bounds__(LP_THREADS) void latent_tiles_kernel(LatentPrefillA
 }
 
 // ---------------------------------------------------------------------------------- expand
-// A 128 x 128 product per workgroup: 128 keys (two key tiles) times 128 of the H 2 d rows of
-// w_kv, contraction over the rank in steps of 64, both operands loaded straight into LDS, two
-// buffers. Keys come through the block table. A wave's 64 output columns are all of one kind:
-// for keys the weights are the MFMA's A operand, so that a lane holds 4 dims of a key; for values
-// the latents are, so that it holds 4 keys of a dim: each is stored along its rows in memory
-// order, and the values come out transposed. Keys that do not exist are stored as zeros.
-constexpr int EX_M = 128, EX_N = 128, EX_K = 64;
+// Keys and values of 128 cache rows (two key tiles). The rows come through the block table into
+// LDS once, whole (128 KiB at rank 512), and stay; then each of the eight waves forms 128 x 64
+// products with 64 rows of w_kv at a time, read straight into registers as MFMA fragments
+// (w_kv lies in the L2: every workgroup reads all its rows). No barrier after the first one.
+// A wave's 64 columns are all of one kind: for keys the weights are the MFMA's A operand, so
+// that a lane holds 4 dims of a key; for values the latents are, so that it holds 4 keys of a
+// dim: each is stored along its rows in memory order, and the values come out transposed. Keys
+// that do not exist are stored as zeros.
+constexpr int EX_THREADS = 512, EX_WAVES = EX_THREADS / WAVE;
+constexpr int EX_M = 128;              // keys of a workgroup
+constexpr int EX_N = 64;               // columns of a wave
+constexpr int EX_COLS = EX_WAVES * EX_N;
 
 // LDS piece (16 bytes) c of row r of a tile with 128-byte rows
 __device__ __forceinline__ int row128(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
 
-__global__ __launch_bounds__(LP_THREADS) void latent_expand_kernel(LatentPrefillArgs a) {
-    __shared__ __align__(16) char lds[2][(EX_M + EX_N) * 128];
+template <int R>
+__global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPrefillArgs a,
+                                                                      int units_per_wg) {
+    constexpr int ROW = R * 2, PIECES = ROW / 16;
+    __shared__ __align__(1024) char lat[EX_M * ROW];
     __shared__ uint32_t slot_of[EX_M];
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int t0 = blockIdx.x * 2;
     const int used = a.key_tile[a.n_seqs];
     if (t0 >= used) return;
-    const int R = a.rank, row_bytes = (R + LP_ROPE) * 2;
+    constexpr size_t CACHE_ROW = (R + LP_ROPE) * 2;
     const char* cache = reinterpret_cast<const char*>(a.cache);
 
     bool ok = false;
@@ -132,111 +143,122 @@ __global__ __launch_bounds__(LP_THREADS) void latent_expand_kernel(LatentPrefill
         slot_of[tid] = slot | (ok ? 0u : 0x80000000u);  // slots stay below 2^31
     }
     __syncthreads();
+    {
+        // 16 rows per wave; piece c of row r lies at piece c ^ (r & 15)
+        const uint32_t mine = slot_of[wave * 16 + (lane & 15)] & 0x7fffffffu;
+        const uint32_t at = lds_offset(lat) + wave * 16 * ROW;
+        if constexpr (PIECES == 64) {
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                load_to_lds(cache + __builtin_amdgcn_readlane(mine, r) * CACHE_ROW,
+                            (uint32_t)((lane ^ r) << 4), at + r * ROW);
+        } else {  // two rows per load
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+                const int rr = r + (lane >> 5);
+                load_to_lds(cache + __shfl(mine, rr, WAVE) * CACHE_ROW + (((lane & 31) ^ rr) << 4),
+                            at + r * ROW);
+            }
+        }
+    }
     if (blockIdx.y == 0) {
         // this pair's rotary keys and existence bits, once for all heads
         if (wave < 2) {
             const uint64_t bits = __ballot(ok);
             if (lane == 0 && t0 + wave < used) a.exist[t0 + wave] = bits;
         }
-        for (int x = tid; x < EX_M * 8; x += LP_THREADS) {
+        for (int x = tid; x < EX_M * 8; x += EX_THREADS) {
             const int r = x >> 3, c = x & 7;
             if (t0 + r / LP_KB < used)
                 *reinterpret_cast<f32x4*>(reinterpret_cast<char*>(a.k_pe) +
                                           ((size_t)t0 * LP_KB + r) * 128 + c * 16) =
                     *reinterpret_cast<const f32x4*>(
-                        cache + (size_t)(slot_of[r] & 0x7fffffffu) * row_bytes + R * 2 + c * 16);
+                        cache + (size_t)(slot_of[r] & 0x7fffffffu) * CACHE_ROW + ROW + c * 16);
         }
     }
-    // loads: 8 rows of 128 bytes each; wave w brings latent rows 32 w .. and weight rows 32 w ..
-    const char* src[4];
-    const char* wsrc = reinterpret_cast<const char*>(a.w_kv) + (size_t)blockIdx.y * EX_N * R * 2;
-    uint32_t woff[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = wave * 32 + i * 8 + (lane >> 3);
-        const int c = (lane & 7) ^ ((r >> 1) & 7);
-        src[i] = cache + (size_t)(slot_of[r] & 0x7fffffffu) * row_bytes + c * 16;
-        woff[i] = (uint32_t)(r * R * 2 + c * 16);
-    }
-    auto load = [&](int k, int buf) {
-        const uint32_t at = lds_offset(lds[buf]) + wave * 32 * 128;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            load_to_lds(src[i] + k * (EX_K * 2), at + i * 1024);
-            load_to_lds(wsrc + k * (EX_K * 2), woff[i], at + EX_M * 128 + i * 1024);
-        }
-    };
+    lds_loads_done();
+    lds_barrier();
     const int col = lane & 15, grp = lane >> 4;
-    const int wm = wave >> 1, wn = wave & 1;
-    const int col0 = blockIdx.y * EX_N + wn * 64;  // this wave's 64 rows of w_kv
-    const int h = col0 / (2 * a.d), in_head = col0 - h * 2 * a.d;
-    const bool value = in_head >= a.d;
-    f32x4 acc[4][4];  // [key block][column block]
+    const int columns = a.H * 2 * a.d;
+    // keys 4 g .. 4 g + 3 of a 16: the middle two groups change places in the values' order
+    const int pos = ((grp & 1) << 3) + ((grp >> 1) << 2);
+    const uint32_t x_at = lds_offset(lat) + col * ROW + ((grp ^ col) << 4);
+    for (int u = 0; u < units_per_wg; u++) {
+        const int col0 = ((int)blockIdx.y * units_per_wg + u) * EX_COLS + wave * EX_N;
+        if (col0 >= columns) return;
+        const int h = col0 / (2 * a.d), in_head = col0 - h * 2 * a.d;
+        const bool value = in_head >= a.d;
+        const bf16* W = reinterpret_cast<const bf16*>(a.w_kv) + (size_t)(col0 + col) * R + grp * 8;
+        f32x4 acc[8][4];  // [16 keys][16 columns]
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+        for (int i = 0; i < 8; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[i][j] = zero4();
-    load(0, 0);
-    const int steps = R / EX_K;
-    for (int k = 0; k < steps; k++) {
-        const char* at = lds[k & 1];
-        lds_loads_done();
-        lds_barrier();
-        if (k + 1 < steps) load(k + 1, (k + 1) & 1);
+            for (int j = 0; j < 4; j++) acc[i][j] = zero4();
+        bf16x8 w[2][4];
 #pragma unroll
-        for (int s = 0; s < EX_K / 32; s++) {
-            bf16x8 x[4], w[4];
+        for (int j = 0; j < 4; j++) w[0][j] = Mma<bf16>::load(W + (size_t)j * 16 * R);
+        auto product = [&](auto first) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                x[i] = *reinterpret_cast<const bf16x8*>(
-                    at + row128(wm * 64 + i * 16 + col, s * 4 + grp));
-                w[i] = *reinterpret_cast<const bf16x8*>(
-                    at + EX_M * 128 + row128(wn * 64 + i * 16 + col, s * 4 + grp));
-            }
-            if (value) {
+            for (int k = 0; k < R / 32; k++) {
+                if (k + 1 < R / 32) {
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++) acc[i][j] = Mma<bf16>::mma(x[i], w[j], acc[i][j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++) acc[i][j] = Mma<bf16>::mma(w[j], x[i], acc[i][j]);
-            }
-        }
-    }
-    const int t = t0 + wm;
-    if (t >= used) return;
-    const size_t head_tile = (size_t)h * a.key_tiles + t;
-    if (value) {
-        bf16* out = reinterpret_cast<bf16*>(a.vt) + head_tile * a.d * LP_KB;
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                float y[4];
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int key = i * 16 + grp * 4 + e;
-                    y[e] = slot_of[wm * 64 + key] >> 31 ? 0.f : acc[i][j][e];
+                    for (int j = 0; j < 4; j++)
+                        w[(k + 1) & 1][j] = Mma<bf16>::load(W + (size_t)j * 16 * R + (k + 1) * 32);
                 }
-                // keys 4 g .. 4 g + 3 of a 16: the middle two groups change places
-                const int pos = i * 16 + ((grp & 1) << 3) + ((grp >> 1) << 2);
-                store4<bf16>(out + (size_t)(in_head - a.d + j * 16 + col) * LP_KB + pos, y);
+                // two bases, within an LDS instruction's immediate offset of 64 KiB each (formed
+                // anew in each step: as constants they would all be kept in registers)
+                uint32_t base[2] = {x_at ^ (k & 3) << 6, (x_at + 64 * ROW) ^ (k & 3) << 6};
+                asm volatile("" : "+v"(base[0]), "+v"(base[1]));
+                bf16x8 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++)  // (16 rows on, the pieces are turned alike)
+                    x[i] = lds_get<bf16x8>(base[i >> 2] + (k >> 2) * 256 + (i & 3) * 16 * ROW);
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        acc[i][j] = decltype(first)::value
+                            ? Mma<bf16>::mma(x[i], w[k & 1][j], acc[i][j])
+                            : Mma<bf16>::mma(w[k & 1][j], x[i], acc[i][j]);
             }
-    } else {
-        bf16* out = reinterpret_cast<bf16*>(a.k) + head_tile * LP_KB * a.d;
+        };
+        if (value) product(std::true_type());
+        else product(std::false_type());
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int key = i * 16 + col;
-            const bool absent = slot_of[wm * 64 + key] >> 31;
+        for (int half = 0; half < 2; half++) {
+            if (t0 + half >= used) break;
+            const size_t head_tile = (size_t)h * a.key_tiles + t0 + half;
+            if (value) {
+                bf16* out = reinterpret_cast<bf16*>(a.vt) + head_tile * a.d * LP_KB;
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                float y[4];
+                for (int i = 0; i < 4; i++) {
+                    bool absent[4];
 #pragma unroll
-                for (int e = 0; e < 4; e++) y[e] = absent ? 0.f : acc[i][j][e];
-                store4<bf16>(out + (size_t)key * a.d + in_head + j * 16 + grp * 4, y);
+                    for (int e = 0; e < 4; e++)
+                        absent[e] = slot_of[half * LP_KB + i * 16 + grp * 4 + e] >> 31;
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        float y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e++) y[e] = absent[e] ? 0.f : acc[half * 4 + i][j][e];
+                        store4<bf16>(out + (size_t)(in_head - a.d + j * 16 + col) * LP_KB + i * 16 +
+                                         pos, y);
+                    }
+                }
+            } else {
+                bf16* out = reinterpret_cast<bf16*>(a.k) + head_tile * LP_KB * a.d;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int key = i * 16 + col;
+                    const bool absent = slot_of[half * LP_KB + key] >> 31;
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        float y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e++) y[e] = absent ? 0.f : acc[half * 4 + i][j][e];
+                        store4<bf16>(out + (size_t)key * a.d + in_head + j * 16 + grp * 4, y);
+                    }
+                }
             }
         }
     }
@@ -548,9 +570,16 @@ hipError_t launch_latent_prefill(const LatentPrefillArgs& a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.q_tiles == 0) return e;
     if (a.key_tiles > 0) {
-        const unsigned columns = (unsigned)(a.H * 2 * a.d / EX_N);  // d 64 or 128: whole tiles
-        hipLaunchKernelGGL(latent_expand_kernel, dim3((unsigned)(a.key_tiles + 1) / 2, columns),
-                           block, 0, s, a);
+        // whole passes over the columns: as few workgroups as still fill the chip twice
+        const int blocks = (a.key_tiles + 1) / 2;
+        const int units = (a.H * 2 * a.d + EX_COLS - 1) / EX_COLS;
+        int per = (int)((int64_t)blocks * units / (2 * device_cu_count()));
+        per = per < 1 ? 1 : per > units ? units : per;
+        const dim3 expand((unsigned)blocks, (unsigned)((units + per - 1) / per));
+        if (a.rank == 512)
+            hipLaunchKernelGGL(latent_expand_kernel<512>, expand, dim3(EX_THREADS), 0, s, a, per);
+        else
+            hipLaunchKernelGGL(latent_expand_kernel<256>, expand, dim3(EX_THREADS), 0, s, a, per);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
