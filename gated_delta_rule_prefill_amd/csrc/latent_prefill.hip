@@ -144,19 +144,21 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
     }
     __syncthreads();
     {
-        // 16 rows per wave; piece c of row r lies at piece c ^ (r & 15)
+        // 16 rows per wave; piece c of row r lies at piece c ^ ((r & 7) | (r >> 4 & 1) << 3), which
+        // takes 16 values over the rows that a fragment's lanes read (below)
+        const int odd = (wave & 1) << 3;
         const uint32_t mine = slot_of[wave * 16 + (lane & 15)] & 0x7fffffffu;
         const uint32_t at = lds_offset(lat) + wave * 16 * ROW;
         if constexpr (PIECES == 64) {
 #pragma unroll
             for (int r = 0; r < 16; r++)
                 load_to_lds(cache + __builtin_amdgcn_readlane(mine, r) * CACHE_ROW,
-                            (uint32_t)((lane ^ r) << 4), at + r * ROW);
+                            (uint32_t)((lane ^ (r & 7) ^ odd) << 4), at + r * ROW);
         } else {  // two rows per load
 #pragma unroll
             for (int r = 0; r < 16; r += 2) {
                 const int rr = r + (lane >> 5);
-                load_to_lds(cache + __shfl(mine, rr, WAVE) * CACHE_ROW + (((lane & 31) ^ rr) << 4),
+                load_to_lds(cache + __shfl(mine, rr, WAVE) * CACHE_ROW + (((lane & 31) ^ (rr & 7) ^ odd) << 4),
                             at + r * ROW);
             }
         }
@@ -180,46 +182,66 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
     lds_barrier();
     const int col = lane & 15, grp = lane >> 4;
     const int columns = a.H * 2 * a.d;
-    // keys 4 g .. 4 g + 3 of a 16: the middle two groups change places in the values' order
-    const int pos = ((grp & 1) << 3) + ((grp >> 1) << 2);
-    const uint32_t x_at = lds_offset(lat) + col * ROW + ((grp ^ col) << 4);
+    // Which rows make up a fragment is free, and chosen so that two fragments give a lane 8
+    // neighbours in memory, one 16-byte store. Keys: lane c of fragments i = 2 p + e reads row
+    // 32 p + 16 (c >> 3) + 8 e + (c & 7); with the values' key order (keys 4 h + (0..3) and
+    // 8 + 4 h + (0..3) of each 16 make up its half h) lane group g then holds places
+    // 32 p + 8 g + 4 e + (0..3). Dims of a key: rows 32 p + 8 (c >> 2) + 4 e + (c & 3) of w_kv.
+    const uint32_t x_at = lds_offset(lat) + (16 * (col >> 3) + (col & 7)) * ROW + ((grp ^ col) << 4);
     for (int u = 0; u < units_per_wg; u++) {
         const int col0 = ((int)blockIdx.y * units_per_wg + u) * EX_COLS + wave * EX_N;
         if (col0 >= columns) return;
         const int h = col0 / (2 * a.d), in_head = col0 - h * 2 * a.d;
         const bool value = in_head >= a.d;
-        const bf16* W = reinterpret_cast<const bf16*>(a.w_kv) + (size_t)(col0 + col) * R + grp * 8;
-        f32x4 acc[8][4];  // [16 keys][16 columns]
+        const bf16* W = reinterpret_cast<const bf16*>(a.w_kv) + (size_t)col0 * R + grp * 8;
+        const bf16* w_row[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            w_row[j] = W + (size_t)(value ? j * 16 + col
+                                          : (j >> 1) * 32 + (col >> 2) * 8 + (j & 1) * 4 + (col & 3)) * R;
+        f32x4 acc[8][4];  // [key fragment][weight fragment]
 #pragma unroll
         for (int i = 0; i < 8; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++) acc[i][j] = zero4();
-        bf16x8 w[2][4];
+        constexpr int AHEAD = 2;  // contraction steps that the weights are read ahead
+        bf16x8 w[AHEAD + 1][4];
+        auto load_w = [&](int k) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) w[0][j] = Mma<bf16>::load(W + (size_t)j * 16 * R);
+            for (int j = 0; j < 4; j++) w[k % (AHEAD + 1)][j] = Mma<bf16>::load(w_row[j] + k * 32);
+        };
+#pragma unroll
+        for (int k = 0; k < AHEAD; k++) load_w(k);
         auto product = [&](auto first) {
-#pragma unroll
-            for (int k = 0; k < R / 32; k++) {
-                if (k + 1 < R / 32) {
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        w[(k + 1) & 1][j] = Mma<bf16>::load(W + (size_t)j * 16 * R + (k + 1) * 32);
+            // the fragment's base in a contraction step, within an LDS instruction's immediate
+            // offset of 64 KiB (formed anew in each step: as constants the compiler would keep
+            // them all in registers)
+            uint32_t base[2];
+            bf16x8 x[3];
+            auto load_x = [&](int n) {
+                const int k = n >> 3, i = n & 7;
+                if (i == 0) {
+                    base[0] = x_at ^ (k & 3) << 6;
+                    base[1] = (x_at + 64 * ROW) ^ (k & 3) << 6;
+                    asm volatile("" : "+v"(base[0]), "+v"(base[1]));
                 }
-                // two bases, within an LDS instruction's immediate offset of 64 KiB each (formed
-                // anew in each step: as constants they would all be kept in registers)
-                uint32_t base[2] = {x_at ^ (k & 3) << 6, (x_at + 64 * ROW) ^ (k & 3) << 6};
-                asm volatile("" : "+v"(base[0]), "+v"(base[1]));
-                bf16x8 x[8];
+                x[n % 3] = lds_get<bf16x8>(base[i >> 2] + (k >> 2) * 256 +
+                                           ((i >> 1 & 1) * 32 + (i & 1) * 8) * ROW);
+            };
+            constexpr int N = R / 32 * 8;
+            load_x(0);
+            load_x(1);
 #pragma unroll
-                for (int i = 0; i < 8; i++)  // (16 rows on, the pieces are turned alike)
-                    x[i] = lds_get<bf16x8>(base[i >> 2] + (k >> 2) * 256 + (i & 3) * 16 * ROW);
+            for (int n = 0; n < N; n++) {
+                const int k = n >> 3, i = n & 7;
+                if (i == 0 && k + AHEAD < R / 32) load_w(k + AHEAD);
+                if (n + 2 < N) load_x(n + 2);
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        acc[i][j] = decltype(first)::value
-                            ? Mma<bf16>::mma(x[i], w[k & 1][j], acc[i][j])
-                            : Mma<bf16>::mma(w[k & 1][j], x[i], acc[i][j]);
+                for (int j = 0; j < 4; j++)
+                    acc[i][j] = decltype(first)::value
+                        ? Mma<bf16>::mma(x[n % 3], w[k % (AHEAD + 1)][j], acc[i][j])
+                        : Mma<bf16>::mma(w[k % (AHEAD + 1)][j], x[n % 3], acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
         if (value) product(std::true_type());
@@ -231,32 +253,36 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
             if (value) {
                 bf16* out = reinterpret_cast<bf16*>(a.vt) + head_tile * a.d * LP_KB;
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    bool absent[4];
+                for (int p = 0; p < 2; p++) {
+                    // the lane's 8 keys: 32 p + 16 (g >> 1) + 4 (g & 1) + 8 e + (0..3)
+                    const int key = half * LP_KB + p * 32 + (grp >> 1) * 16 + (grp & 1) * 4;
+                    bool absent[8];
 #pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        absent[e] = slot_of[half * LP_KB + i * 16 + grp * 4 + e] >> 31;
+                    for (int x = 0; x < 8; x++)
+                        absent[x] = slot_of[key + (x >> 2) * 8 + (x & 3)] >> 31;
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        float y[4];
+                        float y[8];
 #pragma unroll
-                        for (int e = 0; e < 4; e++) y[e] = absent[e] ? 0.f : acc[half * 4 + i][j][e];
-                        store4<bf16>(out + (size_t)(in_head - a.d + j * 16 + col) * LP_KB + i * 16 +
-                                         pos, y);
+                        for (int x = 0; x < 8; x++)
+                            y[x] = absent[x] ? 0.f : acc[half * 4 + 2 * p + (x >> 2)][j][x & 3];
+                        store8<bf16>(out + (size_t)(in_head - a.d + j * 16 + col) * LP_KB + p * 32 +
+                                         grp * 8, y);
                     }
                 }
             } else {
                 bf16* out = reinterpret_cast<bf16*>(a.k) + head_tile * LP_KB * a.d;
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const int key = i * 16 + col;
+                    const int key = (i >> 1) * 32 + 16 * (col >> 3) + (i & 1) * 8 + (col & 7);
                     const bool absent = slot_of[half * LP_KB + key] >> 31;
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        float y[4];
+                    for (int p = 0; p < 2; p++) {
+                        float y[8];
 #pragma unroll
-                        for (int e = 0; e < 4; e++) y[e] = absent ? 0.f : acc[half * 4 + i][j][e];
-                        store4<bf16>(out + (size_t)key * a.d + in_head + j * 16 + grp * 4, y);
+                        for (int x = 0; x < 8; x++)
+                            y[x] = absent ? 0.f : acc[half * 4 + i][2 * p + (x >> 2)][x & 3];
+                        store8<bf16>(out + (size_t)key * a.d + in_head + p * 32 + grp * 8, y);
                     }
                 }
             }
