@@ -103,7 +103,7 @@ __global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeA
 // A workgroup holds one row tile (16 RH query rows) and walks 64 keys at a time:
 //   S^T = K Q^T   each wave takes 16 KS of the keys for 16 of the rows; the queries stay in
 //                 registers, K fragments come from LDS;
-//   softmax       the row maximum goes over the waves through LDS, weights go back as bf16;
+//   softmax       weights go to LDS as bf16; the waves of a row share its running reference;
 //   U^T += C^T P^T  each wave takes its share of the rank for all rows; C^T by transposing LDS
 //                 reads of the very tile the scores came from.
 // So each cache row is read once from memory per row tile; from LDS a tile is read RH times as
@@ -158,7 +158,8 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
     __shared__ __align__(1024) char tile[2 * X::BYTES];
     __shared__ __align__(1024) char wt[ROWS * LD_KB * 2];
     __shared__ float tops[Y::GROUPS][ROWS];  // row maxima of a tile per key group; then row sums
-    __shared__ float shrinks[ROWS];          // what a tile's new maxima scale older sums by
+    __shared__ float shrinks[ROWS];          // what a new reference scales older sums by
+    __shared__ int flags[WAVES];             // a wave's rows have outgrown their reference
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int col = lane & 15, grp = lane >> 4;
     const int kg = wave / RH, part = wave % RH;  // key group and 16-row part of the scores
@@ -181,7 +182,9 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
         }
         if (!a.join.per_unit && threadIdx.x == 0) join_none(a.join, me.worker);
     }
-    const float cs = a.scale * LOG2E;
+    // The scale enters the exponent's multiplication; a negative one is moved into the queries,
+    // so that the largest score is the largest weight (and zero makes the queries zero).
+    const float cs = a.scale == 0.f ? 1.f : fabsf(a.scale) * LOG2E;
     const char* cache = reinterpret_cast<const char*>(a.cache);
 
     // LDS byte offsets of this lane's reads and writes within a tile or the weights. A piece
@@ -269,9 +272,15 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
                 q[f] = Mma<bf16>::load(f < NL ? ql + f * 32 + grp * 8
                                               : qp + (f - NL) * 32 + grp * 8);
         }
+        if (a.scale <= 0.f) {
+#pragma unroll
+            for (int f = 0; f < NF; f++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) q[f][i] = a.scale < 0.f ? -q[f][i] : (bf16)0.f;
+        }
         arrived(q);
         f32x4 acc[RH][NT];
-        float m = -INFINITY, l = 0.f;  // this lane's row: running maximum, share of the sum
+        float ref = -INFINITY, l = 0.f;  // this lane's row: reference, share of the sum
 #pragma unroll
         for (int t = 0; t < RH; t++)
 #pragma unroll
@@ -340,48 +349,49 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         const bool keep = ((here >> (x * 16 + i)) & 1) && x * 16 + i < left;
-                        s[x][i] = keep ? s[x][i] * cs : -INFINITY;
+                        s[x][i] = keep ? s[x][i] : -INFINITY;
                     }
-            } else {
-#pragma unroll
-                for (int x = 0; x < KS; x++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) s[x][i] *= cs;
             }
             float top = s[0][0];
 #pragma unroll
             for (int x = 0; x < KS; x++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) top = fmaxf(top, s[x][i]);
-            top = fmaxf(top, __shfl_xor(top, 16, WAVE));
-            top = fmaxf(top, __shfl_xor(top, 32, WAVE));
-            if (grp == 0) tops[kg][part * 16 + col] = top;
-            lds_barrier();
-            float m1 = m;
+            top = max_groups(top) * cs;
+            float p[KS][4];
+            auto weigh = [&]() {
+                const float shift = ref == -INFINITY ? 0.f : ref;  // a row with no key so far
 #pragma unroll
-            for (int g = 0; g < Y::GROUPS; g++) m1 = fmaxf(m1, tops[g][part * 16 + col]);
-            const float ref = m1 == -INFINITY ? 0.f : m1;  // a row with no key so far
-            const float shrink = __builtin_amdgcn_exp2f(m - ref);
-            // (the exponential is 1 when the maximum stays; a row still without a key has sums
-            // of zero, which its exp2(-inf - 0) = 0 leaves)
-            l *= shrink;
-            if (kg == 0 && grp == 0) shrinks[part * 16 + col] = shrink;
-            m = m1;
+                for (int x = 0; x < KS; x++) {
 #pragma unroll
-            for (int x = 0; x < KS; x++) {
-                float p[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    p[i] = __builtin_amdgcn_exp2f(s[x][i] - ref);
-                    l += p[i];
+                    for (int i = 0; i < 4; i++)
+                        p[x][i] = __builtin_amdgcn_exp2f(fmaf(s[x][i], cs, -shift));
+                    lds_put((weights(part) + put_here) ^ x << 5, bits4(p[x]));
                 }
-                lds_put((weights(part) + put_here) ^ x << 5, bits4(p));
-            }
+            };
+            // Weights by the reference so far. If a row's maximum has outgrown it in any wave (all
+            // see the flags behind the barrier), the waves of a row agree on a new reference and
+            // weigh again: a few tiles of a request, which saves the others a barrier.
+            weigh();
+            const int grew = __any(top > ref + LAG);
+            if (lane == 0) flags[wave] = grew;
             lds_barrier();
+            if (__any(flags[lane % WAVES])) {
+                if (grp == 0) tops[kg][part * 16 + col] = top;
+                lds_barrier();
+                float most = tops[0][part * 16 + col];
 #pragma unroll
-            for (int t = 0; t < RH; t++) {
-                const float f = shrinks[t * 16 + col];
-                if (__any(f != 1.f)) {
+                for (int g = 1; g < Y::GROUPS; g++) most = fmaxf(most, tops[g][part * 16 + col]);
+                const bool grown = most > ref + LAG;
+                const float shrink = grown ? __builtin_amdgcn_exp2f(ref - most) : 1.f;
+                ref = grown ? most : ref;
+                l *= shrink;
+                if (kg == 0 && grp == 0) shrinks[part * 16 + col] = shrink;
+                weigh();
+                lds_barrier();
+#pragma unroll
+                for (int t = 0; t < RH; t++) {
+                    const float f = shrinks[t * 16 + col];
 #pragma unroll
                     for (int j = 0; j < NT; j++)
 #pragma unroll
@@ -389,21 +399,37 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
                 }
             }
 #pragma unroll
-            for (int ks = 0; ks < LD_KB / 32; ks++) {
-                bf16x8 v[NT];
+            for (int x = 0; x < KS; x++)
 #pragma unroll
-                for (int j = 0; j < NT; j++) {
+                for (int i = 0; i < 4; i++) l += p[x][i];
+            // values four fragments at a time, the next four on their way
+            constexpr int VB = NT < 4 ? NT : 4, NB = LD_KB / 32 * (NT / VB);
+            bf16x8 v[2][VB];
+            auto load_v = [&](int n) {
+                const int ks = n / (NT / VB), j0 = n % (NT / VB) * VB;
+#pragma unroll
+                for (int j = 0; j < VB; j++) {
                     // the second half lies 4 rows on, where the lowest piece bit is turned
-                    const uint32_t at = v_here ^ j << 5;
-                    v[j] = join(lds_read_tr(at + ks * (32 * X::LAT)),
-                                lds_read_tr((at ^ 16) + ks * (32 * X::LAT) + 4 * X::LAT));
+                    const uint32_t at = v_here ^ (j0 + j) << 5;
+                    v[n & 1][j] = join(lds_read_tr(at + ks * (32 * X::LAT)),
+                                       lds_read_tr((at ^ 16) + ks * (32 * X::LAT) + 4 * X::LAT));
                 }
+            };
+            load_v(0);
 #pragma unroll
-                for (int t = 0; t < RH; t++) {
-                    const bf16x8 p = lds_get<bf16x8>((weights(t) + p_here) ^ ks << 6);
+            for (int n = 0; n < NB; n++) {
+                const int ks = n / (NT / VB), j0 = n % (NT / VB) * VB;
+                bf16x8 w[RH];
 #pragma unroll
-                    for (int j = 0; j < NT; j++) acc[t][j] = Mma<bf16>::mma(v[j], p, acc[t][j]);
-                }
+                for (int t = 0; t < RH; t++)
+                    w[t] = lds_get<bf16x8>((weights(t) + p_here) ^ ks << 6);
+                if (n + 1 < NB) load_v(n + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int t = 0; t < RH; t++)
+#pragma unroll
+                    for (int j = 0; j < VB; j++)
+                        acc[t][j0 + j] = Mma<bf16>::mma(v[n & 1][j], w[t], acc[t][j0 + j]);
             }
         }
 
@@ -440,7 +466,7 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
             }
         }
         if (!whole && kg == 0 && grp == 0 && live)
-            a.join.part_ml[(part_row + part * 16 + col) * 2] = m;
+            a.join.part_ml[(part_row + part * 16 + col) * 2] = ref;
         lds_barrier();  // the next unit writes tops and the tiles
 
         run.pos += c1 - c0;

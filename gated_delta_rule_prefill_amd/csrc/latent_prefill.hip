@@ -193,12 +193,13 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
         if (col0 >= columns) return;
         const int h = col0 / (2 * a.d), in_head = col0 - h * 2 * a.d;
         const bool value = in_head >= a.d;
-        const bf16* W = reinterpret_cast<const bf16*>(a.w_kv) + (size_t)col0 * R + grp * 8;
-        const bf16* w_row[4];
+        const char* W = reinterpret_cast<const char*>(a.w_kv) + (size_t)col0 * ROW;
+        uint32_t w_at[4];
 #pragma unroll
         for (int j = 0; j < 4; j++)
-            w_row[j] = W + (size_t)(value ? j * 16 + col
-                                          : (j >> 1) * 32 + (col >> 2) * 8 + (j & 1) * 4 + (col & 3)) * R;
+            w_at[j] = (value ? j * 16 + col
+                             : (j >> 1) * 32 + (col >> 2) * 8 + (j & 1) * 4 + (col & 3)) * ROW +
+                      grp * 16;
         f32x4 acc[8][4];  // [key fragment][weight fragment]
 #pragma unroll
         for (int i = 0; i < 8; i++)
@@ -208,7 +209,9 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
         bf16x8 w[AHEAD + 1][4];
         auto load_w = [&](int k) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) w[k % (AHEAD + 1)][j] = Mma<bf16>::load(w_row[j] + k * 32);
+            for (int j = 0; j < 4; j++)
+                w[k % (AHEAD + 1)][j] =
+                    *reinterpret_cast<const bf16x8*>(W + k * 64 + (size_t)w_at[j]);
         };
 #pragma unroll
         for (int k = 0; k < AHEAD; k++) load_w(k);
@@ -403,12 +406,7 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
     for (int j = 0; j < NO; j++)
 #pragma unroll
         for (int i = 0; i < 16; i++) acc[j][i] = 0.f;
-    // The exponents' reference (scaled) and the sum. The reference follows the maximum only once
-    // that is more than 2^LAG above it: weights then reach 2^LAG, which neither fp32 sums nor
-    // bf16 weights mind, and the outputs are rescaled a few times in all instead of at every
-    // tile in which one of 32 rows finds a new maximum.
-    constexpr float LAG = 8.f;
-    float ref = -INFINITY, l = 0.f;
+    float ref = -INFINITY, l = 0.f;  // the exponents' reference (scaled); the sum
 
     // Scores of tile t, unscaled, and beside each pair of MFMAs a slice of other work: the
     // matrix pipe takes 32 cycles for one MFMA, in which the wave can issue eight vector

@@ -11,6 +11,12 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
 
+// A running softmax's exponents are taken against a reference that follows the maximum only once
+// that is more than LAG above it (powers of two). Weights then reach 2^LAG, which neither fp32
+// sums nor bf16 weights mind, and sums and outputs are rescaled a few times in all instead of at
+// every step in which one of a wave's rows finds a new maximum.
+constexpr float LAG = 8.f;
+
 // LDS by 32-bit byte offset: the compiler otherwise carries some addresses as 64-bit generic
 // pointers, two registers each.
 typedef __attribute__((address_space(3))) char lds_char;
@@ -76,6 +82,15 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
     return r;
 }
 
+// Maximum over the four lanes that are equal modulo 16, in the vector pipe.
+__device__ __forceinline__ float max_groups(float x) {
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    uint32_t b = __float_as_uint(x);
+    u32x2 r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    b = __float_as_uint(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+    r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 // Maximum over a lane and its partner 32 lanes on, in the vector pipe: the exchange leaves the
 // lower halves in one register and the upper halves in the other.
 __device__ __forceinline__ float max_halves(float x) {

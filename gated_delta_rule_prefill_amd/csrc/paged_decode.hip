@@ -303,19 +303,18 @@ __global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void pag
                 for (int t = 0; t < NSUB; t++)
 #pragma unroll
                     for (int i = 0; i < 4; i++) top = fmaxf(top, s[rt][t][i]);
-                top = fmaxf(top, __shfl_xor(top, 16, WAVE));
-                top = fmaxf(top, __shfl_xor(top, 32, WAVE));
-                const float m1 = fmaxf(m[rt], top);
-                const float ref = m1 == -INFINITY ? 0.f : m1;  // a row with no key so far
-                if (__any(m1 > m[rt])) {
-                    const float shrink = __builtin_amdgcn_exp2f(m[rt] - ref);
+                top = max_groups(top);
+                const bool grown = top > m[rt] + LAG;
+                if (__any(grown)) {
+                    const float shrink = grown ? __builtin_amdgcn_exp2f(m[rt] - top) : 1.f;
                     l[rt] *= shrink;
 #pragma unroll
                     for (int j = 0; j < D / 16; j++)
 #pragma unroll
                         for (int i = 0; i < 4; i++) acc[rt][j][i] *= shrink;
-                    m[rt] = m1;
+                    m[rt] = grown ? top : m[rt];
                 }
+                const float ref = m[rt] == -INFINITY ? 0.f : m[rt];  // a row with no key so far
 #pragma unroll
                 for (int t = 0; t < NSUB; t++)
 #pragma unroll
