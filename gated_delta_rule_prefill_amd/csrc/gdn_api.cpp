@@ -360,9 +360,10 @@ int check_table(int32_t max_blocks, int32_t block_size) {
     return GDN_OK;
 }
 
-// The split of a decode call counts its key chunks (64 keys at least) in 32 bits.
+// The split of a decode call counts its key chunks (64 keys at least, and SPLIT_EXTRA for a head
+// group of a request) in 32 bits.
 int check_chunks(int32_t batch, int32_t units, int32_t max_blocks, int32_t block_size) {
-    const int64_t chunks = ((int64_t)max_blocks * block_size + 63) / 64;
+    const int64_t chunks = ((int64_t)max_blocks * block_size + 63) / 64 + gdn::SPLIT_EXTRA;
     if (chunks * units > 0x3fffffffll / (batch > 0 ? batch : 1))
         return fail(GDN_ERR_UNSUPPORTED, "batch x heads x table row are too many key chunks (%d x "
                                          "%d x %lld): split the batch", batch, units,

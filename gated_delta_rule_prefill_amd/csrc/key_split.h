@@ -11,6 +11,10 @@
 // worker and the rest have nothing to do, so every worker between the first and the last of a
 // unit holds a part of it.
 //
+// Starting and ending a unit (queries, first keys, results) takes as long as some chunks do, and
+// a run of many short units would be the last to end: each unit is followed by `extra` chunks
+// that exist for the cut only.
+//
 // Query rows beyond one row tile: a worker is then one workgroup per row tile, side by side on
 // the same XCD at the same time, so that the tiles after the first find the keys in its L2.
 #pragma once
@@ -37,15 +41,19 @@ struct SplitShape {
     int batch;
     int units;      // head groups of a request
     int max_keys;   // keys a table row can address
+    int extra;      // chunks that a unit counts for beyond its own, at most SPLIT_EXTRA
 };
+constexpr int SPLIT_EXTRA = 6;
 
 // Keys of request b that the table can address.
 __device__ __forceinline__ int split_keys(const SplitShape& s, int b) {
     return min(max(s.seq_lens[b], 0), s.max_keys);
 }
+// Chunks of a unit of request b in the cut: its own and the extra ones (none without keys).
 template <int KB>
 __device__ __forceinline__ int split_chunks(const SplitShape& s, int b) {
-    return (split_keys(s, b) + KB - 1) / KB;
+    const int n = (split_keys(s, b) + KB - 1) / KB;
+    return n > 0 ? n + s.extra : 0;
 }
 
 // Which worker and row tile a workgroup is. Workgroups are dealt to the 8 XCDs in turn; n is a
@@ -80,10 +88,20 @@ struct SplitCut {
 // Workgroup-uniform values moved to scalar registers.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 // A worker's run of chunks [pos, end), and the request that chunk `pos` lies in, whose first
-// chunk is `base`. All threads of the workgroup call it.
+// chunk is `base`. `pos` may be one of a unit's extra chunks. All threads of the workgroup call
+// it.
 struct SplitRun {
     int pos, end, base, b;
     SplitCut cut;
+    // On to chunk `to`; behind the request's last the next request with keys follows.
+    __device__ __forceinline__ void advance(const SplitShape& s, int to, int request_end) {
+        pos = to;
+        if (pos < end && pos == request_end) {
+            base = pos;
+            do b++;
+            while (b + 1 < s.batch && uniform(split_keys(s, b)) == 0);
+        }
+    }
 };
 template <int KB, int THREADS>
 __device__ SplitRun split_run(const SplitShape& s, int w, int workers) {

@@ -164,8 +164,15 @@ __global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void pag
         const int b = run.b;
         const int nkeys = uniform(split_keys(a.split, b));
         const int nch = (nkeys + KB - 1) / KB;
-        const int kvh = (run.pos - run.base) / nch;
-        const int c0 = run.pos - run.base - kvh * nch;
+        const int per_unit = nch + a.split.extra;
+        const int kvh = (run.pos - run.base) / per_unit;
+        const int c0 = run.pos - run.base - kvh * per_unit;
+        const int next_unit = run.base + (kvh + 1) * per_unit;
+        const int request_end = run.base + a.split.units * per_unit;
+        if (c0 >= nch) {  // the run starts behind the unit's own chunks
+            run.advance(a.split, next_unit, request_end);
+            continue;
+        }
         const int c1 = min(nch, c0 + (run.end - run.pos));
         const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
         const int seen0 = uniform(a.split.seq_lens[b]) - a.n_pos + 1;  // keys that position 0 sees
@@ -393,12 +400,7 @@ __global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void pag
         }
         __syncthreads();  // the merge rows are the next unit's V tiles
 
-        run.pos += c1 - c0;
-        if (run.pos < run.end && run.pos == run.base + nch * a.split.units) {
-            run.base = run.pos;
-            do run.b++;
-            while (run.b + 1 < a.split.batch && uniform(split_keys(a.split, run.b)) == 0);
-        }
+        run.advance(a.split, c1 == nch ? next_unit : run.pos + c1 - c0, request_end);
     }
 }
 
@@ -459,6 +461,8 @@ size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
     a->rt = tiles >= 4 && most >= 4 ? 4 : tiles >= 2 && most >= 2 ? 2 : 1;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
     a->split.units = a->kv_heads;
+    // (128 requests of 30 to 30000 tokens, 4 KV heads: 204 us a call with 0, 201 with 1, 200 with 2)
+    a->split.extra = 2;
     const int cus = device_cu_count();
     a->workers = split_workers(2 * cus, a->row_tiles);
     JoinShape& j = a->join;

@@ -495,8 +495,8 @@ typedef struct {
     float scale;
 } gdn_paged_dims_t;
 
-/* In one decode call batch x num_kv_heads x ceil(max_blocks x block_size / 64) stays below
- * 2^30 (GDN_ERR_UNSUPPORTED otherwise; latent decode: batch x ceil(..)). */
+/* In one decode call batch x num_kv_heads x (ceil(max_blocks x block_size / 64) + 6) stays below
+ * 2^30 (GDN_ERR_UNSUPPORTED otherwise; latent decode: batch x (ceil(..) + 6)). */
 
 /* Workspace of gdn_paged_decode for the current device (host computation). It does not depend
  * on the lengths. */
