@@ -84,6 +84,7 @@ struct LatentPrefillArgs {
     int key_tiles, q_tiles;  // bounds from the host's totals
     void* o;
     int32_t* key_tile;   // [n_seqs + 1] first key tile of each request
+    int2* order;         // [q_tiles] (request, query tile) in the order of their start
     int32_t* q_tile;     // [n_seqs + 1] first query tile
     uint64_t* exist;     // [key_tiles] a bit per key
     void* k_pe;          // [key_tiles][64][64] rotary keys
