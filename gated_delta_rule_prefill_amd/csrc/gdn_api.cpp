@@ -60,6 +60,14 @@ int check_dims(const gdn_dims_t* d) {
         if (!aligned16(p)) return fail(GDN_ERR_ALIGN, "%s is not 16-byte aligned", #p); \
     } while (0)
 
+// Lists that kernels read one entry at a time, so that a part of a longer one will do.
+#define REQUIRE_LIST(p)                                                        \
+    do {                                                                       \
+        if ((p) == nullptr) return fail(GDN_ERR_NULL, "%s is NULL", #p);       \
+        if (reinterpret_cast<uintptr_t>(p) % sizeof(*(p)) != 0)                \
+            return fail(GDN_ERR_ALIGN, "%s is not aligned to its entries", #p); \
+    } while (0)
+
 #define OPT_PTR(p)                                                                   \
     do {                                                                             \
         if ((p) != nullptr && !aligned16(p))                                         \
@@ -447,6 +455,16 @@ int check_latent_rows(const gdn_latent_dims_t* d, int64_t tokens) {
     return GDN_OK;
 }
 
+// A decode call's projections have a workgroup row per 32 (request, position) rows.
+int check_latent_batch(const gdn_latent_dims_t* d, int32_t batch, int32_t n_pos) {
+    const int st = check_batch(batch, n_pos);
+    if (st) return st;
+    if ((int64_t)batch * n_pos > (1 << 20))
+        return fail(GDN_ERR_UNSUPPORTED, "batch x n_pos must be <= 2^20 (got %d x %d): split the "
+                                         "batch", batch, n_pos);
+    return check_latent_rows(d, (int64_t)batch * n_pos);
+}
+
 gdn::LatentDecodeArgs latent_decode_args(const gdn_latent_dims_t* d, int32_t batch,
                                          int32_t n_pos) {
     gdn::LatentDecodeArgs a = {};
@@ -797,8 +815,10 @@ int gdn_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t n,
         REQUIRE_PTR(new_lens);
         REQUIRE_PTR(seq_lens);
         if (max_blocks > 0) REQUIRE_PTR(block_table);
+        if (seq_lens == ctx_lens || seq_lens == new_lens)
+            return fail(GDN_ERR_SHAPE, "seq_lens must not be ctx_lens or new_lens");
     }
-    if (n_free > 0) REQUIRE_PTR(free_blocks);
+    if (n_free > 0) REQUIRE_LIST(free_blocks);
     REQUIRE_PTR(cu_seqlens);
     REQUIRE_PTR(counts);
     if (max_tokens > 0) {
@@ -837,7 +857,7 @@ int gdn_paged_append(int32_t dtype, const void* k, int64_t k_stride, const void*
     if (st || tokens == 0) return st ? st : ok();
     REQUIRE_PTR(k);
     REQUIRE_PTR(v);
-    REQUIRE_PTR(slot_map);
+    REQUIRE_LIST(slot_map);
     REQUIRE_PTR(k_cache);
     REQUIRE_PTR(v_cache);
     const int per = dtype == GDN_DTYPE_BF16 ? 8 : 4;
@@ -875,7 +895,7 @@ int gdn_latent_append(int32_t dtype, const void* c, int64_t c_stride, const void
     if (st || tokens == 0) return st ? st : ok();
     REQUIRE_PTR(c);
     REQUIRE_PTR(k_pe);
-    REQUIRE_PTR(slot_map);
+    REQUIRE_LIST(slot_map);
     REQUIRE_PTR(cache);
     const int per = dtype == GDN_DTYPE_BF16 ? 8 : 4;
     gdn::AppendArgs a;
@@ -945,8 +965,7 @@ int gdn_paged_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_
 int gdn_latent_decode_workspace_bytes(const gdn_latent_dims_t* dims, int32_t batch,
                                       int32_t n_pos, size_t* bytes) {
     int st = check_latent_dims(dims);
-    if (!st) st = check_batch(batch, n_pos);
-    if (!st) st = check_latent_rows(dims, (int64_t)batch * n_pos);
+    if (!st) st = check_latent_batch(dims, batch, n_pos);
     if (st) return st;
     if (bytes == nullptr) return fail(GDN_ERR_NULL, "bytes is NULL");
     gdn::LatentDecodeArgs a = latent_decode_args(dims, batch, n_pos);
@@ -960,8 +979,7 @@ int gdn_latent_decode(const gdn_latent_dims_t* dims, const void* q_nope, const v
                       int32_t batch, int32_t n_pos, void* o, void* workspace, size_t ws_bytes,
                       void* stream) {
     int st = check_latent_dims(dims);
-    if (!st) st = check_batch(batch, n_pos);
-    if (!st) st = check_latent_rows(dims, (int64_t)batch * n_pos);
+    if (!st) st = check_latent_batch(dims, batch, n_pos);
     if (!st) st = check_cache(dims->dtype, 1, n_blocks, block_size);
     if (!st) st = check_table(max_blocks, block_size);
     if (!st) st = check_chunks(batch, 1, max_blocks, block_size);

@@ -489,7 +489,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentDecodeA
 
 // -------------------------------------------------------------------------------------- up
 // o = W_uv u for one head and 32 (request, position) rows. u is taken as the sum of two bf16
-// numbers, its rounding and the rounding of what that leaves (2^-17 of it together): one more
+// numbers, its rounding and the rounding of what that leaves (which leaves 2^-16 of it): one more
 // MFMA each, in a kernel that waits for memory, for an output error that is a third smaller.
 // Everything is requested at once (the weights as the MFMA's A operand into registers, the rows
 // of u into LDS), so a workgroup pays one trip to memory.

@@ -472,13 +472,17 @@ def _space(workspace, need, like, stream, dev):
 
 
 def _new(shape, dtype, like, stream):
-    """A buffer on the tensors' GPU. On another stream than the current one it is marked as
-    used there, so that the allocator does not hand it out before that stream is done."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=like.device)
-        t.record_stream(stream)
+    """A buffer on the tensors' GPU. For a stream that is given it comes from that stream's
+    memory, which work queued on the current stream cannot still be using, and is marked as used
+    on the current stream too, where results are read as a rule."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    now = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(now)
     return t
 
 

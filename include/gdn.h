@@ -432,7 +432,7 @@ int gdn_conv1d_silu(const void* x, const float* w, const int32_t* cu_seqlens, in
  *   - block_size is any number >= 1; pages that are not a multiple of a kernel's key tile only
  *     cost their look-up.
  * Scores, softmax statistics, weighted sums are held in fp32; with bf16 inputs the softmax
- * weights are rounded to bf16 (relative 2^-9 each, not into the sum that divides them) as the
+ * weights are rounded to bf16 (by 2^-8 each at most, not in the sum that divides them) as the
  * MFMA's operand, outputs by round-to-nearest-even once. */
 
 /* Largest num_heads of the attention entry points. */
@@ -455,9 +455,11 @@ int gdn_conv1d_silu(const void* x, const float* w, const int32_t* cu_seqlens, in
  *              than n_free when it was too short; the first min of both were handed out)
  * If the new tokens exceed max_tokens, the tokens from max_tokens on get no slot, and pages
  * that start at one of them are not entered into the table; counts[0] tells.
- *   ctx_lens, new_lens [n] int32; free_blocks [n_free] int32 (device; not changed);
+ *   ctx_lens, new_lens [n] int32; free_blocks [n_free] int32 (device; not changed; may be the
+ *   rest of a longer list: 4-byte alignment will do);
  *   block_table [n, max_blocks] int32 (device), updated in place. n, max_blocks, n_free and
- *   max_tokens may be 0 (the arrays they size may then be NULL). */
+ *   max_tokens may be 0 (the arrays they size may then be NULL). Outputs do not overlap inputs:
+ *   every workgroup reads all lengths. */
 int gdn_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t n,
                    int32_t block_size, int32_t* block_table, int32_t max_blocks,
                    const int32_t* free_blocks, int32_t n_free, int32_t max_tokens,
@@ -467,8 +469,9 @@ int gdn_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t n,
 /* Writes the keys and values of new tokens into their cache slots.
  *   k, v       [tokens] rows of [kv_heads, d] dtype, k_stride / v_stride elements apart (so
  *              that they may be parts of a fused projection's output; a multiple of 16 bytes)
- *   slot_map   [tokens] int64 (device); a slot outside [0, n_blocks * block_size) skips the
- *              token. Valid slots must be distinct within one call (the debug library checks).
+ *   slot_map   [tokens] int64 (device; 8-byte alignment will do); a slot outside
+ *              [0, n_blocks * block_size) skips the token. Valid slots must be distinct within
+ *              one call (the debug library checks).
  *   k_cache, v_cache [n_blocks, kv_heads, block_size, d] dtype (device)
  *   d          64, 128 or 256 */
 int gdn_paged_append(int32_t dtype, const void* k, int64_t k_stride, const void* v,
@@ -496,7 +499,8 @@ typedef struct {
 } gdn_paged_dims_t;
 
 /* In one decode call batch x num_kv_heads x (ceil(max_blocks x block_size / 64) + 6) stays below
- * 2^30 (GDN_ERR_UNSUPPORTED otherwise; latent decode: batch x (ceil(..) + 6)). */
+ * 2^30 (GDN_ERR_UNSUPPORTED otherwise; latent decode: batch x (ceil(..) + 6), and batch x n_pos
+ * at most 2^20). */
 
 /* Workspace of gdn_paged_decode for the current device (host computation). It does not depend
  * on the lengths. */
@@ -551,8 +555,9 @@ int gdn_latent_decode_workspace_bytes(const gdn_latent_dims_t* dims, int32_t bat
  *   cache       [n_blocks, block_size, rank + d_rope]
  *   block_table [batch, max_blocks], seq_lens [batch] int32 (device);  n_pos 1 .. GDN_SPEC_MAX_POS
  *   o           [batch, n_pos, num_heads, d_v]
- * all bf16. W_uk^T q_nope and the softmax-weighted latents are rounded to bf16 as MFMA
- * operands. Workspace, determinism and the newest tokens' values as in gdn_paged_decode. */
+ * all bf16. W_uk^T q_nope is rounded to bf16 as an MFMA operand; the softmax-weighted latents
+ * enter theirs as the sum of two bf16 numbers. Workspace, determinism and the newest tokens'
+ * values as in gdn_paged_decode. */
 int gdn_latent_decode(const gdn_latent_dims_t* dims, const void* q_nope, const void* q_pe,
                       const void* w_kv, const void* cache, int32_t n_blocks, int32_t block_size,
                       const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
