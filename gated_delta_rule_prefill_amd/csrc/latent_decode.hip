@@ -75,27 +75,31 @@ __global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeA
         *reinterpret_cast<f32x4*>(w + ab_place(x >> 4, x & 15)) = in[i];
     }
     __syncthreads();
+    // Two MFMA rows tiles of 16 rank columns each, dealt out so that a lane's four rows of both
+    // are 8 consecutive columns (a transposing read takes any four columns per lane): 8 g + 4 x.
+    bf16x8 A[2][DN / 32];
 #pragma unroll
-    for (int x = 0; x < 2; x++) {  // 2 x 16 rank columns of this wave
-        bf16x8 A[DN / 32];
+    for (int x = 0; x < 2; x++)
 #pragma unroll
         for (int k = 0; k < DN / 32; k++) {
-            const int n = k * 32 + grp * 8 + ((lane >> 2) & 3);
-            const int c = (wave * 2 + x) * 2 + ((lane & 3) >> 1);
-            A[k] = join(lds_read_tr(w + ab_place(n, c) + (lane & 1) * 8),
-                        lds_read_tr(w + ab_place(n + 4, c) + (lane & 1) * 8));
+            const int n = k * 32 + grp * 8 + ((lane >> 2) & 3), c = wave * 4 + (lane & 3);
+            A[x][k] = join(lds_read_tr(w + ab_place(n, c) + x * 8),
+                           lds_read_tr(w + ab_place(n + 4, c) + x * 8));
         }
 #pragma unroll
-        for (int t = 0; t < AB_TILES; t++) {
-            const int row = row0 + t * 16 + col;
-            f32x4 d = zero4();
+    for (int t = 0; t < AB_TILES; t++) {
+        const int row = row0 + t * 16 + col;
+        f32x4 d[2];
 #pragma unroll
-            for (int k = 0; k < DN / 32; k++) d = Mma<bf16>::mma(A[k], B[t][k], d);
-            const float y[4] = {d[0], d[1], d[2], d[3]};
-            if (row < rows)
-                store4<bf16>(reinterpret_cast<bf16*>(a.q_lat) + ((size_t)row * a.H + h) * a.rank +
-                                 r0 + (wave * 2 + x) * 16 + grp * 4, y);
+        for (int x = 0; x < 2; x++) {
+            d[x] = zero4();
+#pragma unroll
+            for (int k = 0; k < DN / 32; k++) d[x] = Mma<bf16>::mma(A[x][k], B[t][k], d[x]);
         }
+        const float y[8] = {d[0][0], d[0][1], d[0][2], d[0][3], d[1][0], d[1][1], d[1][2], d[1][3]};
+        if (row < rows)
+            store8<bf16>(reinterpret_cast<bf16*>(a.q_lat) + ((size_t)row * a.H + h) * a.rank + r0 +
+                             wave * 32 + grp * 8, y);
     }
 }
 

@@ -421,6 +421,7 @@ def gdn_conv1d_silu(x, w, cu_seqlens, planes=1, y=None, stream=None):
 # These calls are short (a decode step's bookkeeping runs 4 us on the GPU), so the checks are
 # kept to a few attribute reads per tensor; a failed one works out its message afterwards.
 _raw_stream = torch._C._cuda_getCurrentRawStream  # handle of a device's current stream
+_current_device = torch._C._cuda_getDevice
 _I32, _I64, _BF16 = torch.int32, torch.int64, torch.bfloat16
 
 
@@ -500,7 +501,7 @@ def _run(name, dev, stream, *args):
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
