@@ -42,8 +42,10 @@ struct SplitShape {
     int units;      // head groups of a request
     int max_keys;   // keys a table row can address
     int extra;      // chunks that a unit counts for beyond its own, at most SPLIT_EXTRA
+    int halve;      // 1: half of the workers, where units have SPLIT_LONG chunks on average
 };
 constexpr int SPLIT_EXTRA = 6;
+constexpr int SPLIT_LONG = 8;  // (the extra ones among them)
 
 // Keys of request b that the table can address.
 __device__ __forceinline__ int split_keys(const SplitShape& s, int b) {
@@ -127,7 +129,8 @@ __device__ SplitRun split_run(const SplitShape& s, int w, int workers) {
         if (i < wave_id()) upto += wave_tot[i];
         total += wave_tot[i];
     }
-    const SplitCut cut = SplitCut::of(uniform(total), workers);
+    const bool fewer = s.halve && total / SPLIT_LONG >= s.batch * s.units;
+    const SplitCut cut = SplitCut::of(uniform(total), fewer ? workers / 2 : workers);
     SplitRun r = {0, 0, 0, 0, cut};
     if (w >= cut.n) return r;
     r.pos = cut.start(w);

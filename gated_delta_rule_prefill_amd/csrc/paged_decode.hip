@@ -455,7 +455,9 @@ hipError_t pick_dim(const PagedDecodeArgs& a, hipStream_t s) {
 size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
     a->group = a->H / a->kv_heads;
     a->rows = a->group * a->n_pos;
-    // rows of a tile: as many as the registers hold beside the head dim
+    // Rows of a tile: as many as the registers hold beside the head dim, so that a workgroup
+    // reads the keys for all of them (48 rows at d = 128: 57 us with two tiles, 79 with one at a
+    // time; 64 rows at d = 64: 45 us with four, 46 with two, 54 with one).
     const int most = a->dtype == 0 || a->d == 256 ? 1 : a->d == 128 ? 2 : 4;
     const int tiles = (a->rows + 15) / 16;
     a->rt = tiles >= 4 && most >= 4 ? 4 : tiles >= 2 && most >= 2 ? 2 : 1;
@@ -464,7 +466,15 @@ size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
     // (128 requests of 30 to 30000 tokens, 4 KV heads: 204 us a call with 0, 201 with 1, 200 with 2)
     a->split.extra = 2;
     const int cus = device_cu_count();
-    a->workers = split_workers(2 * cus, a->row_tiles);
+    // Two workgroups a CU hide each other's starts, where they fit; with long units, whose starts
+    // are few, one a CU leaves fewer parts to write and join. 4 KV heads, d = 128: 300 requests of
+    // 300 tokens 37 us with two, 41 with one; of 1000 tokens 123 and 117; 128 requests of 30 to
+    // 30000 tokens 203 and 197; one of 100000 tokens (8 KV heads) 81 and 78. (Two row tiles side
+    // by side read the same keys, and two of them a CU stay ahead: 40 requests of 200 to 20000
+    // tokens, 32 rows at d = 256, 86 us and 88.)
+    const bool two = a->rt == 1 && (a->dtype == 1 || a->d <= 128);
+    a->split.halve = two && a->row_tiles == 1 ? 1 : 0;
+    a->workers = split_workers(two ? 2 * cus : cus, a->row_tiles);
     JoinShape& j = a->join;
     j.row_tiles = a->row_tiles;
     j.tile = 16 * a->rt;
