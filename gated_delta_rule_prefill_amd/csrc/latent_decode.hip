@@ -35,7 +35,8 @@ __device__ __forceinline__ uint64_t bits4(const float x[4]) {
 // q'^T (rank x rows) = W_uk^T q_nope^T per head: a workgroup takes 128 rank columns of one
 // head's W_uk (through LDS, read back transposed as the MFMA's A operand) and 64 (request,
 // position) rows, all loads issued at once: one trip to memory. q' is rounded to bf16 as the
-// core's MFMA operand.
+// core's MFMA operand. Bound: that trip, and for many rows the weights (16.8 MB at 128 heads,
+// d = 128, rank 512). Measured: 80 rows, 128 heads 12 us; one row, 20 heads 3.4 us.
 constexpr int AB_COLS = 128, AB_TILES = 4;
 
 // LDS position of the 16-byte piece c of row n (rows of AB_COLS elements = 16 pieces): the 16
@@ -112,6 +113,10 @@ __global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeA
 //                 reads of the very tile the scores came from.
 // So each cache row is read once from memory per row tile; from LDS a tile is read RH times as
 // keys and once as values. The next tile loads straight into the other LDS buffer meanwhile.
+// Bound: a unit's start and end (queries, the first tile's trip, results: as long as 6 tiles)
+// and, for 64 rows, a tile's LDS reads and matrix work (2.4 us) beside its trip (2.5 us).
+// Measured at rank 512: 80 requests of 100 to 12000 tokens (223 MB), 128 heads 100 us, 2.2 TB/s
+// and 540 TFLOP/s; one request of 40003 tokens (46 MB), 20 heads 18 us.
 // (64 rows with 32 rows a wave read the keys twice only, but their queries take 144 registers:
 // the compiler then spills inside the key loop, and a reload from scratch memory waits for the
 // tile loads issued before it.)
@@ -496,7 +501,9 @@ __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentDecodeA
 // numbers, its rounding and the rounding of what that leaves (which leaves 2^-16 of it): one more
 // MFMA each, in a kernel that waits for memory, for an output error that is a third smaller.
 // Everything is requested at once (the weights as the MFMA's A operand into registers, the rows
-// of u into LDS), so a workgroup pays one trip to memory.
+// of u into LDS), so a workgroup pays one trip to memory. Measured: 80 rows, 128 heads, rank 512,
+// d = 128 15 us (38 MB); one row, 20 heads 6.6 us. (Joining the parts of a unit here where they
+// are few costs more than the join's pass saves: 20.6 us, the join 10 instead of 14.)
 constexpr int UP_TILES = 2;
 
 template <int R, int DV>

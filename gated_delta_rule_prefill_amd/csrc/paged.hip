@@ -21,7 +21,8 @@ namespace gdn {
 // the L2 after the first) and then maps its own PLAN_TOK tokens, instead of a scan kernel
 // followed by a mapping kernel. A page's table entry is written by the thread of its first
 // token: a page that is new starts at a new token, so each entry has exactly one writer and no
-// workgroup reads an entry that another one writes.
+// workgroup reads an entry that another one writes. Measured: 24 requests of one token 4.4 us,
+// 320 prompts of 169418 tokens 6.5 us.
 constexpr int PLAN_THREADS = 256;
 constexpr int PLAN_PER = 4;  // consecutive tokens of a thread (two 16-byte slot stores)
 constexpr int PLAN_TOK = PLAN_THREADS * PLAN_PER;
@@ -172,7 +173,8 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t s) {
 // ---------------------------------------------------------------------------------- append
 // A copy: cache[slot_map[t]] = row t, in 16-byte pieces; a slot outside the cache skips the
 // token. Bound: HBM (each row read and written once). Consecutive threads take consecutive
-// pieces of a token, so both sides move in whole rows.
+// pieces of a token, so both sides move in whole rows. Measured: 65000 rows of 1152 bytes 33 us
+// (4.5 TB/s; a large copy reaches 5.0), 24 us out of the last-level cache; 96 tokens 2.6 us.
 constexpr int APP_THREADS = 256;
 
 template <bool SPLIT>
