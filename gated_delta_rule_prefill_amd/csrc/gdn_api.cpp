@@ -9,6 +9,7 @@
 
 #include <initializer_list>
 #include <mutex>
+#include <new>
 #include <utility>
 #include <vector>
 
@@ -511,8 +512,14 @@ gdn::LatentPrefillArgs latent_prefill_args(const gdn_latent_dims_t* d, int32_t n
 int debug_distinct_cache_slots(const int64_t* slot_map, int32_t tokens, int64_t n_slots,
                                void* stream, const char* what) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    std::vector<char> seen((size_t)n_slots, 0);
-    std::vector<int64_t> h((size_t)tokens);
+    std::vector<int64_t> h;
+    std::vector<bool> seen;
+    try {
+        h.resize((size_t)tokens);
+        seen.resize((size_t)n_slots);
+    } catch (const std::bad_alloc&) {  // no exception leaves a C entry point
+        return fail(GDN_ERR_LAUNCH, "%s: debug check: out of host memory", what);
+    }
     if (hipMemcpyAsync(h.data(), slot_map, sizeof(int64_t) * h.size(), hipMemcpyDeviceToHost, s) !=
             hipSuccess ||
         hipStreamSynchronize(s) != hipSuccess) {
@@ -523,7 +530,7 @@ int debug_distinct_cache_slots(const int64_t* slot_map, int32_t tokens, int64_t 
         if (v < 0 || v >= n_slots) continue;
         if (seen[(size_t)v])
             return fail(GDN_ERR_SHAPE, "%s: cache slot %lld used twice", what, (long long)v);
-        seen[(size_t)v] = 1;
+        seen[(size_t)v] = true;
     }
     return GDN_OK;
 }

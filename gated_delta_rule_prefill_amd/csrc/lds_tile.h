@@ -32,7 +32,8 @@ __device__ __forceinline__ void lds_put(uint32_t at, V v) {
 // 64 lanes x 16 bytes from `base` + each lane's `offset` to the 1 KiB of LDS at `lds` (wave
 // uniform, lane l's piece at 16 l). No register receives data, and the compiler does not count
 // the load: lds_loads_done() has to come before the barrier behind which the data is read.
-// m0 carries the LDS address; the compiler keeps no value in it across statements.
+// m0 carries the LDS address; it is a reserved register that the compiler sets right before an
+// instruction of its own that reads it, of which these kernels have none (no clobber can be named).
 // (The builtin for the same instruction makes the compiler wait for every such load before any
 // later LDS read, which would end the overlap of one tile's load with the other's use.)
 __device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, uint32_t lds) {

@@ -5,6 +5,7 @@ missing library raises.
 Functions carry the C names. Tensors are torch CUDA (HIP) tensors; the HIP stream is the
 current torch stream unless one is given.
 """
+import contextlib
 import ctypes
 import os
 
@@ -466,7 +467,9 @@ def _rows_arg(name, t, shape, dtype, dev):
 def _space(workspace, need, like, stream, dev):
     """Address and size of the workspace; one is allocated unless given."""
     if workspace is None:
-        workspace = _new((max(need(), 1),), torch.uint8, like, stream)
+        with torch.cuda.device(dev) if _current_device() != dev else contextlib.nullcontext():
+            size = need()  # (the sizes go with the current GPU's CU count)
+        workspace = _new((max(size, 1),), torch.uint8, like, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         _bad("workspace", workspace, workspace.shape, workspace.dtype)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
