@@ -144,9 +144,10 @@ __device__ void lp_order(const LatentPrefillArgs& a, int tid, int threads) {
 // that a lane holds 4 dims of a key; for values the latents are, so that it holds 4 keys of a
 // dim: each is stored along its rows in memory order, and the values come out transposed. Keys
 // that do not exist are stored as zeros.
-// Bound: the matrix pipe, at two waves a SIMD with 128 accumulators each, and the writes (2 d x 2
-// bytes a key and head). Measured at rank 512, d = 128: 8192 keys, 32 heads (69 GFLOP) 97-119 us,
-// 30124 keys of 28 requests, 20 heads (158 GFLOP) 221-266 us: 580-710 TFLOP/s.
+// Bound: by no one thing. Without its stores (2 d x 2 bytes a key and head) a call takes a fifth
+// less time, without its weight loads a fifth less, without its LDS reads the same; the matrix pipe
+// is busy 4 cycles in 10. Measured at rank 512, d = 128: 8192 keys, 32 heads (69 GFLOP) 91-107 us,
+// 30124 keys of 28 requests, 20 heads (158 GFLOP) 207-239 us: 640-760 TFLOP/s.
 constexpr int EX_THREADS = 512, EX_WAVES = EX_THREADS / WAVE;
 constexpr int EX_M = 128;              // keys of a workgroup
 constexpr int EX_N = 64;               // columns of a wave
@@ -235,73 +236,82 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
     // 32 p + 16 (c >> 3) + 8 e + (c & 7); with the values' key order (keys 4 h + (0..3) and
     // 8 + 4 h + (0..3) of each 16 make up its half h) lane group g then holds places
     // 32 p + 8 g + 4 e + (0..3). Dims of a key: rows 32 p + 8 (c >> 2) + 4 e + (c & 3) of w_kv.
-    const uint32_t x_at = lds_offset(lat) + (16 * (col >> 3) + (col & 7)) * ROW + ((grp ^ col) << 4);
-    for (int u = 0; u < units_per_wg; u++) {
-        const int col0 = ((int)blockIdx.y * units_per_wg + u) * EX_COLS + wave * EX_N;
-        if (col0 >= columns) return;
-        const int h = col0 / (2 * a.d), in_head = col0 - h * 2 * a.d;
-        const bool value = in_head >= a.d;
-        const char* W = reinterpret_cast<const char*>(a.w_kv) + (size_t)col0 * ROW;
-        uint32_t w_at[4];
+    const uint32_t x_at = lds_offset(lat) + (16 * (col >> 3) + (col & 7)) * ROW +
+                          (((grp * 2) ^ col) << 4);
+    // The contraction's order is free. Two steps take 128 bytes of a row of w_kv: lane group g 32
+    // of them, the first 16 in one step and the others in the next. Weights of two steps are
+    // requested together, two steps ahead, so that a cache line is fetched once; the first ones
+    // of a unit while the one before it ends.
+    uint32_t w_at[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            w_at[j] = (value ? j * 16 + col
-                             : (j >> 1) * 32 + (col >> 2) * 8 + (j & 1) * 4 + (col & 3)) * ROW +
-                      grp * 16;
+    for (int j = 0; j < 4; j++)
+        w_at[j] = ((j >> 1) * 32 + (col >> 2) * 8 + (j & 1) * 4 + (col & 3)) * ROW + grp * 32;
+    bf16x8 w[4][4];
+    auto load_w = [&](const char* from, int k) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            asm volatile("" : "+v"(w_at[j]));  // (else 64-bit sums of it are kept)
+            w[k][j] = *reinterpret_cast<const bf16x8*>(from + (k >> 1) * 128 + (k & 1) * 16 +
+                                                       (size_t)w_at[j]);
+        }
+    };
+    // 64 columns, of one kind, of weights at `block`; after them those at `next`
+    auto unit = [&](auto kind, int h, int in_head, const char* block, const char* next) {
+        constexpr bool VALUE = decltype(kind)::value;
+        // (copies that the compiler cannot take for the same in every unit: it would work out all
+        // addresses of the stores before the first one and keep them)
+        int col = lane & 15, grp = lane >> 4;
+        asm volatile("" : "+v"(col), "+v"(grp));
         f32x4 acc[8][4];  // [key fragment][weight fragment]
 #pragma unroll
         for (int i = 0; i < 8; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++) acc[i][j] = zero4();
-        constexpr int AHEAD = 2;  // contraction steps that the weights are read ahead
-        bf16x8 w[AHEAD + 1][4];
-        auto load_w = [&](int k) {
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                w[k % (AHEAD + 1)][j] =
-                    *reinterpret_cast<const bf16x8*>(W + k * 64 + (size_t)w_at[j]);
+        bf16x8 x[4];
+        uint32_t base[2], at = x_at;
+        // fragment n & 7 of step n >> 3 of the block at `at`; an LDS instruction's immediate
+        // offset reaches 64 KiB
+        auto load_x = [&](uint32_t from, int n) {
+            const int k = n >> 3 & 3, i = n & 7;
+            if (i == 0) {
+                base[0] = from ^ ((k & 2) << 6 | (k & 1) << 4);
+                base[1] = base[0] + 64 * ROW;
+                asm volatile("" : "+v"(base[0]), "+v"(base[1]));
+            }
+            x[n & 3] = lds_get<bf16x8>(base[i >> 2] + ((i >> 1 & 1) * 32 + (i & 1) * 8) * ROW);
         };
+        load_x(at, 0);
+        load_x(at, 1);
+#pragma unroll 1
+        for (int left = R / 128; left > 0; left--) {  // four steps
 #pragma unroll
-        for (int k = 0; k < AHEAD; k++) load_w(k);
-        auto product = [&](auto first) {
-            // the fragment's base in a contraction step, within an LDS instruction's immediate
-            // offset of 64 KiB (formed anew in each step: as constants the compiler would keep
-            // them all in registers)
-            uint32_t base[2];
-            bf16x8 x[3];
-            auto load_x = [&](int n) {
+            for (int n = 0; n < 32; n++) {
                 const int k = n >> 3, i = n & 7;
-                if (i == 0) {
-                    base[0] = x_at ^ (k & 3) << 6;
-                    base[1] = (x_at + 64 * ROW) ^ (k & 3) << 6;
-                    asm volatile("" : "+v"(base[0]), "+v"(base[1]));
+                if (n == 0) {
+                    load_w(block, 2);
+                    load_w(block, 3);
                 }
-                x[n % 3] = lds_get<bf16x8>(base[i >> 2] + (k >> 2) * 256 +
-                                           ((i >> 1 & 1) * 32 + (i & 1) * 8) * ROW);
-            };
-            constexpr int N = R / 32 * 8;
-            load_x(0);
-            load_x(1);
-#pragma unroll
-            for (int n = 0; n < N; n++) {
-                const int k = n >> 3, i = n & 7;
-                if (i == 0 && k + AHEAD < R / 32) load_w(k + AHEAD);
-                if (n + 2 < N) load_x(n + 2);
+                if (n == 16) {
+                    block = left > 1 ? block + 256 : next;
+                    load_w(block, 0);
+                    load_w(block, 1);
+                }
+                // (the last block's look-ahead reads LDS behind its rows, and is not used)
+                load_x(n + 2 < 32 ? at : at + 256, n + 2);
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                    acc[i][j] = decltype(first)::value
-                        ? Mma<bf16>::mma(x[n % 3], w[k % (AHEAD + 1)][j], acc[i][j])
-                        : Mma<bf16>::mma(w[k % (AHEAD + 1)][j], x[n % 3], acc[i][j]);
+                    acc[i][j] = VALUE ? Mma<bf16>::mma(x[n & 3], w[k][j], acc[i][j])
+                                      : Mma<bf16>::mma(w[k][j], x[n & 3], acc[i][j]);
                 __builtin_amdgcn_sched_barrier(0);
             }
-        };
-        if (value) product(std::true_type());
-        else product(std::false_type());
+            at += 256;
+        }
+        asm volatile("" : "+v"(col), "+v"(grp));
 #pragma unroll
         for (int half = 0; half < 2; half++) {
             if (t0 + half >= used) break;
             const size_t head_tile = (size_t)h * a.key_tiles + t0 + half;
-            if (value) {
+            if constexpr (VALUE) {
                 bf16* out = reinterpret_cast<bf16*>(a.vt) + head_tile * a.d * LP_KB;
 #pragma unroll
                 for (int p = 0; p < 2; p++) {
@@ -309,16 +319,17 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
                     const int key = half * LP_KB + p * 32 + (grp >> 1) * 16 + (grp & 1) * 4;
                     bool absent[8];
 #pragma unroll
-                    for (int x = 0; x < 8; x++)
-                        absent[x] = slot_of[key + (x >> 2) * 8 + (x & 3)] >> 31;
+                    for (int y = 0; y < 8; y++)
+                        absent[y] = slot_of[key + (y >> 2) * 8 + (y & 3)] >> 31;
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
                         float y[8];
 #pragma unroll
-                        for (int x = 0; x < 8; x++)
-                            y[x] = absent[x] ? 0.f : acc[half * 4 + 2 * p + (x >> 2)][j][x & 3];
-                        store8<bf16>(out + (size_t)(in_head - a.d + j * 16 + col) * LP_KB + p * 32 +
-                                         grp * 8, y);
+                        for (int e = 0; e < 8; e++)
+                            y[e] = absent[e] ? 0.f : acc[half * 4 + 2 * p + (e >> 2)][j][e & 3];
+                        const int dim = (j >> 1) * 32 + (col >> 2) * 8 + (j & 1) * 4 + (col & 3);
+                        store8<bf16>(out + (size_t)(in_head - a.d + dim) * LP_KB + p * 32 + grp * 8,
+                                     y);
                     }
                 }
             } else {
@@ -331,13 +342,27 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
                     for (int p = 0; p < 2; p++) {
                         float y[8];
 #pragma unroll
-                        for (int x = 0; x < 8; x++)
-                            y[x] = absent ? 0.f : acc[half * 4 + i][2 * p + (x >> 2)][x & 3];
+                        for (int e = 0; e < 8; e++)
+                            y[e] = absent ? 0.f : acc[half * 4 + i][2 * p + (e >> 2)][e & 3];
                         store8<bf16>(out + (size_t)key * a.d + in_head + p * 32 + grp * 8, y);
                     }
                 }
             }
         }
+    };
+    int col0 = (int)blockIdx.y * units_per_wg * EX_COLS + wave * EX_N;
+    if (col0 >= columns) return;
+    const char* block = reinterpret_cast<const char*>(a.w_kv) + (size_t)col0 * ROW;
+    load_w(block, 0);
+    load_w(block, 1);
+    for (int u = 0; u < units_per_wg && col0 < columns; u++, col0 += EX_COLS) {
+        const int h = col0 / (2 * a.d), in_head = col0 - h * 2 * a.d;
+        // (behind the last unit the same weights again, which are not used)
+        const bool more = u + 1 < units_per_wg && col0 + EX_COLS < columns;
+        const char* next = block + (more ? (size_t)EX_COLS * ROW : 0);
+        if (in_head >= a.d) unit(std::true_type(), h, in_head, block, next);
+        else unit(std::false_type(), h, in_head, block, next);
+        block = next;
     }
 }
 
@@ -643,11 +668,21 @@ hipError_t launch_latent_prefill(const LatentPrefillArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(latent_tiles_kernel, dim3(1), block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.q_tiles == 0) return e;
-    // whole passes over the columns: as few workgroups as still fill the chip twice
-    const int blocks = (a.key_tiles + 1) / 2;
+    // The columns in equal runs of units, a workgroup each (one fits a CU): as many runs as end
+    // soonest, a workgroup's start (its latents) counted as a third of a unit. (28 requests with
+    // 250 key blocks, 10 units: one run 239 us, three 265.)
+    const int blocks = (a.key_tiles + 1) / 2, cus = device_cu_count();
     const int units = (a.H * 2 * a.d + EX_COLS - 1) / EX_COLS;
-    int per = (int)((int64_t)blocks * units / (2 * device_cu_count()));
-    per = per < 1 ? 1 : per > units ? units : per;
+    int per = units;
+    int64_t best = INT64_MAX;
+    for (int runs = 1; runs <= units; runs++) {
+        const int n = (units + runs - 1) / runs;
+        const int64_t cost = (((int64_t)blocks * runs + cus - 1) / cus) * (3 * n + 1);
+        if (cost < best) {
+            best = cost;
+            per = n;
+        }
+    }
     const dim3 expand((unsigned)blocks + 1, (unsigned)((units + per - 1) / per));
     if (a.rank == 512)
         hipLaunchKernelGGL(latent_expand_kernel<512>, expand, dim3(EX_THREADS), 0, s, a, per);
