@@ -64,6 +64,7 @@ __global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeA
     bf16x8 B[AB_TILES][DN / 32];
 #pragma unroll
     for (int t = 0; t < AB_TILES; t++) {
+        if (row0 + t * 16 >= rows) break;
         const bf16* q = reinterpret_cast<const bf16*>(a.q_nope) +
                         ((size_t)min(row0 + t * 16 + col, rows - 1) * a.H + h) * DN;
 #pragma unroll
@@ -89,6 +90,7 @@ __global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeA
         }
 #pragma unroll
     for (int t = 0; t < AB_TILES; t++) {
+        if (row0 + t * 16 >= rows) break;
         const int row = row0 + t * 16 + col;
         f32x4 d[2];
 #pragma unroll
@@ -519,13 +521,15 @@ __global__ __launch_bounds__(LD_THREADS, 2) void latent_up_kernel(LatentDecodeAr
                     ((size_t)h * (a.d_nope + DV) + a.d_nope) * R;
     f32x4 u[UP_TILES][PER];
 #pragma unroll
-    for (int t = 0; t < UP_TILES; t++)
+    for (int t = 0; t < UP_TILES; t++) {
+        if (row0 + t * 16 >= rows) break;
 #pragma unroll
         for (int i = 0; i < PER; i++) {
             const int x = i * LD_THREADS + threadIdx.x, r = x / (R / 4), c = x % (R / 4);
             u[t][i] = *reinterpret_cast<const f32x4*>(
                 a.o_lat + ((size_t)min(row0 + t * 16 + r, rows - 1) * a.H + h) * R + c * 4);
         }
+    }
     bf16x8 w[NJ][R / 32];
 #pragma unroll
     for (int j = 0; j < NJ; j++)
@@ -535,7 +539,8 @@ __global__ __launch_bounds__(LD_THREADS, 2) void latent_up_kernel(LatentDecodeAr
                                       grp * 8);
     sched_fence();
 #pragma unroll
-    for (int t = 0; t < UP_TILES; t++)
+    for (int t = 0; t < UP_TILES; t++) {
+        if (row0 + t * 16 >= rows) break;
 #pragma unroll
         for (int i = 0; i < PER; i++) {
             const int x = i * LD_THREADS + threadIdx.x, r = x / (R / 4), c = x % (R / 4);
@@ -548,9 +553,11 @@ __global__ __launch_bounds__(LD_THREADS, 2) void latent_up_kernel(LatentDecodeAr
             *reinterpret_cast<uint64_t*>(lds[t][0] + r * PITCH + c * 8) = bits4(hi);
             *reinterpret_cast<uint64_t*>(lds[t][1] + r * PITCH + c * 8) = bits4(lo);
         }
+    }
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < UP_TILES; t++) {
+        if (row0 + t * 16 >= rows) break;
         f32x4 d[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; j++) d[j] = zero4();
