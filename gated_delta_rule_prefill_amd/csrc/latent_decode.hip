@@ -148,6 +148,12 @@ __device__ __forceinline__ int ld_weight(int row, int piece) {
     return row * (LD_KB * 2) + ((piece ^ ((row >> 1) & 7)) << 4);
 }
 
+// Four keys of 16 that rows 4 a .. of a key fragment are: 0, 2, 3, 1. A 16-byte LDS read takes
+// lanes 0-3, 12-15, 20-23 and 24-27 at a time (then 4-11, 16-19, 28-31; then those 32 on), and in
+// this order their pieces lie in 16 different bank groups (in memory order a tile's key reads took
+// twice as long; 80 requests, 128 heads: 143.5 and 137.5 us a call).
+__device__ __forceinline__ int ld_quad(int a) { return ((a ^ a >> 1) & 1) << 1 | a >> 1; }
+
 template <int RH, int KS>
 struct LdWaves {
     static constexpr int KEYS = 16 * KS;            // keys of a wave
@@ -201,9 +207,10 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
     // LDS byte offsets of this lane's reads and writes within a tile or the weights. A piece
     // index is xored with a function of the row, so its constant part can be xored in last, and
     // one offset serves all pieces of a kind.
-    const uint32_t k_at = X::lat(key_row + col, grp), pe_at = X::rope(key_row + col, grp);
+    const int key_of = ld_quad(col >> 2) * 4 + (col & 3);
+    const uint32_t k_at = X::lat(key_row + key_of, grp), pe_at = X::rope(key_row + key_of, grp);
     const uint32_t p_at = ld_weight(col, grp);
-    const uint32_t p_put = ld_weight(col, kg * KS * 2 + (grp >> 1)) + (grp & 1) * 8;
+    const uint32_t p_put = ld_weight(col, kg * KS * 2 + (ld_quad(grp) >> 1)) + (ld_quad(grp) & 1) * 8;
     const uint32_t v_at = X::lat(grp * 8 + ((lane >> 2) & 3), wave * NT * 2 + ((lane & 3) >> 1)) +
                           (lane & 1) * 8;
 
@@ -354,9 +361,9 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
             }
             const int key0 = c * LD_KB + key_row;
             if (exist != ALL || key0 + KEYS > seen0) {
-                // this lane's keys are key0 + first + 16 x + i (hidden from the compiler, which
+                // this lane's keys are key0 + first + 16 x + i (`first` hidden from the compiler, which
                 // would keep what depends on it in registers across the key loop)
-                int first = grp * 4;
+                int first = ld_quad(grp) * 4;
                 asm volatile("" : "+v"(first));
                 const uint64_t here = exist >> first;
                 const int left = lim - key0 - first;
@@ -504,7 +511,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentDecodeA
 // MFMA each, in a kernel that waits for memory, for an output error that is a third smaller.
 // Everything is requested at once (the weights as the MFMA's A operand into registers, the rows
 // of u into LDS), so a workgroup pays one trip to memory. Measured: 80 rows, 128 heads, rank 512,
-// d = 128 15 us (38 MB); one row, 20 heads 6.6 us. (Joining the parts of a unit here where they
+// d = 128 15 us (38 MB); one row, 20 heads 5.7 us. (Joining the parts of a unit here where they
 // are few costs more than the join's pass saves: 20.6 us, the join 10 instead of 14.)
 constexpr int UP_TILES = 2;
 
