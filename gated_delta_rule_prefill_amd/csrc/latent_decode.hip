@@ -117,8 +117,8 @@ __global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeA
 // keys and once as values. The next tile loads straight into the other LDS buffer meanwhile.
 // Bound: a unit's start and end (queries, the first tile's trip, results: as long as 6 tiles)
 // and, for 64 rows, a tile's LDS reads and matrix work (2.4 us) beside its trip (2.5 us).
-// Measured at rank 512: 80 requests of 100 to 12000 tokens (223 MB), 128 heads 100 us, 2.2 TB/s
-// and 540 TFLOP/s; one request of 40003 tokens (46 MB), 20 heads 18 us.
+// Measured at rank 512: 80 requests of 100 to 12000 tokens (223 MB), 128 heads 93 us, 2.4 TB/s
+// and 580 TFLOP/s; one request of 40003 tokens (46 MB), 20 heads 18 us.
 // (64 rows with 32 rows a wave read the keys twice only, but their queries take 144 registers:
 // the compiler then spills inside the key loop, and a reload from scratch memory waits for the
 // tile loads issued before it.)
