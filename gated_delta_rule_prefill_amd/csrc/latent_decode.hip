@@ -137,7 +137,9 @@ struct LdTile {
     __device__ __forceinline__ static int turn(int r) {
         return ((r & 3) << 1) | (r & 8) | ((r >> 2) & 1);
     }
-    __device__ __forceinline__ static int lat(int r, int c) { return r * LAT + ((c ^ turn(r)) << 4); }
+    __device__ __forceinline__ static int lat(int r, int c) {
+        return r * LAT + ((c ^ turn(r)) << 4);
+    }
     __device__ __forceinline__ static int rope(int r, int c) {
         return ROPE_AT + r * (LD_ROPE * 2) + ((c ^ ((r >> 1) & 7)) << 4);
     }
@@ -210,7 +212,8 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
     const int key_of = ld_quad(col >> 2) * 4 + (col & 3);
     const uint32_t k_at = X::lat(key_row + key_of, grp), pe_at = X::rope(key_row + key_of, grp);
     const uint32_t p_at = ld_weight(col, grp);
-    const uint32_t p_put = ld_weight(col, kg * KS * 2 + (ld_quad(grp) >> 1)) + (ld_quad(grp) & 1) * 8;
+    const uint32_t p_put = ld_weight(col, kg * KS * 2 + (ld_quad(grp) >> 1)) +
+                           (ld_quad(grp) & 1) * 8;
     const uint32_t v_at = X::lat(grp * 8 + ((lane >> 2) & 3), wave * NT * 2 + ((lane & 3) >> 1)) +
                           (lane & 1) * 8;
 

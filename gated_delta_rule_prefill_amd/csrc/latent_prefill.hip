@@ -145,9 +145,9 @@ __device__ void lp_order(const LatentPrefillArgs& a, int tid, int threads) {
 // dim: each is stored along its rows in memory order, and the values come out transposed. Keys
 // that do not exist are stored as zeros.
 // Bound: by no one thing. Without its stores (2 d x 2 bytes a key and head) a call takes a fifth
-// less time, without its weight loads a fifth less, without its LDS reads the same; the matrix pipe
-// is busy 4 cycles in 10. Measured at rank 512, d = 128: 8192 keys, 32 heads (69 GFLOP) 91-107 us,
-// 30124 keys of 28 requests, 20 heads (158 GFLOP) 207-239 us: 640-760 TFLOP/s.
+// less time, without its weight loads a fifth less, without its LDS reads the same; the matrix
+// pipe is busy a third of the time. Measured at rank 512, d = 128: 8192 keys, 32 heads (69 GFLOP)
+// 91-107 us, 30124 keys of 28 requests, 20 heads (158 GFLOP) 207-239 us: 640-760 TFLOP/s.
 constexpr int EX_THREADS = 512, EX_WAVES = EX_THREADS / WAVE;
 constexpr int EX_M = 128;              // keys of a workgroup
 constexpr int EX_N = 64;               // columns of a wave
@@ -207,7 +207,8 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
 #pragma unroll
             for (int r = 0; r < 16; r += 2) {
                 const int rr = r + (lane >> 5);
-                load_to_lds(cache + __shfl(mine, rr, WAVE) * CACHE_ROW + (((lane & 31) ^ (rr & 7) ^ odd) << 4),
+                load_to_lds(cache + __shfl(mine, rr, WAVE) * CACHE_ROW +
+                                (((lane & 31) ^ (rr & 7) ^ odd) << 4),
                             at + r * ROW);
             }
         }

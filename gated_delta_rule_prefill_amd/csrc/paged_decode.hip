@@ -132,7 +132,8 @@ template <typename T, int D, int RT>
 constexpr int PD_WAVES_PER_SIMD = RT == 1 && (sizeof(T) == 2 || D <= 128) ? 2 : 1;
 
 template <typename T, int D, int RT>
-__global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void paged_decode_kernel(PagedDecodeArgs a) {
+__global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void paged_decode_kernel(
+    PagedDecodeArgs a) {
     using X = PdTile<T, D>;
     using L = PdLds<T, D, RT>;
     typedef typename X::frag frag;
@@ -158,7 +159,8 @@ __global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void pag
             for (size_t i = tid * 4; i < n; i += PD_THREADS * 4)
                 store4<T>(reinterpret_cast<T*>(a.o) + (size_t)b * n + i, z);
             if (a.join.per_unit)
-                for (int u = tid; u < a.kv_heads; u += PD_THREADS) join_none(a.join, b * a.kv_heads + u);
+                for (int u = tid; u < a.kv_heads; u += PD_THREADS)
+                    join_none(a.join, b * a.kv_heads + u);
         }
         if (!a.join.per_unit && tid == 0) join_none(a.join, me.worker);
     }
@@ -468,7 +470,8 @@ size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
     a->rt = tiles >= 4 && most >= 4 ? 4 : tiles >= 2 && most >= 2 ? 2 : 1;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
     a->split.units = a->kv_heads;
-    // (128 requests of 30 to 30000 tokens, 4 KV heads: 204 us a call with 0, 201 with 1, 200 with 2)
+    // (128 requests of 30 to 30000 tokens, 4 KV heads: 204 us a call with 0, 201 with 1, 200
+    // with 2)
     a->split.extra = 2;
     const int cus = device_cu_count();
     // Two workgroups a CU hide each other's starts, where they fit; with long units, whose starts
