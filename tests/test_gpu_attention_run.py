@@ -67,8 +67,8 @@ def test_hybrid_model_run_matches_reference():
         for i in range(n):
             flat[i, :ctx[i]] = rows[i]
         own = torch.arange(n, dtype=I32).view(n, 1)
-        want = attention.latent_expanded(qn, qp, w, flat.double(), own, [0] + np.cumsum(new).tolist(),
-                                         ctx, scale)
+        want = attention.latent_expanded(qn, qp, w, flat.double(), own,
+                                         [0] + np.cumsum(new).tolist(), ctx, scale)
         if step < 2:
             o = gdn.gdn_latent_prefill(qn.to(DEV), qp.to(DEV), w.to(DEV), cache, table, cu, lens,
                                        sum(ctx), scale=scale)
@@ -193,6 +193,50 @@ def test_negative_and_zero_scales(scale):
     case = list(lat._prefill_case(53, [0, 70], [130, 40], 2, 512, 128, 16, q_scale=0.7))
     case[7] = scale
     lat._check_prefill(tuple(case), every=3)
+
+
+def test_nan_of_one_request_stays_with_it():
+    """A NaN query row spoils itself only; NaN and infinite cache rows their own request."""
+    say("case NaN kept apart")
+    nan, lens = float("nan"), [200, 90, 300]
+    for mod, q_at, rows in ((pag, 0, (1, 2)), (lat, 0, (3,))):
+        if mod is pag:
+            case = list(pag._decode_case(54, lens, 2, 8, 2, 64, 16, BF16, poison=False))
+        else:
+            case = list(lat._decode_case(55, lens, 2, 4, 256, 64, 16, poison=False))
+        table = case[3] if mod is pag else case[4]
+        want = mod._run_decode(tuple(case))
+        bad = list(case)
+        bad[q_at] = case[q_at].clone()
+        bad[q_at][1, 0, 1, 3] = nan
+        got = mod._run_decode(tuple(bad))
+        assert torch.isnan(got[1, 0, 1].float()).all()
+        mask = torch.ones(got.shape[:3], dtype=torch.bool)
+        mask[1, 0, 1] = False
+        assert torch.equal(got[mask], want[mask])
+        bad = list(case)
+        for r in rows:
+            bad[r] = case[r].clone()
+            bad[r][int(table[1, 2])] = nan if r % 2 else float("inf")
+        got = mod._run_decode(tuple(bad))
+        assert torch.isnan(got[1].float()).all()
+        assert torch.equal(got[[0, 2]], want[[0, 2]])
+    case = list(lat._prefill_case(56, [0, 30, 0], [70, 60, 130], 2, 256, 64, 16, poison=False))
+    want = lat._run_prefill(tuple(case))
+    bad = list(case)
+    bad[0] = case[0].clone()
+    bad[0][75, 1, 0] = nan
+    got = lat._run_prefill(tuple(bad))
+    assert torch.isnan(got[75, 1].float()).all()
+    mask = torch.ones(got.shape[:2], dtype=torch.bool)
+    mask[75, 1] = False
+    assert torch.equal(got[mask], want[mask])
+    bad = list(case)
+    bad[3] = case[3].clone()
+    bad[3][int(case[4][1, 0])] = nan
+    got = lat._run_prefill(tuple(bad))
+    assert torch.isnan(got[70:130].float()).all()
+    assert torch.equal(got[:70], want[:70]) and torch.equal(got[130:], want[130:])
 
 
 # ------------------------------------------------------------------ graphs and streams
@@ -407,6 +451,28 @@ def test_pools_past_32_bit_offsets():
     for x, y in zip(*outs):
         assert torch.equal(x, y)
     assert outs[0][0].float().abs().max() > 0.01 and outs[0][3].float().abs().max() > 1
+
+
+# -------------------------------------------------------------------- sizes at the limits
+@pytest.mark.parametrize("H,kv,P", [(1024, 1, 1), (1024, 1024, 1), (512, 1, 16)])
+def test_most_heads_paged(H, kv, P):
+    say(f"case limits paged H={H} kv={kv} P={P}")
+    pag._check_decode(pag._decode_case(95, [37, 0, 150], P, H, kv, 64, 16, BF16))
+
+
+@pytest.mark.parametrize("H,P", [(1024, 1), (128, 16)])
+def test_most_heads_latent(H, P):
+    say(f"case limits latent H={H} P={P}")
+    lat._check_decode(lat._decode_case(96, [70, 0, 18], P, H, 256, 64, 16))
+    if P == 1:
+        lat._check_prefill(lat._prefill_case(97, [30, 0], [2, 1], H, 256, 64, 16))
+
+
+def test_pages_of_one_token():
+    say("case limits: block size 1")
+    pag._check_decode(pag._decode_case(98, [130, 1, 0, 64], 2, 8, 2, 128, 1, BF16))
+    lat._check_decode(lat._decode_case(99, [130, 1, 0, 64], 2, 4, 512, 128, 1))
+    lat._check_prefill(lat._prefill_case(100, [0, 70], [66, 3], 2, 256, 64, 1))
 
 
 # ---------------------------------------------------------------------------- refusals
