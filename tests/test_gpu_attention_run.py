@@ -475,6 +475,16 @@ def test_pages_of_one_token():
     lat._check_prefill(lat._prefill_case(100, [0, 70], [66, 3], 2, 256, 64, 1))
 
 
+def test_prefill_without_keys_gives_zeros():
+    """total_keys 0 (and lengths of 0 under a positive one): no query sees a token."""
+    say("case limits: no keys")
+    case = list(lat._prefill_case(101, [0], [40], 2, 256, 64, 16))
+    o = torch.full((40, 2, 64), 7.0, dtype=BF16, device=DEV)
+    assert not lat._run_prefill(tuple(case), keys=0, o=o).any()
+    case[6] = torch.zeros(1, dtype=I32)
+    assert not lat._run_prefill(tuple(case), keys=64, o=o.fill_(7.0)).any()
+
+
 # ---------------------------------------------------------------------------- refusals
 def test_debug_library_rejects_repeated_cache_slots():
     say("case debug build: an append with a repeated cache slot")
