@@ -31,9 +31,14 @@ __device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// Keys of request i that its table can address, and its new tokens.
+// Length of request i without the tokens that lie behind total_tokens: those have no rows here
+// (a step that overflowed its buffers), and the rows before them keep their positions.
+__device__ __forceinline__ int lp_len(const LatentPrefillArgs& a, int i) {
+    return max(a.seq_lens[i], 0) - (max(a.cu_seqlens[i + 1], a.total_tokens) - a.total_tokens);
+}
+// Keys of it that its table can address, and its new tokens.
 __device__ __forceinline__ int lp_keys(const LatentPrefillArgs& a, int i) {
-    return min(max(a.seq_lens[i], 0), a.max_keys);
+    return min(max(lp_len(a, i), 0), a.max_keys);
 }
 __device__ __forceinline__ int lp_new(const LatentPrefillArgs& a, int i) {
     const int s = min(max(a.cu_seqlens[i], 0), a.total_tokens);
@@ -54,7 +59,7 @@ __device__ __forceinline__ int lp_find(const int32_t* first, int n, int t) {
 __device__ __forceinline__ int lp_key_tiles(const LatentPrefillArgs& a, int i, int qt) {
     const int fresh = lp_new(a, i), q0 = (qt - a.q_tile[i]) * LP_QB;
     const int keys = min(lp_keys(a, i), (a.key_tile[i + 1] - a.key_tile[i]) * LP_KB);
-    const int reach = min(keys, a.seq_lens[i] - fresh + min(q0 + LP_QB, fresh));
+    const int reach = min(keys, lp_len(a, i) - fresh + min(q0 + LP_QB, fresh));
     return reach > 0 ? (reach + LP_KB - 1) / LP_KB : 0;
 }
 
@@ -409,7 +414,7 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
     const int seq = uniform(who.x), qt = uniform(who.y);
     const int q0 = (qt - a.q_tile[seq]) * LP_QB;
     const int fresh = lp_new(a, seq);
-    const int first_pos = a.seq_lens[seq] - fresh;      // of the request's first new token
+    const int first_pos = lp_len(a, seq) - fresh;       // of the request's first new token
     const int kt0 = a.key_tile[seq];
     const int nt = uniform(lp_key_tiles(a, seq, qt));
 

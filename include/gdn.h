@@ -578,7 +578,9 @@ int gdn_latent_prefill_workspace_bytes(const gdn_latent_dims_t* dims, int32_t n_
  *   q_nope      [total_tokens, num_heads, d_nope],  q_pe [total_tokens, num_heads, d_rope]
  *   w_kv, cache, block_table [n_seqs, max_blocks], seq_lens [n_seqs] as in gdn_latent_decode
  *   cu_seqlens  [n_seqs + 1] int32 (device), as in gdn_prefill_chunked. Rows of o from
- *               cu_seqlens[n_seqs] on (a padded batch) are left as they are.
+ *               cu_seqlens[n_seqs] on (a padded batch) are left as they are. Where cu_seqlens
+ *               passes total_tokens (gdn_paged_plan's max_tokens was too small), the tokens
+ *               behind it have no rows and are no keys; the others keep their positions.
  *   total_keys  at least the sum of seq_lens over the requests with max_blocks * block_size
  *               as each one's limit (the host keeps these lengths to size its pages). If the
  *               device lengths exceed it, keys past it are not seen; no memory is touched
