@@ -482,7 +482,9 @@ def _new(shape, dtype, like, stream):
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        # (handle 0 is the default stream; ExternalStream would take some other one for it)
+        stream = (torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream)
+                  else torch.cuda.default_stream(like.device))
     now = torch.cuda.current_stream(like.device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=like.device)
