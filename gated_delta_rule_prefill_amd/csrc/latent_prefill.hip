@@ -559,7 +559,9 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
         bf16x8 p[LP_KB / 16];
         // slices 0 and 1: the tile's maximum; 2: over both halves; from 3 on: the weights
         constexpr int PER = (32 + NF - 4) / (NF - 3);
-        scores(t + 1 < mine ? t + 1 : t, next, [&](int f) {
+        // (behind this wave's last tile the scores are nobody's: that buffer is not being filled,
+        // tile t's may be)
+        scores(t + 1, next, [&](int f) {
             if (f < 2) {
 #pragma unroll
                 for (int i = 0; i < 16; i++) top = fmaxf(top, s[f][i]);
