@@ -86,10 +86,11 @@ struct LatentPrefillArgs {
     int32_t* key_tile;   // [n_seqs + 1] first key tile of each request
     int2* order;         // [q_tiles] (request, query tile) in the order of their start
     int32_t* q_tile;     // [n_seqs + 1] first query tile
-    uint64_t* exist;     // [key_tiles] a bit per key
-    void* k_pe;          // [key_tiles][64][64] rotary keys
-    void* k;             // [H][key_tiles][64][d]
-    void* vt;            // [H][key_tiles][d][64], keys of each 16 in the order of the weights
+    int32_t* head_shift; // [H][2] powers of two that its keys and values are written times
+    int4* tile;          // [key_tiles] x, y: a bit per existing key; z: power of two below 1 / that
+    void* k_pe;          // [key_tiles][64][64] rotary keys (bf16)
+    void* k;             // [H][key_tiles][64][d] (fp16)
+    void* vt;            // [H][key_tiles][d][64] (fp16), keys of each 16 in the order of the weights
 };
 size_t latent_prefill_layout(LatentPrefillArgs* a, int64_t total_keys, void* ws);
 hipError_t launch_latent_prefill(const LatentPrefillArgs& a, hipStream_t stream);

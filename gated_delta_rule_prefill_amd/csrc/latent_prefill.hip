@@ -27,8 +27,63 @@ constexpr float LOG2E = 1.4426950408889634f;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
 __device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma32(f16x8 a, f16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// Written-out keys and values, and the softmax weights, are the roundings that this form makes
+// between its inputs and its outputs. They are kept in fp16 (11 significant bits): with bf16
+// outputs were off by 0.0030 (relative 2-norm; 0.0017 is their own rounding), with fp16 by 0.0017.
+// A call takes 4 % longer: the matrix pipe draws more power (a library product of 8192^3 reaches
+// 1.41 PFLOP/s in bf16 and 1.34 in fp16). fp16's range is made to do by exact scalings by powers of
+// two. With |c| < 2^(t + 8) for the latents of a key tile, t a multiple of 16, and
+// |w| < 2^(x + 1) for a head's rows of w_kv, a key or value is below rank 2^(t + x + 9); it is
+// written times 2^(s - t) with s = 6 - log2 rank - x, that is below 2^15. Tiles whose largest latent
+// lies between 2^-8 and 2^8 (a normalised one does) have t = 0, and with weights of about
+// rank^-1/2 s is about 0 as well. What is below 2^-14 then is held to 2^-25: that is 2^-15 of a
+// typical number of the tile (2^-8.5 of its bound) where the latents are smallest for their t.
+//   scores   2^(a - s + t) (q 2^-a . k 2^(s - t) + q_pe 2^(s - a) . r 2^-t), 2^a by a row's largest
+//            |q|: its fp16 numbers are below 2
+//   outputs  over tiles with different t, sums are kept at the largest so far
+constexpr int LP_T_MIN = -48, LP_T_MAX = 64;  // (weights of tiles 2^112 apart stay in fp32's range)
+
+__device__ __forceinline__ float exp2i(int e) { return ldexpf(1.f, e); }
+// Larger magnitudes of two pairs of bf16 numbers, as bits; infinities and NaN in x do not count
+// (they make up what they reach, and must not take the others' bits).
+__device__ __forceinline__ uint32_t max_magnitudes(uint32_t most, uint32_t x) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+    u16x2 v = __builtin_bit_cast(u16x2, x & 0x7fff7fffu);
+    v &= ~__builtin_bit_cast(u16x2, __builtin_bit_cast(i16x2, v + (uint16_t)0x80) >> (int16_t)15);
+    return __builtin_bit_cast(uint32_t,
+                              __builtin_elementwise_max(__builtin_bit_cast(u16x2, most), v));
+}
+template <typename V>
+__device__ __forceinline__ uint32_t max_magnitudes_of(uint32_t most, V eight) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 x = __builtin_bit_cast(u32x4, eight);
+#pragma unroll
+    for (int i = 0; i < 4; i++) most = max_magnitudes(most, x[i]);
+    return most;
+}
+__device__ __forceinline__ int larger_half(uint32_t most) {
+    return (int)max(most & 0xffffu, most >> 16);
+}
+__device__ __forceinline__ int wave_max(int x) {
+#pragma unroll
+    for (int off = WAVE / 2; off > 0; off >>= 1) x = max(x, __shfl_xor(x, off, WAVE));
+    return x;
+}
+// t by the largest magnitude of a tile's latents (bf16 bits).
+__device__ __forceinline__ int lp_shift(int bits) {
+    if (bits == 0) return 0;
+    const int t = ((bits >> 7) - 127 + 8) & ~15;
+    return min(max(t, LP_T_MIN), LP_T_MAX);
 }
 
 // Length of request i without the tokens that lie behind total_tokens: those have no rows here
@@ -65,9 +120,31 @@ __device__ __forceinline__ int lp_key_tiles(const LatentPrefillArgs& a, int i, i
 
 // ---------------------------------------------------------------------------------- tables
 // Prefix sums of each request's key and query tiles, cut off at the host's bounds (lengths
-// that break the contract then lose keys or rows, never memory). 3 us.
+// that break the contract then lose keys or rows, never memory): the first workgroup. 3 us.
+// The others: s of a head's keys or values, from its largest weight; 5.5 us in all.
+__device__ __forceinline__ void lp_head_shift(const LatentPrefillArgs& a, int n) {
+    __shared__ int most[LP_WAVES];
+    const int rows = a.d * a.rank / 8;  // pieces of 8 weights
+    const f32x4* w = reinterpret_cast<const f32x4*>(a.w_kv) + (size_t)n * rows;
+    uint32_t m = 0;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < rows; i += LP_THREADS) m = max_magnitudes_of(m, w[i]);
+    const int mine = wave_max(larger_half(m));
+    if (lane_id() == 0) most[wave_id()] = mine;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    int x = most[0];
+#pragma unroll
+    for (int i = 1; i < LP_WAVES; i++) x = max(x, most[i]);
+    x = min(max((x >> 7) - 127, -80), 80);
+    a.head_shift[n] = 6 - (a.rank == 512 ? 9 : 8) - x;
+}
 __global__ __launch_bounds__(LP_THREADS) void latent_tiles_kernel(LatentPrefillArgs a) {
     __shared__ int64_t part[LP_WAVES][2];
+    if (blockIdx.x > 0) {
+        lp_head_shift(a, blockIdx.x - 1);
+        return;
+    }
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
     const int per = (a.n_seqs + LP_THREADS - 1) / LP_THREADS;
     const int i0 = min(tid * per, a.n_seqs), i1 = min(i0 + per, a.n_seqs);
@@ -167,6 +244,7 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
     constexpr int ROW = R * 2, PIECES = ROW / 16;
     __shared__ __align__(1024) char lat[EX_M * ROW];
     __shared__ uint32_t slot_of[EX_M];
+    __shared__ int most[EX_WAVES];  // largest magnitude of 16 rows' latents
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
     static_assert(LP_CLASSES <= EX_THREADS, "lp_order has a thread per class");
@@ -197,11 +275,12 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
         slot_of[tid] = slot | (ok ? 0u : 0x80000000u);  // slots stay below 2^31
     }
     __syncthreads();
+    const uint32_t flagged = slot_of[wave * 16 + (lane & 15)];
     {
         // 16 rows per wave; piece c of row r lies at piece c ^ ((r & 7) | (r >> 4 & 1) << 3), which
         // takes 16 values over the rows that a fragment's lanes read (below)
         const int odd = (wave & 1) << 3;
-        const uint32_t mine = slot_of[wave * 16 + (lane & 15)] & 0x7fffffffu;
+        const uint32_t mine = flagged & 0x7fffffffu;
         const uint32_t at = lds_offset(lat) + wave * 16 * ROW;
         if constexpr (PIECES == 64) {
 #pragma unroll
@@ -218,23 +297,55 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
             }
         }
     }
+    bf16x8 pe[EX_M * 8 / EX_THREADS];  // rotary keys of the pair: tile i, row tid / 8
+    static_assert(EX_M * 8 / EX_THREADS == 2 && EX_THREADS / 8 == LP_KB, "a tile a step");
     if (blockIdx.y == 0) {
-        // this pair's rotary keys and existence bits, once for all heads
-        if (wave < 2) {
-            const uint64_t bits = __ballot(ok);
-            if (lane == 0 && t0 + wave < used) a.exist[t0 + wave] = bits;
-        }
-        for (int x = tid; x < EX_M * 8; x += EX_THREADS) {
-            const int r = x >> 3, c = x & 7;
-            if (t0 + r / LP_KB < used)
-                *reinterpret_cast<f32x4*>(reinterpret_cast<char*>(a.k_pe) +
-                                          ((size_t)t0 * LP_KB + r) * 128 + c * 16) =
-                    *reinterpret_cast<const f32x4*>(
-                        cache + (size_t)(slot_of[r] & 0x7fffffffu) * CACHE_ROW + ROW + c * 16);
-        }
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            pe[i] = *reinterpret_cast<const bf16x8*>(
+                cache + (size_t)(slot_of[i * LP_KB + (tid >> 3)] & 0x7fffffffu) * CACHE_ROW + ROW +
+                (tid & 7) * 16);
     }
     lds_loads_done();
+    {
+        // this wave's 16 rows are here; what absent keys' slots hold does not count
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < 16; r += 64 / PIECES) {
+            const uint32_t row = r + lane / PIECES;
+            const bool absent = __shfl(flagged, row, WAVE) >> 31;
+            const uint32_t x = max_magnitudes_of(
+                0, lds_get<f32x4>(lds_offset(lat) + (wave * 16 + row) * ROW + lane % PIECES * 16));
+            m = max_magnitudes(m, absent ? 0u : x);
+        }
+        const int x = wave_max(larger_half(m));
+        if (lane == 0) most[wave] = x;
+    }
     lds_barrier();
+    int shift[2];  // t of the two tiles
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        shift[i] = uniform(lp_shift(max(max(most[4 * i], most[4 * i + 1]),
+                                        max(most[4 * i + 2], most[4 * i + 3]))));
+    if (blockIdx.y == 0) {
+        // the pair's existence bits, shifts and rotary keys, once for all heads
+        if (wave < 2) {
+            const uint64_t bits = __ballot(ok);
+            if (lane == 0 && t0 + wave < used)
+                a.tile[t0 + wave] = make_int4((int)bits, (int)(bits >> 32), shift[wave], 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            if (t0 + i >= used) break;
+            if (shift[i] != 0) {
+                const float f = exp2i(-shift[i]);
+#pragma unroll
+                for (int e = 0; e < 8; e++) pe[i][e] = (bf16)((float)pe[i][e] * f);
+            }
+            *reinterpret_cast<bf16x8*>(reinterpret_cast<char*>(a.k_pe) +
+                                       (size_t)(t0 + i) * LP_KB * 128 + tid * 16) = pe[i];
+        }
+    }
     const int col = lane & 15, grp = lane >> 4;
     const int columns = a.H * 2 * a.d;
     // Which rows make up a fragment is free, and chosen so that two fragments give a lane 8
@@ -264,6 +375,7 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
     // 64 columns, of one kind, of weights at `block`; after them those at `next`
     auto unit = [&](auto kind, int h, int in_head, const char* block, const char* next) {
         constexpr bool VALUE = decltype(kind)::value;
+        const int s = a.head_shift[h * 2 + VALUE];
         // (copies that the compiler cannot take for the same in every unit: it would work out all
         // addresses of the stores before the first one and keep them)
         int col = lane & 15, grp = lane >> 4;
@@ -317,8 +429,15 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
         for (int half = 0; half < 2; half++) {
             if (t0 + half >= used) break;
             const size_t head_tile = (size_t)h * a.key_tiles + t0 + half;
+            const float f = exp2i(s - shift[half]);
+            auto store = [&](_Float16* to, const float (&y)[8]) {
+                f16x8 v;
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[e] = (_Float16)y[e];
+                *reinterpret_cast<f16x8*>(to) = v;
+            };
             if constexpr (VALUE) {
-                bf16* out = reinterpret_cast<bf16*>(a.vt) + head_tile * a.d * LP_KB;
+                _Float16* out = reinterpret_cast<_Float16*>(a.vt) + head_tile * a.d * LP_KB;
 #pragma unroll
                 for (int p = 0; p < 2; p++) {
                     // the lane's 8 keys: 32 p + 16 (g >> 1) + 4 (g & 1) + 8 e + (0..3)
@@ -332,14 +451,13 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
                         float y[8];
 #pragma unroll
                         for (int e = 0; e < 8; e++)
-                            y[e] = absent[e] ? 0.f : acc[half * 4 + 2 * p + (e >> 2)][j][e & 3];
+                            y[e] = absent[e] ? 0.f : acc[half * 4 + 2 * p + (e >> 2)][j][e & 3] * f;
                         const int dim = (j >> 1) * 32 + (col >> 2) * 8 + (j & 1) * 4 + (col & 3);
-                        store8<bf16>(out + (size_t)(in_head - a.d + dim) * LP_KB + p * 32 + grp * 8,
-                                     y);
+                        store(out + (size_t)(in_head - a.d + dim) * LP_KB + p * 32 + grp * 8, y);
                     }
                 }
             } else {
-                bf16* out = reinterpret_cast<bf16*>(a.k) + head_tile * LP_KB * a.d;
+                _Float16* out = reinterpret_cast<_Float16*>(a.k) + head_tile * LP_KB * a.d;
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int key = (i >> 1) * 32 + 16 * (col >> 3) + (i & 1) * 8 + (col & 7);
@@ -349,8 +467,8 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
                         float y[8];
 #pragma unroll
                         for (int e = 0; e < 8; e++)
-                            y[e] = absent ? 0.f : acc[half * 4 + i][2 * p + (e >> 2)][e & 3];
-                        store8<bf16>(out + (size_t)key * a.d + in_head + p * 32 + grp * 8, y);
+                            y[e] = absent ? 0.f : acc[half * 4 + i][2 * p + (e >> 2)][e & 3] * f;
+                        store(out + (size_t)key * a.d + in_head + p * 32 + grp * 8, y);
                     }
                 }
             }
@@ -383,8 +501,8 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
 // A tile's scores (matrix pipe) are formed beside the previous tile's softmax (vector pipe): keys
 // and values have two LDS buffers each, and the keys run one tile ahead of the values.
 // Bound: the matrix pipe beside the softmax's vector work at two waves a SIMD (2.5 us a tile).
-// Measured at d = 128: one prompt of 8192 tokens, 32 heads (687 GFLOP) 637-715 us, 0.96-1.08
-// PFLOP/s (a large bf16 product reaches 1.57); 28 ragged prompts, 20 heads 288-328 us.
+// Measured at d = 128: one prompt of 8192 tokens, 32 heads (687 GFLOP) 669-723 us, 0.95-1.03
+// PFLOP/s (a large bf16 product reaches 1.57); 28 ragged prompts, 20 heads 307-332 us.
 template <int D>
 struct LpTile {
     static constexpr int K_BYTES = LP_KB * (D + LP_ROPE) * 2;     // [64][D] keys, [64][64] rotary
@@ -429,8 +547,7 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
                          (live ? row : q0);
     // The scale enters the exponent's multiplication; a negative one is moved into the queries,
     // so that the largest score is the largest weight (and zero makes the queries zero).
-    const float cs = a.scale == 0.f ? 1.f : fabsf(a.scale) * LOG2E;
-    bf16x8 q[NK + NR];
+    bf16x8 q[NK + NR];  // (the first NK hold fp16)
     {
         const bf16* qn = reinterpret_cast<const bf16*>(a.q_nope) + (token * a.H + h) * D;
         const bf16* qp = reinterpret_cast<const bf16*>(a.q_pe) + (token * a.H + h) * LP_ROPE;
@@ -444,6 +561,29 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
         for (int f = 0; f < NK + NR; f++)
 #pragma unroll
             for (int i = 0; i < 8; i++) q[f][i] = a.scale < 0.f ? -q[f][i] : (bf16)0.f;
+    }
+    const int key_s = uniform(a.head_shift[h * 2]), value_s = uniform(a.head_shift[h * 2 + 1]);
+    float cs;  // of this lane's row, for tiles with t = 0
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int f = 0; f < NK; f++) m = max_magnitudes_of(m, q[f]);
+        int x = larger_half(m);
+        x = max(x, __shfl_xor(x, 32, WAVE)) >> 7;
+        const int row_a = x == 0 ? 0 : max(x - 127, -64);
+        const float down = exp2i(-row_a), pe_down = exp2i(key_s - row_a);
+#pragma unroll
+        for (int f = 0; f < NK; f++) {
+            f16x8 to;
+#pragma unroll
+            for (int i = 0; i < 8; i++) to[i] = (_Float16)((float)q[f][i] * down);
+            q[f] = __builtin_bit_cast(bf16x8, to);
+        }
+#pragma unroll
+        for (int f = NK; f < NK + NR; f++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) q[f][i] = (bf16)((float)q[f][i] * pe_down);
+        cs = ldexpf(a.scale == 0.f ? 1.f : fabsf(a.scale) * LOG2E, row_a - key_s);
     }
     arrived(q);
     const char* ksrc = reinterpret_cast<const char*>(a.k) +
@@ -487,6 +627,9 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
 #pragma unroll
         for (int i = 0; i < 16; i++) acc[j][i] = 0.f;
     float ref = -INFINITY, l = 0.f;  // the exponents' reference (scaled); the sum
+    int sums_t = LP_T_MIN;           // t that the sums of values are kept at
+    // Weights are taken 2^7 times as large: up to 2^(7 + LAG), and down to 2^-31 in fp16.
+    constexpr int WEIGHT_SHIFT = 7;
 
     // Scores of tile t, unscaled, and beside each pair of MFMAs a slice of other work: the
     // matrix pipe takes 32 cycles for one MFMA, in which the wave can issue eight vector
@@ -513,7 +656,12 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
         for (int f = 0; f < NF; f++) {
             if (f + AHEAD < NF) load(f + AHEAD);
 #pragma unroll
-            for (int x = 0; x < 2; x++) s[x] = mma32(k[f % (AHEAD + 1)][x], q[f], s[x]);
+            for (int x = 0; x < 2; x++) {
+                const bf16x8 y = k[f % (AHEAD + 1)][x];
+                s[x] = f < NK ? mma32(__builtin_bit_cast(f16x8, y), __builtin_bit_cast(f16x8, q[f]),
+                                      s[x])
+                              : mma32(y, q[f], s[x]);
+            }
             beside(f);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -535,20 +683,27 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
                 s[x][i] = ((here >> k) & 1) && k <= left ? s[x][i] : -INFINITY;
             }
     };
-    uint64_t exist_next = 0;
-    auto take_exist = [&]() {
+    int4 tile_next = make_int4(0, 0, 0, 0);
+    struct Tile {
+        uint64_t exist;
+        int t;
+    };
+    auto take_tile = [&]() -> Tile {
         // moved to scalar registers where nothing else is in flight: a wait for the ordinary
         // load further down would also wait for the tile loads issued behind it
-        return (uint64_t)(uint32_t)uniform((int)(exist_next >> 32)) << 32 |
-               (uint32_t)uniform((int)exist_next);
+        return {(uint64_t)(uint32_t)uniform(tile_next.y) << 32 | (uint32_t)uniform(tile_next.x),
+                uniform(tile_next.z)};
     };
+    int now_t = 0;  // of the tile whose weights come next
     // One tile: its weights from s (masked), its values added; meanwhile the next tile's scores.
     auto step = [&](int t, f32x16 (&s)[2], f32x16 (&next)[2]) {
         lds_loads_done();
-        const uint64_t exist = take_exist();  // of tile t + 1
+        const Tile after = take_tile();  // tile t + 1
+        const int tile_t = now_t;
+        now_t = after.t;
         lds_barrier();  // keys t + 1 and values t are whole; all are done with what they replace
         if (t + 2 < nt) {
-            exist_next = a.exist[kt0 + t + 2];
+            tile_next = a.tile[kt0 + t + 2];
             sched_fence();
             load_keys(t + 2);
         }
@@ -556,7 +711,11 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
         if (t >= mine) return;
         float top = -INFINITY, shift = 0.f;
         bool grown = false;
-        bf16x8 p[LP_KB / 16];
+        f16x8 p[LP_KB / 16];
+        const float cs_t = ldexpf(cs, tile_t);
+        const int raise = max(tile_t - sums_t, 0);  // of the sums' t
+        sums_t += raise;
+        const float weight_shift = (float)(WEIGHT_SHIFT + tile_t - sums_t);
         // slices 0 and 1: the tile's maximum; 2: over both halves; from 3 on: the weights
         constexpr int PER = (32 + NF - 4) / (NF - 3);
         // (behind this wave's last tile the scores are nobody's: that buffer is not being filled,
@@ -566,35 +725,38 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
 #pragma unroll
                 for (int i = 0; i < 16; i++) top = fmaxf(top, s[f][i]);
             } else if (f == 2) {
-                top = max_halves(top) * cs;
+                top = max_halves(top) * cs_t;
                 grown = top > ref + LAG;
                 const float to = grown ? top : ref;
                 shift = to == -INFINITY ? 0.f : to;  // a row with no key so far
             } else {
+                const float up = weight_shift - shift;
 #pragma unroll
                 for (int i = (f - 3) * PER; i < (f - 2) * PER && i < 32; i++) {
-                    float w = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], cs, -shift));
+                    float w = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], cs_t, up));
                     asm volatile("" : "+v"(w));  // formed here, not where it is used
                     s[i >> 4][i & 15] = w;
-                    p[i >> 3][i & 7] = (bf16)w;
+                    p[i >> 3][i & 7] = (_Float16)w;
                 }
             }
         });
-        if (__any(grown)) {
+        if (__any(grown) || raise > 0) {
             // (a row without a reference so far has sums of zero)
-            const float shrink = grown ? __builtin_amdgcn_exp2f(ref - shift) : 1.f;
+            float shrink = grown ? __builtin_amdgcn_exp2f(ref - shift) : 1.f;
             ref = grown ? shift : ref;
             l *= shrink;
+            shrink = ldexpf(shrink, -raise);
 #pragma unroll
             for (int j = 0; j < NO; j++)
 #pragma unroll
                 for (int i = 0; i < 16; i++) acc[j][i] *= shrink;
         }
         const uint32_t value = fixed(lds_offset(v_tile[t & 1]) + r_at);
-        bf16x8 v[AHEAD + 1];
+        f16x8 v[AHEAD + 1];
+        float sum = 0.f;
         constexpr int NV = LP_KB / 16 * NO;
         auto load = [&](int n) {
-            v[n % (AHEAD + 1)] = lds_get<bf16x8>((value ^ (n / NO) << 5) + n % NO * (32 * 128));
+            v[n % (AHEAD + 1)] = lds_get<f16x8>((value ^ (n / NO) << 5) + n % NO * (32 * 128));
         };
 #pragma unroll
         for (int n = 0; n < AHEAD; n++) load(n);
@@ -603,28 +765,30 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
             if (n + AHEAD < NV) load(n + AHEAD);
             acc[n % NO] = mma32(v[n % (AHEAD + 1)], p[n / NO], acc[n % NO]);
 #pragma unroll
-            for (int i = n * 32 / NV; i < (n + 1) * 32 / NV; i++) l += s[i >> 4][i & 15];
+            for (int i = n * 32 / NV; i < (n + 1) * 32 / NV; i++) sum += s[i >> 4][i & 15];
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (t + 1 < mine) mask(t + 1, exist, next);
+        l += ldexpf(sum, sums_t - tile_t);
+        if (t + 1 < mine) mask(t + 1, after.exist, next);
     };
     if (nt > 0) {
         f32x16 s0[2], s1[2];
-        exist_next = a.exist[kt0];
+        tile_next = a.tile[kt0];
         sched_fence();
         load_keys(0);
         lds_loads_done();
-        const uint64_t exist = take_exist();
+        const Tile first = take_tile();
+        now_t = first.t;
         lds_barrier();
         if (nt > 1) {
-            exist_next = a.exist[kt0 + 1];
+            tile_next = a.tile[kt0 + 1];
             sched_fence();
             load_keys(1);
         }
         load_values(0);
         if (mine > 0) {
             scores(0, s0, [](int) {});
-            mask(0, exist, s0);
+            mask(0, first.exist, s0);
         }
         for (int t = 0; t < nt; t += 2) {
             step(t, s0, s1);
@@ -632,7 +796,8 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
         }
     }
     l += __shfl_xor(l, 32, WAVE);
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros
+    // no key: zeros. (The sum holds 2^7 as the weights do.)
+    const float inv = l == 0.f ? 0.f : ldexpf(1.f / l, sums_t - value_s);
     if (live) {
         bf16* out = reinterpret_cast<bf16*>(a.o) + (token * a.H + h) * D;
 #pragma unroll
@@ -663,7 +828,8 @@ size_t latent_prefill_layout(LatentPrefillArgs* a, int64_t total_keys, void* ws)
     a->key_tile = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * (size_t)(a->n_seqs + 1)));
     a->q_tile = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * (size_t)(a->n_seqs + 1)));
     a->order = reinterpret_cast<int2*>(take(sizeof(int2) * (size_t)a->q_tiles));
-    a->exist = reinterpret_cast<uint64_t*>(take(sizeof(uint64_t) * tiles));
+    a->head_shift = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * 2 * (size_t)a->H));
+    a->tile = reinterpret_cast<int4*>(take(sizeof(int4) * tiles));
     a->k_pe = take(tiles * LP_KB * LP_ROPE * 2);
     a->k = take(tiles * LP_KB * a->d * 2 * a->H);
     a->vt = take(tiles * LP_KB * a->d * 2 * a->H);
@@ -673,7 +839,7 @@ size_t latent_prefill_layout(LatentPrefillArgs* a, int64_t total_keys, void* ws)
 hipError_t launch_latent_prefill(const LatentPrefillArgs& a, hipStream_t s) {
     (void)hipGetLastError();  // report only errors raised by this call's launches
     const dim3 block(LP_THREADS);
-    hipLaunchKernelGGL(latent_tiles_kernel, dim3(1), block, 0, s, a);
+    hipLaunchKernelGGL(latent_tiles_kernel, dim3(1u + 2u * (unsigned)a.H), block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.q_tiles == 0) return e;
     // The columns in equal runs of units, a workgroup each (one fits a CU): as many runs as end

@@ -432,8 +432,8 @@ int gdn_conv1d_silu(const void* x, const float* w, const int32_t* cu_seqlens, in
  *   - block_size is any number >= 1; pages that are not a multiple of a kernel's key tile only
  *     cost their look-up.
  * Scores, softmax statistics, weighted sums are held in fp32; with bf16 inputs the softmax
- * weights are rounded to bf16 (by 2^-8 each at most, not in the sum that divides them) as the
- * MFMA's operand, outputs by round-to-nearest-even once. */
+ * weights are rounded to bf16 (by 2^-8 each at most, not in the sum that divides them; less in
+ * gdn_latent_prefill) as the MFMA's operand, outputs by round-to-nearest-even once. */
 
 /* Largest num_heads of the attention entry points. */
 #define GDN_ATTN_MAX_HEADS 1024
@@ -571,7 +571,10 @@ int gdn_latent_prefill_workspace_bytes(const gdn_latent_dims_t* dims, int32_t n_
 
 /* Latent attention of packed new tokens over the cache, which already holds them, in the
  * expanded form: every head's keys (W_uk,h c_j, r_j) and values W_uv,h c_j are written out to
- * the workspace (bf16) and attended causally. The new tokens of request i are its last
+ * the workspace and attended causally. They and the softmax weights are rounded to 11 significant
+ * bits (fp16, scaled by powers of two by the largest latent of each 64 tokens and the head's
+ * largest weight; |c| below 2^72, and numbers far below the others of their 64 tokens keep fewer
+ * bits). The new tokens of request i are its last
  * w = cu_seqlens[i + 1] - cu_seqlens[i]; what comes before them (a cached prefix, earlier
  * chunks of the prompt) is read from its pages like they are. New token t sees the request's
  * tokens j <= seq_lens[i] - w + t that exist; zeros if there is none.
