@@ -31,12 +31,53 @@ __device__ __forceinline__ uint64_t bits4(const float x[4]) {
     return __builtin_bit_cast(uint64_t, v);
 }
 
+// The absorbed queries enter the core's products as the sum of two numbers: their rounding to bf16
+// and what that leaves, the rest, in 4 bits (fp4, e2m1) times a unit that 128 columns of a row share,
+// 2^-10 of the binade of the largest: a rest is 4 units at most, held to half a unit and a quarter
+// where it is small. One bf16 number moves a row's scores by its rounding of q', and outputs were off
+// by 0.0025 to 0.0029 (relative 2-norm; their own rounding leaves 0.0017); with the rests by 0.0019,
+// the weights' rounding. A second bf16 number would take 64 registers, which the tile of 64 rows does
+// not have. The rests cost a product for each one of the latents' scores: 80 requests, 128 heads
+// 136 -> 157 us a call, one request of 40003 tokens, 20 heads 33.7 -> 36 us.
+// Until the core writes a row's outputs, its rests lie in their place: only workers that hold a part
+// of a unit read them, and one that writes there holds all of it.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <int R>
+struct LdRest {
+    static constexpr int PER_GROUP = R / 32;  // words of 8 codes that a lane group reads
+    static constexpr int UNITS_AT = R / 8;    // float offset of the units
+    __device__ __forceinline__ static uint32_t* word(float* o_row, int grp, int f) {
+        return reinterpret_cast<uint32_t*>(o_row) + grp * PER_GROUP + f;
+    }
+};
+// The unit of 128 columns, by the largest: 2^-10 of its binade.
+__device__ __forceinline__ float rest_unit(float top) {
+    return __uint_as_float((max(__float_as_uint(top) >> 23, 11u) - 10u) << 23);
+}
+// 8 numbers to codes of a unit, and back.
+__device__ __forceinline__ uint32_t to_fp4(const float (&x)[8], float unit) {
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0], x[1], unit, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], unit, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4], x[5], unit, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6], x[7], unit, 3);
+    return c;
+}
+__device__ __forceinline__ bf16x8 from_fp4(uint32_t c, float unit) {
+    return __builtin_bit_cast(
+        bf16x8,
+        u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, unit, 0)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, unit, 1)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, unit, 2)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, unit, 3))});
+}
+
 // ---------------------------------------------------------------------------------- absorb
 // q'^T (rank x rows) = W_uk^T q_nope^T per head: a workgroup takes 128 rank columns of one
 // head's W_uk (through LDS, read back transposed as the MFMA's A operand) and 64 (request,
-// position) rows, all loads issued at once: one trip to memory. q' is rounded to bf16 as the
-// core's MFMA operand. Bound: that trip, and for many rows the weights (16.8 MB at 128 heads,
-// d = 128, rank 512). Measured: 80 rows, 128 heads 12 us; one row, 20 heads 3.4 us.
+// position) rows, all loads issued at once: one trip to memory. Bound: that trip, and for many rows
+// the weights (16.8 MB at 128 heads, d = 128, rank 512). Measured: 80 rows, 128 heads 14 us; one
+// row, 20 heads 3.7 us.
 constexpr int AB_COLS = 128, AB_TILES = 4;
 
 // LDS position of the 16-byte piece c of row n (rows of AB_COLS elements = 16 pieces): the 16
@@ -46,20 +87,21 @@ __device__ __forceinline__ int ab_place(int n, int c) {
     return n * (AB_COLS * 2) + ((c ^ (turn << 1)) << 4);
 }
 
-template <int DN>
+template <int DN, int R>
 __global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeArgs a) {
     __shared__ __align__(16) char w[DN * AB_COLS * 2];
+    __shared__ float tops[LD_WAVES][AB_TILES * 16];  // largest |q'| of a wave's columns of a row
     const int h = blockIdx.x, r0 = blockIdx.y * AB_COLS;
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
     const int col = lane & 15, grp = lane >> 4;
     const int rows = a.split.batch * a.n_pos, row0 = blockIdx.z * (AB_TILES * 16);
     const bf16* W = reinterpret_cast<const bf16*>(a.w_kv) +
-                    (size_t)h * (a.d_nope + a.d_v) * a.rank + r0;
+                    (size_t)h * (a.d_nope + a.d_v) * R + r0;
     f32x4 in[DN * 16 / LD_THREADS];
 #pragma unroll
     for (int i = 0; i < DN * 16 / LD_THREADS; i++) {
         const int x = i * LD_THREADS + tid;
-        in[i] = *reinterpret_cast<const f32x4*>(W + (size_t)(x >> 4) * a.rank + (x & 15) * 8);
+        in[i] = *reinterpret_cast<const f32x4*>(W + (size_t)(x >> 4) * R + (x & 15) * 8);
     }
     bf16x8 B[AB_TILES][DN / 32];
 #pragma unroll
@@ -88,21 +130,51 @@ __global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeA
             A[x][k] = join(lds_read_tr(w + ab_place(n, c) + x * 8),
                            lds_read_tr(w + ab_place(n + 4, c) + x * 8));
         }
+    float y[AB_TILES][8];
+#pragma unroll
+    for (int t = 0; t < AB_TILES; t++) {
+        if (row0 + t * 16 >= rows) break;
+        float top = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+            f32x4 d = zero4();
+#pragma unroll
+            for (int k = 0; k < DN / 32; k++) d = Mma<bf16>::mma(A[x][k], B[t][k], d);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                y[t][x * 4 + i] = d[i];
+                top = fmaxf(top, fabsf(d[i]));
+            }
+        }
+        top = max_groups(top);
+        if (grp == 0) tops[wave][t * 16 + col] = top;
+    }
+    __syncthreads();
+    // words of the rests through LDS (where the weights were), stored 16 bytes a lane
+    uint32_t* words = reinterpret_cast<uint32_t*>(w);  // [row][lane group][wave]
+    auto unit_of = [&](int r) {
+        return rest_unit(fmaxf(fmaxf(tops[0][r], tops[1][r]), fmaxf(tops[2][r], tops[3][r])));
+    };
 #pragma unroll
     for (int t = 0; t < AB_TILES; t++) {
         if (row0 + t * 16 >= rows) break;
         const int row = row0 + t * 16 + col;
-        f32x4 d[2];
+        float rest[8];
 #pragma unroll
-        for (int x = 0; x < 2; x++) {
-            d[x] = zero4();
-#pragma unroll
-            for (int k = 0; k < DN / 32; k++) d[x] = Mma<bf16>::mma(A[x][k], B[t][k], d[x]);
-        }
-        const float y[8] = {d[0][0], d[0][1], d[0][2], d[0][3], d[1][0], d[1][1], d[1][2], d[1][3]};
+        for (int i = 0; i < 8; i++) rest[i] = y[t][i] - (float)(bf16)y[t][i];
+        words[(t * 16 + col) * 16 + grp * 4 + wave] = to_fp4(rest, unit_of(t * 16 + col));
         if (row < rows)
-            store8<bf16>(reinterpret_cast<bf16*>(a.q_lat) + ((size_t)row * a.H + h) * a.rank + r0 +
-                             wave * 32 + grp * 8, y);
+            store8<bf16>(reinterpret_cast<bf16*>(a.q_lat) + ((size_t)row * a.H + h) * R + r0 +
+                             wave * 32 + grp * 8, y[t]);
+    }
+    __syncthreads();
+    static_assert(AB_TILES * 16 * 4 == LD_THREADS && LD_WAVES == 4, "a thread for each 16 bytes");
+    const int r = tid >> 2, row = row0 + r;
+    if (row < rows) {
+        float* o_row = a.o_lat + ((size_t)row * a.H + h) * R;
+        *reinterpret_cast<u32x4*>(LdRest<R>::word(o_row, tid & 3, r0 / 32)) =
+            *reinterpret_cast<const u32x4*>(words + tid * 4);
+        if ((tid & 3) == 0) o_row[LdRest<R>::UNITS_AT + r0 / AB_COLS] = unit_of(r);
     }
 }
 
@@ -115,13 +187,14 @@ __global__ __launch_bounds__(LD_THREADS) void latent_absorb_kernel(LatentDecodeA
 //                 reads of the very tile the scores came from.
 // So each cache row is read once from memory per row tile; from LDS a tile is read RH times as
 // keys and once as values. The next tile loads straight into the other LDS buffer meanwhile.
-// Bound: a unit's start and end (queries, the first tile's trip, results: as long as 6 tiles)
-// and, for 64 rows, a tile's LDS reads and matrix work (2.4 us) beside its trip (2.5 us).
-// Measured at rank 512: 80 requests of 100 to 12000 tokens (223 MB), 128 heads 93 us, 2.4 TB/s
-// and 580 TFLOP/s; one request of 40003 tokens (46 MB), 20 heads 18 us.
+// Bound: a unit's start and end (queries, the first tile's trip, results: as long as 6 tiles) and,
+// for 64 rows, a tile's matrix work, LDS reads and conversions of rests.
+// Measured at rank 512: 80 requests of 100 to 12000 tokens (223 MB), 128 heads 113 us, 2.0 TB/s; one
+// request of 40003 tokens (46 MB), 20 heads 19 us.
 // (64 rows with 32 rows a wave read the keys twice only, but their queries take 144 registers:
 // the compiler then spills inside the key loop, and a reload from scratch memory waits for the
-// tile loads issued before it.)
+// tile loads issued before it. As it is, 11 registers of the kernel for 64 rows of rank 512 are
+// spilled before its first unit and come back at the end of one: none inside the key loop.)
 constexpr int LD_KB = 64;
 
 template <int R>
@@ -286,25 +359,44 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
         load_tile(c0, 0, c0 + 1);
 
         bf16x8 q[NF];
+        uint32_t rest[NL];  // of the absorbed query
+        float unit[NL / 4];
         const int q_row = row0 + part * 16 + col;
         const bool live = q_row < a.rows;
         const int lim = live ? seen0 + q_row / a.H : 0;
         {
-            const size_t at = (size_t)b * a.rows + (live ? q_row : 0);
+            const size_t at = (size_t)b * a.rows + (live ? q_row : row0);
             const bf16* ql = reinterpret_cast<const bf16*>(a.q_lat) + at * R;
             const bf16* qp = reinterpret_cast<const bf16*>(a.q_pe) + at * LD_ROPE;
 #pragma unroll
             for (int f = 0; f < NF; f++)
                 q[f] = Mma<bf16>::load(f < NL ? ql + f * 32 + grp * 8
                                               : qp + (f - NL) * 32 + grp * 8);
+            float* o_row = a.o_lat + at * R;
+            typedef float units __attribute__((ext_vector_type(NL / 4)));
+#pragma unroll
+            for (int f = 0; f < NL; f += 4) {
+                const u32x4 x = *reinterpret_cast<const u32x4*>(LdRest<R>::word(o_row, grp, f));
+#pragma unroll
+                for (int i = 0; i < 4; i++) rest[f + i] = x[i];
+            }
+            const units u = *reinterpret_cast<const units*>(o_row + LdRest<R>::UNITS_AT);
+#pragma unroll
+            for (int i = 0; i < NL / 4; i++) unit[i] = u[i];
         }
         if (a.scale <= 0.f) {
+#pragma unroll
+            for (int f = 0; f < NL; f++) rest[f] = a.scale < 0.f ? rest[f] ^ 0x88888888u : 0u;
 #pragma unroll
             for (int f = 0; f < NF; f++)
 #pragma unroll
                 for (int i = 0; i < 8; i++) q[f][i] = a.scale < 0.f ? -q[f][i] : (bf16)0.f;
         }
         arrived(q);
+#pragma unroll
+        for (int f = 0; f < NL; f++) asm volatile("" : "+v"(rest[f]));
+#pragma unroll
+        for (int f = 0; f < NL / 4; f++) asm volatile("" : "+v"(unit[f]));
         f32x4 acc[RH][NT];
         float ref = -INFINITY, l = 0.f;  // this lane's row: reference, share of the sum
 #pragma unroll
@@ -338,8 +430,10 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
             f32x4 s[KS];
 #pragma unroll
             for (int x = 0; x < KS; x++) s[x] = zero4();
-            // key fragments two steps of the contraction at a time, the next two on their way
-            bf16x8 k[2][2][KS];
+            // key fragments SF steps of the contraction at a time, the next ones on their way; rests
+            // one step ahead
+            constexpr int SF = KS == 1 ? 2 : 1;
+            bf16x8 k[2][SF][KS];
             auto load_k = [&](int f, bf16x8 (&to)[KS]) {
 #pragma unroll
                 for (int x = 0; x < KS; x++)  // (16 rows on, the pieces are turned alike)
@@ -347,20 +441,34 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
                         f < NL ? (k_here ^ (f & 3) << 6) + (f >> 2) * 256 + x * (16 * X::LAT)
                                : (pe_here ^ (f - NL) << 6) + x * (16 * LD_ROPE * 2));
             };
-            load_k(0, k[0][0]);
-            load_k(1, k[0][1]);
 #pragma unroll
-            for (int f = 0; f < NF; f += 2) {
-                const int now = (f >> 1) & 1;
-                if (f + 2 < NF) {
-                    load_k(f + 2, k[now ^ 1][0]);
-                    load_k(f + 3, k[now ^ 1][1]);
+            for (int e = 0; e < SF; e++) load_k(e, k[0][e]);
+            auto rest_at = [&](int f) {
+                // (converted anew for every tile: the compiler would keep all of them)
+                asm volatile("" : "+v"(rest[f]));
+                return from_fp4(rest[f], unit[f / 4]);
+            };
+            bf16x8 low_next = rest_at(0);
+#pragma unroll
+            for (int f = 0; f < NF; f += SF) {
+                const int now = f / SF & 1;
+                if (f + SF < NF) {
+#pragma unroll
+                    for (int e = 0; e < SF; e++) load_k(f + SF + e, k[now ^ 1][e]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int e = 0; e < 2; e++)
+                for (int e = 0; e < SF; e++) {
+                    const bf16x8 low = low_next;
+                    if (f + e + 1 < NL) low_next = rest_at(f + e + 1);
 #pragma unroll
                     for (int x = 0; x < KS; x++) s[x] = Mma<bf16>::mma(k[now][e][x], q[f + e], s[x]);
+                    if (f + e < NL) {
+#pragma unroll
+                        for (int x = 0; x < KS; x++)
+                            s[x] = Mma<bf16>::mma(k[now][e][x], low, s[x]);
+                    }
+                }
             }
             const int key0 = c * LD_KB + key_row;
             if (exist != ALL || key0 + KEYS > seen0) {
@@ -428,8 +536,8 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
             for (int x = 0; x < KS; x++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) l += p[x][i];
-            // values four fragments at a time, the next four on their way
-            constexpr int VB = NT < 4 ? NT : 4, NB = LD_KB / 32 * (NT / VB);
+            // values VB fragments at a time, the next ones on their way
+            constexpr int VB = RH == 4 ? 2 : NT < 4 ? NT : 4, NB = LD_KB / 32 * (NT / VB);
             bf16x8 v[2][VB];
             auto load_v = [&](int n) {
                 const int ks = n / (NT / VB), j0 = n % (NT / VB) * VB;
@@ -442,13 +550,15 @@ __global__ __launch_bounds__((LdWaves<RH, KS>::WAVES * WAVE)) void latent_core_k
                 }
             };
             load_v(0);
+            bf16x8 w[RH];
 #pragma unroll
             for (int n = 0; n < NB; n++) {
                 const int ks = n / (NT / VB), j0 = n % (NT / VB) * VB;
-                bf16x8 w[RH];
+                if (j0 == 0) {
 #pragma unroll
-                for (int t = 0; t < RH; t++)
-                    w[t] = lds_get<bf16x8>((weights(t) + p_here) ^ ks << 6);
+                    for (int t = 0; t < RH; t++)
+                        w[t] = lds_get<bf16x8>((weights(t) + p_here) ^ ks << 6);
+                }
                 if (n + 1 < NB) load_v(n + 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -590,11 +700,11 @@ __global__ __launch_bounds__(LD_THREADS, 2) void latent_up_kernel(LatentDecodeAr
     }
 }
 
-template <int DN>
+template <int DN, int R>
 void run_absorb(const LatentDecodeArgs& a, hipStream_t s) {
     const int tiles = (a.split.batch * a.n_pos + 16 * AB_TILES - 1) / (16 * AB_TILES);
-    hipLaunchKernelGGL(latent_absorb_kernel<DN>,
-                       dim3((unsigned)a.H, (unsigned)(a.rank / AB_COLS), (unsigned)tiles),
+    hipLaunchKernelGGL((latent_absorb_kernel<DN, R>),
+                       dim3((unsigned)a.H, (unsigned)(R / AB_COLS), (unsigned)tiles),
                        dim3(LD_THREADS), 0, s, a);
 }
 
@@ -625,7 +735,11 @@ hipError_t run_up(const LatentDecodeArgs& a, hipStream_t s) {
 
 template <int R>
 hipError_t run_rank(const LatentDecodeArgs& a, hipStream_t s) {
-    hipError_t e = run_core<R>(a, s);
+    if (a.d_nope == 128) run_absorb<128, R>(a, s);
+    else run_absorb<64, R>(a, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    e = run_core<R>(a, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(latent_join_kernel<R>, dim3(join_grid(a.join)), dim3(JOIN_THREADS),
                        0, s, a);
@@ -674,10 +788,6 @@ size_t latent_decode_layout(LatentDecodeArgs* a, void* ws) {
 
 hipError_t launch_latent_decode(const LatentDecodeArgs& a, hipStream_t s) {
     (void)hipGetLastError();  // report only errors raised by this call's launches
-    if (a.d_nope == 128) run_absorb<128>(a, s);
-    else run_absorb<64>(a, s);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
     return a.rank == 512 ? run_rank<512>(a, s) : run_rank<256>(a, s);
 }
 

@@ -555,8 +555,9 @@ int gdn_latent_decode_workspace_bytes(const gdn_latent_dims_t* dims, int32_t bat
  *   cache       [n_blocks, block_size, rank + d_rope]
  *   block_table [batch, max_blocks], seq_lens [batch] int32 (device);  n_pos 1 .. GDN_SPEC_MAX_POS
  *   o           [batch, n_pos, num_heads, d_v]
- * all bf16. W_uk^T q_nope is rounded to bf16 as an MFMA operand; the softmax-weighted latents
- * enter theirs as the sum of two bf16 numbers. Workspace, determinism and the newest tokens'
+ * all bf16. W_uk^T q_nope enters its product as the sum of a bf16 and a 4-bit number (errors of
+ * about a tenth of a bf16 rounding's), the softmax-weighted latents theirs as the sum of two bf16
+ * numbers. Workspace, determinism and the newest tokens'
  * values as in gdn_paged_decode. */
 int gdn_latent_decode(const gdn_latent_dims_t* dims, const void* q_nope, const void* q_pe,
                       const void* w_kv, const void* cache, int32_t n_blocks, int32_t block_size,

@@ -1,6 +1,6 @@
-"""gdn_latent_prefill over the range of its bf16 inputs: latents, weights and queries far from 1, in
-tiles of 64 keys that differ by many powers of two, which its fp16 keys, values and weights have
-to be scaled for."""
+"""The latent forms over the range of their bf16 inputs: latents, weights and queries far from 1, in
+tiles of 64 keys that differ by many powers of two. gdn_latent_prefill has to scale its fp16 keys,
+values and weights for them, gdn_latent_decode the 4-bit rests of its absorbed queries."""
 import pytest
 import torch
 
@@ -113,3 +113,49 @@ def test_a_bad_weight_spoils_its_own_dim_only(value):
     keep[1, 5] = False
     assert torch.equal(got[:, keep], want[:, keep])
     assert not torch.isfinite(got[:, 1, 5].float()).any()
+
+
+# ---------------------------------------------------------------------------------- decode
+def _decode(seed, R, d, H, P):
+    return list(lat._decode_case(seed, [130, 70, 0, 5], P, H, R, d, 16, poison=False))
+
+
+@pytest.mark.parametrize("R,d,H,P", [(512, 128, 3, 1), (256, 64, 20, 2), (512, 64, 40, 2)])
+@pytest.mark.parametrize("power", [60, -60, -110])
+def test_decode_queries_of_any_size(R, d, H, P, power):
+    say(f"case ranges decode queries R={R} 2^{power}")
+    case = _decode(20, R, d, H, P)
+    case[0] *= 2.0 ** power
+    case[1] *= 2.0 ** power
+    case[6] *= 2.0 ** -power
+    lat._check_decode(tuple(case))
+
+
+@pytest.mark.parametrize("power", [20, -20, 6])
+def test_decode_columns_of_any_size(power):
+    """Columns of the latents and of the weights that differ by powers of two that cancel: every
+    absorbed query's number counts, the small ones beside the large."""
+    say(f"case ranges decode columns 2^{power}")
+    case = _decode(21, 512, 128, 20, 1)
+    for at in (slice(0, 40), slice(130, 131), slice(300, 420)):
+        case[2][:, :128, at] *= 2.0 ** power
+        case[3][..., at] *= 2.0 ** -power
+    case[2][:, 128:] *= 2.0 ** -abs(power)     # (the values are not what is looked at)
+    lat._check_decode(tuple(case))
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_decode_bad_numbers_stay_in_their_row(value):
+    say(f"case ranges decode {value}")
+    case = _decode(22, 512, 128, 20, 2)
+    want = lat._run_decode(tuple(case))
+    bad = list(case)
+    bad[0] = case[0].clone()
+    bad[0][1, 1, 7, 5] = value
+    bad[0][0, 0, 3] = 0.0
+    got = lat._run_decode(tuple(bad))
+    keep = torch.ones(got.shape[:3], dtype=torch.bool)
+    keep[1, 1, 7] = keep[0, 0, 3] = False
+    assert torch.equal(got[keep], want[keep])
+    assert not torch.isfinite(got[1, 1, 7].float()).any()
+    assert torch.isfinite(got[0, 0, 3].float()).all()
