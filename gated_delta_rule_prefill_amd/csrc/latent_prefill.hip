@@ -39,36 +39,42 @@ __device__ __forceinline__ f32x16 mma32(f16x8 a, f16x8 b, f32x16 c) {
 // Written-out keys and values, and the softmax weights, are the roundings that this form makes
 // between its inputs and its outputs. They are kept in fp16 (11 significant bits): with bf16
 // outputs were off by 0.0030 (relative 2-norm; 0.0017 is their own rounding), with fp16 by 0.0017.
-// A call takes 4 % longer: the matrix pipe draws more power (a library product of 8192^3 reaches
-// 1.41 PFLOP/s in bf16 and 1.34 in fp16). fp16's range is made to do by exact scalings by powers of
-// two. With |c| < 2^(t + 8) for the latents of a key tile, t a multiple of 16, and
-// |w| < 2^(x + 1) for a head's rows of w_kv, a key or value is below rank 2^(t + x + 9); it is
-// written times 2^(s - t) with s = 6 - log2 rank - x, that is below 2^15. Tiles whose largest latent
-// lies between 2^-8 and 2^8 (a normalised one does) have t = 0, and with weights of about
-// rank^-1/2 s is about 0 as well. What is below 2^-14 then is held to 2^-25: that is 2^-15 of a
-// typical number of the tile (2^-8.5 of its bound) where the latents are smallest for their t.
+// A call takes 5 % longer, mostly because the matrix pipe draws more power (a library product of
+// 8192^3 reaches 1.41 PFLOP/s in bf16 and 1.34 in fp16). fp16's range is made to do by exact
+// scalings by powers of two. With |c| < 2^(t + 6) for the latents of a key tile, t a multiple of 8,
+// and |w| < 2^(x + 1) for a head's rows of w_kv, a key or value is below rank 2^(t + x + 7); it is
+// written times 2^(s - t) with s = 8 - log2 rank - x, that is below 2^15. Tiles whose largest
+// latent lies between 2^-2 and 2^6 (a normalised one does) have t = 0, and with weights of about
+// rank^-1/2 s is about 2. A tile's typical number (2^-8.5 of the bound) is then 2^-2 at least, and
+// one 2^12 times smaller still has as many bits as in bf16.
 //   scores   2^(a - s + t) (q 2^-a . k 2^(s - t) + q_pe 2^(s - a) . r 2^-t), 2^a by a row's largest
 //            |q|: its fp16 numbers are below 2
-//   outputs  over tiles with different t, sums are kept at the largest so far
-constexpr int LP_T_MIN = -48, LP_T_MAX = 64;  // (weights of tiles 2^112 apart stay in fp32's range)
+//   outputs  a row's sums are kept at the t of the last tile added; a tile whose t the range of the
+//            sums does not reach could not add 2^-64 of them, and is left out
+constexpr int LP_T_MIN = -48, LP_T_MAX = 64;
 
 __device__ __forceinline__ float exp2i(int e) { return ldexpf(1.f, e); }
-// Larger magnitudes of two pairs of bf16 numbers, as bits; infinities and NaN in x do not count
-// (they make up what they reach, and must not take the others' bits).
+// Larger magnitudes of two pairs of bf16 numbers, as bits.
 __device__ __forceinline__ uint32_t max_magnitudes(uint32_t most, uint32_t x) {
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
-    u16x2 v = __builtin_bit_cast(u16x2, x & 0x7fff7fffu);
-    v &= ~__builtin_bit_cast(u16x2, __builtin_bit_cast(i16x2, v + (uint16_t)0x80) >> (int16_t)15);
     return __builtin_bit_cast(uint32_t,
-                              __builtin_elementwise_max(__builtin_bit_cast(u16x2, most), v));
+                              __builtin_elementwise_max(__builtin_bit_cast(u16x2, most),
+                                                        __builtin_bit_cast(u16x2, x & 0x7fff7fffu)));
 }
-template <typename V>
+// x without infinities and NaN: they make up what they reach, and must not take the others' bits.
+__device__ __forceinline__ uint32_t finite_magnitudes(uint32_t x) {
+    x &= 0x7fff7fffu;
+    uint32_t no;  // from 0x7f80 on, 0x80 more are negative
+    asm("v_pk_ashrrev_i16 %0, %1, %2" : "=v"(no) : "s"(0x000f000fu), "v"(x + 0x00800080u));
+    return x & ~no;
+}
+template <bool FINITE, typename V>
 __device__ __forceinline__ uint32_t max_magnitudes_of(uint32_t most, V eight) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     const u32x4 x = __builtin_bit_cast(u32x4, eight);
 #pragma unroll
-    for (int i = 0; i < 4; i++) most = max_magnitudes(most, x[i]);
+    for (int i = 0; i < 4; i++)
+        most = max_magnitudes(most, FINITE ? finite_magnitudes(x[i]) : x[i]);
     return most;
 }
 __device__ __forceinline__ int larger_half(uint32_t most) {
@@ -82,7 +88,7 @@ __device__ __forceinline__ int wave_max(int x) {
 // t by the largest magnitude of a tile's latents (bf16 bits).
 __device__ __forceinline__ int lp_shift(int bits) {
     if (bits == 0) return 0;
-    const int t = ((bits >> 7) - 127 + 8) & ~15;
+    const int t = ((bits >> 7) - 127 + 2) & ~7;
     return min(max(t, LP_T_MIN), LP_T_MAX);
 }
 
@@ -121,14 +127,19 @@ __device__ __forceinline__ int lp_key_tiles(const LatentPrefillArgs& a, int i, i
 // ---------------------------------------------------------------------------------- tables
 // Prefix sums of each request's key and query tiles, cut off at the host's bounds (lengths
 // that break the contract then lose keys or rows, never memory): the first workgroup. 3 us.
-// The others: s of a head's keys or values, from its largest weight; 5.5 us in all.
+// The others: s of a head's keys or values, from its largest weight; 7 us in all.
 __device__ __forceinline__ void lp_head_shift(const LatentPrefillArgs& a, int n) {
     __shared__ int most[LP_WAVES];
     const int rows = a.d * a.rank / 8;  // pieces of 8 weights
     const f32x4* w = reinterpret_cast<const f32x4*>(a.w_kv) + (size_t)n * rows;
     uint32_t m = 0;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < rows; i += LP_THREADS) m = max_magnitudes_of(m, w[i]);
+    for (int i = threadIdx.x; i < rows; i += 8 * LP_THREADS) {  // (2048 pieces or a multiple)
+        f32x4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) x[k] = w[i + k * LP_THREADS];
+#pragma unroll
+        for (int k = 0; k < 8; k++) m = max_magnitudes_of<true>(m, x[k]);
+    }
     const int mine = wave_max(larger_half(m));
     if (lane_id() == 0) most[wave_id()] = mine;
     __syncthreads();
@@ -137,7 +148,7 @@ __device__ __forceinline__ void lp_head_shift(const LatentPrefillArgs& a, int n)
 #pragma unroll
     for (int i = 1; i < LP_WAVES; i++) x = max(x, most[i]);
     x = min(max((x >> 7) - 127, -80), 80);
-    a.head_shift[n] = 6 - (a.rank == 512 ? 9 : 8) - x;
+    a.head_shift[n] = 8 - (a.rank == 512 ? 9 : 8) - x;
 }
 __global__ __launch_bounds__(LP_THREADS) void latent_tiles_kernel(LatentPrefillArgs a) {
     __shared__ int64_t part[LP_WAVES][2];
@@ -314,7 +325,7 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
         for (int r = 0; r < 16; r += 64 / PIECES) {
             const uint32_t row = r + lane / PIECES;
             const bool absent = __shfl(flagged, row, WAVE) >> 31;
-            const uint32_t x = max_magnitudes_of(
+            const uint32_t x = max_magnitudes_of<true>(
                 0, lds_get<f32x4>(lds_offset(lat) + (wave * 16 + row) * ROW + lane % PIECES * 16));
             m = max_magnitudes(m, absent ? 0u : x);
         }
@@ -501,8 +512,8 @@ __global__ __launch_bounds__(EX_THREADS, 2) void latent_expand_kernel(LatentPref
 // A tile's scores (matrix pipe) are formed beside the previous tile's softmax (vector pipe): keys
 // and values have two LDS buffers each, and the keys run one tile ahead of the values.
 // Bound: the matrix pipe beside the softmax's vector work at two waves a SIMD (2.5 us a tile).
-// Measured at d = 128: one prompt of 8192 tokens, 32 heads (687 GFLOP) 669-723 us, 0.95-1.03
-// PFLOP/s (a large bf16 product reaches 1.57); 28 ragged prompts, 20 heads 307-332 us.
+// Measured at d = 128: one prompt of 8192 tokens, 32 heads (687 GFLOP) 654-725 us, 0.95-1.05
+// PFLOP/s (a large bf16 product reaches 1.57); 28 ragged prompts, 20 heads 299-332 us.
 template <int D>
 struct LpTile {
     static constexpr int K_BYTES = LP_KB * (D + LP_ROPE) * 2;     // [64][D] keys, [64][64] rotary
@@ -567,10 +578,10 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
     {
         uint32_t m = 0;
 #pragma unroll
-        for (int f = 0; f < NK; f++) m = max_magnitudes_of(m, q[f]);
+        for (int f = 0; f < NK; f++) m = max_magnitudes_of<false>(m, q[f]);
         int x = larger_half(m);
         x = max(x, __shfl_xor(x, 32, WAVE)) >> 7;
-        const int row_a = x == 0 ? 0 : max(x - 127, -64);
+        const int row_a = x == 0 ? 0 : min(max(x - 127, -64), 127);
         const float down = exp2i(-row_a), pe_down = exp2i(key_s - row_a);
 #pragma unroll
         for (int f = 0; f < NK; f++) {
@@ -627,9 +638,9 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
 #pragma unroll
         for (int i = 0; i < 16; i++) acc[j][i] = 0.f;
     float ref = -INFINITY, l = 0.f;  // the exponents' reference (scaled); the sum
-    int sums_t = LP_T_MIN;           // t that the sums of values are kept at
+    int sums_t = 0;                  // t that this row's sums of values are kept at
     // Weights are taken 2^7 times as large: up to 2^(7 + LAG), and down to 2^-31 in fp16.
-    constexpr int WEIGHT_SHIFT = 7;
+    constexpr float WEIGHT_SHIFT = 7.f;
 
     // Scores of tile t, unscaled, and beside each pair of MFMAs a slice of other work: the
     // matrix pipe takes 32 cycles for one MFMA, in which the wave can issue eight vector
@@ -711,11 +722,7 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
         if (t >= mine) return;
         float top = -INFINITY, shift = 0.f;
         bool grown = false;
-        f16x8 p[LP_KB / 16];
         const float cs_t = ldexpf(cs, tile_t);
-        const int raise = max(tile_t - sums_t, 0);  // of the sums' t
-        sums_t += raise;
-        const float weight_shift = (float)(WEIGHT_SHIFT + tile_t - sums_t);
         // slices 0 and 1: the tile's maximum; 2: over both halves; from 3 on: the weights
         constexpr int PER = (32 + NF - 4) / (NF - 3);
         // (behind this wave's last tile the scores are nobody's: that buffer is not being filled,
@@ -730,30 +737,55 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
                 const float to = grown ? top : ref;
                 shift = to == -INFINITY ? 0.f : to;  // a row with no key so far
             } else {
-                const float up = weight_shift - shift;
+                const float up = WEIGHT_SHIFT - shift;
 #pragma unroll
                 for (int i = (f - 3) * PER; i < (f - 2) * PER && i < 32; i++) {
                     float w = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], cs_t, up));
                     asm volatile("" : "+v"(w));  // formed here, not where it is used
                     s[i >> 4][i & 15] = w;
-                    p[i >> 3][i & 7] = (_Float16)w;
                 }
             }
         });
-        if (__any(grown) || raise > 0) {
+        if (__any(grown)) {
             // (a row without a reference so far has sums of zero)
-            float shrink = grown ? __builtin_amdgcn_exp2f(ref - shift) : 1.f;
+            const float shrink = grown ? __builtin_amdgcn_exp2f(ref - shift) : 1.f;
             ref = grown ? shift : ref;
             l *= shrink;
-            shrink = ldexpf(shrink, -raise);
 #pragma unroll
             for (int j = 0; j < NO; j++)
 #pragma unroll
                 for (int i = 0; i < 16; i++) acc[j][i] *= shrink;
         }
+        if (__any(sums_t != tile_t)) {
+            float most = 0.f;
+#pragma unroll
+            for (int j = 0; j < NO; j++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) most = fmaxf(most, fabsf(acc[j][i]));
+            const int to = ldexpf(max_halves(most), sums_t - tile_t) < 0x1p100f ? tile_t : sums_t;
+            const float f = exp2i(sums_t - to);
+#pragma unroll
+            for (int j = 0; j < NO; j++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) acc[j][i] *= f;
+            if (to != tile_t) {  // this tile's share would be lost in the sums
+#pragma unroll
+                for (int i = 0; i < 32; i++) {
+                    l += s[i >> 4][i & 15];
+                    s[i >> 4][i & 15] = 0.f;
+                }
+            }
+            sums_t = to;
+        }
         const uint32_t value = fixed(lds_offset(v_tile[t & 1]) + r_at);
+        auto weights = [&](int n) {  // 8 of them, an operand
+            f16x8 w;
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[i] = (_Float16)s[n >> 1][(n & 1) * 8 + i];
+            return w;
+        };
+        f16x8 p[4] = {weights(0), weights(1), weights(2), weights(3)};
         f16x8 v[AHEAD + 1];
-        float sum = 0.f;
         constexpr int NV = LP_KB / 16 * NO;
         auto load = [&](int n) {
             v[n % (AHEAD + 1)] = lds_get<f16x8>((value ^ (n / NO) << 5) + n % NO * (32 * 128));
@@ -765,10 +797,9 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
             if (n + AHEAD < NV) load(n + AHEAD);
             acc[n % NO] = mma32(v[n % (AHEAD + 1)], p[n / NO], acc[n % NO]);
 #pragma unroll
-            for (int i = n * 32 / NV; i < (n + 1) * 32 / NV; i++) sum += s[i >> 4][i & 15];
+            for (int i = n * 32 / NV; i < (n + 1) * 32 / NV; i++) l += s[i >> 4][i & 15];
             __builtin_amdgcn_sched_barrier(0);
         }
-        l += ldexpf(sum, sums_t - tile_t);
         if (t + 1 < mine) mask(t + 1, after.exist, next);
     };
     if (nt > 0) {

@@ -574,7 +574,7 @@ int gdn_latent_prefill_workspace_bytes(const gdn_latent_dims_t* dims, int32_t n_
  * expanded form: every head's keys (W_uk,h c_j, r_j) and values W_uv,h c_j are written out to
  * the workspace and attended causally. They and the softmax weights are rounded to 11 significant
  * bits (fp16, scaled by powers of two by the largest latent of each 64 tokens and the head's
- * largest weight; |c| below 2^72, and numbers far below the others of their 64 tokens keep fewer
+ * largest weight; |c| below 2^70, and numbers far below the others of their 64 tokens keep fewer
  * bits). The new tokens of request i are its last
  * w = cu_seqlens[i + 1] - cu_seqlens[i]; what comes before them (a cached prefix, earlier
  * chunks of the prompt) is read from its pages like they are. New token t sees the request's

@@ -38,6 +38,24 @@ def test_latents_of_any_size(R, d, powers):
     lat._check_prefill(tuple(case), every=4)
 
 
+@pytest.mark.parametrize("powers", [[20, 0, 0, 0, 0, 0], [0, 50, 0, 0, 0, 0], [-30, 30, -30, 0, 0, 0],
+                                    [0, 60, -40, 60, -40, 0], [12, 0, 12, 0, 12, 0]])
+def test_tiles_of_large_latents_that_no_query_looks_at(powers):
+    """Their weights are 2^-100 or less of the others': outputs are those of the small tiles."""
+    say(f"case ranges ignored {powers}")
+    R = 512
+    case, lens = _case(11, R, 128, 2)
+    for i, n in enumerate(lens):
+        for t in range(0, n, 64):
+            rows = _rows(case[4], i, t, min(t + 64, n))
+            p = powers[(t // 64) % len(powers)]
+            case[3][rows[0], rows[1], :R] *= 2.0 ** p
+            case[3][rows[0], rows[1], R] = 0.0 if p <= min(powers) else -1500.0
+    case[0].zero_()
+    case[1][..., 0] = 1.0
+    lat._check_prefill(tuple(case), every=3)
+
+
 @pytest.mark.parametrize("power", [30, -30, 12])
 def test_weights_and_queries_of_any_size(power):
     """Heads whose key weights and queries differ by powers of two that cancel, value weights
