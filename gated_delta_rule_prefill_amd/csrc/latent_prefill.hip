@@ -237,9 +237,9 @@ __device__ void lp_order(const LatentPrefillArgs& a, int tid, int threads) {
 // that a lane holds 4 dims of a key; for values the latents are, so that it holds 4 keys of a
 // dim: each is stored along its rows in memory order, and the values come out transposed. Keys
 // that do not exist are stored as zeros.
-// Bound: by no one thing. Without its stores (2 d x 2 bytes a key and head) a call takes a fifth
-// less time, without its weight loads a fifth less, without its LDS reads the same; the matrix
-// pipe is busy a third of the time. Measured at rank 512, d = 128: 8192 keys, 32 heads (69 GFLOP)
+// Bound: its two waves a SIMD wait for weights and for room to store. Without its stores (2 d x 2
+// bytes a key and head) a call takes a fifth less time, without its weight loads a fifth less,
+// without its LDS reads the same; the matrix pipe is busy a third of the time. Measured at rank 512, d = 128: 8192 keys, 32 heads (69 GFLOP)
 // 91-107 us, 30124 keys of 28 requests, 20 heads (158 GFLOP) 207-239 us: 640-760 TFLOP/s.
 constexpr int EX_THREADS = 512, EX_WAVES = EX_THREADS / WAVE;
 constexpr int EX_M = 128;              // keys of a workgroup

@@ -471,7 +471,7 @@ size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
     a->split.units = a->kv_heads;
     // (128 requests of 30 to 30000 tokens, 4 KV heads: 204 us a call with 0, 201 with 1, 200
-    // with 2)
+    // with 2; 1 and 2 are within the spread of runs)
     a->split.extra = 2;
     const int cus = device_cu_count();
     // Two workgroups a CU hide each other's starts, where they fit; with long units, whose starts

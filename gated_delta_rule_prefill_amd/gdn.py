@@ -421,8 +421,7 @@ def gdn_conv1d_silu(x, w, cu_seqlens, planes=1, y=None, stream=None):
 # ------------------------------------------------- paged softmax attention (hybrid models)
 # These calls are short (a decode step's bookkeeping runs 4 us on the GPU), so the checks are
 # kept to a few attribute reads per tensor; a failed one works out its message afterwards.
-# Private names save 1.2 us a call; a torch without a GPU backend lacks them and imports this all the
-# same.
+# Private names save 1.2 us a call; a torch without a GPU backend lacks them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",  # handle of a device's current stream
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)

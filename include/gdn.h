@@ -454,7 +454,8 @@ int gdn_conv1d_silu(const void* x, const float* w, const int32_t* cu_seqlens, in
  *   counts     [2] int32: cu_seqlens[n], and the number of pages asked of the free list (more
  *              than n_free when it was too short; the first min of both were handed out)
  * If the new tokens exceed max_tokens, the tokens from max_tokens on get no slot, and pages
- * that start at one of them are not entered into the table; counts[0] tells.
+ * that start at one of them are not entered into the table; counts[0] tells. cu_seqlens and
+ * seq_lens count these tokens all the same.
  *   ctx_lens, new_lens [n] int32; free_blocks [n_free] int32 (device; not changed; may be the
  *   rest of a longer list: 4-byte alignment will do);
  *   block_table [n, max_blocks] int32 (device), updated in place. n, max_blocks, n_free and
