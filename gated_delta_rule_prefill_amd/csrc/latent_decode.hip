@@ -34,11 +34,11 @@ __device__ __forceinline__ uint64_t bits4(const float x[4]) {
 // The absorbed queries enter the core's products as the sum of two numbers: their rounding to bf16
 // and what that leaves, the rest, in 4 bits (fp4, e2m1) times a unit that 128 columns of a row
 // share, 2^-10 of the binade of the largest: a rest is 4 units at most, held to half a unit, to a
-// quarter where it is small. One bf16 number moves a row's scores by its rounding of q', and outputs were
-// off by 0.0025 to 0.0029 (relative 2-norm; their own rounding leaves 0.0017); with the rests by
-// 0.0019, the weights' rounding. A second bf16 number would take 64 registers, which the tile of 64
-// rows does not have. The rests cost a product for each one of the latents' scores: 80 requests, 128 heads
-// 136 -> 157 us a call, one request of 40003 tokens, 20 heads 33.7 -> 36 us.
+// quarter where it is small. One bf16 number moves a row's scores by its rounding of q', and
+// outputs were off by 0.0025 to 0.0029 (relative 2-norm; their own rounding leaves 0.0017); with
+// the rests by 0.0019, the weights' rounding. A second bf16 number would take 64 registers, which
+// the tile of 64 rows does not have. The rests cost a product for each one of the latents' scores:
+// 80 requests, 128 heads 136 -> 157 us a call, one request of 40003 tokens, 20 heads 33.7 -> 36 us.
 // Until the core writes a row's outputs, its rests lie in their place: only workers that hold a part
 // of a unit read them, and one that writes there holds all of it.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -758,10 +758,11 @@ size_t latent_decode_layout(LatentDecodeArgs* a, void* ws) {
     a->rt = tiles > 2 ? 4 : tiles;
     a->row_tiles = (tiles + a->rt - 1) / a->rt;
     a->split.units = 1;
-    // A unit's queries, first tile and results take as long as about 6 chunks (10 us) for tiles of 64
-    // rows at rank 512: 80 requests of 100 to 12000 tokens, 128 heads, took 175 us a call with 0, 164
-    // with 1, 149 with 4, 144.5 with 6, 151 with 8 and 150 with 12 (one product a score then). Smaller
-    // tiles and rank 256 start and end sooner; they were not measured and use the same number.
+    // A unit's queries, first tile and results take as long as about 6 chunks (10 us) for tiles of
+    // 64 rows at rank 512: 80 requests of 100 to 12000 tokens, 128 heads, took 175 us a call with
+    // 0, 164 with 1, 149 with 4, 144.5 with 6, 151 with 8 and 150 with 12 (one product a score
+    // then). Smaller tiles and rank 256 start and end sooner; they were not measured and use the
+    // same number.
     a->split.extra = SPLIT_EXTRA;
     a->split.halve = 0;  // a tile's buffers leave room for one workgroup a CU
     const int cus = device_cu_count();

@@ -239,8 +239,9 @@ __device__ void lp_order(const LatentPrefillArgs& a, int tid, int threads) {
 // that do not exist are stored as zeros.
 // Bound: its two waves a SIMD wait for weights and for room to store. Without its stores (2 d x 2
 // bytes a key and head) a call takes a fifth less time, without its weight loads a fifth less,
-// without its LDS reads the same; the matrix pipe is busy a third of the time. Measured at rank 512, d = 128: 8192 keys, 32 heads (69 GFLOP)
-// 91-107 us, 30124 keys of 28 requests, 20 heads (158 GFLOP) 207-239 us: 640-760 TFLOP/s.
+// without its LDS reads the same; the matrix pipe is busy a third of the time. Measured at rank
+// 512, d = 128: 8192 keys, 32 heads (69 GFLOP) 91-107 us, 30124 keys of 28 requests, 20 heads (158
+// GFLOP) 207-239 us: 640-760 TFLOP/s.
 constexpr int EX_THREADS = 512, EX_WAVES = EX_THREADS / WAVE;
 constexpr int EX_M = 128;              // keys of a workgroup
 constexpr int EX_N = 64;               // columns of a wave
@@ -581,7 +582,8 @@ __global__ __launch_bounds__(LP_THREADS, 2) void latent_attend_kernel(LatentPref
         for (int f = 0; f < NK; f++) m = max_magnitudes_of<false>(m, q[f]);
         int x = larger_half(m);
         x = max(x, __shfl_xor(x, 32, WAVE)) >> 7;
-        const int row_a = x == 0 ? 0 : min(max(x - 127, -64), 127);
+        // (the rotary part's 2^(s - a) is kept in range: by then the rest of a score is nothing)
+        const int row_a = min(max(x == 0 ? 0 : x - 127, key_s - 60), 127);
         const float down = exp2i(-row_a), pe_down = exp2i(key_s - row_a);
 #pragma unroll
         for (int f = 0; f < NK; f++) {

@@ -80,6 +80,17 @@ def test_scales_that_cancel_the_queries(power):
     lat._check_prefill(tuple(case), every=4)
 
 
+@pytest.mark.parametrize("power", [-60, -100, 0])
+def test_key_weights_that_vanish(power):
+    """Scores of the rotary keys alone, beside queries of any size."""
+    say(f"case ranges vanishing weights 2^{power}")
+    for weights in (0.0, 2.0 ** -100):
+        case, _ = _case(12, 256, 64, 2)
+        case[2][:, :64] *= weights
+        case[0] *= 2.0 ** power
+        lat._check_prefill(tuple(case), every=4)
+
+
 def test_zeros():
     """No latent, no weight or no query that could say how large the others may be."""
     say("case ranges zeros")
