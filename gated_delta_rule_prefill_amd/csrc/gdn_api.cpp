@@ -546,6 +546,124 @@ int debug_distinct_cache_slots(const int64_t* slot_map, int32_t tokens, int64_t 
     } while (0)
 #endif
 
+// Debug builds: the destinations of one call's pairs are distinct, and none is a source (the pairs
+// of one launch are not ordered). Pairs that the kernels skip do not count.
+#ifdef GDN_DEBUG_CHECKS
+int debug_destinations(const int32_t* src, const int32_t* dst, int32_t n, const int32_t* count,
+                       int32_t limit, void* stream, const char* what) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    std::vector<int32_t> a, b;
+    std::vector<bool> seen;
+    try {
+        a.resize((size_t)n);
+        b.resize((size_t)n);
+        seen.resize((size_t)limit);
+    } catch (const std::bad_alloc&) {  // no exception leaves a C entry point
+        return fail(GDN_ERR_LAUNCH, "%s: debug check: out of host memory", what);
+    }
+    int32_t most = n;
+    if (hipMemcpyAsync(a.data(), src, sizeof(int32_t) * a.size(), hipMemcpyDeviceToHost, s) !=
+            hipSuccess ||
+        hipMemcpyAsync(b.data(), dst, sizeof(int32_t) * b.size(), hipMemcpyDeviceToHost, s) !=
+            hipSuccess ||
+        (count != nullptr && hipMemcpyAsync(&most, count, sizeof(int32_t), hipMemcpyDeviceToHost,
+                                            s) != hipSuccess) ||
+        hipStreamSynchronize(s) != hipSuccess) {
+        (void)hipGetLastError();
+        return fail(GDN_ERR_LAUNCH, "%s: debug check could not read the pairs", what);
+    }
+    auto skipped = [&](int32_t i) {
+        return a[(size_t)i] < 0 || a[(size_t)i] >= limit || b[(size_t)i] < 0 ||
+               b[(size_t)i] >= limit || a[(size_t)i] == b[(size_t)i];
+    };
+    for (int32_t i = 0; i < n && i < most; i++) {
+        if (skipped(i)) continue;
+        if (seen[(size_t)b[(size_t)i]])
+            return fail(GDN_ERR_SHAPE, "%s: destination %d used twice", what, b[(size_t)i]);
+        seen[(size_t)b[(size_t)i]] = true;
+    }
+    for (int32_t i = 0; i < n && i < most; i++)
+        if (!skipped(i) && seen[(size_t)a[(size_t)i]])
+            return fail(GDN_ERR_SHAPE, "%s: %d is a source and a destination", what, a[(size_t)i]);
+    return GDN_OK;
+}
+#define DEBUG_DESTINATIONS(src, dst, n, count, limit, what)                                 \
+    do {                                                                                    \
+        int st_ = debug_destinations(src, dst, n, count, limit, stream, what);              \
+        if (st_) return st_;                                                                \
+    } while (0)
+#else
+#define DEBUG_DESTINATIONS(src, dst, n, count, limit, what) \
+    do {                                                    \
+        (void)(what);                                       \
+    } while (0)
+#endif
+
+// Sizes that the page calls share.
+int check_pages(int32_t n, int32_t n_rows, int32_t max_blocks, int32_t block_size,
+                int32_t n_blocks) {
+    if (n < 0 || n_rows < 0 || n_blocks < 1 || block_size < 1)
+        return fail(GDN_ERR_SHAPE, "counts must be >= 0, n_blocks and block_size >= 1 (got %d, %d, "
+                                   "%d, %d)", n, n_rows, n_blocks, block_size);
+    if (n > (1 << 24) || n_rows > (1 << 24))
+        return fail(GDN_ERR_UNSUPPORTED, "at most 2^24 rows in a call (got %d, %d)", n, n_rows);
+    return check_table(max_blocks, block_size);
+}
+
+// The call's query rows are counted in 32 bits.
+int check_attend_rows(const gdn_paged_dims_t* d, int64_t tokens, int32_t n_seqs) {
+    if (n_seqs > (1 << 24) || tokens * d->num_heads > 0x7fffffffll)
+        return fail(GDN_ERR_UNSUPPORTED, "tokens x heads must stay below 2^31, sequences within "
+                                         "2^24 (got %lld x %d, %d): split the call",
+                    (long long)tokens, d->num_heads, n_seqs);
+    return GDN_OK;
+}
+
+void attend_args(const gdn_paged_dims_t* d, gdn::AttendArgs* a) {
+    a->dtype = d->dtype;
+    a->H = d->num_heads;
+    a->kv_heads = d->num_kv_heads;
+    a->d = d->d;
+    a->scale = d->scale;
+}
+
+int check_paged_prefill(const gdn_paged_dims_t* dims, int32_t n_seqs, int32_t total_tokens) {
+    const int st = check_paged_dims(dims, 0, 1);
+    if (st) return st;
+    if (n_seqs < 0 || total_tokens < 0)
+        return fail(GDN_ERR_SHAPE, "n_seqs and total_tokens must be >= 0 (got %d, %d)", n_seqs,
+                    total_tokens);
+    return check_attend_rows(dims, total_tokens, n_seqs);
+}
+
+gdn::PagedPrefillArgs paged_prefill_args(const gdn_paged_dims_t* dims, int32_t n_seqs,
+                                         int32_t total_tokens) {
+    gdn::PagedPrefillArgs a = {};
+    attend_args(dims, &a.at);
+    a.at.n_seqs = n_seqs;
+    a.total_tokens = total_tokens;
+    return a;
+}
+
+int check_shared_decode(const gdn_paged_dims_t* dims, int32_t batch, int32_t n_pos,
+                        int32_t n_groups) {
+    const int st = check_paged_dims(dims, batch, n_pos);
+    if (st) return st;
+    if (n_groups < 0) return fail(GDN_ERR_SHAPE, "n_groups must be >= 0 (got %d)", n_groups);
+    return check_attend_rows(dims, (int64_t)batch * n_pos, batch > n_groups ? batch : n_groups);
+}
+
+gdn::SharedDecodeArgs shared_decode_args(const gdn_paged_dims_t* dims, int32_t batch,
+                                         int32_t n_pos, int32_t n_groups) {
+    gdn::SharedDecodeArgs a = {};
+    attend_args(dims, &a.at);
+    a.at.n_pos = n_pos;
+    a.at.n_seqs = n_groups;
+    a.own = paged_args(dims, batch, n_pos);
+    a.batch = batch;
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -967,6 +1085,273 @@ int gdn_paged_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_
     a.o = o;
     return launch_status(gdn::launch_paged_decode(a, static_cast<hipStream_t>(stream)),
                          "gdn_paged_decode");
+}
+
+int gdn_paged_fork(const int32_t* src_rows, const int32_t* dst_rows, const int32_t* fork_lens,
+                   int32_t n, int32_t* block_table, int32_t n_rows, int32_t max_blocks,
+                   int32_t block_size, int32_t* shares, int32_t n_blocks,
+                   const int32_t* free_blocks, int32_t n_free, int32_t* copy_src,
+                   int32_t* copy_dst, int32_t* counts, void* stream) {
+    const char* what = "gdn_paged_fork";
+    int st = check_pages(n, n_rows, max_blocks, block_size, n_blocks);
+    if (st) return st;
+    if (n_free < 0) return fail(GDN_ERR_SHAPE, "n_free must be >= 0 (got %d)", n_free);
+    if (n > 0) {
+        REQUIRE_LIST(src_rows);
+        REQUIRE_LIST(dst_rows);
+        REQUIRE_LIST(fork_lens);
+        REQUIRE_PTR(block_table);
+        REQUIRE_PTR(shares);
+        REQUIRE_LIST(copy_src);
+        REQUIRE_LIST(copy_dst);
+    }
+    if (n_free > 0) REQUIRE_LIST(free_blocks);
+    REQUIRE_LIST(counts);
+    gdn::ForkArgs a;
+    a.src_rows = src_rows;
+    a.dst_rows = dst_rows;
+    a.lens = fork_lens;
+    a.n = n;
+    a.table = block_table;
+    a.n_rows = n_rows;
+    a.max_blocks = max_blocks;
+    a.block_size = block_size;
+    a.shares = shares;
+    a.n_blocks = n_blocks;
+    a.free_blocks = free_blocks;
+    a.n_free = n_free;
+    a.copy_src = copy_src;
+    a.copy_dst = copy_dst;
+    a.counts = counts;
+    DEBUG_DESTINATIONS(src_rows, dst_rows, n, nullptr, n_rows, what);
+    return launch_status(gdn::launch_paged_fork(a, static_cast<hipStream_t>(stream)), what);
+}
+
+int gdn_paged_free_workspace_bytes(int32_t n_blocks, size_t* bytes) {
+    if (n_blocks < 1) return fail(GDN_ERR_SHAPE, "n_blocks must be >= 1 (got %d)", n_blocks);
+    if (bytes == nullptr) return fail(GDN_ERR_NULL, "bytes is NULL");
+    gdn::FreeArgs a;
+    a.n_blocks = n_blocks;
+    *bytes = gdn::paged_free_layout(&a, nullptr);
+    return ok();
+}
+
+int gdn_paged_free(const int32_t* rows, const int32_t* lens, int32_t n, int32_t* block_table,
+                   int32_t n_rows, int32_t max_blocks, int32_t block_size, int32_t* shares,
+                   int32_t n_blocks, int32_t* freed, int32_t max_freed, int32_t* counts,
+                   void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_pages(n, n_rows, max_blocks, block_size, n_blocks);
+    if (st) return st;
+    if (max_freed < 0) return fail(GDN_ERR_SHAPE, "max_freed must be >= 0 (got %d)", max_freed);
+    if (n > 0) {
+        REQUIRE_LIST(rows);
+        REQUIRE_LIST(lens);
+        REQUIRE_PTR(block_table);
+    }
+    REQUIRE_PTR(shares);
+    if (max_freed > 0) REQUIRE_LIST(freed);
+    REQUIRE_LIST(counts);
+    REQUIRE_PTR(workspace);
+    gdn::FreeArgs a;
+    a.rows = rows;
+    a.lens = lens;
+    a.n = n;
+    a.table = block_table;
+    a.n_rows = n_rows;
+    a.max_blocks = max_blocks;
+    a.block_size = block_size;
+    a.shares = shares;
+    a.n_blocks = n_blocks;
+    a.freed = freed;
+    a.max_freed = max_freed;
+    a.counts = counts;
+    const size_t need = gdn::paged_free_layout(&a, workspace);
+    if (ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    return launch_status(gdn::launch_paged_free(a, static_cast<hipStream_t>(stream)),
+                         "gdn_paged_free");
+}
+
+int gdn_paged_compact_workspace_bytes(int32_t n_blocks, size_t* bytes) {
+    if (n_blocks < 1) return fail(GDN_ERR_SHAPE, "n_blocks must be >= 1 (got %d)", n_blocks);
+    if (bytes == nullptr) return fail(GDN_ERR_NULL, "bytes is NULL");
+    gdn::CompactArgs a;
+    a.n_blocks = n_blocks;
+    *bytes = gdn::paged_compact_layout(&a, nullptr);
+    return ok();
+}
+
+int gdn_paged_compact(const int32_t* seq_lens, int32_t n_rows, int32_t* block_table,
+                      int32_t max_blocks, int32_t block_size, int32_t* shares, int32_t n_blocks,
+                      int32_t* copy_src, int32_t* copy_dst, int32_t max_copies, int32_t* counts,
+                      void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_pages(0, n_rows, max_blocks, block_size, n_blocks);
+    if (st) return st;
+    if (max_copies < 0) return fail(GDN_ERR_SHAPE, "max_copies must be >= 0 (got %d)", max_copies);
+    if (n_rows > 0) {
+        REQUIRE_LIST(seq_lens);
+        REQUIRE_PTR(block_table);
+    }
+    REQUIRE_PTR(shares);
+    if (max_copies > 0) {
+        REQUIRE_LIST(copy_src);
+        REQUIRE_LIST(copy_dst);
+    }
+    REQUIRE_LIST(counts);
+    REQUIRE_PTR(workspace);
+    gdn::CompactArgs a;
+    a.seq_lens = seq_lens;
+    a.n_rows = n_rows;
+    a.table = block_table;
+    a.max_blocks = max_blocks;
+    a.block_size = block_size;
+    a.shares = shares;
+    a.n_blocks = n_blocks;
+    a.copy_src = copy_src;
+    a.copy_dst = copy_dst;
+    a.max_copies = max_copies;
+    a.counts = counts;
+    const size_t need = gdn::paged_compact_layout(&a, workspace);
+    if (ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    return launch_status(gdn::launch_paged_compact(a, static_cast<hipStream_t>(stream)),
+                         "gdn_paged_compact");
+}
+
+int gdn_paged_copy(void* const* caches, int32_t n_caches, int64_t page_bytes, int32_t n_blocks,
+                   const int32_t* copy_src, const int32_t* copy_dst, int32_t n,
+                   const int32_t* count, void* stream) {
+    const char* what = "gdn_paged_copy";
+    if (n_caches < 0 || n < 0 || n_blocks < 1 || page_bytes < 1)
+        return fail(GDN_ERR_SHAPE, "n_caches and n must be >= 0, n_blocks and page_bytes >= 1 (got "
+                                   "%d, %d, %d, %lld)", n_caches, n, n_blocks,
+                    (long long)page_bytes);
+    if (n_caches > GDN_COPY_MAX_CACHES)
+        return fail(GDN_ERR_UNSUPPORTED, "at most %d caches in a call (got %d)",
+                    GDN_COPY_MAX_CACHES, n_caches);
+    if (page_bytes % 16 != 0 || page_bytes > ((int64_t)1 << 40))
+        return fail(GDN_ERR_UNSUPPORTED, "pages must be a multiple of 16 bytes, at most 2^40 (got "
+                                         "%lld)", (long long)page_bytes);
+    if (n_caches == 0 || n == 0) return ok();
+    if (caches == nullptr) return fail(GDN_ERR_NULL, "caches is NULL");
+    gdn::CopyArgs a = {};
+    for (int32_t i = 0; i < n_caches; i++) {
+        void* const cache = caches[i];
+        REQUIRE_PTR(cache);
+        a.caches[i] = cache;
+    }
+    REQUIRE_LIST(copy_src);
+    REQUIRE_LIST(copy_dst);
+    if (count != nullptr) REQUIRE_LIST(count);
+    a.page_bytes = page_bytes;
+    a.n_blocks = n_blocks;
+    a.src = copy_src;
+    a.dst = copy_dst;
+    a.n = n;
+    a.count = count;
+    DEBUG_DESTINATIONS(copy_src, copy_dst, n, count, n_blocks, what);
+    return launch_status(gdn::launch_paged_copy(a, n_caches, static_cast<hipStream_t>(stream)),
+                         what);
+}
+
+int gdn_paged_shared_decode_workspace_bytes(const gdn_paged_dims_t* dims, int32_t batch,
+                                            int32_t n_pos, int32_t n_groups, size_t* bytes) {
+    int st = check_shared_decode(dims, batch, n_pos, n_groups);
+    if (st) return st;
+    if (bytes == nullptr) return fail(GDN_ERR_NULL, "bytes is NULL");
+    gdn::SharedDecodeArgs a = shared_decode_args(dims, batch, n_pos, n_groups);
+    *bytes = batch == 0 ? 0 : gdn::shared_decode_layout(&a, nullptr);
+    return ok();
+}
+
+int gdn_paged_shared_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_cache,
+                            const void* v_cache, int32_t n_blocks, int32_t block_size,
+                            const int32_t* block_table, int32_t max_blocks,
+                            const int32_t* seq_lens, int32_t batch, int32_t n_pos,
+                            const int32_t* group_cu, const int32_t* prefix_lens, int32_t n_groups,
+                            void* o, void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_shared_decode(dims, batch, n_pos, n_groups);
+    if (!st) st = check_cache(dims->dtype, dims->num_kv_heads, n_blocks, block_size);
+    if (!st) st = check_table(max_blocks, block_size);
+    if (!st) st = check_chunks(batch, dims->num_kv_heads, max_blocks, block_size);
+    if (st) return st;
+    if (batch == 0) return ok();
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(k_cache);
+    REQUIRE_PTR(v_cache);
+    REQUIRE_PTR(block_table);
+    REQUIRE_PTR(seq_lens);
+    if (n_groups > 0) {
+        REQUIRE_LIST(group_cu);
+        REQUIRE_LIST(prefix_lens);
+    }
+    REQUIRE_PTR(o);
+    REQUIRE_PTR(workspace);
+    gdn::SharedDecodeArgs a = shared_decode_args(dims, batch, n_pos, n_groups);
+    const size_t need = gdn::shared_decode_layout(&a, workspace);
+    if (ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    a.at.q = a.own.q = q;
+    a.at.k_cache = a.own.k_cache = k_cache;
+    a.at.v_cache = a.own.v_cache = v_cache;
+    a.at.n_blocks = a.own.n_blocks = n_blocks;
+    a.at.block = a.own.block = gdn::FastDiv::of((uint32_t)block_size);
+    a.at.block_table = a.own.block_table = block_table;
+    a.at.max_blocks = a.own.max_blocks = max_blocks;
+    a.at.max_keys = a.own.split.max_keys = max_blocks * block_size;
+    a.at.seq_lens = a.own.seq_lens = seq_lens;
+    a.own.o = o;
+    a.group_cu = group_cu;
+    a.prefix_lens = prefix_lens;
+    return launch_status(gdn::launch_shared_decode(a, static_cast<hipStream_t>(stream)),
+                         "gdn_paged_shared_decode");
+}
+
+int gdn_paged_prefill_workspace_bytes(const gdn_paged_dims_t* dims, int32_t n_seqs,
+                                      int32_t total_tokens, size_t* bytes) {
+    int st = check_paged_prefill(dims, n_seqs, total_tokens);
+    if (st) return st;
+    if (bytes == nullptr) return fail(GDN_ERR_NULL, "bytes is NULL");
+    gdn::PagedPrefillArgs a = paged_prefill_args(dims, n_seqs, total_tokens);
+    *bytes = n_seqs == 0 || total_tokens == 0 ? 0 : gdn::paged_prefill_layout(&a, nullptr);
+    return ok();
+}
+
+int gdn_paged_prefill(const gdn_paged_dims_t* dims, const void* q, const void* k_cache,
+                      const void* v_cache, int32_t n_blocks, int32_t block_size,
+                      const int32_t* block_table, int32_t max_blocks, const int32_t* cu_seqlens,
+                      const int32_t* seq_lens, int32_t n_seqs, int32_t total_tokens, void* o,
+                      void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_paged_prefill(dims, n_seqs, total_tokens);
+    if (!st) st = check_cache(dims->dtype, dims->num_kv_heads, n_blocks, block_size);
+    if (!st) st = check_table(max_blocks, block_size);
+    if (st) return st;
+    if (n_seqs == 0 || total_tokens == 0) return ok();
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(k_cache);
+    REQUIRE_PTR(v_cache);
+    REQUIRE_PTR(block_table);
+    REQUIRE_PTR(cu_seqlens);
+    REQUIRE_PTR(seq_lens);
+    REQUIRE_PTR(o);
+    REQUIRE_PTR(workspace);
+    gdn::PagedPrefillArgs a = paged_prefill_args(dims, n_seqs, total_tokens);
+    const size_t need = gdn::paged_prefill_layout(&a, workspace);
+    if (ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    a.at.q = q;
+    a.at.k_cache = k_cache;
+    a.at.v_cache = v_cache;
+    a.at.n_blocks = n_blocks;
+    a.at.block = gdn::FastDiv::of((uint32_t)block_size);
+    a.at.block_table = block_table;
+    a.at.max_blocks = max_blocks;
+    a.at.max_keys = max_blocks * block_size;
+    a.at.seq_lens = seq_lens;
+    a.at.o = o;
+    a.cu_seqlens = cu_seqlens;
+    return launch_status(gdn::launch_paged_prefill(a, static_cast<hipStream_t>(stream)),
+                         "gdn_paged_prefill");
 }
 
 int gdn_latent_decode_workspace_bytes(const gdn_latent_dims_t* dims, int32_t batch,

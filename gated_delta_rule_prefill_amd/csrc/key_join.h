@@ -60,28 +60,25 @@ __device__ __forceinline__ void join_note(const JoinShape& j, const SplitShape& 
         join_none(j, b * s.units + unit);
 }
 
-// One workgroup's share of a note's rows, NC pieces of 128 columns from column `first` on, U
-// parts on their way at a time per group.
-template <int COLS, int NC, int U, typename Store>
-__device__ __forceinline__ void join_rows(const JoinShape& s, int4 note, int step0, int first,
-                                          Store store) {
+// One workgroup's share of a unit's rows, NC pieces of 128 columns from column `first` on, U
+// parts on their way at a time per group. at(i, r): where part i of row r lies, i < parts_of(r),
+// which is `most` or less; store(r, column, x[4]).
+template <int COLS, int NC, int U, typename Parts, typename At, typename Store>
+__device__ __forceinline__ void join_rows(const JoinShape& s, int most, Parts parts_of, At where,
+                                          int step0, int first, Store store) {
     __shared__ float red[JOIN_GROUPS][NC * 128 + 4];
     __shared__ float weight[JOIN_MAX_WORKERS];
     __shared__ float wave_part[JOIN_THREADS / WAVE];
-    const int b = note.x, unit = note.y, w0 = note.z >> 1, late = note.z & 1, w1 = note.w;
     const int tid = threadIdx.x, group = tid >> 5, lane = tid & 31;
-    const size_t rows_per_part = (size_t)s.row_tiles * s.tile;
-    const int parts = w1 - w0 + 1;
     int gpr = 1;  // groups per row: U parts each, if there are groups enough
-    while (gpr < JOIN_GROUPS && gpr * U < parts) gpr *= 2;
+    while (gpr < JOIN_GROUPS && gpr * U < most) gpr *= 2;
     const int rows_here = JOIN_GROUPS / gpr, turn = group & (gpr - 1);
     for (int step = step0; step * rows_here < s.rows; step += s.share) {
         const int row = step * rows_here + group / gpr;
         const bool live = row < s.rows;
         const int r = live ? row : 0;
-        auto at = [&](int i) {  // part i of the unit
-            return (size_t)(2 * (w0 + i) + (i == 0 ? late : 0)) * rows_per_part + r;
-        };
+        const int parts = parts_of(r);
+        auto at = [&](int i) { return where(i, r); };
         // the parts' weights: lane i's is part i's, or all of them in LDS where a row has so
         // many that the whole workgroup shares it
         float f = 0.f, sum = 0.f;
@@ -181,7 +178,7 @@ __device__ __forceinline__ void join_rows(const JoinShape& s, int4 note, int ste
                 const int col = first + c * 128 + lane * 4;
                 if (COLS % 128 != 0 && col >= COLS) continue;
                 const float y[4] = {x[c][0] * inv, x[c][1] * inv, x[c][2] * inv, x[c][3] * inv};
-                store(b, unit, row, col, y);
+                store(row, col, y);
             }
         }
     }
@@ -195,10 +192,17 @@ __device__ __forceinline__ void join_parts(const JoinShape& s, Store store) {
     const int4 note = s.notes[blockIdx.x / per_note];
     if (note.w < 0) return;
     const int rest = blockIdx.x % per_note;
+    const int w0 = note.z >> 1, late = note.z & 1, parts = note.w - w0 + 1;
+    const size_t rows_per_part = (size_t)s.row_tiles * s.tile;
+    auto parts_of = [&](int) { return parts; };
+    auto at = [&](int i, int r) {
+        return (size_t)(2 * (w0 + i) + (i == 0 ? late : 0)) * rows_per_part + r;
+    };
+    auto put = [&](int row, int col, const float x[4]) { store(note.x, note.y, row, col, x); };
     if (s.slices == 1) {
-        join_rows<COLS, NC, 4>(s, note, rest, 0, store);
+        join_rows<COLS, NC, 4>(s, parts, parts_of, at, rest, 0, put);
     } else if constexpr (NC > 1) {
-        join_rows<COLS, 1, 8>(s, note, rest / s.slices, rest % s.slices * 128, store);
+        join_rows<COLS, 1, 8>(s, parts, parts_of, at, rest / s.slices, rest % s.slices * 128, put);
     }
 }
 

@@ -1,0 +1,614 @@
+// Attention of many query rows over a paged key/value cache, grouped heads: the kernel of
+// gdn_paged_prefill (packed prompts, causal) and of the shared part of gdn_paged_shared_decode.
+//
+// Query rows that share a key/value head (tokens x group) are packed into tiles of A::ROWS rows, so
+// that the keys are read once for all heads of a group, and a causal tile of few tokens reaches
+// little beyond its own diagonal. A tile and a key/value head make a unit; the 64-key steps
+// (32 in fp32) of all units are laid end to end and cut into equal runs, one per worker, one
+// worker a CU: work is even to a few steps whatever the lengths, which are device data. A unit
+// cut between workers leaves partial results (key_join.h's form) that a joining launch combines.
+//
+// Per step and wave, for its 32 rows (16 in fp32):
+//   S^T = K Q^T     queries in registers as the MFMA's B operand, so that a query is an accumulator
+//                   column: a lane's scores are reduced in registers, then over its partners;
+//   O^T += V^T P^T  the accumulator layout of S^T is the B operand's with the keys renumbered, so
+//                   weights stay in registers; V^T comes from transposing LDS reads (bf16) or
+//                   column reads (fp32).
+// Keys and values go from their pages straight into LDS, two buffers each, the keys one step ahead
+// of the values: a step's scores (matrix pipe) are formed beside the previous step's softmax
+// (vector pipe), with one barrier a step. Rows that do not exist are loaded from a row of zeros:
+// a zero weight would not cancel what a page's unused rows hold.
+#pragma once
+#include "attn_launch.h"
+#include "gdn_common.h"
+#include "gdn_launch.h"
+#include "key_join.h"
+#include "lds_tile.h"
+
+namespace gdn {
+
+constexpr uint32_t AT_NO_ROW = 0xffffffffu;
+constexpr float AT_LOG2E = 1.4426950408889634f;
+
+static __device__ __align__(16) char at_zero_row[1024];  // the longest row
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// ------------------------------------------------------------------ one wave's arithmetic
+// A step's pieces in LDS lie row by row, 16-byte pieces turned by a function of their row.
+template <typename T, int D> struct AttendTile;
+
+template <int D> struct AttendTile<bf16, D> {
+    // One wave a SIMD at d = 256 (outputs and queries alone take 192 registers), else two.
+    static constexpr int WAVES = D == 256 ? 4 : 8;
+    static constexpr int WAVES_PER_SIMD = WAVES / 4;
+    static constexpr int WAVE_ROWS = 32, KB = 64;
+    static constexpr int ROW = D * 2, PIECES = ROW / 16;
+    static constexpr int NQ = D / 16, NO = D / 32;
+    typedef f32x16 Scores[2];
+    bf16x8 q[NQ];
+    f32x16 acc[NO];
+
+    __device__ __forceinline__ static int k_turn(int r) { return D >= 128 ? r & 15 : (r >> 1) & 7; }
+    // (pairs of pieces: a transposing read takes 32 bytes of each of 8 rows, twice side by side)
+    __device__ __forceinline__ static int v_turn(int r) {
+        return (D >= 128 ? r & 7 : (r >> 1) & 3) << 1;
+    }
+    __device__ __forceinline__ static int row_of_lane(int lane) { return lane & 31; }
+    __device__ __forceinline__ static int first_key(int lane) { return (lane >> 5) * 4; }
+    __device__ __forceinline__ static int key(int x, int i) {  // + first_key
+        return x * 32 + (i >> 2) * 8 + (i & 3);
+    }
+    static constexpr int SX = 2, SI = 16;
+    __device__ __forceinline__ static float max_partners(float x) { return max_halves(x); }
+    __device__ __forceinline__ static float sum_partners(float x) {
+        return x + __shfl_xor(x, 32, WAVE);
+    }
+    __device__ __forceinline__ void load_q(const bf16* src, int lane, float sign) {
+#pragma unroll
+        for (int f = 0; f < NQ; f++) q[f] = Mma<bf16>::load(src + f * 16 + (lane >> 5) * 8);
+        if (sign != 1.f) {
+#pragma unroll
+            for (int f = 0; f < NQ; f++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) q[f][i] = (bf16)(sign == 0.f ? 0.f : -(float)q[f][i]);
+        }
+        arrived(q);
+    }
+    __device__ __forceinline__ static f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    // Scores of the keys at `kt`; beside(f) is other work for the time of two MFMAs (64 cycles).
+    // The fences keep the compiler from taking the two apart again.
+    static constexpr int SLICES = NQ, AHEAD = 3;
+    template <typename Beside>
+    __device__ __forceinline__ void scores(uint32_t kt, int lane, Scores& s, Beside beside) const {
+        const int r = lane & 31, half = lane >> 5;
+        uint32_t at = kt + r * ROW + ((half ^ k_turn(r)) << 4);
+        asm volatile("" : "+v"(at));
+        bf16x8 k[AHEAD + 1][2];
+        auto load = [&](int f) {
+#pragma unroll
+            for (int x = 0; x < 2; x++)  // (32 rows on, the pieces are turned alike)
+                k[f % (AHEAD + 1)][x] = lds_get<bf16x8>((at ^ (f << 5)) + x * 32 * ROW);
+        };
+#pragma unroll
+        for (int f = 0; f < AHEAD && f < NQ; f++) load(f);
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) s[x][i] = 0.f;
+#pragma unroll
+        for (int f = 0; f < NQ; f++) {
+            if (f + AHEAD < NQ) load(f + AHEAD);
+#pragma unroll
+            for (int x = 0; x < 2; x++) s[x] = mma(k[f % (AHEAD + 1)][x], q[f], s[x]);
+            beside(f);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // acc += V^T P^T for the weights s; l += their sum. The weights are rounded to bf16 (2^-8 of
+    // each at most) as the MFMA's operand, not in l.
+    __device__ __forceinline__ void values(uint32_t vt, int lane, const Scores& s, float* l) {
+        // lanes 0-15 and 16-31 read 16 columns each of 4 keys, the upper half of the next 4
+        const int r = (lane >> 5) * 4 + ((lane >> 2) & 3);
+        uint32_t at = vt + r * ROW + ((((lane >> 4) & 1) << 5) ^ (v_turn(r) << 4)) + (lane & 3) * 8;
+        asm volatile("" : "+v"(at));
+        constexpr int NV = KB / 16 * NO;
+        bf16x8 p[4], v[AHEAD + 1];
+#pragma unroll
+        for (int n = 0; n < 4; n++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) p[n][i] = (bf16)s[n >> 1][(n & 1) * 8 + i];
+        auto load = [&](int n) {
+            // keys 16 g + r and 16 g + 8 + r: rows 8 on are turned alike
+            const int g = n / NO, j = n % NO;
+            const uint32_t x = (at ^ (j << 6)) + g * 16 * ROW;
+            v[n % (AHEAD + 1)] = join(lds_read_tr(x), lds_read_tr(x + 8 * ROW));
+        };
+#pragma unroll
+        for (int n = 0; n < AHEAD; n++) load(n);
+#pragma unroll
+        for (int n = 0; n < NV; n++) {
+            if (n + AHEAD < NV) load(n + AHEAD);
+            acc[n % NO] = mma(v[n % (AHEAD + 1)], p[n / NO], acc[n % NO]);
+#pragma unroll
+            for (int i = n * 32 / NV; i < (n + 1) * 32 / NV; i++) *l += s[i >> 4][i & 15];
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < NO; j++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) acc[j][i] = 0.f;
+    }
+    __device__ __forceinline__ void shrink(float f) {
+#pragma unroll
+        for (int j = 0; j < NO; j++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) acc[j][i] *= f;
+    }
+    // store(column, x[4]) for this lane's pieces of its row, times f
+    template <typename Store>
+    __device__ __forceinline__ void results(int lane, float f, Store store) const {
+#pragma unroll
+        for (int j = 0; j < NO; j++)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float y[4] = {acc[j][i] * f, acc[j][i + 1] * f, acc[j][i + 2] * f,
+                                    acc[j][i + 3] * f};
+                store(j * 32 + (i >> 2) * 8 + (lane >> 5) * 4, y);
+            }
+    }
+};
+
+template <int D> struct AttendTile<float, D> {
+    static constexpr int WAVES = 8, WAVES_PER_SIMD = 2;
+    static constexpr int WAVE_ROWS = 16, KB = 32;
+    static constexpr int ROW = D * 4, PIECES = ROW / 16;
+    static constexpr int NQ = D / 16, NO = D / 16;
+    typedef f32x4 Scores[2];
+    f32x4 q[NQ];
+    f32x4 acc[NO];
+
+    __device__ __forceinline__ static int k_turn(int r) { return r & 15; }
+    // (a column read takes 64 bytes of each of 4 rows 4 apart)
+    __device__ __forceinline__ static int v_turn(int r) { return ((r >> 2) & 3) << 2; }
+    __device__ __forceinline__ static int row_of_lane(int lane) { return lane & 15; }
+    __device__ __forceinline__ static int first_key(int lane) { return (lane >> 4) * 4; }
+    __device__ __forceinline__ static int key(int x, int i) { return x * 16 + i; }
+    static constexpr int SX = 2, SI = 4;
+    __device__ __forceinline__ static float max_partners(float x) { return max_groups(x); }
+    __device__ __forceinline__ static float sum_partners(float x) {
+        x += __shfl_xor(x, 16, WAVE);
+        return x + __shfl_xor(x, 32, WAVE);
+    }
+    __device__ __forceinline__ void load_q(const float* src, int lane, float sign) {
+#pragma unroll
+        for (int f = 0; f < NQ; f++)
+            q[f] = sign == 0.f ? zero4()
+                               : *reinterpret_cast<const f32x4*>(src + f * 16 + (lane >> 4) * 4) * sign;
+#pragma unroll
+        for (int f = 0; f < NQ; f++) asm volatile("" : "+v"(q[f]));  // as arrived()
+    }
+    static constexpr int SLICES = 0;
+    template <typename Beside>
+    __device__ __forceinline__ void scores(uint32_t kt, int lane, Scores& s, Beside) const {
+        const int r = lane & 15;
+        uint32_t at = kt + r * ROW + (((lane >> 4) ^ k_turn(r)) << 4);
+        asm volatile("" : "+v"(at));
+        s[0] = zero4();
+        s[1] = zero4();
+#pragma unroll
+        for (int f = 0; f < NQ; f++)
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                const f32x4 k = lds_get<f32x4>((at ^ (f << 6)) + x * 16 * ROW);
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[x] = Mma<float>::mma(k[e], q[f][e], s[x]);
+            }
+    }
+    __device__ __forceinline__ void values(uint32_t vt, int lane, const Scores& s, float* l) {
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = x * 16 + (lane >> 4) * 4 + i;
+                const uint32_t at = vt + r * ROW + (lane & 15) * 4;
+#pragma unroll
+                for (int j = 0; j < NO; j++)
+                    acc[j] = Mma<float>::mma(lds_get<float>(at + (((j << 2) ^ v_turn(r)) << 4)),
+                                             s[x][i], acc[j]);
+                *l += s[x][i];
+            }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < NO; j++) acc[j] = zero4();
+    }
+    __device__ __forceinline__ void shrink(float f) {
+#pragma unroll
+        for (int j = 0; j < NO; j++) acc[j] *= f;
+    }
+    template <typename Store>
+    __device__ __forceinline__ void results(int lane, float f, Store store) const {
+#pragma unroll
+        for (int j = 0; j < NO; j++) {
+            const float y[4] = {acc[j][0] * f, acc[j][1] * f, acc[j][2] * f, acc[j][3] * f};
+            store(j * 16 + (lane >> 4) * 4, y);
+        }
+    }
+};
+
+// ------------------------------------------------------------------------------- the units
+// Positions in the stream that a unit has beyond its steps: its start and end take as long.
+constexpr int ATTEND_EXTRA = 2;
+// No worker is given fewer positions than this: a run's start, and the parts that a cut leaves to
+// be joined, cost as much.
+constexpr int ATTEND_MIN_RUN = 4;
+
+// The stream of all units (total positions per key/value head) cut over the workers.
+struct AttendCut {
+    int64_t each;
+    int n, more;
+    __device__ __forceinline__ static AttendCut of(int64_t total, int workers) {
+        int64_t n = (total + ATTEND_MIN_RUN - 1) / ATTEND_MIN_RUN;
+        n = n < workers ? n : workers;
+        if (n == 0) return {0, 0, 0};
+        return {total / n, (int)n, (int)(total % n)};
+    }
+    __device__ __forceinline__ int64_t start(int w) const { return w * each + min(w, more); }
+    __device__ __forceinline__ int owner(int64_t x) const {
+        const int64_t big = more * (each + 1);
+        return (int)(x < big ? x / (each + 1) : more + (x - big) / each);
+    }
+};
+
+// Rows of a tile, for the host.
+inline int attend_tile_rows(int dtype, int d) { return dtype == 0 || d == 256 ? 128 : 256; }
+
+// Sections of a workspace, 256 bytes apart.
+struct Layout {
+    char* base;
+    size_t size = 0;
+    explicit Layout(void* ws) : base(static_cast<char*>(ws)) {}
+    template <typename V> V* take(size_t n) {
+        V* p = base == nullptr ? nullptr : reinterpret_cast<V*>(base + size);
+        size += (n * sizeof(V) + 255) & ~(size_t)255;
+        return p;
+    }
+};
+inline void attend_table_layout(AttendArgs* a, Layout* l) {
+    a->head = l->take<int32_t>(1);
+    a->total = l->take<int64_t>(1);
+    a->seq_tile = l->take<int32_t>((size_t)a->n_seqs + 1);
+    a->first = l->take<int64_t>((size_t)a->tiles + 1);
+    a->tile = l->take<AttendUnit>((size_t)a->tiles);
+}
+
+// One workgroup lays out the tiles: rows_of(i) of each sequence, then each tile's unit.
+// Sums that the host's bound does not hold (lengths that break the contract) are cut off there.
+constexpr int AT_TABLE_THREADS = 1024;
+template <typename RowsOf, typename UnitOf>
+__device__ __forceinline__ void attend_tables(const AttendArgs& a, int rows_a_tile, int kb,
+                                              RowsOf rows_of, UnitOf unit_of) {
+    __shared__ int64_t part[AT_TABLE_THREADS / WAVE];
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+    auto scan = [&](int64_t x, int64_t* total) {  // exclusive
+        int64_t upto = x;
+#pragma unroll
+        for (int off = 1; off < WAVE; off <<= 1) {
+            const int64_t t = __shfl_up(upto, off, WAVE);
+            if (lane >= off) upto += t;
+        }
+        __syncthreads();
+        if (lane == WAVE - 1) part[wave] = upto;
+        __syncthreads();
+        int64_t before = 0, all = 0;
+        for (int w = 0; w < AT_TABLE_THREADS / WAVE; w++) {
+            if (w < wave) before += part[w];
+            all += part[w];
+        }
+        *total = all;
+        return before + upto - x;
+    };
+    auto tiles_of = [&](int i) {
+        return ((int64_t)rows_of(i) + rows_a_tile - 1) / rows_a_tile;
+    };
+    const int per = (a.n_seqs + AT_TABLE_THREADS - 1) / AT_TABLE_THREADS;
+    const int i0 = (int)min((int64_t)tid * per, (int64_t)a.n_seqs), i1 = min(i0 + per, a.n_seqs);
+    int64_t mine = 0, all;
+    for (int i = i0; i < i1; i++) mine += tiles_of(i);
+    int64_t at = scan(mine, &all);
+    for (int i = i0; i < i1; i++) {
+        a.seq_tile[i] = (int)min(at, (int64_t)a.tiles);
+        at += tiles_of(i);
+    }
+    const int n_tiles = (int)min(all, (int64_t)a.tiles);
+    if (tid == 0) a.seq_tile[a.n_seqs] = n_tiles;
+    __threadfence();
+    __syncthreads();
+    int64_t base = 0;
+    for (int t0 = 0; t0 < n_tiles; t0 += AT_TABLE_THREADS) {
+        const int t = t0 + tid;
+        int64_t len = 0;
+        if (t < n_tiles) {
+            int lo = 0, hi = a.n_seqs;  // the last sequence whose first tile is t or before
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (a.seq_tile[mid] <= t) lo = mid; else hi = mid;
+            }
+            const AttendUnit u = unit_of(lo, (t - a.seq_tile[lo]) * rows_a_tile);
+            a.tile[t] = u;
+            len = (u.reach + kb - 1) / kb + ATTEND_EXTRA;
+        }
+        int64_t block;
+        const int64_t first = base + scan(len, &block);
+        if (t < n_tiles) a.first[t] = first;
+        base += block;
+    }
+    if (tid == 0) {
+        a.first[n_tiles] = base;
+        a.head[0] = n_tiles;
+        a.total[0] = base;
+    }
+}
+
+// ------------------------------------------------------------------------------ the kernel
+// SHARED: the rows are decode positions of a group's requests, whose results are always parts;
+// else tokens of a prompt, causal.
+template <typename T, int D, bool SHARED>
+__global__ __launch_bounds__((AttendTile<T, D>::WAVES * WAVE), (AttendTile<T, D>::WAVES_PER_SIMD))
+void paged_attend_kernel(AttendArgs a) {
+    using X = AttendTile<T, D>;
+    constexpr int THREADS = X::WAVES * WAVE, KB = X::KB, ROW = X::ROW;
+    constexpr int ROWS = X::WAVES * X::WAVE_ROWS;
+    constexpr int LOADS = KB * ROW / 1024 / X::WAVES;  // 1 KiB loads of a wave per tile
+    constexpr int ROWS_A_LOAD = 1024 / ROW;
+    constexpr uint64_t ALL = KB == 64 ? ~0ull : (1ull << (KB & 63)) - 1;
+    __shared__ __align__(1024) char k_tile[2][KB * ROW];
+    __shared__ __align__(1024) char v_tile[2][KB * ROW];
+    __shared__ uint32_t key_row[4][KB];  // cache rows of four steps' keys
+    __shared__ uint64_t key_exists[4];   // a bit per key
+    __shared__ int found;
+    const int tid = threadIdx.x, lane = lane_id(), wave = uniform(wave_id());
+    // neighbours in the stream read the same keys: they sit on one XCD
+    const int w = (int)(blockIdx.x & 7) * (a.workers >> 3) + (int)(blockIdx.x >> 3);
+    const int n_tiles = a.head[0];
+    const int64_t total = a.total[0];
+    const AttendCut cut = AttendCut::of(total * a.kv_heads, a.workers);
+    if constexpr (!SHARED)
+        if (tid == 0) join_none(a.join, w);
+    if (w >= cut.n) return;
+    int64_t pos = cut.start(w);
+    const int64_t run_start = pos, end = cut.start(w + 1);
+    int kvh = (int)(pos / total);
+    {
+        const int64_t x = pos - kvh * total;
+        for (int t = tid; t < n_tiles; t += THREADS)
+            if (a.first[t] <= x && x < a.first[t + 1]) found = t;
+        __syncthreads();
+    }
+    int t = uniform(found);
+    const float sign = a.scale > 0.f ? 1.f : a.scale < 0.f ? -1.f : 0.f;
+    // The scale enters the exponent's multiplication; a negative one is moved into the queries, so
+    // that the largest score is the largest weight (and zero makes the queries zero).
+    const float cs = a.scale == 0.f ? 1.f : fabsf(a.scale) * AT_LOG2E;
+    const T* k_cache = reinterpret_cast<const T*>(a.k_cache);
+    const T* v_cache = reinterpret_cast<const T*>(a.v_cache);
+
+    for (; pos < end; t + 1 < n_tiles ? t++ : (t = 0, kvh++)) {
+        const AttendUnit u = a.tile[t];
+        const int64_t unit_start = kvh * total + a.first[t];
+        const int reach = uniform(u.reach);
+        const int nch = (reach + KB - 1) / KB;
+        const int c0 = (int)(pos - unit_start);
+        const int64_t unit_next = unit_start + nch + ATTEND_EXTRA;
+        if (c0 >= nch && c0 > 0) {  // the run starts behind the unit's own steps
+            pos = unit_next;
+            continue;
+        }
+        const int c1 = (int)min((int64_t)nch, c0 + (end - pos));
+        const int32_t* table = a.block_table + (size_t)uniform(u.seq) * a.max_blocks;
+        const bool late = pos != run_start;
+
+        const int row = u.row0 + wave * X::WAVE_ROWS + X::row_of_lane(lane);
+        const bool live = row < u.rows;
+        const int tok = (int)a.by_group((uint32_t)(live ? row : u.rows - 1));
+        const int head = kvh * a.group + (live ? row : u.rows - 1) - tok * a.group;
+        const size_t q_row = (size_t)(u.token0 + tok) * a.H + head;
+        X x;
+        x.load_q(reinterpret_cast<const T*>(a.q) + q_row * D, lane, sign);
+        int lim;  // keys that this lane's row sees
+        if constexpr (SHARED) {
+            const int b = (int)a.by_pos((uint32_t)(u.token0 + tok));
+            lim = a.seq_lens[b] - a.n_pos + (u.token0 + tok - b * a.n_pos) + 1;
+        } else {
+            lim = u.pos0 + tok + 1;
+        }
+        int low = lim, high = lim;
+#pragma unroll
+        for (int off = X::WAVE_ROWS / 2; off > 0; off >>= 1) {
+            low = min(low, __shfl_xor(low, off, WAVE));
+            high = max(high, __shfl_xor(high, off, WAVE));
+        }
+        low = uniform(low);
+        // steps that this wave's rows see
+        const bool any = u.row0 + wave * X::WAVE_ROWS < u.rows;
+        const int mine = uniform(any ? min(c1, (max(min(high, reach), 0) + KB - 1) / KB) : 0);
+
+        // Wave 0 looks up the pages: three steps ahead of the loads of the values, two of the
+        // keys', one step after it has asked for the table entries.
+        auto page_of = [&](int c) {
+            const uint32_t key = (uint32_t)(c * KB + lane);
+            return table[min(a.block(key), (uint32_t)a.max_blocks - 1)];
+        };
+        auto put_rows = [&](int c, int page) {
+            const uint32_t key = (uint32_t)(c * KB + lane), off = key - a.block(key) * a.block.div;
+            const bool ok = lane < KB && (int)key < reach && page >= 0 && page < a.n_blocks;
+            const uint32_t r = ((uint32_t)page * a.kv_heads + kvh) * a.block.div + off;
+            if (lane < KB) key_row[c & 3][lane] = ok ? r : AT_NO_ROW;
+            const uint64_t exist = __ballot(ok);
+            if (lane == 0) key_exists[c & 3] = exist;
+        };
+        auto load_tile = [&](const T* cache, int c, uint32_t lds, auto turn) {
+#pragma unroll
+            for (int i = 0; i < LOADS; i++) {
+                const int r = (wave * LOADS + i) * ROWS_A_LOAD + lane / X::PIECES;
+                const uint32_t from = key_row[c & 3][r];
+                const int piece = (lane % X::PIECES) ^ turn(r);
+                const char* base = from == AT_NO_ROW
+                    ? at_zero_row : reinterpret_cast<const char*>(cache + (size_t)from * D);
+                load_to_lds(base + piece * 16, lds + (wave * LOADS + i) * 1024);
+            }
+        };
+        auto load_keys = [&](int c) {
+            load_tile(k_cache, c, lds_offset(k_tile[c & 1]), [](int r) { return X::k_turn(r); });
+        };
+        auto load_values = [&](int c) {
+            load_tile(v_cache, c, lds_offset(v_tile[c & 1]), [](int r) { return X::v_turn(r); });
+        };
+        auto mask = [&](int c, typename X::Scores& s) {
+            const uint64_t exist = key_exists[c & 3];
+            const int key0 = c * KB;
+            if (exist == ALL && key0 + KB <= low) return;
+            int first = X::first_key(lane);
+            asm volatile("" : "+v"(first));  // formed here, not kept across the key loop
+            const uint64_t here = exist >> first;
+            const int left = lim - key0 - first;
+#pragma unroll
+            for (int y = 0; y < X::SX; y++)
+#pragma unroll
+                for (int i = 0; i < X::SI; i++) {
+                    const int k = X::key(y, i);
+                    s[y][i] = ((here >> k) & 1) && k < left ? s[y][i] : -INFINITY;
+                }
+        };
+
+        x.clear();
+        float ref = -INFINITY, l = 0.f;  // the exponents' reference (scaled); the sum
+        int page = 0;
+        auto step = [&](int c, typename X::Scores& s, typename X::Scores& next) {
+            lds_loads_done();
+            if (wave == 0 && c + 3 < c1) {
+                arrived(page);
+                put_rows(c + 3, page);
+            }
+            lds_barrier();  // keys c + 1 and values c are whole; all are done with what they replace
+            if (wave == 0 && c + 4 < c1) {
+                page = page_of(c + 4);
+                sched_fence();
+            }
+            if (c + 2 < c1) load_keys(c + 2);
+            if (c + 1 < c1) load_values(c + 1);
+            if (c >= mine) return;
+            float top = -INFINITY, shift = 0.f;
+            bool grown = false;
+            auto maximum = [&](int y) {
+#pragma unroll
+                for (int i = 0; i < X::SI; i++) top = fmaxf(top, s[y][i]);
+            };
+            auto reference = [&]() {
+                top = X::max_partners(top) * cs;
+                grown = top > ref + LAG;
+                const float to = grown ? top : ref;
+                shift = to == -INFINITY ? 0.f : to;  // a row with no key so far
+            };
+            auto weight = [&](int n) {
+                float e = __builtin_amdgcn_exp2f(fmaf(s[n / X::SI][n % X::SI], cs, -shift));
+                if constexpr (X::SLICES > 0) asm volatile("" : "+v"(e));  // formed here
+                s[n / X::SI][n % X::SI] = e;
+            };
+            constexpr int N = X::SX * X::SI;
+            const uint32_t kt = lds_offset(k_tile[(c + 1) & 1]);
+            if constexpr (X::SLICES > 0) {
+                // the first slices find the maximum, the rest form the weights
+                constexpr int WS = X::SLICES - 3, PER = (N + WS - 1) / WS;
+                x.scores(kt, lane, next, [&](int f) {
+                    if (f < 2) maximum(f);
+                    else if (f == 2) reference();
+                    else
+#pragma unroll
+                        for (int n = (f - 3) * PER; n < (f - 2) * PER && n < N; n++) weight(n);
+                });
+            } else {
+                maximum(0);
+                maximum(1);
+                reference();
+#pragma unroll
+                for (int n = 0; n < N; n++) weight(n);
+                x.scores(kt, lane, next, [](int) {});
+            }
+            if (__any(grown)) {
+                // (a row without a reference so far has sums of zero)
+                const float f = grown ? __builtin_amdgcn_exp2f(ref - shift) : 1.f;
+                ref = grown ? shift : ref;
+                l *= f;
+                x.shrink(f);
+            }
+            x.values(lds_offset(v_tile[c & 1]), lane, s, &l);
+            if (c + 1 < mine) mask(c + 1, next);
+        };
+        if (c1 > c0) {
+            typename X::Scores s0, s1;
+            __syncthreads();  // the unit before is done with its tiles and rows
+            if (wave == 0) {
+                const int p0 = page_of(c0), p1 = page_of(c0 + 1), p2 = page_of(c0 + 2);
+                put_rows(c0, p0);
+                put_rows(c0 + 1, p1);
+                put_rows(c0 + 2, p2);
+            }
+            lds_barrier();
+            load_keys(c0);
+            lds_loads_done();
+            lds_barrier();
+            if (wave == 0 && c0 + 3 < c1) {
+                page = page_of(c0 + 3);
+                sched_fence();
+            }
+            if (c0 + 1 < c1) load_keys(c0 + 1);
+            load_values(c0);
+            if (c0 < mine) {
+                x.scores(lds_offset(k_tile[c0 & 1]), lane, s0, [](int) {});
+                mask(c0, s0);
+            }
+            for (int c = c0; c < c1; c += 2) {
+                step(c, s0, s1);
+                if (c + 1 < c1) step(c + 1, s1, s0);
+            }
+        }
+        l = X::sum_partners(l);
+        const bool whole = c0 == 0 && c1 == nch;
+        if (!SHARED && whole) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros
+            if (live) {
+                T* out = reinterpret_cast<T*>(a.o) + q_row * D;
+                x.results(lane, inv, [&](int col, const float y[4]) { store4<T>(out + col, y); });
+            }
+        } else {
+            const int last = cut.owner(unit_start + nch - 1);
+            int64_t slot;
+            if constexpr (SHARED) {  // one slot per unit, and one per worker that goes on with one
+                const int unit = kvh * a.tiles + t;
+                slot = c0 == 0 ? (int64_t)a.workers + unit : w;
+                if (c0 == 0 && tid == 0) a.prefix_notes[unit] = make_int2(w, last);
+            } else {
+                slot = 2 * w + (late ? 1 : 0);
+                if (c0 == 0 && tid == 0) a.join.notes[w] = make_int4(t, kvh, (int)slot, last);
+            }
+            if (live) {
+                const size_t at = (size_t)slot * ROWS + wave * X::WAVE_ROWS + X::row_of_lane(lane);
+                float* out = a.join.part_o + at * D;
+                x.results(lane, 1.f, [&](int col, const float y[4]) { store4<float>(out + col, y); });
+                if (X::first_key(lane) == 0) {
+                    a.join.part_ml[at * 2] = ref;
+                    a.join.part_ml[at * 2 + 1] = l;
+                }
+            }
+        }
+        pos = c1 == nch ? unit_next : end;
+    }
+}
+
+}  // namespace gdn

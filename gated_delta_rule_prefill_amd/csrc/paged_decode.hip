@@ -131,7 +131,9 @@ constexpr uint32_t NO_ROW = 0xffffffffu;
 template <typename T, int D, int RT>
 constexpr int PD_WAVES_PER_SIMD = RT == 1 && (sizeof(T) == 2 || D <= 128) ? 2 : 1;
 
-template <typename T, int D, int RT>
+// BEHIND: the keys behind a shared prefix (a.start of them), whose results join those of the
+// prefix: a unit of a request that has one leaves parts also where one worker covers it whole.
+template <typename T, int D, int RT, bool BEHIND>
 __global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void paged_decode_kernel(
     PagedDecodeArgs a) {
     using X = PdTile<T, D>;
@@ -154,15 +156,21 @@ __global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void pag
         for (int b = me.worker; b < a.split.batch; b += a.workers) {
             if (b != me.worker) own_keys = split_keys(a.split, b);
             if (uniform(own_keys) != 0) continue;
+            if constexpr (BEHIND) {
+                const bool joined = uniform(a.start[b]) > 0;
+                for (int u = tid; u < a.kv_heads; u += PD_THREADS)
+                    a.join.notes[b * a.kv_heads + u] = make_int4(0, 0, 0, joined ? 0 : -1);
+                if (joined) continue;
+            }
             const size_t n = (size_t)a.n_pos * a.H * D;
             const float z[4] = {0.f, 0.f, 0.f, 0.f};
             for (size_t i = tid * 4; i < n; i += PD_THREADS * 4)
                 store4<T>(reinterpret_cast<T*>(a.o) + (size_t)b * n + i, z);
-            if (a.join.per_unit)
+            if (!BEHIND && a.join.per_unit)
                 for (int u = tid; u < a.kv_heads; u += PD_THREADS)
                     join_none(a.join, b * a.kv_heads + u);
         }
-        if (!a.join.per_unit && tid == 0) join_none(a.join, me.worker);
+        if (!BEHIND && !a.join.per_unit && tid == 0) join_none(a.join, me.worker);
     }
     char* vlds = smem + wave * L::VTILE;
     const float cs = a.scale * LOG2E;
@@ -182,7 +190,9 @@ __global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void pag
         }
         const int c1 = min(nch, c0 + (run.end - run.pos));
         const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
-        const int seen0 = uniform(a.split.seq_lens[b]) - a.n_pos + 1;  // keys that position 0 sees
+        const int skip = BEHIND ? uniform(a.start[b]) : 0;
+        // keys that position 0 sees
+        const int seen0 = uniform((BEHIND ? a.seq_lens : a.split.seq_lens)[b]) - skip - a.n_pos + 1;
 
         frag q[RT][NF];
         int lim[RT];
@@ -215,7 +225,7 @@ __global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void pag
         auto load_pages = [&](int c) {
 #pragma unroll
             for (int t = 0; t < NSUB; t++) {
-                const uint32_t key = (uint32_t)(c * KB + wave * KW + t * 16 + col);
+                const uint32_t key = (uint32_t)(c * KB + wave * KW + t * 16 + col + skip);
                 page[t] = table[min(a.block(key), (uint32_t)a.max_blocks - 1)];
             }
         };
@@ -224,9 +234,9 @@ __global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void pag
 #pragma unroll
             for (int t = 0; t < NSUB; t++) {
                 arrived(page[t]);
-                const uint32_t key = (uint32_t)(c * KB + wave * KW + t * 16 + col);
+                const uint32_t key = (uint32_t)(c * KB + wave * KW + t * 16 + col + skip);
                 const uint32_t off = key - a.block(key) * a.block.div;
-                const bool ok = (int)key < nkeys && page[t] >= 0 && page[t] < a.n_blocks;
+                const bool ok = (int)key < nkeys + skip && page[t] >= 0 && page[t] < a.n_blocks;
                 row[t] = ok ? ((uint32_t)page[t] * a.kv_heads + kvh) * a.block.div + off : NO_ROW;
             }
         };
@@ -341,10 +351,18 @@ __global__ __launch_bounds__(PD_THREADS, (PD_WAVES_PER_SIMD<T, D, RT>)) void pag
         }
 
         // merge the four waves, one 16-row tile at a time
-        const bool whole = c0 == 0 && c1 == nch;
-        if (c0 == 0 && me.row_tile == 0 && tid == 0)
-            join_note(a.join, a.split, run, me.worker, b, kvh, c1, nch, run.pos != run_start);
-        const int slot = 2 * me.worker + (run.pos == run_start ? 0 : 1);
+        const bool covered = c0 == 0 && c1 == nch, whole = covered && (!BEHIND || skip == 0);
+        const int unit = b * a.kv_heads + kvh;
+        int slot = 2 * me.worker + (run.pos == run_start ? 0 : 1);
+        if (BEHIND && covered) slot = 2 * a.workers + unit;
+        if (c0 == 0 && me.row_tile == 0 && tid == 0) {
+            if constexpr (BEHIND) {  // (parts, the first one's slot; the others' are 2 w)
+                const int parts = covered ? 1 : run.cut.owner(run.pos + nch - 1) - me.worker + 1;
+                a.join.notes[unit] = make_int4(parts, me.worker, slot, whole ? -1 : 0);
+            } else {
+                join_note(a.join, a.split, run, me.worker, b, kvh, c1, nch, run.pos != run_start);
+            }
+        }
         const size_t part_row = ((size_t)slot * a.row_tiles + me.row_tile) * (16 * RT);
         float* mrow = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -422,37 +440,37 @@ __global__ __launch_bounds__(JOIN_THREADS) void paged_join_kernel(PagedDecodeArg
     });
 }
 
-template <typename T, int D, int RT>
+template <typename T, int D, int RT, bool BEHIND>
 hipError_t run_decode(const PagedDecodeArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((paged_decode_kernel<T, D, RT>), dim3((unsigned)(a.workers * a.row_tiles)),
-                       dim3(PD_THREADS), 0, s, a);
+    hipLaunchKernelGGL((paged_decode_kernel<T, D, RT, BEHIND>),
+                       dim3((unsigned)(a.workers * a.row_tiles)), dim3(PD_THREADS), 0, s, a);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || BEHIND) return e;
     hipLaunchKernelGGL((paged_join_kernel<T, D>), dim3(join_grid(a.join)), dim3(JOIN_THREADS),
                        0, s, a);
     return hipGetLastError();
 }
 
-template <typename T, int D>
+template <typename T, int D, bool BEHIND>
 hipError_t pick_rows(const PagedDecodeArgs& a, hipStream_t s) {
     switch (a.rt) {
-        case 1: return run_decode<T, D, 1>(a, s);
+        case 1: return run_decode<T, D, 1, BEHIND>(a, s);
         case 2:
-            if constexpr (sizeof(T) == 2 && D <= 128) return run_decode<T, D, 2>(a, s);
+            if constexpr (sizeof(T) == 2 && D <= 128) return run_decode<T, D, 2, BEHIND>(a, s);
             break;
         case 4:
-            if constexpr (sizeof(T) == 2 && D == 64) return run_decode<T, D, 4>(a, s);
+            if constexpr (sizeof(T) == 2 && D == 64) return run_decode<T, D, 4, BEHIND>(a, s);
             break;
     }
     return hipErrorInvalidValue;
 }
 
-template <typename T>
+template <typename T, bool BEHIND>
 hipError_t pick_dim(const PagedDecodeArgs& a, hipStream_t s) {
     switch (a.d) {
-        case 64: return pick_rows<T, 64>(a, s);
-        case 128: return pick_rows<T, 128>(a, s);
-        case 256: return pick_rows<T, 256>(a, s);
+        case 64: return pick_rows<T, 64, BEHIND>(a, s);
+        case 128: return pick_rows<T, 128, BEHIND>(a, s);
+        case 256: return pick_rows<T, 256, BEHIND>(a, s);
     }
     return hipErrorInvalidValue;
 }
@@ -497,7 +515,11 @@ size_t paged_decode_layout(PagedDecodeArgs* a, void* ws) {
 
 hipError_t launch_paged_decode(const PagedDecodeArgs& a, hipStream_t s) {
     (void)hipGetLastError();  // report only errors raised by this call's launches
-    return a.dtype == 1 ? pick_dim<bf16>(a, s) : pick_dim<float>(a, s);
+    return a.dtype == 1 ? pick_dim<bf16, false>(a, s) : pick_dim<float, false>(a, s);
+}
+
+hipError_t launch_own_keys(const PagedDecodeArgs& a, hipStream_t s) {
+    return a.dtype == 1 ? pick_dim<bf16, true>(a, s) : pick_dim<float, true>(a, s);
 }
 
 }  // namespace gdn

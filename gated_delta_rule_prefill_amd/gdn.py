@@ -17,6 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("GDN_LIB") or os.path.join(HERE, "libgdn.so")
 
 GDN_DTYPE_F32, GDN_DTYPE_BF16 = 0, 1
+# include/gdn.h GDN_COPY_MAX_CACHES: most pools of one gdn_paged_copy call
+GDN_COPY_MAX_CACHES = 128
 # include/gdn.h GDN_NOALLOC_SCRATCH_BYTES: the allocation-free prefill's per-GPU workspace
 GDN_NOALLOC_SCRATCH_BYTES = 128 << 20
 GDN_GATE_SCALAR, GDN_GATE_PER_KEY = 0, 1
@@ -83,6 +85,17 @@ _SIGS = {
     "gdn_paged_plan": [_P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P],
     "gdn_paged_append": [_I, _P, _L, _P, _L, _P, _I, _I, _I, _P, _P, _I, _I, _P],
     "gdn_latent_append": [_I, _P, _L, _P, _L, _P, _I, _I, _I, _P, _I, _I, _P],
+    "gdn_paged_fork": [_P, _P, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P],
+    "gdn_paged_free_workspace_bytes": [_I, ctypes.POINTER(_SZ)],
+    "gdn_paged_free": [_P, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P, _P, _SZ, _P],
+    "gdn_paged_compact_workspace_bytes": [_I, ctypes.POINTER(_SZ)],
+    "gdn_paged_compact": [_P, _I, _P, _I, _I, _P, _I, _P, _P, _I, _P, _P, _SZ, _P],
+    "gdn_paged_copy": [_P, _I, _L, _I, _P, _P, _I, _P, _P],
+    "gdn_paged_shared_decode_workspace_bytes": [_PAGED, _I, _I, _I, ctypes.POINTER(_SZ)],
+    "gdn_paged_shared_decode": [_PAGED, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _I, _P, _P,
+                                _SZ, _P],
+    "gdn_paged_prefill_workspace_bytes": [_PAGED, _I, _I, ctypes.POINTER(_SZ)],
+    "gdn_paged_prefill": [_PAGED, _P, _P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P, _SZ, _P],
     "gdn_paged_decode_workspace_bytes": [_PAGED, _I, _I, ctypes.POINTER(_SZ)],
     "gdn_paged_decode": [_PAGED, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _SZ, _P],
     "gdn_latent_decode_workspace_bytes": [_LATENT, _I, _I, ctypes.POINTER(_SZ)],
@@ -612,6 +625,182 @@ def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=1.0, o=No
          _arg("v_cache", v_cache, (n_blocks, kv, bs, d), dt, dev), n_blocks, bs,
          _table_arg(block_table, B, dev), block_table.shape[1],
          _arg("seq_lens", seq_lens, (B,), _I32, dev), B, P, _arg("o", o, shape, dt, dev), ws,
+         ws_bytes)
+    return o
+
+
+def _table_rows(t, dev):
+    """Address and shape of a table of which some rows are named."""
+    return _table_arg(t, t.shape[0], dev), t.shape[0], t.shape[1]
+
+
+def _pool_args(shares, dev):
+    return _arg("shares", shares, (shares.numel(),), _I32, dev), shares.numel()
+
+
+def gdn_paged_fork(src_rows, dst_rows, fork_lens, block_table, block_size, shares, free_blocks,
+                   copy_src=None, copy_dst=None, counts=None, stream=None):
+    """Requests that continue others: row dst_rows[i] of the table gets the first fork_lens[i]
+    tokens of row src_rows[i] ([n] int32 each), sharing the whole pages (shares [n_blocks] int32
+    counts a page's holders beyond the first) and taking a page of free_blocks for the rest.
+    block_table [rows, max_blocks] int32 and shares are updated in place. Returns (copy_src [n],
+    copy_dst [n]: pages to copy with gdn_paged_copy, -1 for none; counts [2]: pages asked of the
+    free list, pages handed out)."""
+    n, dev = src_rows.numel(), _gpu(block_table)
+    n_free = free_blocks.numel()
+    copy_src = _new((n,), _I32, block_table, stream) if copy_src is None else copy_src
+    copy_dst = _new((n,), _I32, block_table, stream) if copy_dst is None else copy_dst
+    counts = _new((2,), _I32, block_table, stream) if counts is None else counts
+    _run("gdn_paged_fork", dev, stream, _arg("src_rows", src_rows, (n,), _I32, dev),
+         _arg("dst_rows", dst_rows, (n,), _I32, dev), _arg("fork_lens", fork_lens, (n,), _I32, dev),
+         n, *_table_rows(block_table, dev), int(block_size), *_pool_args(shares, dev),
+         _arg("free_blocks", free_blocks, (n_free,), _I32, dev), n_free,
+         _arg("copy_src", copy_src, (n,), _I32, dev), _arg("copy_dst", copy_dst, (n,), _I32, dev),
+         _arg("counts", counts, (2,), _I32, dev))
+    return copy_src, copy_dst, counts
+
+
+def _bytes_of(name, *args):
+    out = _SZ(0)
+    _check(name, getattr(lib(), name)(*args, ctypes.byref(out)))
+    return int(out.value)
+
+
+def gdn_paged_free_workspace_bytes(n_blocks):
+    return _bytes_of("gdn_paged_free_workspace_bytes", int(n_blocks))
+
+
+def gdn_paged_free(rows, lens, block_table, block_size, shares, freed=None, max_freed=None,
+                   counts=None, workspace=None, stream=None):
+    """Requests that end: the pages of rows[i] ([n] int32) of the table for lens[i] tokens have a
+    holder less, their entries become -1. Returns (freed [max_freed] int32: the pages that nobody
+    holds any more in the order of their ids, then -1; counts [1]: how many). max_freed is by
+    default as many as the rows can hold; `freed` may be a part of a longer list."""
+    n, dev = rows.numel(), _gpu(block_table)
+    if freed is None:
+        most = min(n * block_table.shape[1], shares.numel()) if max_freed is None else max_freed
+        freed = _new((int(most),), _I32, block_table, stream)
+    counts = _new((1,), _I32, block_table, stream) if counts is None else counts
+    ws, ws_bytes = _space(workspace, lambda: gdn_paged_free_workspace_bytes(shares.numel()),
+                          block_table, stream, dev)
+    most = freed.numel()
+    _run("gdn_paged_free", dev, stream, _arg("rows", rows, (n,), _I32, dev),
+         _arg("lens", lens, (n,), _I32, dev), n, *_table_rows(block_table, dev), int(block_size),
+         *_pool_args(shares, dev), _arg("freed", freed, (most,), _I32, dev), most,
+         _arg("counts", counts, (1,), _I32, dev), ws, ws_bytes)
+    return freed, counts
+
+
+def gdn_paged_compact_workspace_bytes(n_blocks):
+    return _bytes_of("gdn_paged_compact_workspace_bytes", int(n_blocks))
+
+
+def gdn_paged_compact(seq_lens, block_table, block_size, shares, max_copies=None, copy_src=None,
+                      copy_dst=None, counts=None, workspace=None, stream=None):
+    """Moves the live pages (those that the table's rows hold for seq_lens [rows] int32 tokens) to
+    the front of the pool. block_table [rows, max_blocks] and shares [n_blocks] are updated in
+    place. Returns (copy_src, copy_dst [max_copies] int32: the moves, to be made in every cache
+    with gdn_paged_copy, then -1; counts [2]: live pages, moves). max_copies is by default as many
+    as there can be."""
+    n, dev = seq_lens.numel(), _gpu(block_table)
+    if max_copies is None:
+        max_copies = shares.numel() // 2 if copy_src is None else copy_src.numel()
+    m = int(max_copies)
+    copy_src = _new((m,), _I32, block_table, stream) if copy_src is None else copy_src
+    copy_dst = _new((m,), _I32, block_table, stream) if copy_dst is None else copy_dst
+    counts = _new((2,), _I32, block_table, stream) if counts is None else counts
+    ws, ws_bytes = _space(workspace, lambda: gdn_paged_compact_workspace_bytes(shares.numel()),
+                          block_table, stream, dev)
+    _run("gdn_paged_compact", dev, stream, _arg("seq_lens", seq_lens, (n,), _I32, dev), n,
+         _table_arg(block_table, n, dev), block_table.shape[1], int(block_size),
+         *_pool_args(shares, dev), _arg("copy_src", copy_src, (m,), _I32, dev),
+         _arg("copy_dst", copy_dst, (m,), _I32, dev), m, _arg("counts", counts, (2,), _I32, dev),
+         ws, ws_bytes)
+    return copy_src, copy_dst, counts
+
+
+def gdn_paged_copy(caches, copy_src, copy_dst, count=None, stream=None):
+    """Pages copy_src[i] copied to pages copy_dst[i] ([n] int32; -1: none) within each of the
+    caches: contiguous tensors of one length (pages) and one number of bytes a page, of any type
+    and shape (key, value and latent caches, state pools). count [1] int32 on the GPU, or None:
+    pairs from it on are not looked at."""
+    n, dev = copy_src.numel(), _gpu(copy_src)
+    addresses, like = [], None
+    for c in caches:
+        now = (c.shape[0], c.stride(0) * c.element_size())
+        like = now if like is None else like
+        if now != like or c.get_device() != dev or not c.is_contiguous():
+            raise ValueError("caches must be contiguous, on one GPU, and alike in their pages: got "
+                             f"{tuple(c.shape)} {c.dtype} on {c.device}")
+        addresses.append(c.data_ptr())
+    if like is None:
+        return
+    count = None if count is None else _arg("count", count, (1,), _I32, dev)
+    _run("gdn_paged_copy", dev, stream, (_P * len(addresses))(*addresses), len(addresses), like[1],
+         like[0], _arg("copy_src", copy_src, (n,), _I32, dev),
+         _arg("copy_dst", copy_dst, (n,), _I32, dev), n, count)
+
+
+def gdn_paged_shared_decode_workspace_bytes(H, kv_heads, d, dtype, batch, n_pos, n_groups):
+    dims = gdn_paged_dims_t(int(H), int(kv_heads), int(d), _code(dtype), 1.0)
+    return _bytes_of("gdn_paged_shared_decode_workspace_bytes", ctypes.byref(dims), int(batch),
+                     int(n_pos), int(n_groups))
+
+
+def gdn_paged_shared_decode(q, k_cache, v_cache, block_table, seq_lens, group_cu, prefix_lens,
+                            scale=1.0, o=None, workspace=None, stream=None):
+    """gdn_paged_decode for a batch in which groups of requests share a prefix, read once for the
+    group: requests group_cu[g] .. group_cu[g + 1] - 1 ([groups + 1] int32) hold the same pages for
+    their first prefix_lens[g] tokens ([groups] int32). Returns o, shaped as q."""
+    shape, dt = q.shape, q.dtype
+    if len(shape) == 3:  # one position per request
+        (B, H, d), P = shape, 1
+    else:
+        B, P, H, d = shape
+    n_blocks, kv, bs, _ = k_cache.shape
+    groups = prefix_lens.numel()
+    dev = _gpu(q)
+    code = _dtype_code(q)
+    o = _new(shape, dt, q, stream) if o is None else o
+    ws, ws_bytes = _space(workspace, lambda: gdn_paged_shared_decode_workspace_bytes(
+        H, kv, d, code, B, P, groups), q, stream, dev)
+    _run("gdn_paged_shared_decode", dev, stream, gdn_paged_dims_t(H, kv, d, code, scale),
+         _arg("q", q, shape, dt, dev), _arg("k_cache", k_cache, (n_blocks, kv, bs, d), dt, dev),
+         _arg("v_cache", v_cache, (n_blocks, kv, bs, d), dt, dev), n_blocks, bs,
+         _table_arg(block_table, B, dev), block_table.shape[1],
+         _arg("seq_lens", seq_lens, (B,), _I32, dev), B, P,
+         _arg("group_cu", group_cu, (groups + 1,), _I32, dev),
+         _arg("prefix_lens", prefix_lens, (groups,), _I32, dev), groups,
+         _arg("o", o, shape, dt, dev), ws, ws_bytes)
+    return o
+
+
+def gdn_paged_prefill_workspace_bytes(H, kv_heads, d, dtype, n_seqs, total_tokens):
+    dims = gdn_paged_dims_t(int(H), int(kv_heads), int(d), _code(dtype), 1.0)
+    return _bytes_of("gdn_paged_prefill_workspace_bytes", ctypes.byref(dims), int(n_seqs),
+                     int(total_tokens))
+
+
+def gdn_paged_prefill(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scale=1.0, o=None,
+                      workspace=None, stream=None):
+    """Attention of packed new tokens over a paged cache that already holds them, causal. q
+    [T, H, d]; k_cache, v_cache [n_blocks, kv_heads, block_size, d]; block_table [n, max_blocks]
+    int32; cu_seqlens [n + 1] int32; seq_lens [n] int32, the new tokens included. Returns o
+    [T, H, d]."""
+    T, H, d = q.shape
+    n = seq_lens.numel()
+    n_blocks, kv, bs, _ = k_cache.shape
+    dt, dev = q.dtype, _gpu(q)
+    code = _dtype_code(q)
+    o = _new((T, H, d), dt, q, stream) if o is None else o
+    ws, ws_bytes = _space(workspace, lambda: gdn_paged_prefill_workspace_bytes(
+        H, kv, d, code, n, T), q, stream, dev)
+    _run("gdn_paged_prefill", dev, stream, gdn_paged_dims_t(H, kv, d, code, scale),
+         _arg("q", q, (T, H, d), dt, dev), _arg("k_cache", k_cache, (n_blocks, kv, bs, d), dt, dev),
+         _arg("v_cache", v_cache, (n_blocks, kv, bs, d), dt, dev), n_blocks, bs,
+         _table_arg(block_table, n, dev), block_table.shape[1],
+         _arg("cu_seqlens", cu_seqlens, (n + 1,), _I32, dev),
+         _arg("seq_lens", seq_lens, (n,), _I32, dev), n, T, _arg("o", o, (T, H, d), dt, dev), ws,
          ws_bytes)
     return o
 

@@ -527,6 +527,140 @@ int gdn_paged_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_
                      int32_t batch, int32_t n_pos, void* o, void* workspace, size_t ws_bytes,
                      void* stream);
 
+/* ---- pages that requests share ----
+ * Requests that begin alike (samples and beams of one prompt, turns behind one system prompt) hold
+ * the pages of their common prefix together: their table rows name the same pages. The counts
+ * that this takes:
+ *   - shares [n_blocks] int32 (device): holders of a page beyond the first. It starts as zeros; a
+ *     page that gdn_paged_plan hands out, and every free page, has 0, so that plan, append and
+ *     the attention calls need not know of it.
+ * Only whole pages are shared, and a holder writes to the page behind its last whole one, so no
+ * call writes into a page that another request reads. A fork of a hybrid request also needs its
+ * linear layers' states: gdn_paged_copy copies slots of a state pool (one slot a page) as well.
+ * Rows and pages outside their ranges are skipped, as slots are; lengths count as 0 when negative
+ * and as max_blocks * block_size when longer. One call takes at most 2^24 rows. */
+
+/* Requests that continue others. Fork i gives row dst_rows[i] the first fork_lens[i] tokens of row
+ * src_rows[i]: with whole = floor(fork_lens[i] / block_size), the entries 0 .. whole - 1 are
+ * entered into the row and each page that they name has one holder more (null entries stay null);
+ * if tokens are left over, entry `whole` becomes the next id of free_blocks (handed out in the
+ * order of the forks; -1 once they are used up, and -1 where the source's entry is null, which
+ * takes none), and the page of the source with the left-over tokens is to be copied there. Entries
+ * behind that stay as they are. A fork whose rows are out of [0, n_rows), or the same, is skipped.
+ *   src_rows, dst_rows, fork_lens [n] int32 (device). dst_rows are distinct, and none of them is
+ *              in src_rows (the debug library checks)
+ *   block_table [n_rows, max_blocks] int32 (device), updated in place
+ *   shares     [n_blocks] int32 (device), updated in place
+ *   free_blocks [n_free] int32 (device; not changed; may be the rest of a longer list)
+ *   copy_src, copy_dst [n] int32: the page to be copied and its destination (gdn_paged_copy), -1
+ *              and -1 for a fork that needs no copy or got no page
+ *   counts     [2] int32: pages asked of the free list, pages handed out
+ * The lists need the alignment of their entries only. n == 0 sets the counts to 0. */
+int gdn_paged_fork(const int32_t* src_rows, const int32_t* dst_rows, const int32_t* fork_lens,
+                   int32_t n, int32_t* block_table, int32_t n_rows, int32_t max_blocks,
+                   int32_t block_size, int32_t* shares, int32_t n_blocks,
+                   const int32_t* free_blocks, int32_t n_free, int32_t* copy_src,
+                   int32_t* copy_dst, int32_t* counts, void* stream);
+
+/* Workspace of gdn_paged_free (host computation). */
+int gdn_paged_free_workspace_bytes(int32_t n_blocks, size_t* bytes);
+
+/* Requests that end. The entries 0 .. ceil(lens[i] / block_size) - 1 of row rows[i] become -1, and
+ * each page that they named has one holder less; the pages that had no other holder are listed.
+ * A row listed twice ends once (with the longer of both lengths).
+ *   rows, lens [n] int32 (device)
+ *   block_table [n_rows, max_blocks], shares [n_blocks] int32 (device), updated in place
+ *   freed      [max_freed] int32: the freed pages in the order of their ids, then -1. It may be
+ *              the rest of a longer list (the free list that gdn_paged_plan takes from). Of more
+ *              than max_freed the first max_freed are listed, and counts tells
+ *   counts     [1] int32: freed pages
+ *   workspace  device scratch; its contents need no initialisation and carry no meaning
+ *              afterwards. Calls that may overlap need one each. */
+int gdn_paged_free(const int32_t* rows, const int32_t* lens, int32_t n, int32_t* block_table,
+                   int32_t n_rows, int32_t max_blocks, int32_t block_size, int32_t* shares,
+                   int32_t n_blocks, int32_t* freed, int32_t max_freed, int32_t* counts,
+                   void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace of gdn_paged_compact (host computation). */
+int gdn_paged_compact_workspace_bytes(int32_t n_blocks, size_t* bytes);
+
+/* Moves live pages to the front of the pool, so that its end can be given back or lent. Live are
+ * the pages that the table's entries 0 .. ceil(seq_lens[i] / block_size) - 1 name (0 for a row
+ * that is not in use). With n of them, those from id n on go to the ids below n that are not live,
+ * the k-th of both in the order of their ids: the fewest moves there are, from pages at n and above
+ * to pages below n. Entries and shares follow; afterwards the free pages are n .. n_blocks - 1.
+ * With more moves than max_copies the first max_copies are made (call again for the rest).
+ *   seq_lens   [n_rows] int32 (device)
+ *   block_table [n_rows, max_blocks], shares [n_blocks] int32 (device), updated in place
+ *   copy_src, copy_dst [max_copies] int32: the moves, to be made in every cache (gdn_paged_copy)
+ *              before a page is read or written again; then -1
+ *   counts     [2] int32: live pages, moves (those beyond max_copies included)
+ *   workspace  as gdn_paged_free */
+int gdn_paged_compact(const int32_t* seq_lens, int32_t n_rows, int32_t* block_table,
+                      int32_t max_blocks, int32_t block_size, int32_t* shares, int32_t n_blocks,
+                      int32_t* copy_src, int32_t* copy_dst, int32_t max_copies, int32_t* counts,
+                      void* workspace, size_t ws_bytes, void* stream);
+
+/* Largest n_caches of gdn_paged_copy. */
+#define GDN_COPY_MAX_CACHES 128
+
+/* Copies pages copy_src[i] to pages copy_dst[i] within each of several pools, in one launch.
+ *   caches     [n_caches] HOST array of device pointers, each to n_blocks pages of page_bytes
+ *              bytes (a multiple of 16): key, value or latent caches of the layers, or state pools
+ *   copy_src, copy_dst [n] int32 (device). A pair with a page outside [0, n_blocks) is skipped.
+ *              Destinations are distinct and no source is one (the debug library checks)
+ *   count      [1] int32 (device) or NULL: pairs from *count on are not looked at */
+int gdn_paged_copy(void* const* caches, int32_t n_caches, int64_t page_bytes, int32_t n_blocks,
+                   const int32_t* copy_src, const int32_t* copy_dst, int32_t n,
+                   const int32_t* count, void* stream);
+
+/* Workspace of gdn_paged_shared_decode for the current device (host computation). */
+int gdn_paged_shared_decode_workspace_bytes(const gdn_paged_dims_t* dims, int32_t batch,
+                                            int32_t n_pos, int32_t n_groups, size_t* bytes);
+
+/* gdn_paged_decode for a batch in which groups of requests share a prefix: its keys are read once
+ * for the group. Same results up to rounding, and the same arguments, plus:
+ *   group_cu    [n_groups + 1] int32 (device), non-decreasing within [0, batch]: group g is the
+ *               requests group_cu[g] .. group_cu[g + 1] - 1. Requests before the first and behind
+ *               the last group share nothing
+ *   prefix_lens [n_groups] int32 (device): the first prefix_lens[g] tokens of a group's requests
+ *               lie in the same pages (any number, whole pages or not; those of the row of its
+ *               first request are read). A request may be shorter (a padded row of length 0 too)
+ * n_groups may be 0 (the arrays may then be NULL). A NaN or infinity in a value row of the prefix
+ * reaches all requests of the group; in the newest n_pos tokens as in gdn_paged_decode. Workspace
+ * and determinism as there. */
+int gdn_paged_shared_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_cache,
+                            const void* v_cache, int32_t n_blocks, int32_t block_size,
+                            const int32_t* block_table, int32_t max_blocks,
+                            const int32_t* seq_lens, int32_t batch, int32_t n_pos,
+                            const int32_t* group_cu, const int32_t* prefix_lens, int32_t n_groups,
+                            void* o, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace of gdn_paged_prefill for the current device (host computation). It does not depend on
+ * the lengths of the requests. */
+int gdn_paged_prefill_workspace_bytes(const gdn_paged_dims_t* dims, int32_t n_seqs,
+                                      int32_t total_tokens, size_t* bytes);
+
+/* Attention of packed new tokens over the cache, which already holds them (gdn_paged_append), causal:
+ * whole prompts, chunks of them, turns behind a cached or shared prefix, single tokens. The new
+ * tokens of request i are its last w = cu_seqlens[i + 1] - cu_seqlens[i];
+ *   o[cu_seqlens[i] + t, h] = sum_j softmax_j(scale q[cu_seqlens[i] + t, h] . k_j) v_j
+ * over the request's tokens j <= seq_lens[i] - w + t that exist; zeros if there is none.
+ *   q, o        [total_tokens, num_heads, d] dtype
+ *   k_cache, v_cache, block_table [n_seqs, max_blocks], seq_lens [n_seqs] as in gdn_paged_decode
+ *   cu_seqlens  [n_seqs + 1] int32 (device), as in gdn_prefill_chunked. Rows of o from
+ *               cu_seqlens[n_seqs] on (a padded batch) are left as they are. Where cu_seqlens
+ *               passes total_tokens, the tokens behind it have no rows and are no keys; the
+ *               others keep their positions.
+ * Workspace and determinism as in gdn_paged_decode. A NaN or infinity in the value row of one of a
+ * request's tokens can reach the outputs of up to 94 tokens before it. n_seqs == 0 and
+ * total_tokens == 0 are no-ops. */
+int gdn_paged_prefill(const gdn_paged_dims_t* dims, const void* q, const void* k_cache,
+                      const void* v_cache, int32_t n_blocks, int32_t block_size,
+                      const int32_t* block_table, int32_t max_blocks, const int32_t* cu_seqlens,
+                      const int32_t* seq_lens, int32_t n_seqs, int32_t total_tokens, void* o,
+                      void* workspace, size_t ws_bytes, void* stream);
+
 /* Latent attention: a token's cache row is one latent c (rank elements) that all heads share,
  * followed by one rotary key r (d_rope). With head h's up projections W_uk,h [d_nope, rank]
  * and W_uv,h [d_v, rank], its key is (W_uk,h c, r) and its value W_uv,h c.
