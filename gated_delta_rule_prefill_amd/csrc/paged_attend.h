@@ -80,7 +80,7 @@ template <int D> struct AttendTile<bf16, D> {
     }
     // Scores of the keys at `kt`; beside(f) is other work for the time of two MFMAs (64 cycles).
     // The fences keep the compiler from taking the two apart again.
-    static constexpr int SLICES = NQ, AHEAD = 3;
+    static constexpr int AHEAD = 3;
     template <typename Beside>
     __device__ __forceinline__ void scores(uint32_t kt, int lane, Scores& s, Beside beside) const {
         const int r = lane & 31, half = lane >> 5;
@@ -108,18 +108,17 @@ template <int D> struct AttendTile<bf16, D> {
         }
     }
     // acc += V^T P^T for the weights s; l += their sum. The weights are rounded to bf16 (2^-8 of
-    // each at most) as the MFMA's operand, not in l.
-    __device__ __forceinline__ void values(uint32_t vt, int lane, const Scores& s, float* l) {
+    // each at most) as the MFMA's operand, not in l. beside(n) is other work for the time of one
+    // MFMA; weights of the second half of the keys may be formed there until n = LAST_WEIGHT.
+    static constexpr int NV = KB / 16 * NO, LAST_WEIGHT = NV * 5 / 8;
+    template <typename Beside>
+    __device__ __forceinline__ void values(uint32_t vt, int lane, const Scores& s, float* l,
+                                           Beside beside) {
         // lanes 0-15 and 16-31 read 16 columns each of 4 keys, the upper half of the next 4
         const int r = (lane >> 5) * 4 + ((lane >> 2) & 3);
         uint32_t at = vt + r * ROW + ((((lane >> 4) & 1) << 5) ^ (v_turn(r) << 4)) + (lane & 3) * 8;
         asm volatile("" : "+v"(at));
-        constexpr int NV = KB / 16 * NO;
-        bf16x8 p[4], v[AHEAD + 1];
-#pragma unroll
-        for (int n = 0; n < 4; n++)
-#pragma unroll
-            for (int i = 0; i < 8; i++) p[n][i] = (bf16)s[n >> 1][(n & 1) * 8 + i];
+        bf16x8 p, v[AHEAD + 1];
         auto load = [&](int n) {
             // keys 16 g + r and 16 g + 8 + r: rows 8 on are turned alike
             const int g = n / NO, j = n % NO;
@@ -131,9 +130,15 @@ template <int D> struct AttendTile<bf16, D> {
 #pragma unroll
         for (int n = 0; n < NV; n++) {
             if (n + AHEAD < NV) load(n + AHEAD);
-            acc[n % NO] = mma(v[n % (AHEAD + 1)], p[n / NO], acc[n % NO]);
+            const int g = n / NO;
+            if (n % NO == 0)
+#pragma unroll
+                for (int i = 0; i < 8; i++) p[i] = (bf16)s[g >> 1][(g & 1) * 8 + i];
+            acc[n % NO] = mma(v[n % (AHEAD + 1)], p, acc[n % NO]);
 #pragma unroll
             for (int i = n * 32 / NV; i < (n + 1) * 32 / NV; i++) *l += s[i >> 4][i & 15];
+            asm volatile("" : "+v"(*l));  // added here, beside the MFMAs
+            beside(n);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -192,7 +197,7 @@ template <int D> struct AttendTile<float, D> {
 #pragma unroll
         for (int f = 0; f < NQ; f++) asm volatile("" : "+v"(q[f]));  // as arrived()
     }
-    static constexpr int SLICES = 0;
+    static constexpr int NV = 0, LAST_WEIGHT = 0;
     template <typename Beside>
     __device__ __forceinline__ void scores(uint32_t kt, int lane, Scores& s, Beside) const {
         const int r = lane & 15;
@@ -209,19 +214,32 @@ template <int D> struct AttendTile<float, D> {
                 for (int e = 0; e < 4; e++) s[x] = Mma<float>::mma(k[e], q[f][e], s[x]);
             }
     }
-    __device__ __forceinline__ void values(uint32_t vt, int lane, const Scores& s, float* l) {
+    // A step's sums are formed by themselves and added once: a long sequence is then summed in
+    // two levels, and the roundings of n / 32 additions reach a result instead of those of n / 4.
+    template <typename Beside>
+    __device__ __forceinline__ void values(uint32_t vt, int lane, const Scores& s, float* l, Beside) {
+        constexpr int JN = 2;  // columns of tiles on their way
+        const uint32_t at = vt + (lane >> 4) * 4 * ROW + (lane & 15) * 4;
 #pragma unroll
-        for (int x = 0; x < 2; x++)
+        for (int j0 = 0; j0 < NO; j0 += JN) {
+            f32x4 sum[JN];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int r = x * 16 + (lane >> 4) * 4 + i;
-                const uint32_t at = vt + r * ROW + (lane & 15) * 4;
+            for (int j = 0; j < JN; j++) sum[j] = zero4();
 #pragma unroll
-                for (int j = 0; j < NO; j++)
-                    acc[j] = Mma<float>::mma(lds_get<float>(at + (((j << 2) ^ v_turn(r)) << 4)),
-                                             s[x][i], acc[j]);
-                *l += s[x][i];
-            }
+            for (int x = 0; x < 2; x++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int j = 0; j < JN; j++)
+                        sum[j] = Mma<float>::mma(
+                            lds_get<float>(at + (x * 16 + i) * ROW +
+                                           ((((j0 + j) << 2) ^ v_turn((lane >> 4) * 4)) << 4)),
+                            s[x][i], sum[j]);
+#pragma unroll
+            for (int j = 0; j < JN; j++) acc[j0 + j] += sum[j];
+        }
+        *l += ((s[0][0] + s[0][1]) + (s[0][2] + s[0][3])) +
+              ((s[1][0] + s[1][1]) + (s[1][2] + s[1][3]));
     }
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -246,7 +264,10 @@ template <int D> struct AttendTile<float, D> {
 constexpr int ATTEND_EXTRA = 2;
 // No worker is given fewer positions than this: a run's start, and the parts that a cut leaves to
 // be joined, cost as much.
-constexpr int ATTEND_MIN_RUN = 4;
+#ifndef AMR
+#define AMR 2
+#endif
+constexpr int ATTEND_MIN_RUN = AMR;
 
 // The stream of all units (total positions per key/value head) cut over the workers.
 struct AttendCut {
@@ -290,11 +311,26 @@ inline void attend_table_layout(AttendArgs* a, Layout* l) {
 // One workgroup lays out the tiles: rows_of(i) of each sequence, then each tile's unit.
 // Sums that the host's bound does not hold (lengths that break the contract) are cut off there.
 constexpr int AT_TABLE_THREADS = 1024;
+constexpr int AT_TABLE_SEQS = 2048;  // sequences whose bounds are kept in LDS for the searches
+
+// The last i < n with first(i) <= x.
+template <typename First>
+__device__ __forceinline__ int last_at(int n, int x, First first) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first(mid) <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
 template <typename RowsOf, typename UnitOf>
 __device__ __forceinline__ void attend_tables(const AttendArgs& a, int rows_a_tile, int kb,
                                               RowsOf rows_of, UnitOf unit_of) {
     __shared__ int64_t part[AT_TABLE_THREADS / WAVE];
+    __shared__ int near_tile[AT_TABLE_SEQS];
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+    const bool near = a.n_seqs <= AT_TABLE_SEQS;
     auto scan = [&](int64_t x, int64_t* total) {  // exclusive
         int64_t upto = x;
 #pragma unroll
@@ -322,24 +358,23 @@ __device__ __forceinline__ void attend_tables(const AttendArgs& a, int rows_a_ti
     for (int i = i0; i < i1; i++) mine += tiles_of(i);
     int64_t at = scan(mine, &all);
     for (int i = i0; i < i1; i++) {
-        a.seq_tile[i] = (int)min(at, (int64_t)a.tiles);
-        at += tiles_of(i);
+        const int t = (int)min(at, (int64_t)a.tiles);
+        a.seq_tile[i] = t;
+        if (near) near_tile[i] = t;
+        if (i + 1 < i1) at += tiles_of(i);
     }
     const int n_tiles = (int)min(all, (int64_t)a.tiles);
     if (tid == 0) a.seq_tile[a.n_seqs] = n_tiles;
-    __threadfence();
+    if (!near) __threadfence();
     __syncthreads();
     int64_t base = 0;
     for (int t0 = 0; t0 < n_tiles; t0 += AT_TABLE_THREADS) {
         const int t = t0 + tid;
         int64_t len = 0;
         if (t < n_tiles) {
-            int lo = 0, hi = a.n_seqs;  // the last sequence whose first tile is t or before
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (a.seq_tile[mid] <= t) lo = mid; else hi = mid;
-            }
-            const AttendUnit u = unit_of(lo, (t - a.seq_tile[lo]) * rows_a_tile);
+            auto tile_of = [&](int i) { return near ? near_tile[i] : a.seq_tile[i]; };
+            const int i = last_at(a.n_seqs, t, tile_of);
+            const AttendUnit u = unit_of(i, (t - tile_of(i)) * rows_a_tile);
             a.tile[t] = u;
             len = (u.reach + kb - 1) / kb + ATTEND_EXTRA;
         }
@@ -487,8 +522,36 @@ void paged_attend_kernel(AttendArgs a) {
         };
 
         x.clear();
-        float ref = -INFINITY, l = 0.f;  // the exponents' reference (scaled); the sum
+        // the exponents' reference (scaled), and what is taken off them; the sum
+        float ref = -INFINITY, shift = 0.f, l = 0.f;
+        constexpr int N = X::SX * X::SI;
+        auto weight = [&](typename X::Scores& s, int n) {
+            float e = __builtin_amdgcn_exp2f(fmaf(s[n / X::SI][n % X::SI], cs, -shift));
+            if constexpr (X::NV > 0) asm volatile("" : "+v"(e));  // formed here
+            s[n / X::SI][n % X::SI] = e;
+        };
+        // The reference for scores whose largest (of this lane) is `top`: sums are taken along.
+        auto refer = [&](float top) {
+            top = X::max_partners(top) * cs;
+            const bool grown = top > ref + LAG;
+            if (__any(grown)) {
+                shift = grown ? top : shift;  // (a row without a key so far: sums of zero, shift 0)
+                const float f = grown ? __builtin_amdgcn_exp2f(ref - top) : 1.f;
+                ref = grown ? top : ref;
+                l *= f;
+                x.shrink(f);
+            }
+        };
+        auto largest = [&](const typename X::Scores& s, int n0, int n1, float top) {
+#pragma unroll
+            for (int n = n0; n < n1; n++) top = fmaxf(top, s[n / X::SI][n % X::SI]);
+            return top;
+        };
         int page = 0;
+        // One step: the weights of s (masked, their reference known), its values added; meanwhile
+        // the next step's scores and their maximum. Beside the MFMAs of the scores go 5 in 8 of the
+        // weights, beside those of the values the others, the sum and the maximum: about as many
+        // cycles of the vector pipe as of the matrix pipe in both halves.
         auto step = [&](int c, typename X::Scores& s, typename X::Scores& next) {
             lds_loads_done();
             if (wave == 0 && c + 3 < c1) {
@@ -503,52 +566,32 @@ void paged_attend_kernel(AttendArgs a) {
             if (c + 2 < c1) load_keys(c + 2);
             if (c + 1 < c1) load_values(c + 1);
             if (c >= mine) return;
-            float top = -INFINITY, shift = 0.f;
-            bool grown = false;
-            auto maximum = [&](int y) {
-#pragma unroll
-                for (int i = 0; i < X::SI; i++) top = fmaxf(top, s[y][i]);
-            };
-            auto reference = [&]() {
-                top = X::max_partners(top) * cs;
-                grown = top > ref + LAG;
-                const float to = grown ? top : ref;
-                shift = to == -INFINITY ? 0.f : to;  // a row with no key so far
-            };
-            auto weight = [&](int n) {
-                float e = __builtin_amdgcn_exp2f(fmaf(s[n / X::SI][n % X::SI], cs, -shift));
-                if constexpr (X::SLICES > 0) asm volatile("" : "+v"(e));  // formed here
-                s[n / X::SI][n % X::SI] = e;
-            };
-            constexpr int N = X::SX * X::SI;
-            const uint32_t kt = lds_offset(k_tile[(c + 1) & 1]);
-            if constexpr (X::SLICES > 0) {
-                // the first slices find the maximum, the rest form the weights
-                constexpr int WS = X::SLICES - 3, PER = (N + WS - 1) / WS;
+            const uint32_t kt = lds_offset(k_tile[(c + 1) & 1]), vt = lds_offset(v_tile[c & 1]);
+            float top = -INFINITY;
+            if constexpr (X::NV > 0) {
+                constexpr int FIRST = N * 5 / 8, REST = N - FIRST;
                 x.scores(kt, lane, next, [&](int f) {
-                    if (f < 2) maximum(f);
-                    else if (f == 2) reference();
-                    else
 #pragma unroll
-                        for (int n = (f - 3) * PER; n < (f - 2) * PER && n < N; n++) weight(n);
+                    for (int n = f * FIRST / X::NQ; n < (f + 1) * FIRST / X::NQ; n++) weight(s, n);
+                });
+                if (c + 1 < mine) mask(c + 1, next);
+                x.values(vt, lane, s, &l, [&](int v) {
+                    constexpr int L = X::LAST_WEIGHT;
+                    if (v < L)
+#pragma unroll
+                        for (int n = v * REST / L; n < (v + 1) * REST / L; n++) weight(s, FIRST + n);
+                    top = largest(next, v * N / X::NV, (v + 1) * N / X::NV, top);
+                    asm volatile("" : "+v"(top));
                 });
             } else {
-                maximum(0);
-                maximum(1);
-                reference();
 #pragma unroll
-                for (int n = 0; n < N; n++) weight(n);
+                for (int n = 0; n < N; n++) weight(s, n);
                 x.scores(kt, lane, next, [](int) {});
+                if (c + 1 < mine) mask(c + 1, next);
+                x.values(vt, lane, s, &l, [](int) {});
+                top = largest(next, 0, N, top);
             }
-            if (__any(grown)) {
-                // (a row without a reference so far has sums of zero)
-                const float f = grown ? __builtin_amdgcn_exp2f(ref - shift) : 1.f;
-                ref = grown ? shift : ref;
-                l *= f;
-                x.shrink(f);
-            }
-            x.values(lds_offset(v_tile[c & 1]), lane, s, &l);
-            if (c + 1 < mine) mask(c + 1, next);
+            if (c + 1 < mine) refer(top);
         };
         if (c1 > c0) {
             typename X::Scores s0, s1;
@@ -572,6 +615,7 @@ void paged_attend_kernel(AttendArgs a) {
             if (c0 < mine) {
                 x.scores(lds_offset(k_tile[c0 & 1]), lane, s0, [](int) {});
                 mask(c0, s0);
+                refer(largest(s0, 0, N, -INFINITY));
             }
             for (int c = c0; c < c1; c += 2) {
                 step(c, s0, s1);

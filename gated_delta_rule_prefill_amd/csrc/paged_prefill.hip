@@ -92,7 +92,10 @@ size_t paged_prefill_layout(PagedPrefillArgs* a, void* ws) {
     j.tile = j.rows = rows;
     j.per_unit = 0;
     j.count = at.workers;
-    j.share = 4;  // (workgroups of a note)
+#ifndef PJS
+#define PJS 16
+#endif
+    j.share = PJS;  // (workgroups of a note)
     j.slices = 1;
     j.part_o = l.take<float>((size_t)2 * at.workers * rows * at.d);
     j.part_ml = l.take<float>((size_t)2 * at.workers * rows * 2);

@@ -13,6 +13,11 @@ namespace gdn {
 
 namespace {
 
+#ifndef JWG
+#define JWG 16
+#endif
+constexpr int JOIN_WGS = JWG;
+
 // A group whose prefix is attended apart. One request alone has nothing to share: its prefix is
 // left to the decode kernel.
 struct SharedGroup {
@@ -41,13 +46,13 @@ __global__ __launch_bounds__(AT_TABLE_THREADS) void shared_tables_kernel(SharedD
         return;
     }
     // which group each request is in, and what it has to attend itself
+    __shared__ int near_cu[AT_TABLE_SEQS];
+    const bool near = groups <= AT_TABLE_SEQS;
+    for (int g = threadIdx.x; near && g < groups; g += AT_TABLE_THREADS) near_cu[g] = a.group_cu[g];
+    __syncthreads();
     const int b = (int)(blockIdx.x - 1) * AT_TABLE_THREADS + threadIdx.x;
     if (b >= a.batch) return;
-    int lo = 0, hi = groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.group_cu[mid] <= b) lo = mid; else hi = mid;
-    }
+    const int lo = last_at(groups, b, [&](int g) { return near ? near_cu[g] : a.group_cu[g]; });
     int start = 0;
     int2 place = make_int2(-1, 0);
     if (groups > 0) {
@@ -161,7 +166,7 @@ size_t shared_decode_layout(SharedDecodeArgs* a, void* ws) {
     const int64_t units = (int64_t)a->batch * at.kv_heads;
     j.count = (int)units;
     j.per_unit = 1;
-    const int64_t share = units > 0 ? 4 * cus / units : 1;
+    const int64_t share = units > 0 ? JOIN_WGS * (int64_t)cus / units : 1;
     j.share = share < 1 ? 1 : share < j.rows ? (int)share : j.rows;
     j.slices = 1;
     const size_t own_rows = ((size_t)2 * own.workers + (size_t)units) * own.row_tiles * j.tile;
