@@ -39,15 +39,28 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 template <typename T, int D> struct AttendTile;
 
 template <int D> struct AttendTile<bf16, D> {
-    // One wave a SIMD at d = 256 (outputs and queries alone take 192 registers), else two.
-    static constexpr int WAVES = D == 256 ? 4 : 8;
-    static constexpr int WAVES_PER_SIMD = WAVES / 4;
+    // One wave a SIMD at d = 256 (outputs and queries alone take 192 registers), else two. (Waves
+    // of 64 rows, one a SIMD, halve the LDS reads, and lose more: a prompt of 12000 tokens, 32
+    // heads, 1860 us in steps of 32 keys, and 3160 with 64, where registers spill; 1290 with two.)
     static constexpr int WAVE_ROWS = 32, KB = 64;
+    static constexpr int WAVES = D == 256 ? 4 : 8, WAVES_PER_SIMD = WAVES / 4;
     static constexpr int ROW = D * 2, PIECES = ROW / 16;
-    static constexpr int NQ = D / 16, NO = D / 32;
-    typedef f32x16 Scores[2];
+    // Steps that keys and values are loaded ahead of the one that waits for them: the first pieces
+    // of a step's keys can then be read before its barrier. (Three buffers each; at d = 256 two
+    // fit.)
+    static constexpr int LEAD = D == 256 ? 0 : 1;
+    static constexpr int NQ = D / 16, NO = D / 32, NV = KB / 16 * NO;
+    static constexpr int AHEAD = D == 256 ? 3 : 2;  // pieces on their way (3 spill at d = 128)
+    static constexpr bool INTERLEAVED = true;
+    struct Scores {
+        f32x16 v[2];
+        __device__ __forceinline__ float get(int n) const { return v[n >> 4][n & 15]; }
+        __device__ __forceinline__ void set(int n, float z) { v[n >> 4][n & 15] = z; }
+    };
+    static constexpr int N = 32;  // scores of a lane
     bf16x8 q[NQ];
     f32x16 acc[NO];
+    bf16x8 kf[AHEAD + 1][2], vf[AHEAD + 1];
 
     __device__ __forceinline__ static int k_turn(int r) { return D >= 128 ? r & 15 : (r >> 1) & 7; }
     // (pairs of pieces: a transposing read takes 32 bytes of each of 8 rows, twice side by side)
@@ -56,10 +69,9 @@ template <int D> struct AttendTile<bf16, D> {
     }
     __device__ __forceinline__ static int row_of_lane(int lane) { return lane & 31; }
     __device__ __forceinline__ static int first_key(int lane) { return (lane >> 5) * 4; }
-    __device__ __forceinline__ static int key(int x, int i) {  // + first_key
-        return x * 32 + (i >> 2) * 8 + (i & 3);
+    __device__ __forceinline__ static int key(int n) {  // of score n, + first_key
+        return (n >> 4) * 32 + ((n & 15) >> 2) * 8 + (n & 3);
     }
-    static constexpr int SX = 2, SI = 16;
     __device__ __forceinline__ static float max_partners(float x) { return max_halves(x); }
     __device__ __forceinline__ static float sum_partners(float x) {
         return x + __shfl_xor(x, 32, WAVE);
@@ -78,66 +90,76 @@ template <int D> struct AttendTile<bf16, D> {
     __device__ __forceinline__ static f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
-    // Scores of the keys at `kt`; beside(f) is other work for the time of two MFMAs (64 cycles).
-    // The fences keep the compiler from taking the two apart again.
-    static constexpr int AHEAD = 3;
-    template <typename Beside>
-    __device__ __forceinline__ void scores(uint32_t kt, int lane, Scores& s, Beside beside) const {
-        const int r = lane & 31, half = lane >> 5;
-        uint32_t at = kt + r * ROW + ((half ^ k_turn(r)) << 4);
-        asm volatile("" : "+v"(at));
-        bf16x8 k[AHEAD + 1][2];
-        auto load = [&](int f) {
-#pragma unroll
-            for (int x = 0; x < 2; x++)  // (32 rows on, the pieces are turned alike)
-                k[f % (AHEAD + 1)][x] = lds_get<bf16x8>((at ^ (f << 5)) + x * 32 * ROW);
-        };
-#pragma unroll
-        for (int f = 0; f < AHEAD && f < NQ; f++) load(f);
-#pragma unroll
-        for (int x = 0; x < 2; x++)
-#pragma unroll
-            for (int i = 0; i < 16; i++) s[x][i] = 0.f;
-#pragma unroll
-        for (int f = 0; f < NQ; f++) {
-            if (f + AHEAD < NQ) load(f + AHEAD);
-#pragma unroll
-            for (int x = 0; x < 2; x++) s[x] = mma(k[f % (AHEAD + 1)][x], q[f], s[x]);
-            beside(f);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+    // Places of this lane's first pieces in the tiles at `kt` and `vt`.
+    __device__ __forceinline__ static uint32_t key_place(uint32_t kt, int lane) {
+        const int r = lane & 31;
+        uint32_t at = kt + r * ROW + (((lane >> 5) ^ k_turn(r)) << 4);
+        asm volatile("" : "+v"(at));  // (formed here: one register, not one for each piece)
+        return at;
     }
-    // acc += V^T P^T for the weights s; l += their sum. The weights are rounded to bf16 (2^-8 of
-    // each at most) as the MFMA's operand, not in l. beside(n) is other work for the time of one
-    // MFMA; weights of the second half of the keys may be formed there until n = LAST_WEIGHT.
-    static constexpr int NV = KB / 16 * NO, LAST_WEIGHT = NV * 5 / 8;
-    template <typename Beside>
-    __device__ __forceinline__ void values(uint32_t vt, int lane, const Scores& s, float* l,
-                                           Beside beside) {
+    __device__ __forceinline__ static uint32_t value_place(uint32_t vt, int lane) {
         // lanes 0-15 and 16-31 read 16 columns each of 4 keys, the upper half of the next 4
         const int r = (lane >> 5) * 4 + ((lane >> 2) & 3);
         uint32_t at = vt + r * ROW + ((((lane >> 4) & 1) << 5) ^ (v_turn(r) << 4)) + (lane & 3) * 8;
         asm volatile("" : "+v"(at));
-        bf16x8 p, v[AHEAD + 1];
-        auto load = [&](int n) {
-            // keys 16 g + r and 16 g + 8 + r: rows 8 on are turned alike
-            const int g = n / NO, j = n % NO;
-            const uint32_t x = (at ^ (j << 6)) + g * 16 * ROW;
-            v[n % (AHEAD + 1)] = join(lds_read_tr(x), lds_read_tr(x + 8 * ROW));
-        };
+        return at;
+    }
+    __device__ __forceinline__ void load_key(uint32_t at, int f) {
 #pragma unroll
-        for (int n = 0; n < AHEAD; n++) load(n);
+        for (int x = 0; x < 2; x++)  // (32 rows on, the pieces are turned alike)
+            kf[f % (AHEAD + 1)][x] = lds_get<bf16x8>((at ^ (f << 5)) + x * 32 * ROW);
+    }
+    __device__ __forceinline__ void load_value(uint32_t at, int n) {
+        // keys 16 g + r and 16 g + 8 + r: rows 8 on are turned alike
+        const uint32_t x = (at ^ (n % NO << 6)) + n / NO * 16 * ROW;
+        vf[n % (AHEAD + 1)] = join(lds_read_tr(x), lds_read_tr(x + 8 * ROW));
+    }
+    // The first pieces of a tile, ahead of scores() and values().
+    __device__ __forceinline__ void start_keys(uint32_t kt, int lane) {
+        const uint32_t at = key_place(kt, lane);
+#pragma unroll
+        for (int f = 0; f < AHEAD; f++) load_key(at, f);
+    }
+    __device__ __forceinline__ void start_values(uint32_t vt, int lane) {
+        const uint32_t at = value_place(vt, lane);
+#pragma unroll
+        for (int n = 0; n < AHEAD; n++) load_value(at, n);
+    }
+    // Scores of the keys at `kt`. beside(m) is other work for the time of MFMA m (32 cycles, in
+    // which the wave can issue eight vector instructions); the fences keep the compiler from taking
+    // the two apart again.
+    static constexpr int SCORE_MFMAS = NQ * 2, VALUE_MFMAS = NV;
+    template <typename Beside>
+    __device__ __forceinline__ void scores(uint32_t kt, int lane, Scores& s, Beside beside) {
+        const uint32_t at = key_place(kt, lane);
+        f32x16 zero;
+#pragma unroll
+        for (int i = 0; i < 16; i++) zero[i] = 0.f;
+#pragma unroll
+        for (int f = 0; f < NQ; f++) {
+            if (f + AHEAD < NQ) load_key(at, f + AHEAD);
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                s.v[x] = mma(kf[f % (AHEAD + 1)][x], q[f], f == 0 ? zero : s.v[x]);
+                beside(f * 2 + x);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+    // acc += V^T P^T for the weights s. The weights are rounded to bf16 (2^-8 of each at most) as
+    // the MFMA's operand. Those of the second half of the keys may be formed in beside(m) until
+    // m = VALUE_MFMAS * 5 / 8.
+    template <typename Beside>
+    __device__ __forceinline__ void values(uint32_t vt, int lane, Scores& s, Beside beside) {
+        const uint32_t at = value_place(vt, lane);
+        bf16x8 p;
 #pragma unroll
         for (int n = 0; n < NV; n++) {
-            if (n + AHEAD < NV) load(n + AHEAD);
-            const int g = n / NO;
+            if (n + AHEAD < NV) load_value(at, n + AHEAD);
             if (n % NO == 0)
 #pragma unroll
-                for (int i = 0; i < 8; i++) p[i] = (bf16)s[g >> 1][(g & 1) * 8 + i];
-            acc[n % NO] = mma(v[n % (AHEAD + 1)], p, acc[n % NO]);
-#pragma unroll
-            for (int i = n * 32 / NV; i < (n + 1) * 32 / NV; i++) *l += s[i >> 4][i & 15];
-            asm volatile("" : "+v"(*l));  // added here, beside the MFMAs
+                for (int i = 0; i < 8; i++) p[i] = (bf16)s.get(n / NO * 8 + i);
+            acc[n % NO] = mma(vf[n % (AHEAD + 1)], p, acc[n % NO]);
             beside(n);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -172,8 +194,15 @@ template <int D> struct AttendTile<float, D> {
     static constexpr int WAVES = 8, WAVES_PER_SIMD = 2;
     static constexpr int WAVE_ROWS = 16, KB = 32;
     static constexpr int ROW = D * 4, PIECES = ROW / 16;
+    static constexpr int LEAD = 0;
     static constexpr int NQ = D / 16, NO = D / 16;
-    typedef f32x4 Scores[2];
+    static constexpr bool INTERLEAVED = false;
+    struct Scores {
+        f32x4 v[2];
+        __device__ __forceinline__ float get(int n) const { return v[n >> 2][n & 3]; }
+        __device__ __forceinline__ void set(int n, float z) { v[n >> 2][n & 3] = z; }
+    };
+    static constexpr int N = 8;
     f32x4 q[NQ];
     f32x4 acc[NO];
 
@@ -182,8 +211,7 @@ template <int D> struct AttendTile<float, D> {
     __device__ __forceinline__ static int v_turn(int r) { return ((r >> 2) & 3) << 2; }
     __device__ __forceinline__ static int row_of_lane(int lane) { return lane & 15; }
     __device__ __forceinline__ static int first_key(int lane) { return (lane >> 4) * 4; }
-    __device__ __forceinline__ static int key(int x, int i) { return x * 16 + i; }
-    static constexpr int SX = 2, SI = 4;
+    __device__ __forceinline__ static int key(int n) { return (n >> 2) * 16 + (n & 3); }
     __device__ __forceinline__ static float max_partners(float x) { return max_groups(x); }
     __device__ __forceinline__ static float sum_partners(float x) {
         x += __shfl_xor(x, 16, WAVE);
@@ -197,27 +225,27 @@ template <int D> struct AttendTile<float, D> {
 #pragma unroll
         for (int f = 0; f < NQ; f++) asm volatile("" : "+v"(q[f]));  // as arrived()
     }
-    static constexpr int NV = 0, LAST_WEIGHT = 0;
+    __device__ __forceinline__ void start_keys(uint32_t, int) {}
     template <typename Beside>
-    __device__ __forceinline__ void scores(uint32_t kt, int lane, Scores& s, Beside) const {
+    __device__ __forceinline__ void scores(uint32_t kt, int lane, Scores& s, Beside) {
         const int r = lane & 15;
         uint32_t at = kt + r * ROW + (((lane >> 4) ^ k_turn(r)) << 4);
         asm volatile("" : "+v"(at));
-        s[0] = zero4();
-        s[1] = zero4();
+        s.v[0] = zero4();
+        s.v[1] = zero4();
 #pragma unroll
         for (int f = 0; f < NQ; f++)
 #pragma unroll
             for (int x = 0; x < 2; x++) {
                 const f32x4 k = lds_get<f32x4>((at ^ (f << 6)) + x * 16 * ROW);
 #pragma unroll
-                for (int e = 0; e < 4; e++) s[x] = Mma<float>::mma(k[e], q[f][e], s[x]);
+                for (int e = 0; e < 4; e++) s.v[x] = Mma<float>::mma(k[e], q[f][e], s.v[x]);
             }
     }
     // A step's sums are formed by themselves and added once: a long sequence is then summed in
     // two levels, and the roundings of n / 32 additions reach a result instead of those of n / 4.
     template <typename Beside>
-    __device__ __forceinline__ void values(uint32_t vt, int lane, const Scores& s, float* l, Beside) {
+    __device__ __forceinline__ void values(uint32_t vt, int lane, Scores& s, Beside) {
         constexpr int JN = 2;  // columns of tiles on their way
         const uint32_t at = vt + (lane >> 4) * 4 * ROW + (lane & 15) * 4;
 #pragma unroll
@@ -226,20 +254,16 @@ template <int D> struct AttendTile<float, D> {
 #pragma unroll
             for (int j = 0; j < JN; j++) sum[j] = zero4();
 #pragma unroll
-            for (int x = 0; x < 2; x++)
+            for (int n = 0; n < N; n++)
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-#pragma unroll
-                    for (int j = 0; j < JN; j++)
-                        sum[j] = Mma<float>::mma(
-                            lds_get<float>(at + (x * 16 + i) * ROW +
-                                           ((((j0 + j) << 2) ^ v_turn((lane >> 4) * 4)) << 4)),
-                            s[x][i], sum[j]);
+                for (int j = 0; j < JN; j++)
+                    sum[j] = Mma<float>::mma(
+                        lds_get<float>(at + key(n) * ROW +
+                                       ((((j0 + j) << 2) ^ v_turn((lane >> 4) * 4)) << 4)),
+                        s.get(n), sum[j]);
 #pragma unroll
             for (int j = 0; j < JN; j++) acc[j0 + j] += sum[j];
         }
-        *l += ((s[0][0] + s[0][1]) + (s[0][2] + s[0][3])) +
-              ((s[1][0] + s[1][1]) + (s[1][2] + s[1][3]));
     }
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -259,15 +283,15 @@ template <int D> struct AttendTile<float, D> {
     }
 };
 
+template <typename T, int D>
+constexpr int ATTEND_ROWS = AttendTile<T, D>::WAVES * AttendTile<T, D>::WAVE_ROWS;
+
 // ------------------------------------------------------------------------------- the units
 // Positions in the stream that a unit has beyond its steps: its start and end take as long.
 constexpr int ATTEND_EXTRA = 2;
 // No worker is given fewer positions than this: a run's start, and the parts that a cut leaves to
 // be joined, cost as much.
-#ifndef AMR
-#define AMR 2
-#endif
-constexpr int ATTEND_MIN_RUN = AMR;
+constexpr int ATTEND_MIN_RUN = 2;
 
 // The stream of all units (total positions per key/value head) cut over the workers.
 struct AttendCut {
@@ -397,15 +421,16 @@ template <typename T, int D, bool SHARED>
 __global__ __launch_bounds__((AttendTile<T, D>::WAVES * WAVE), (AttendTile<T, D>::WAVES_PER_SIMD))
 void paged_attend_kernel(AttendArgs a) {
     using X = AttendTile<T, D>;
-    constexpr int THREADS = X::WAVES * WAVE, KB = X::KB, ROW = X::ROW;
-    constexpr int ROWS = X::WAVES * X::WAVE_ROWS;
+    using Scores = typename X::Scores;
+    constexpr int THREADS = X::WAVES * WAVE, KB = X::KB, ROW = X::ROW, N = X::N;
+    constexpr int ROWS = ATTEND_ROWS<T, D>, LEAD = X::LEAD, NB = 2 + LEAD;
     constexpr int LOADS = KB * ROW / 1024 / X::WAVES;  // 1 KiB loads of a wave per tile
     constexpr int ROWS_A_LOAD = 1024 / ROW;
     constexpr uint64_t ALL = KB == 64 ? ~0ull : (1ull << (KB & 63)) - 1;
-    __shared__ __align__(1024) char k_tile[2][KB * ROW];
-    __shared__ __align__(1024) char v_tile[2][KB * ROW];
-    __shared__ uint32_t key_row[4][KB];  // cache rows of four steps' keys
-    __shared__ uint64_t key_exists[4];   // a bit per key
+    __shared__ __align__(1024) char k_tile[NB][KB * ROW];
+    __shared__ __align__(1024) char v_tile[NB][KB * ROW];
+    __shared__ uint32_t key_row[8][KB];  // cache rows of the next steps' keys
+    __shared__ uint64_t key_exists[8];   // a bit per key
     __shared__ int found;
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform(wave_id());
     // neighbours in the stream read the same keys: they sit on one XCD
@@ -432,6 +457,8 @@ void paged_attend_kernel(AttendArgs a) {
     const float cs = a.scale == 0.f ? 1.f : fabsf(a.scale) * AT_LOG2E;
     const T* k_cache = reinterpret_cast<const T*>(a.k_cache);
     const T* v_cache = reinterpret_cast<const T*>(a.v_cache);
+    auto keys_at = [&](int c) { return lds_offset(k_tile[LEAD ? c % NB : c & 1]); };
+    auto values_at = [&](int c) { return lds_offset(v_tile[LEAD ? c % NB : c & 1]); };
 
     for (; pos < end; t + 1 < n_tiles ? t++ : (t = 0, kvh++)) {
         const AttendUnit u = a.tile[t];
@@ -448,14 +475,14 @@ void paged_attend_kernel(AttendArgs a) {
         const int32_t* table = a.block_table + (size_t)uniform(u.seq) * a.max_blocks;
         const bool late = pos != run_start;
 
-        const int row = u.row0 + wave * X::WAVE_ROWS + X::row_of_lane(lane);
-        const bool live = row < u.rows;
-        const int tok = (int)a.by_group((uint32_t)(live ? row : u.rows - 1));
-        const int head = kvh * a.group + (live ? row : u.rows - 1) - tok * a.group;
-        const size_t q_row = (size_t)(u.token0 + tok) * a.H + head;
         X x;
+        const int tile_row = wave * X::WAVE_ROWS + X::row_of_lane(lane);  // of this lane
+        const bool live = u.row0 + tile_row < u.rows;
+        const int row = live ? u.row0 + tile_row : u.rows - 1;
+        const int tok = (int)a.by_group((uint32_t)row);
+        const size_t q_row = (size_t)(u.token0 + tok) * a.H + kvh * a.group + (row - tok * a.group);
         x.load_q(reinterpret_cast<const T*>(a.q) + q_row * D, lane, sign);
-        int lim;  // keys that this lane's row sees
+        int lim;  // keys that the row sees
         if constexpr (SHARED) {
             const int b = (int)a.by_pos((uint32_t)(u.token0 + tok));
             lim = a.seq_lens[b] - a.n_pos + (u.token0 + tok - b * a.n_pos) + 1;
@@ -473,8 +500,9 @@ void paged_attend_kernel(AttendArgs a) {
         const bool any = u.row0 + wave * X::WAVE_ROWS < u.rows;
         const int mine = uniform(any ? min(c1, (max(min(high, reach), 0) + KB - 1) / KB) : 0);
 
-        // Wave 0 looks up the pages: three steps ahead of the loads of the values, two of the
-        // keys', one step after it has asked for the table entries.
+        // The waves take turns in looking up the pages of a step: a table entry is asked for in one
+        // step, its keys' rows put down in the next, read in the one after, and loaded from in the
+        // fourth.
         auto page_of = [&](int c) {
             const uint32_t key = (uint32_t)(c * KB + lane);
             return table[min(a.block(key), (uint32_t)a.max_blocks - 1)];
@@ -483,29 +511,41 @@ void paged_attend_kernel(AttendArgs a) {
             const uint32_t key = (uint32_t)(c * KB + lane), off = key - a.block(key) * a.block.div;
             const bool ok = lane < KB && (int)key < reach && page >= 0 && page < a.n_blocks;
             const uint32_t r = ((uint32_t)page * a.kv_heads + kvh) * a.block.div + off;
-            if (lane < KB) key_row[c & 3][lane] = ok ? r : AT_NO_ROW;
+            if (lane < KB) key_row[c & 7][lane] = ok ? r : AT_NO_ROW;
             const uint64_t exist = __ballot(ok);
-            if (lane == 0) key_exists[c & 3] = exist;
+            if (lane == 0) key_exists[c & 7] = exist;
         };
-        auto load_tile = [&](const T* cache, int c, uint32_t lds, auto turn) {
+        // Cache rows of the loads to come, read a step ahead where they are few registers.
+        constexpr bool ROWS_EARLY = LOADS <= 4;
+        uint32_t k_rows[LOADS], v_rows[LOADS];
+        auto rows_of = [&](int c, uint32_t (&rows)[LOADS]) {
 #pragma unroll
-            for (int i = 0; i < LOADS; i++) {
-                const int r = (wave * LOADS + i) * ROWS_A_LOAD + lane / X::PIECES;
-                const uint32_t from = key_row[c & 3][r];
-                const int piece = (lane % X::PIECES) ^ turn(r);
-                const char* base = from == AT_NO_ROW
-                    ? at_zero_row : reinterpret_cast<const char*>(cache + (size_t)from * D);
-                load_to_lds(base + piece * 16, lds + (wave * LOADS + i) * 1024);
-            }
+            for (int i = 0; i < LOADS; i++)
+                rows[i] = key_row[c & 7][(wave * LOADS + i) * ROWS_A_LOAD + lane / X::PIECES];
+        };
+        auto load = [&](const T* cache, uint32_t from, int i, uint32_t lds, auto turn) {
+            const int r = (wave * LOADS + i) * ROWS_A_LOAD + lane / X::PIECES;
+            const int piece = (lane % X::PIECES) ^ turn(r);
+            const char* base = from == AT_NO_ROW
+                ? at_zero_row : reinterpret_cast<const char*>(cache + (size_t)from * D);
+            load_to_lds(base + piece * 16, lds + (wave * LOADS + i) * 1024);
+        };
+        auto load_key = [&](int c, int i) {
+            load(k_cache, k_rows[i], i, keys_at(c), [](int r) { return X::k_turn(r); });
+        };
+        auto load_value = [&](int c, int i) {
+            load(v_cache, v_rows[i], i, values_at(c), [](int r) { return X::v_turn(r); });
         };
         auto load_keys = [&](int c) {
-            load_tile(k_cache, c, lds_offset(k_tile[c & 1]), [](int r) { return X::k_turn(r); });
+#pragma unroll
+            for (int i = 0; i < LOADS; i++) load_key(c, i);
         };
         auto load_values = [&](int c) {
-            load_tile(v_cache, c, lds_offset(v_tile[c & 1]), [](int r) { return X::v_turn(r); });
+#pragma unroll
+            for (int i = 0; i < LOADS; i++) load_value(c, i);
         };
-        auto mask = [&](int c, typename X::Scores& s) {
-            const uint64_t exist = key_exists[c & 3];
+        auto mask = [&](int c, Scores& s) {
+            const uint64_t exist = key_exists[c & 7];
             const int key0 = c * KB;
             if (exist == ALL && key0 + KB <= low) return;
             int first = X::first_key(lane);
@@ -513,126 +553,150 @@ void paged_attend_kernel(AttendArgs a) {
             const uint64_t here = exist >> first;
             const int left = lim - key0 - first;
 #pragma unroll
-            for (int y = 0; y < X::SX; y++)
-#pragma unroll
-                for (int i = 0; i < X::SI; i++) {
-                    const int k = X::key(y, i);
-                    s[y][i] = ((here >> k) & 1) && k < left ? s[y][i] : -INFINITY;
-                }
+            for (int n = 0; n < N; n++) {
+                const int k = X::key(n);
+                s.set(n, ((here >> k) & 1) && k < left ? s.get(n) : -INFINITY);
+            }
         };
 
         x.clear();
         // the exponents' reference (scaled), and what is taken off them; the sum
         float ref = -INFINITY, shift = 0.f, l = 0.f;
-        constexpr int N = X::SX * X::SI;
-        auto weight = [&](typename X::Scores& s, int n) {
-            float e = __builtin_amdgcn_exp2f(fmaf(s[n / X::SI][n % X::SI], cs, -shift));
-            if constexpr (X::NV > 0) asm volatile("" : "+v"(e));  // formed here
-            s[n / X::SI][n % X::SI] = e;
+        auto weight = [&](Scores& s, int n) {
+            float z = __builtin_amdgcn_exp2f(fmaf(s.get(n), cs, -shift));
+            if constexpr (X::INTERLEAVED) asm volatile("" : "+v"(z));  // formed here
+            s.set(n, z);
         };
-        // The reference for scores whose largest (of this lane) is `top`: sums are taken along.
+        // The reference for scores whose largest is `top`: sums are taken along. A row without a key
+        // so far has sums of zero, and shift 0.
         auto refer = [&](float top) {
-            top = X::max_partners(top) * cs;
             const bool grown = top > ref + LAG;
-            if (__any(grown)) {
-                shift = grown ? top : shift;  // (a row without a key so far: sums of zero, shift 0)
-                const float f = grown ? __builtin_amdgcn_exp2f(ref - top) : 1.f;
-                ref = grown ? top : ref;
-                l *= f;
-                x.shrink(f);
-            }
+            if (!__any(grown)) return;
+            const float f = grown ? __builtin_amdgcn_exp2f(ref - top) : 1.f;
+            ref = grown ? top : ref;
+            shift = grown ? top : shift;
+            l *= f;
+            x.shrink(f);
         };
-        auto largest = [&](const typename X::Scores& s, int n0, int n1, float top) {
+        auto largest = [&](const Scores& s, int n0, int n1, float top) {
 #pragma unroll
-            for (int n = n0; n < n1; n++) top = fmaxf(top, s[n / X::SI][n % X::SI]);
+            for (int n = n0; n < n1; n++) top = fmaxf(top, s.get(n));
             return top;
         };
         int page = 0;
-        // One step: the weights of s (masked, their reference known), its values added; meanwhile
+        // One step: the weights of s (masked, their references known), its values added; meanwhile
         // the next step's scores and their maximum. Beside the MFMAs of the scores go 5 in 8 of the
-        // weights, beside those of the values the others, the sum and the maximum: about as many
+        // weights, beside those of the values the others, the maximum and the sums: about as many
         // cycles of the vector pipe as of the matrix pipe in both halves.
-        auto step = [&](int c, typename X::Scores& s, typename X::Scores& next) {
+        auto step = [&](int c, Scores& s, Scores& next) {
             lds_loads_done();
-            if (wave == 0 && c + 3 < c1) {
-                arrived(page);
-                put_rows(c + 3, page);
+            // keys c + 1 + LEAD and values c + LEAD are whole; all are done with what comes next
+            lds_barrier();
+            if (!ROWS_EARLY) rows_of(c + 2 + LEAD, k_rows);
+            if (c + 2 + LEAD < c1) load_keys(c + 2 + LEAD);
+            if (!ROWS_EARLY) rows_of(c + 1 + LEAD, v_rows);
+            if (c + 1 + LEAD < c1) load_values(c + 1 + LEAD);
+            if (ROWS_EARLY) {
+                rows_of(c + 3 + LEAD, k_rows);
+                rows_of(c + 2 + LEAD, v_rows);
             }
-            lds_barrier();  // keys c + 1 and values c are whole; all are done with what they replace
-            if (wave == 0 && c + 4 < c1) {
-                page = page_of(c + 4);
+            if (wave == (c & (X::WAVES - 1)) && c + 4 + LEAD < c1) {
+                arrived(page);
+                put_rows(c + 4 + LEAD, page);
+            }
+            if (wave == ((c + 1) & (X::WAVES - 1)) && c + 5 + LEAD < c1) {
+                page = page_of(c + 5 + LEAD);
                 sched_fence();
             }
-            if (c + 2 < c1) load_keys(c + 2);
-            if (c + 1 < c1) load_values(c + 1);
             if (c >= mine) return;
-            const uint32_t kt = lds_offset(k_tile[(c + 1) & 1]), vt = lds_offset(v_tile[c & 1]);
+            const uint32_t kt = keys_at(c + 1), vt = values_at(c);
             float top = -INFINITY;
-            if constexpr (X::NV > 0) {
+            if constexpr (X::INTERLEAVED) {
                 constexpr int FIRST = N * 5 / 8, REST = N - FIRST;
-                x.scores(kt, lane, next, [&](int f) {
+                constexpr int MS = X::SCORE_MFMAS, MV = X::VALUE_MFMAS;
+                if constexpr (LEAD == 0) x.start_keys(kt, lane);
+                x.scores(kt, lane, next, [&](int m) {
 #pragma unroll
-                    for (int n = f * FIRST / X::NQ; n < (f + 1) * FIRST / X::NQ; n++) weight(s, n);
+                    for (int n = m * FIRST / MS; n < (m + 1) * FIRST / MS; n++) weight(s, n);
+                    if (m == MS - 2) x.start_values(vt, lane);
                 });
                 if (c + 1 < mine) mask(c + 1, next);
-                x.values(vt, lane, s, &l, [&](int v) {
-                    constexpr int L = X::LAST_WEIGHT;
-                    if (v < L)
+                x.values(vt, lane, s, [&](int m) {
+                    constexpr int L = MV * 5 / 8, HALF = MV / 2;
+                    if (m < L)
 #pragma unroll
-                        for (int n = v * REST / L; n < (v + 1) * REST / L; n++) weight(s, FIRST + n);
-                    top = largest(next, v * N / X::NV, (v + 1) * N / X::NV, top);
-                    asm volatile("" : "+v"(top));
+                        for (int n = m * REST / L; n < (m + 1) * REST / L; n++) weight(s, FIRST + n);
+                    if (m < HALF) {
+                        top = largest(next, m * N / HALF, (m + 1) * N / HALF, top);
+                        asm volatile("" : "+v"(top));
+                    } else {
+#pragma unroll
+                        for (int n = (m - HALF) * N / HALF; n < (m + 1 - HALF) * N / HALF; n++)
+                            l += s.get(n);
+                        asm volatile("" : "+v"(l));
+                    }
+                    if (m == HALF + 1) top = X::max_partners(top) * cs;
+                    if (LEAD > 0 && m == MV - 2) x.start_keys(keys_at(c + 2), lane);
                 });
             } else {
 #pragma unroll
                 for (int n = 0; n < N; n++) weight(s, n);
                 x.scores(kt, lane, next, [](int) {});
                 if (c + 1 < mine) mask(c + 1, next);
-                x.values(vt, lane, s, &l, [](int) {});
-                top = largest(next, 0, N, top);
+                x.values(vt, lane, s, [](int) {});
+                float sum = 0.f;  // (as the values: a step's by themselves)
+#pragma unroll
+                for (int n = 0; n < N; n++) sum += s.get(n);
+                l += sum;
+                top = X::max_partners(largest(next, 0, N, top)) * cs;
             }
             if (c + 1 < mine) refer(top);
         };
         if (c1 > c0) {
-            typename X::Scores s0, s1;
+            Scores s0, s1;
             __syncthreads();  // the unit before is done with its tiles and rows
-            if (wave == 0) {
-                const int p0 = page_of(c0), p1 = page_of(c0 + 1), p2 = page_of(c0 + 2);
-                put_rows(c0, p0);
-                put_rows(c0 + 1, p1);
-                put_rows(c0 + 2, p2);
-            }
+            for (int i = wave; i < 4 + LEAD; i += X::WAVES) put_rows(c0 + i, page_of(c0 + i));
             lds_barrier();
+            rows_of(c0, k_rows);
             load_keys(c0);
+            if (LEAD > 0 && c0 + 1 < c1) {
+                rows_of(c0 + 1, k_rows);
+                load_keys(c0 + 1);
+            }
             lds_loads_done();
             lds_barrier();
-            if (wave == 0 && c0 + 3 < c1) {
-                page = page_of(c0 + 3);
+            if (wave == (c0 & (X::WAVES - 1)) && c0 + 4 + LEAD < c1) {
+                page = page_of(c0 + 4 + LEAD);
                 sched_fence();
             }
-            if (c0 + 1 < c1) load_keys(c0 + 1);
+            rows_of(c0 + 1 + LEAD, k_rows);
+            rows_of(c0, v_rows);
+            if (c0 + 1 + LEAD < c1) load_keys(c0 + 1 + LEAD);
             load_values(c0);
+            if (LEAD > 0 && c0 + 1 < c1) {
+                rows_of(c0 + 1, v_rows);
+                load_values(c0 + 1);
+            }
+            if (ROWS_EARLY) {
+                rows_of(c0 + 2 + LEAD, k_rows);
+                rows_of(c0 + 1 + LEAD, v_rows);
+            }
             if (c0 < mine) {
-                x.scores(lds_offset(k_tile[c0 & 1]), lane, s0, [](int) {});
+                x.start_keys(keys_at(c0), lane);
+                x.scores(keys_at(c0), lane, s0, [](int) {});
                 mask(c0, s0);
-                refer(largest(s0, 0, N, -INFINITY));
+                refer(X::max_partners(largest(s0, 0, N, -INFINITY)) * cs);
+                if constexpr (LEAD > 0) x.start_keys(keys_at(c0 + 1), lane);
             }
             for (int c = c0; c < c1; c += 2) {
                 step(c, s0, s1);
                 if (c + 1 < c1) step(c + 1, s1, s0);
             }
         }
-        l = X::sum_partners(l);
         const bool whole = c0 == 0 && c1 == nch;
-        if (!SHARED && whole) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros
-            if (live) {
-                T* out = reinterpret_cast<T*>(a.o) + q_row * D;
-                x.results(lane, inv, [&](int col, const float y[4]) { store4<T>(out + col, y); });
-            }
-        } else {
+        int64_t slot = 0;
+        if (SHARED || !whole) {
             const int last = cut.owner(unit_start + nch - 1);
-            int64_t slot;
             if constexpr (SHARED) {  // one slot per unit, and one per worker that goes on with one
                 const int unit = kvh * a.tiles + t;
                 slot = c0 == 0 ? (int64_t)a.workers + unit : w;
@@ -641,14 +705,19 @@ void paged_attend_kernel(AttendArgs a) {
                 slot = 2 * w + (late ? 1 : 0);
                 if (c0 == 0 && tid == 0) a.join.notes[w] = make_int4(t, kvh, (int)slot, last);
             }
-            if (live) {
-                const size_t at = (size_t)slot * ROWS + wave * X::WAVE_ROWS + X::row_of_lane(lane);
-                float* out = a.join.part_o + at * D;
-                x.results(lane, 1.f, [&](int col, const float y[4]) { store4<float>(out + col, y); });
-                if (X::first_key(lane) == 0) {
-                    a.join.part_ml[at * 2] = ref;
-                    a.join.part_ml[at * 2 + 1] = l;
-                }
+        }
+        const float sum = X::sum_partners(l);
+        if (live && !SHARED && whole) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
+            T* out = reinterpret_cast<T*>(a.o) + q_row * D;
+            x.results(lane, inv, [&](int col, const float z[4]) { store4<T>(out + col, z); });
+        } else if (live) {
+            const size_t at = (size_t)slot * ROWS + tile_row;
+            float* out = a.join.part_o + at * D;
+            x.results(lane, 1.f, [&](int col, const float z[4]) { store4<float>(out + col, z); });
+            if (X::first_key(lane) == 0) {
+                a.join.part_ml[at * 2] = ref;
+                a.join.part_ml[at * 2 + 1] = sum;
             }
         }
         pos = c1 == nch ? unit_next : end;

@@ -13,10 +13,7 @@ namespace gdn {
 
 namespace {
 
-#ifndef JWG
-#define JWG 16
-#endif
-constexpr int JOIN_WGS = JWG;
+constexpr int JOIN_WGS = 16;  // workgroups of the joining launch a CU
 
 // A group whose prefix is attended apart. One request alone has nothing to share: its prefix is
 // left to the decode kernel.
@@ -33,7 +30,7 @@ __device__ __forceinline__ SharedGroup shared_group(const SharedDecodeArgs& a, i
 template <typename T, int D>
 __global__ __launch_bounds__(AT_TABLE_THREADS) void shared_tables_kernel(SharedDecodeArgs a) {
     using X = AttendTile<T, D>;
-    constexpr int ROWS = X::WAVES * X::WAVE_ROWS;
+    constexpr int ROWS = ATTEND_ROWS<T, D>;
     const int per_request = a.at.n_pos * a.at.group, groups = a.at.n_seqs;
     if (blockIdx.x == 0) {
         attend_tables(
@@ -72,7 +69,7 @@ __global__ __launch_bounds__(AT_TABLE_THREADS) void shared_tables_kernel(SharedD
 // then the prefix kernel's.
 template <typename T, int D>
 __global__ __launch_bounds__(JOIN_THREADS) void shared_join_kernel(SharedDecodeArgs a) {
-    constexpr int ROWS = AttendTile<T, D>::WAVES * AttendTile<T, D>::WAVE_ROWS;
+    constexpr int ROWS = ATTEND_ROWS<T, D>;
     const JoinShape& j = a.own.join;
     const int unit = (int)blockIdx.x / j.share, b = unit / a.at.kv_heads;
     const int kvh = unit - b * a.at.kv_heads;
@@ -100,7 +97,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void shared_join_kernel(SharedDecodeA
         const int64_t slot = i == 0 ? (int64_t)a.at.workers + kvh * a.at.tiles + t : w0 + i;
         return prefix0 + (size_t)slot * ROWS + row % ROWS;
     };
-    join_rows<D, (D + 127) / 128, 4>(
+        join_rows<D, (D + 127) / 128, 4>(
         j, note.x + most, parts_of, at, (int)blockIdx.x % j.share, 0,
         [&](int row, int col, const float x[4]) {
             const int p = row / a.at.group, h = row - p * a.at.group;

@@ -495,7 +495,7 @@ def _new(shape, dtype, like, stream):
     memory, which work queued on the current stream cannot still be using, and is marked as used
     on the current stream too, where results are read as a rule."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     if not hasattr(stream, "cuda_stream"):
         # (handle 0 is the default stream; ExternalStream would take some other one for it)
         stream = (torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream)
