@@ -63,15 +63,17 @@ __device__ __forceinline__ void join_note(const JoinShape& j, const SplitShape& 
 // One workgroup's share of a unit's rows, NC pieces of 128 columns from column `first` on, U
 // parts on their way at a time per group. at(i, r): where part i of row r lies, i < parts_of(r),
 // which is `most` or less; store(r, column, x[4]).
-template <int COLS, int NC, int U, typename Parts, typename At, typename Store>
+template <int COLS, int NC, int U, int MOST_GROUPS = JOIN_GROUPS, typename Parts, typename At,
+          typename Store>
 __device__ __forceinline__ void join_rows(const JoinShape& s, int most, Parts parts_of, At where,
                                           int step0, int first, Store store) {
     __shared__ float red[JOIN_GROUPS][NC * 128 + 4];
     __shared__ float weight[JOIN_MAX_WORKERS];
     __shared__ float wave_part[JOIN_THREADS / WAVE];
     const int tid = threadIdx.x, group = tid >> 5, lane = tid & 31;
-    int gpr = 1;  // groups per row: U parts each, if there are groups enough
-    while (gpr < JOIN_GROUPS && gpr * U < most) gpr *= 2;
+    // groups per row: U parts each, if there are groups enough (all of them for over 32 parts)
+    int gpr = 1;
+    while (gpr < JOIN_GROUPS && gpr * U < most && (gpr < MOST_GROUPS || most > 32)) gpr *= 2;
     const int rows_here = JOIN_GROUPS / gpr, turn = group & (gpr - 1);
     for (int step = step0; step * rows_here < s.rows; step += s.share) {
         const int row = step * rows_here + group / gpr;

@@ -13,7 +13,10 @@ namespace gdn {
 
 namespace {
 
-constexpr int JOIN_WGS = 16;  // workgroups of the joining launch a CU
+// Workgroups of the joining launch a CU, and groups of lanes that share a row of up to 32 parts (128
+// requests, 17 parts a row: 148 us a call with 8 and 4, 157 with 16 and 4, 153 with 8 and 2, 151 with
+// 16 and 8).
+constexpr int JOIN_WGS = 8, JOIN_ROW_GROUPS = 4;
 
 // A group whose prefix is attended apart. One request alone has nothing to share: its prefix is
 // left to the decode kernel.
@@ -97,7 +100,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void shared_join_kernel(SharedDecodeA
         const int64_t slot = i == 0 ? (int64_t)a.at.workers + kvh * a.at.tiles + t : w0 + i;
         return prefix0 + (size_t)slot * ROWS + row % ROWS;
     };
-        join_rows<D, (D + 127) / 128, 4>(
+        join_rows<D, (D + 127) / 128, 4, JOIN_ROW_GROUPS>(
         j, note.x + most, parts_of, at, (int)blockIdx.x % j.share, 0,
         [&](int row, int col, const float x[4]) {
             const int p = row / a.at.group, h = row - p * a.at.group;
