@@ -161,6 +161,7 @@ struct SharedDecodeArgs {
     PagedDecodeArgs own;
     const int32_t *group_cu, *prefix_lens;
     int batch;
+    int64_t min_bytes;    // spared reads from which on prefixes are attended apart; < 0: by rule
     int32_t *start, *own_keys;  // [batch] keys of the prefix, and behind it
     int2* place;          // [batch] group (-1: none), first row in it
     int2* prefix_notes;   // [kv_heads x tiles] first and last worker of a unit

@@ -650,6 +650,10 @@ int check_shared_decode(const gdn_paged_dims_t* dims, int32_t batch, int32_t n_p
     const int st = check_paged_dims(dims, batch, n_pos);
     if (st) return st;
     if (n_groups < 0) return fail(GDN_ERR_SHAPE, "n_groups must be >= 0 (got %d)", n_groups);
+    // the joining launch has a workgroup per request and key/value head
+    if ((int64_t)batch * dims->num_kv_heads >= (1 << 24))
+        return fail(GDN_ERR_UNSUPPORTED, "batch x num_kv_heads must stay below 2^24 (got %d x %d): "
+                                         "split the batch", batch, dims->num_kv_heads);
     return check_attend_rows(dims, (int64_t)batch * n_pos, batch > n_groups ? batch : n_groups);
 }
 
@@ -1269,7 +1273,8 @@ int gdn_paged_shared_decode(const gdn_paged_dims_t* dims, const void* q, const v
                             const int32_t* block_table, int32_t max_blocks,
                             const int32_t* seq_lens, int32_t batch, int32_t n_pos,
                             const int32_t* group_cu, const int32_t* prefix_lens, int32_t n_groups,
-                            void* o, void* workspace, size_t ws_bytes, void* stream) {
+                            int64_t min_bytes, void* o, void* workspace, size_t ws_bytes,
+                            void* stream) {
     int st = check_shared_decode(dims, batch, n_pos, n_groups);
     if (!st) st = check_cache(dims->dtype, dims->num_kv_heads, n_blocks, block_size);
     if (!st) st = check_table(max_blocks, block_size);
@@ -1303,6 +1308,7 @@ int gdn_paged_shared_decode(const gdn_paged_dims_t* dims, const void* q, const v
     a.own.o = o;
     a.group_cu = group_cu;
     a.prefix_lens = prefix_lens;
+    a.min_bytes = min_bytes;
     return launch_status(gdn::launch_shared_decode(a, static_cast<hipStream_t>(stream)),
                          "gdn_paged_shared_decode");
 }

@@ -18,6 +18,17 @@ namespace {
 // 16 and 8).
 constexpr int JOIN_WGS = 8, JOIN_ROW_GROUPS = 4;
 
+// Prefixes are attended apart where that spares reads of so many bytes in all: the prefix kernel's
+// start and the parts that it leaves cost as much as reading a prefix again out of the caches, which
+// a plain decode mostly does. Spared MB, us a call apart and not, bf16, 60 own tokens each: 8 requests,
+// 4 heads of 128, 59 MB 29 and 23, 235 MB 36 and 49; 4 groups of 2, 134 MB 49 and 53; 64 requests, 4
+// heads, 132 MB 42 and 23, 529 MB 49 and 49, 2114 MB 62 and 156; 7 requests, 4 heads of 64, 101 MB 27
+// and 28. fp32: 8 requests, 8 heads of 128, 235 MB 49 and 48, 940 MB 100 and 146.
+constexpr int64_t SHARED_LEAST_BF16 = (int64_t)128 << 20, SHARED_LEAST_F32 = (int64_t)256 << 20;
+// In fp32 a wave's 16 rows take as long as the reads of several requests: 4 groups of 2 requests (16
+// rows), 268 MB, 166 us apart, 92 not; 8 requests (64 rows), 470 MB, 69 and 82.
+constexpr int SHARED_ROWS_F32 = 64;
+
 // A group whose prefix is attended apart. One request alone has nothing to share: its prefix is
 // left to the decode kernel.
 struct SharedGroup {
@@ -26,7 +37,9 @@ struct SharedGroup {
 __device__ __forceinline__ SharedGroup shared_group(const SharedDecodeArgs& a, int g) {
     const int b0 = min(max(a.group_cu[g], 0), a.batch), b1 = min(max(a.group_cu[g + 1], 0), a.batch);
     const int prefix = min(max(a.prefix_lens[g], 0), a.at.max_keys);
-    const bool apart = b1 - b0 >= 2 && prefix > 0;
+    const int least_rows = a.min_bytes < 0 && a.at.dtype == 0 ? SHARED_ROWS_F32 : 0;
+    const bool apart = b1 - b0 >= 2 && prefix > 0 &&
+                       (int64_t)(b1 - b0) * a.at.n_pos * a.at.group >= least_rows;
     return {b0, apart ? b1 - b0 : 0, apart ? prefix : 0};
 }
 
@@ -35,9 +48,26 @@ __global__ __launch_bounds__(AT_TABLE_THREADS) void shared_tables_kernel(SharedD
     using X = AttendTile<T, D>;
     constexpr int ROWS = ATTEND_ROWS<T, D>;
     const int per_request = a.at.n_pos * a.at.group, groups = a.at.n_seqs;
+    // keys that need not be read again; every workgroup comes to the same decision
+    __shared__ int64_t part[AT_TABLE_THREADS / WAVE];
+    int64_t spared = 0;
+    for (int g = threadIdx.x; g < groups; g += AT_TABLE_THREADS) {
+        const SharedGroup s = shared_group(a, g);
+        spared += (int64_t)max(s.size - 1, 0) * s.prefix;
+    }
+#pragma unroll
+    for (int off = WAVE / 2; off > 0; off >>= 1) spared += __shfl_xor(spared, off, WAVE);
+    if (lane_id() == 0) part[wave_id()] = spared;
+    __syncthreads();
+    spared = 0;
+#pragma unroll
+    for (int w = 0; w < AT_TABLE_THREADS / WAVE; w++) spared += part[w];
+    const int64_t least = a.min_bytes >= 0 ? a.min_bytes
+                          : sizeof(T) == 2 ? SHARED_LEAST_BF16 : SHARED_LEAST_F32;
+    const bool apart = spared * a.at.kv_heads * (2 * D * (int)sizeof(T)) >= least;
     if (blockIdx.x == 0) {
         attend_tables(
-            a.at, ROWS, X::KB, [&](int g) { return shared_group(a, g).size * per_request; },
+            a.at, ROWS, X::KB, [&](int g) { return apart ? shared_group(a, g).size * per_request : 0; },
             [&](int g, int row0) {
                 const SharedGroup s = shared_group(a, g);
                 return AttendUnit{s.first, s.first * a.at.n_pos, row0, s.size * per_request,
@@ -55,7 +85,7 @@ __global__ __launch_bounds__(AT_TABLE_THREADS) void shared_tables_kernel(SharedD
     const int lo = last_at(groups, b, [&](int g) { return near ? near_cu[g] : a.group_cu[g]; });
     int start = 0;
     int2 place = make_int2(-1, 0);
-    if (groups > 0) {
+    if (groups > 0 && apart) {
         const SharedGroup s = shared_group(a, lo);
         if (b >= s.first && b < s.first + s.size) {
             start = s.prefix;

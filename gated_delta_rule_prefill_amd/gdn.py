@@ -92,8 +92,8 @@ _SIGS = {
     "gdn_paged_compact": [_P, _I, _P, _I, _I, _P, _I, _P, _P, _I, _P, _P, _SZ, _P],
     "gdn_paged_copy": [_P, _I, _L, _I, _P, _P, _I, _P, _P],
     "gdn_paged_shared_decode_workspace_bytes": [_PAGED, _I, _I, _I, ctypes.POINTER(_SZ)],
-    "gdn_paged_shared_decode": [_PAGED, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _I, _P, _P,
-                                _SZ, _P],
+    "gdn_paged_shared_decode": [_PAGED, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _I, _L, _P,
+                                _P, _SZ, _P],
     "gdn_paged_prefill_workspace_bytes": [_PAGED, _I, _I, ctypes.POINTER(_SZ)],
     "gdn_paged_prefill": [_PAGED, _P, _P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P, _SZ, _P],
     "gdn_paged_decode_workspace_bytes": [_PAGED, _I, _I, ctypes.POINTER(_SZ)],
@@ -727,7 +727,7 @@ def gdn_paged_copy(caches, copy_src, copy_dst, count=None, stream=None):
     n, dev = copy_src.numel(), _gpu(copy_src)
     addresses, like = [], None
     for c in caches:
-        now = (c.shape[0], c.stride(0) * c.element_size())
+        now = (c.shape[0], c.numel() // max(c.shape[0], 1) * c.element_size())
         like = now if like is None else like
         if now != like or c.get_device() != dev or not c.is_contiguous():
             raise ValueError("caches must be contiguous, on one GPU, and alike in their pages: got "
@@ -748,10 +748,11 @@ def gdn_paged_shared_decode_workspace_bytes(H, kv_heads, d, dtype, batch, n_pos,
 
 
 def gdn_paged_shared_decode(q, k_cache, v_cache, block_table, seq_lens, group_cu, prefix_lens,
-                            scale=1.0, o=None, workspace=None, stream=None):
+                            scale=1.0, min_bytes=-1, o=None, workspace=None, stream=None):
     """gdn_paged_decode for a batch in which groups of requests share a prefix, read once for the
     group: requests group_cu[g] .. group_cu[g + 1] - 1 ([groups + 1] int32) hold the same pages for
-    their first prefix_lens[g] tokens ([groups] int32). Returns o, shaped as q."""
+    their first prefix_lens[g] tokens ([groups] int32). Where that spares less than min_bytes of
+    reads (negative: the library's rule) each request reads its own. Returns o, shaped as q."""
     shape, dt = q.shape, q.dtype
     if len(shape) == 3:  # one position per request
         (B, H, d), P = shape, 1
@@ -770,7 +771,7 @@ def gdn_paged_shared_decode(q, k_cache, v_cache, block_table, seq_lens, group_cu
          _table_arg(block_table, B, dev), block_table.shape[1],
          _arg("seq_lens", seq_lens, (B,), _I32, dev), B, P,
          _arg("group_cu", group_cu, (groups + 1,), _I32, dev),
-         _arg("prefix_lens", prefix_lens, (groups,), _I32, dev), groups,
+         _arg("prefix_lens", prefix_lens, (groups,), _I32, dev), groups, int(min_bytes),
          _arg("o", o, shape, dt, dev), ws, ws_bytes)
     return o
 

@@ -626,6 +626,10 @@ int gdn_paged_shared_decode_workspace_bytes(const gdn_paged_dims_t* dims, int32_
  *   prefix_lens [n_groups] int32 (device): the first prefix_lens[g] tokens of a group's requests
  *               lie in the same pages (any number, whole pages or not; those of the row of its
  *               first request are read). A request may be shorter (a padded row of length 0 too)
+ *   min_bytes   the prefixes are attended apart if that spares this many bytes of reads in all
+ *               (sum over the groups of (size - 1) x prefix x 2 num_kv_heads d elements), else each
+ *               request reads its own; negative: the library's rule (128 MiB; with fp32 256 MiB, and
+ *               groups of 64 rows of a key/value head at least)
  * n_groups may be 0 (the arrays may then be NULL). A NaN or infinity in a value row of the prefix
  * reaches all requests of the group; in the newest n_pos tokens as in gdn_paged_decode. Workspace
  * and determinism as there. */
@@ -634,7 +638,8 @@ int gdn_paged_shared_decode(const gdn_paged_dims_t* dims, const void* q, const v
                             const int32_t* block_table, int32_t max_blocks,
                             const int32_t* seq_lens, int32_t batch, int32_t n_pos,
                             const int32_t* group_cu, const int32_t* prefix_lens, int32_t n_groups,
-                            void* o, void* workspace, size_t ws_bytes, void* stream);
+                            int64_t min_bytes, void* o, void* workspace, size_t ws_bytes,
+                            void* stream);
 
 /* Workspace of gdn_paged_prefill for the current device (host computation). It does not depend on
  * the lengths of the requests. */

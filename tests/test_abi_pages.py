@@ -110,7 +110,7 @@ def paged(H=32, kv=8, d=128, dtype=1):
 
 SHARED = dict(dims=paged(), q=FAKE, k_cache=FAKE, v_cache=FAKE, n_blocks=100, block_size=16,
               block_table=FAKE, max_blocks=20, seq_lens=FAKE, batch=6, n_pos=1, group_cu=FAKE,
-              prefix_lens=FAKE, n_groups=2, o=FAKE, workspace=FAKE, ws_bytes=1 << 40, stream=None)
+              prefix_lens=FAKE, n_groups=2, min_bytes=-1, o=FAKE, workspace=FAKE, ws_bytes=1 << 40, stream=None)
 PREFILL = dict(dims=paged(), q=FAKE, k_cache=FAKE, v_cache=FAKE, n_blocks=100, block_size=16,
                block_table=FAKE, max_blocks=20, cu_seqlens=FAKE, seq_lens=FAKE, n_seqs=3,
                total_tokens=50, o=FAKE, workspace=FAKE, ws_bytes=1 << 40, stream=None)
@@ -133,6 +133,7 @@ BOTH = [
     (dict(batch=-1), SHAPE), (dict(n_groups=-1), SHAPE), (dict(n_pos=0), UNSUPPORTED),
     (dict(n_pos=17), UNSUPPORTED), (dict(max_blocks=1 << 22, batch=1 << 8), UNSUPPORTED),
     (dict(batch=1 << 23, n_pos=16, max_blocks=1), UNSUPPORTED), (dict(n_groups=1 << 25), UNSUPPORTED),
+    (dict(dims=paged(H=8), batch=1 << 21, max_blocks=1), UNSUPPORTED),
 ])
 def test_shared_decode_refuses(kw, status):
     refused(status, call("gdn_paged_shared_decode", SHARED, kw))

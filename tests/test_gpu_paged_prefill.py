@@ -169,3 +169,12 @@ def test_no_rows_are_no_ops(gpu_lib):
     assert out.shape == (0, 4, 64)
     out = gpu_lib.gdn_paged_prefill(q, k, v, table[:0], cu[:1], lens[:0], o=torch.full_like(q, 3.0))
     assert bool((out == 3.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_requests_than_are_kept_near(gpu_lib, dtype):
+    """2500 requests of 1 to 3 tokens, some of none: more bounds than the tables keep in LDS, more
+    tiles than one pass of their kernel."""
+    new = [(i * 7) % 4 for i in range(2500)]
+    lens = [w + i % 9 if w else 0 for i, w in enumerate(new)]
+    check(gpu_lib, make(15, lens, new, 2, 1, 64, 4, dtype), 0.125, "many requests")

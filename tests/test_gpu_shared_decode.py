@@ -59,7 +59,7 @@ def make(seed, sizes, prefix, own, P, H, kv, d, block, dtype, before=0, part=Tru
 def check(lib, args, scale, what):
     q, k, v, table, lens, cu, prefix = args
     dev = [x.to(DEV) for x in args]
-    o = lib.gdn_paged_shared_decode(*dev, scale=scale)
+    o = lib.gdn_paged_shared_decode(*dev, scale=scale, min_bytes=0)  # (apart, however little)
     want, mag, top = oracle_pages.shared_decode(q, torch.nan_to_num(k.float()),
                                                 torch.nan_to_num(v.float()), table, lens, cu,
                                                 prefix, scale)
@@ -92,6 +92,10 @@ def test_shared(gpu_lib, case, part, dtype, d):
     dev, o, want, tol = check(gpu_lib, args, d ** -0.5, "shared")
     plain = gpu_lib.gdn_paged_decode(*dev[:5], scale=d ** -0.5)
     assert_within(plain, want, tol, "plain decode of the same batch")
+    rule = gpu_lib.gdn_paged_shared_decode(*dev, scale=d ** -0.5)  # too little to be spared
+    assert_within(rule, want, tol, "each request its own prefix")
+    assert torch.equal(rule, gpu_lib.gdn_paged_shared_decode(*dev, scale=d ** -0.5,
+                                                             min_bytes=2 ** 62))
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -137,9 +141,9 @@ def test_no_groups_is_a_decode_step(gpu_lib):
 
 def test_the_same_from_run_to_run(gpu_lib):
     args = [x.to(DEV) for x in make(27, [5, 4], [700, 333], [30] * 10, 2, 16, 2, 128, 32, BF16)]
-    one = gpu_lib.gdn_paged_shared_decode(*args, scale=0.1)
+    one = gpu_lib.gdn_paged_shared_decode(*args, scale=0.1, min_bytes=0)
     for _ in range(3):
-        assert torch.equal(one, gpu_lib.gdn_paged_shared_decode(*args, scale=0.1))
+        assert torch.equal(one, gpu_lib.gdn_paged_shared_decode(*args, scale=0.1, min_bytes=0))
 
 
 def test_groups_that_break_the_contract_touch_nothing_else(gpu_lib):
@@ -147,6 +151,31 @@ def test_groups_that_break_the_contract_touch_nothing_else(gpu_lib):
     args = [x.to(DEV) for x in make(28, [3, 3], [64, 64], [9] * 6, 1, 4, 2, 64, 16, F32)]
     for cu in ([0, 6, 3], [4, 2, 6], [-5, 3, 60], [0, 6, 6], [7, 8, 9]):
         args[5] = torch.tensor(cu, dtype=torch.int32, device=DEV)
-        o = gpu_lib.gdn_paged_shared_decode(*args, scale=0.1)
+        o = gpu_lib.gdn_paged_shared_decode(*args, scale=0.1, min_bytes=0)
         assert o.shape == args[0].shape
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_the_rule_takes_prefixes_apart_where_much_is_spared(gpu_lib, dtype):
+    """40 requests behind 2000 tokens, 2 heads of 256: 160 MB (320 in fp32)."""
+    args = make(29, [40], [2000], list(range(1, 41)), 1, 4, 2, 256, 64, dtype)
+    dev, o, want, tol = check(gpu_lib, args, 1 / 16, "apart")
+    assert torch.equal(o, gpu_lib.gdn_paged_shared_decode(*dev, scale=1 / 16))
+
+
+def test_the_rule_leaves_fp32_groups_of_few_rows_to_the_decode_kernel(gpu_lib):
+    args = [x.to(DEV) for x in make(30, [3], [9000], [9, 9, 9], 1, 8, 8, 256, 64, F32)]
+    rule = gpu_lib.gdn_paged_shared_decode(*args, scale=1 / 16)  # 295 MB spared, 3 rows
+    assert torch.equal(rule, gpu_lib.gdn_paged_shared_decode(*args, scale=1 / 16, min_bytes=2 ** 62))
+    # bf16 ones are taken apart
+    half = [x.to(BF16) if x.dtype == F32 else x for x in args]
+    apart = gpu_lib.gdn_paged_shared_decode(*half, scale=1 / 16)
+    assert torch.equal(apart, gpu_lib.gdn_paged_shared_decode(*half, scale=1 / 16, min_bytes=0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_groups_than_are_kept_near(gpu_lib, dtype):
+    """2100 groups, and tables of more tiles than one pass of their kernel."""
+    args = make(31, [2] * 2100, [5] * 2100, [1] * 4201, 1, 2, 1, 64, 4, dtype, part=False)
+    check(gpu_lib, args, 0.125, "many groups")

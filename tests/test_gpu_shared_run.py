@@ -106,7 +106,7 @@ def test_a_serving_run(gpu_lib, dtype, d, block):
     def shared(P):
         def attend(q, _, lens):
             return gdn.gdn_paged_shared_decode(q.view(-1, P, H, d), e.kc, e.vc, e.table, lens, cu,
-                                               prefix, scale=e.scale)
+                                               prefix, scale=e.scale, min_bytes=0)
         return attend
     for P in (1, 1, 3, 1):
         e.step([P] * rows, shared(P))
@@ -161,7 +161,7 @@ def test_captured_graph_of_a_step(gpu_lib):
         a, b, n = gdn.gdn_paged_fork(src, dst, flen, s["table"], block, s["shares"], free)
         gdn.gdn_paged_copy([s["kc"], s["vc"]], a, b)
         o = gdn.gdn_paged_shared_decode(s["q"], s["kc"], s["vc"], s["table"][:rows], lens, cu, prefix,
-                                        scale=0.125)
+                                        scale=0.125, min_bytes=0)
         p = gdn.gdn_paged_prefill(s["pq"], pk, pv, ptable, pcu, plens, scale=0.125)
         freed, k = gdn.gdn_paged_free(ints_1, flen[1:], s["table"], block, s["shares"])
         after = torch.where(torch.arange(rows + 4, device=DEV) == rows + 1, 0, all_lens).to(I32)
@@ -197,7 +197,7 @@ def test_other_streams_and_used_workspaces(gpu_lib):
     workspace give the default call's bits."""
     a = [x.to(DEV) for x in sha.make(60, [4], [300], [40] * 5, 2, 8, 2, 128, 16, BF16)]
     b = [x.to(DEV) for x in pre.make(61, [400, 90], [300, 1], 8, 2, 128, 16, BF16)]
-    want = gdn.gdn_paged_shared_decode(*a, scale=0.1), gdn.gdn_paged_prefill(*b, scale=0.1)
+    want = gdn.gdn_paged_shared_decode(*a, scale=0.1, min_bytes=0), gdn.gdn_paged_prefill(*b, scale=0.1)
     size = max(gdn.gdn_paged_shared_decode_workspace_bytes(8, 2, 128, BF16, 5, 2, 1),
                gdn.gdn_paged_prefill_workspace_bytes(8, 2, 128, BF16, 2, 301))
     torch.cuda.synchronize()
@@ -206,13 +206,13 @@ def test_other_streams_and_used_workspaces(gpu_lib):
         ws = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
         torch.cuda.synchronize()
         for _ in range(2):
-            x = gdn.gdn_paged_shared_decode(*a, scale=0.1, workspace=ws, stream=stream)
+            x = gdn.gdn_paged_shared_decode(*a, scale=0.1, min_bytes=0, workspace=ws, stream=stream)
             y = gdn.gdn_paged_prefill(*b, scale=0.1, workspace=ws, stream=stream)
-        z = gdn.gdn_paged_shared_decode(*a, scale=0.1, stream=stream)
+        z = gdn.gdn_paged_shared_decode(*a, scale=0.1, min_bytes=0, stream=stream)
         torch.cuda.synchronize()
         assert torch.equal(x, want[0]) and torch.equal(y, want[1]) and torch.equal(z, want[0])
     with torch.cuda.stream(side):
-        x, y = gdn.gdn_paged_shared_decode(*a, scale=0.1), gdn.gdn_paged_prefill(*b, scale=0.1)
+        x, y = gdn.gdn_paged_shared_decode(*a, scale=0.1, min_bytes=0), gdn.gdn_paged_prefill(*b, scale=0.1)
     torch.cuda.synchronize()
     assert torch.equal(x, want[0]) and torch.equal(y, want[1])
 
@@ -254,9 +254,11 @@ def test_pools_beyond_four_gigabytes(gpu_lib):
     two = ints([[ids[1], ids[2], ids[0]], [ids[1], ids[2], ids[4]]])
     two_near = ints([[1, 2, 0], [1, 2, 4]])
     rest = q[:2].contiguous(), lens, ints([0, 2]), ints([128])
-    far = gdn.gdn_paged_shared_decode(rest[0], kc, vc, two, *rest[1:], scale=0.1)
-    assert torch.equal(far, gdn.gdn_paged_shared_decode(rest[0], sk, sv, two_near, *rest[1:],
-                                                        scale=0.1))
+    for least in (0, 2 ** 62):
+        far = gdn.gdn_paged_shared_decode(rest[0], kc, vc, two, *rest[1:], scale=0.1, min_bytes=least)
+        near = gdn.gdn_paged_shared_decode(rest[0], sk, sv, two_near, *rest[1:], scale=0.1,
+                                           min_bytes=least)
+        assert torch.equal(far, near)
 
 
 def test_states_fork_with_their_requests(gpu_lib):
