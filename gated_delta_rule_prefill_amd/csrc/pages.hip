@@ -280,29 +280,29 @@ __global__ __launch_bounds__(PG_THREADS) void compact_mark_kernel(CompactArgs a)
     });
 }
 
-// Movers and holes among the pages of one word, r of whose first page is `rank`.
-__device__ __forceinline__ void list_word(const CompactArgs& a, int64_t w, uint32_t bits, int rank,
-                                          int n, int r0) {
-    const int first = (int)(w * 32);
-    for (int b = 0; b < 32 && first + b < a.n_blocks; b++) {
-        const int id = first + b;
-        if ((bits >> b) & 1) {
-            if (id >= n && rank - r0 < a.max_copies) a.copy_src[rank - r0] = id;
-            rank++;
-        } else if (id < n && id - rank < a.max_copies) {
-            a.copy_dst[id - rank] = id;
-        }
-    }
-}
 __device__ __forceinline__ int bits_below(uint32_t bits, int b) {
     return __popc(bits & ((1u << b) - 1));
 }
 
-// A workgroup lists the pages of PG_THREADS words, and counts all words itself (4 KB of them for
-// 32768 pages, out of the L2) instead of waiting for a launch that would.
+// Page id's place in the lists, r(id) being `rank`.
+__device__ __forceinline__ void list_page(const CompactArgs& a, int id, bool live, int rank, int n,
+                                          int r0) {
+    if (live) {
+        if (id >= n && rank - r0 < a.max_copies) a.copy_src[rank - r0] = id;
+    } else if (id < n && id - rank < a.max_copies) {
+        a.copy_dst[id - rank] = id;
+    }
+}
+
+// A workgroup lists the pages of LIST_WORDS words, and counts all words itself (4 KB of them for
+// 32768 pages, out of the L2) instead of waiting for a launch that would. A thread takes a page at a
+// time: a word at a time, its pages one after another, 29000 pages took 8.5 us.
+constexpr int LIST_WORDS = 64;
 __global__ __launch_bounds__(PG_THREADS) void compact_list_kernel(CompactArgs a) {
     const int tid = threadIdx.x;
-    const int64_t w0 = (int64_t)blockIdx.x * PG_THREADS;
+    __shared__ uint32_t word[LIST_WORDS];
+    __shared__ int word_rank[LIST_WORDS];
+    const int64_t w0 = (int64_t)blockIdx.x * LIST_WORDS;
     int mine = 0, all = 0, base, n, below = 0, r0, unused;
     for (int64_t w = tid; w < a.words; w += PG_THREADS) {
         const int c = __popc(a.bits[w]);
@@ -315,13 +315,22 @@ __global__ __launch_bounds__(PG_THREADS) void compact_list_kernel(CompactArgs a)
         below += w < n >> 5 ? __popc(a.bits[w]) : bits_below(a.bits[w], n & 31);
     block_scan<PG_THREADS>(below, &r0);
     const int64_t w = w0 + tid;
-    const uint32_t bits = w < a.words ? a.bits[w] : 0;
+    const uint32_t bits = tid < LIST_WORDS && w < a.words ? a.bits[w] : 0;
     const int rank = base + block_scan<PG_THREADS>(__popc(bits), &unused);
-    if (w < a.words) {
-        a.rank[w] = rank;
-        list_word(a, w, bits, rank, n, r0);
+    if (tid < LIST_WORDS) {
+        word[tid] = bits;
+        word_rank[tid] = rank;
+        if (w < a.words) a.rank[w] = rank;
     }
-    for (int64_t k = (int64_t)(n - r0) + w; k < a.max_copies; k += (int64_t)gridDim.x * PG_THREADS) {
+    __syncthreads();
+    for (int i = tid; i < LIST_WORDS * 32; i += PG_THREADS) {
+        const int64_t id = w0 * 32 + i;
+        if (id >= a.n_blocks) break;
+        const uint32_t x = word[i >> 5];
+        list_page(a, (int)id, (x >> (i & 31)) & 1, word_rank[i >> 5] + bits_below(x, i & 31), n, r0);
+    }
+    for (int64_t k = (int64_t)(n - r0) + blockIdx.x * PG_THREADS + tid; k < a.max_copies;
+         k += (int64_t)gridDim.x * PG_THREADS) {
         a.copy_src[k] = -1;
         a.copy_dst[k] = -1;
     }
@@ -379,7 +388,11 @@ __global__ __launch_bounds__(COMPACT_ONE_THREADS) void compact_one_kernel(Compac
     block_scan<COMPACT_ONE_THREADS>(
         first + 32 <= n ? __popc(mine) : first < n ? bits_below(mine, n & 31) : 0, &r0);
     ranks[tid] = rank;
-    if (tid < a.words) list_word(a, tid, mine, rank, n, r0);
+    __syncthreads();
+    for (int id = tid; id < a.n_blocks; id += COMPACT_ONE_THREADS) {
+        const uint32_t x = bits[id >> 5];
+        list_page(a, id, (x >> (id & 31)) & 1, ranks[id >> 5] + bits_below(x, id & 31), n, r0);
+    }
     for (int64_t k = (int64_t)(n - r0) + tid; k < a.max_copies; k += COMPACT_ONE_THREADS) {
         a.copy_src[k] = -1;
         a.copy_dst[k] = -1;
@@ -484,7 +497,8 @@ hipError_t launch_paged_compact(const CompactArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(compact_mark_kernel, dim3(by_row), block, 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(compact_list_kernel, dim3(by_word), block, 0, s, a);
+    hipLaunchKernelGGL(compact_list_kernel, dim3((unsigned)((a.words + LIST_WORDS - 1) / LIST_WORDS)),
+                       block, 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(compact_rewrite_kernel, dim3(by_row), block, 0, s, a);
