@@ -91,6 +91,7 @@ def test_fork_of_nothing(gpu_lib):
 @pytest.mark.parametrize("rows,ends,block,hi,pool,cut", [
     (4, 1, 16, 90, 64, None), (30, 30, 8, 300, 2000, None), (30, 11, 8, 300, 2000, 17),
     (6, 3, 64, 5000, 70001, None), (400, 300, 8, 700, 40000, None), (500, 77, 4, 500, 66000, 1000),
+    (6, 3, 64, 5000, 32768, None), (6, 3, 64, 5000, 32769, None), (3, 2, 16, 8000, 9000, None),
 ])
 def test_free(gpu_lib, rows, ends, block, hi, pool, cut):
     say("free", rows, ends, block, hi, pool)
