@@ -1,7 +1,7 @@
 // Attention of many query rows over a paged key/value cache, grouped heads: the kernel of
 // gdn_paged_prefill (packed prompts, causal) and of the shared part of gdn_paged_shared_decode.
 //
-// Query rows that share a key/value head (tokens x group) are packed into tiles of A::ROWS rows, so
+// Query rows that share a key/value head (tokens x group) are packed into tiles of 128 or 256, so
 // that the keys are read once for all heads of a group, and a causal tile of few tokens reaches
 // little beyond its own diagonal. A tile and a key/value head make a unit; the 64-key steps
 // (32 in fp32) of all units are laid end to end and cut into equal runs, one per worker, one
@@ -14,10 +14,20 @@
 //   O^T += V^T P^T  the accumulator layout of S^T is the B operand's with the keys renumbered, so
 //                   weights stay in registers; V^T comes from transposing LDS reads (bf16) or
 //                   column reads (fp32).
-// Keys and values go from their pages straight into LDS, two buffers each, the keys one step ahead
-// of the values: a step's scores (matrix pipe) are formed beside the previous step's softmax
-// (vector pipe), with one barrier a step. Rows that do not exist are loaded from a row of zeros:
-// a zero weight would not cancel what a page's unused rows hold.
+// Keys and values go from their pages straight into LDS, two or three buffers each, the keys one
+// step ahead of the values: a step's scores (matrix pipe) are formed beside the previous step's
+// softmax (vector pipe), with one barrier a step. Rows that do not exist are loaded from a row of
+// zeros: a zero weight would not cancel what a page's unused rows hold.
+//
+// Bound (bf16): the matrix pipe at the clock that the chip keeps under this load. 12000 tokens, 32
+// heads, 8 KV heads, d = 128 (1.18 TFLOP): 1240-1290 us, 0.91-0.95 PFLOP/s (a 16384^3 product on the
+// same chips 1.37-1.57); counters: matrix pipe busy for half of the cycles, the vector pipe for as many,
+// LDS for 40 %; 1.8 GHz. With a quarter of the CUs at work a step takes 1.84 us instead of 2.28. Leaving
+// work out moves the time little: no tile loads 10 %, no exponentials 5 %, no score products 15 %. 24
+// turns of 3 to 1500 tokens behind up to 16000, 32 heads, 4 KV heads: 600-620 us, 0.76 PFLOP/s; 128
+// requests behind 32000 shared tokens 87 us, 0.77; groups of 6 behind 500 to 16000 tokens, 16 heads of
+// 256, 50 us. fp32 is bound by its matrix instructions (a step of 32 keys 1.8 us at d = 64 and full
+// tiles, by their rate).
 #pragma once
 #include "attn_launch.h"
 #include "gdn_common.h"
@@ -290,7 +300,8 @@ constexpr int ATTEND_ROWS = AttendTile<T, D>::WAVES * AttendTile<T, D>::WAVE_ROW
 // Positions in the stream that a unit has beyond its steps: its start and end take as long.
 constexpr int ATTEND_EXTRA = 2;
 // No worker is given fewer positions than this: a run's start, and the parts that a cut leaves to
-// be joined, cost as much.
+// be joined, cost as much (three turns of 5 to 200 tokens, fp32: 29.7 us a call with 1, 25.7 with 2,
+// 28.4 with 3, 30.7 with 4, 42.5 with 8).
 constexpr int ATTEND_MIN_RUN = 2;
 
 // The stream of all units (total positions per key/value head) cut over the workers.
