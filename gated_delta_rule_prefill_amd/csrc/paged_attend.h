@@ -496,7 +496,7 @@ void paged_attend_kernel(AttendArgs a) {
         int lim;  // keys that the row sees
         if constexpr (SHARED) {
             const int b = (int)a.by_pos((uint32_t)(u.token0 + tok));
-            lim = a.seq_lens[b] - a.n_pos + (u.token0 + tok - b * a.n_pos) + 1;
+            lim = max(a.seq_lens[b], 0) - a.n_pos + (u.token0 + tok - b * a.n_pos) + 1;
         } else {
             lim = u.pos0 + tok + 1;
         }

@@ -136,7 +136,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void shared_join_kernel(SharedDecodeA
         const int64_t slot = i == 0 ? (int64_t)a.at.workers + kvh * a.at.tiles + t : w0 + i;
         return prefix0 + (size_t)slot * ROWS + row % ROWS;
     };
-        join_rows<D, (D + 127) / 128, 4, JOIN_ROW_GROUPS>(
+    join_rows<D, (D + 127) / 128, 4, JOIN_ROW_GROUPS>(
         j, note.x + most, parts_of, at, (int)blockIdx.x % j.share, 0,
         [&](int row, int col, const float x[4]) {
             const int p = row / a.at.group, h = row - p * a.at.group;

@@ -538,7 +538,8 @@ int gdn_paged_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_
  * call writes into a page that another request reads. A fork of a hybrid request also needs its
  * linear layers' states: gdn_paged_copy copies slots of a state pool (one slot a page) as well.
  * Rows and pages outside their ranges are skipped, as slots are; lengths count as 0 when negative
- * and as max_blocks * block_size when longer. One call takes at most 2^24 rows. */
+ * and as max_blocks * block_size when longer. One call takes at most 2^24 rows. Calls that update
+ * the same table or the same shares follow one another. */
 
 /* Requests that continue others. Fork i gives row dst_rows[i] the first fork_lens[i] tokens of row
  * src_rows[i]: with whole = floor(fork_lens[i] / block_size), the entries 0 .. whole - 1 are
@@ -546,7 +547,8 @@ int gdn_paged_decode(const gdn_paged_dims_t* dims, const void* q, const void* k_
  * if tokens are left over, entry `whole` becomes the next id of free_blocks (handed out in the
  * order of the forks; -1 once they are used up, and -1 where the source's entry is null, which
  * takes none), and the page of the source with the left-over tokens is to be copied there. Entries
- * behind that stay as they are. A fork whose rows are out of [0, n_rows), or the same, is skipped.
+ * behind that stay as they are. What the row named before is overwritten, not freed: a request that
+ * held the row ends first (gdn_paged_free). A fork whose rows are out of [0, n_rows), or the same, is skipped.
  *   src_rows, dst_rows, fork_lens [n] int32 (device). dst_rows are distinct, and none of them is
  *              in src_rows (the debug library checks)
  *   block_table [n_rows, max_blocks] int32 (device), updated in place
@@ -625,7 +627,8 @@ int gdn_paged_shared_decode_workspace_bytes(const gdn_paged_dims_t* dims, int32_
  *               the last group share nothing
  *   prefix_lens [n_groups] int32 (device): the first prefix_lens[g] tokens of a group's requests
  *               lie in the same pages (any number, whole pages or not; those of the row of its
- *               first request are read). A request may be shorter (a padded row of length 0 too)
+ *               first request are read, whatever its own length). A request may be shorter (a
+ *               padded row of length 0 too)
  *   min_bytes   the prefixes are attended apart if that spares this many bytes of reads in all
  *               (sum over the groups of (size - 1) x prefix x 2 num_kv_heads d elements), else each
  *               request reads its own; negative: the library's rule (128 MiB; with fp32 256 MiB, and

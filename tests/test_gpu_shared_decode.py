@@ -118,6 +118,17 @@ def test_short_and_padded_requests(gpu_lib, dtype):
     assert bool((o[1] == 0).all()) and bool((o[2, 0] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_negative_lengths_count_as_none(gpu_lib, dtype):
+    """Down to the smallest number there is, also where several positions come before it."""
+    args = [x.to(DEV) for x in make(32, [4], [200], [5] * 5, 4, 8, 2, 64, 16, dtype)]
+    args[4][1], args[4][2] = 0, 0
+    want = gpu_lib.gdn_paged_shared_decode(*args, scale=0.125, min_bytes=0)
+    args[4][1], args[4][2] = -2 ** 31, -3
+    o = gpu_lib.gdn_paged_shared_decode(*args, scale=0.125, min_bytes=0)
+    assert bool((o[1:3] == 0).all()) and torch.equal(o, want)
+
+
 def test_null_pages(gpu_lib):
     args = make(24, [4], [128], [30] * 5, 1, 8, 4, 64, 16, BF16)
     args[3][:4, 2] = -1                        # of the prefix
