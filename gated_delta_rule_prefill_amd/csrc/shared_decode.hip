@@ -8,9 +8,10 @@
 //   o = (e^{m1 - M} acc1 + e^{m2 - M} acc2) / (e^{m1 - M} l1 + e^{m2 - M} l2).
 // Four launches: tables, prefixes, own keys, join.
 //
-// Bound: the prefixes by the matrix pipe (paged_attend.h), the own keys by the latency of their few
-// reads, the join by its parts. 128 requests, 32 heads, 8 KV heads, d = 128, behind one prefix of 32000
-// tokens, 1 to 100 tokens of their own, bf16: 4 + 87 + 37 + 17 us, 144-153 a call; gdn_paged_decode 619.
+// Bound: the prefixes by the matrix pipe (paged_attend.h), the own keys by HBM and their units'
+// starts, the join by its parts. 128 requests, 32 heads, 4 KV heads, d = 128, behind one prefix of 32000
+// tokens, 30 to 2000 tokens of their own, bf16: 4 + 87 + 37 + 17 us, 144-153 a call; gdn_paged_decode 619.
+// (Own keys of up to 128 or 256 tokens taken by a wave alone, without a cut or a merge: no quicker.)
 // 48 requests of 4 positions, 16 heads of 256, in 8 groups behind 500 to 16000 tokens: 4 + 51 + 20 + 14
 // us, 88 a call; gdn_paged_decode 105.
 #include "paged_attend.h"
