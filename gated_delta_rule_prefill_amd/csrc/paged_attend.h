@@ -304,20 +304,21 @@ constexpr int ATTEND_EXTRA = 2;
 // 28.4 with 3, 30.7 with 4, 42.5 with 8).
 constexpr int ATTEND_MIN_RUN = 2;
 
-// The stream of all units (total positions per key/value head) cut over the workers.
+// The stream of all units (total positions) cut over the workers, the longer runs spread evenly
+// among them: where units are equally long and their number divides the workers', as with one
+// prefix that all share, the tiles of a head are cut alike, and the workers that read the same
+// keys do so at the same time.
 struct AttendCut {
-    int64_t each;
-    int n, more;
+    int64_t total;
+    int n;
     __device__ __forceinline__ static AttendCut of(int64_t total, int workers) {
-        int64_t n = (total + ATTEND_MIN_RUN - 1) / ATTEND_MIN_RUN;
-        n = n < workers ? n : workers;
-        if (n == 0) return {0, 0, 0};
-        return {total / n, (int)n, (int)(total % n)};
+        const int64_t n = (total + ATTEND_MIN_RUN - 1) / ATTEND_MIN_RUN;
+        return {total, (int)(n < workers ? n : workers)};
     }
-    __device__ __forceinline__ int64_t start(int w) const { return w * each + min(w, more); }
+    __device__ __forceinline__ int64_t start(int w) const { return w * total / n; }
+    // the last w with start(w) <= x
     __device__ __forceinline__ int owner(int64_t x) const {
-        const int64_t big = more * (each + 1);
-        return (int)(x < big ? x / (each + 1) : more + (x - big) / each);
+        return (int)(((x + 1) * n - 1) / total);
     }
 };
 
