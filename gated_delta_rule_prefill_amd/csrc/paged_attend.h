@@ -20,12 +20,12 @@
 // zeros: a zero weight would not cancel what a page's unused rows hold.
 //
 // Bound (bf16): the matrix pipe at the clock that the chip keeps under this load. 12000 tokens, 32
-// heads, 8 KV heads, d = 128 (1.18 TFLOP): 1240-1290 us, 0.91-0.95 PFLOP/s (a 16384^3 product on the
+// heads, 8 KV heads, d = 128 (1.18 TFLOP): 1230-1290 us, 0.91-0.96 PFLOP/s (a 16384^3 product on the
 // same chips 1.37-1.57); counters: matrix pipe busy for half of the cycles, the vector pipe for as many,
 // LDS for 40 %; 1.8 GHz. With a quarter of the CUs at work a step takes 1.84 us instead of 2.28. Leaving
 // work out moves the time little: no tile loads 10 %, no exponentials 5 %, no score products 15 %. 24
 // turns of 3 to 1500 tokens behind up to 16000, 32 heads, 4 KV heads: 600-620 us, 0.76 PFLOP/s; 128
-// requests behind 32000 shared tokens 87 us, 0.77; groups of 6 behind 500 to 16000 tokens, 16 heads of
+// requests behind 32000 shared tokens 85 us, 0.8; groups of 6 behind 500 to 16000 tokens, 16 heads of
 // 256, 50 us. fp32 is bound by its matrix instructions (a step of 32 keys 1.8 us at d = 64 and full
 // tiles, by their rate).
 #pragma once

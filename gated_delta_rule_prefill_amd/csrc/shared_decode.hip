@@ -10,7 +10,7 @@
 //
 // Bound: the prefixes by the matrix pipe (paged_attend.h), the own keys by HBM and their units'
 // starts, the join by its parts. 128 requests, 32 heads, 4 KV heads, d = 128, behind one prefix of 32000
-// tokens, 30 to 2000 tokens of their own, bf16: 4 + 87 + 37 + 17 us, 144-153 a call; gdn_paged_decode 619.
+// tokens, 30 to 2000 tokens of their own, bf16: 4 + 85 + 37 + 17 us, 141-151 a call; gdn_paged_decode 619.
 // (Own keys of up to 128 or 256 tokens taken by a wave alone, without a cut or a merge: no quicker.)
 // 48 requests of 4 positions, 16 heads of 256, in 8 groups behind 500 to 16000 tokens: 4 + 51 + 20 + 14
 // us, 88 a call; gdn_paged_decode 105.
