@@ -156,11 +156,28 @@ template <int D> struct AttendTile<bf16, D> {
             }
         }
     }
-    // acc += V^T P^T for the weights s. The weights are rounded to bf16 (2^-8 of each at most) as
-    // the MFMA's operand. Those of the second half of the keys may be formed in beside(m) until
-    // m = VALUE_MFMAS * 5 / 8.
+    // l + the weights p.
+    __device__ __forceinline__ static float add(const bf16x8& p, float l) {
+        typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const bf16x2 ones = {(bf16)1.f, (bf16)1.f};
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+            l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{p[i], p[i + 1]}, ones, l, false);
+        return l;
+    }
+    // acc += V^T P^T for the weights s, l += their sum. The weights are rounded to bf16 (2^-8 of
+    // each at most) as the MFMA's operand, and the sum takes them as rounded: what is left of the
+    // roundings is weighted by a value's distance from the output, so that a weight that outweighs
+    // the others has none (relative 2-norm errors 0.0017-0.0021 where one rounding of the outputs
+    // leaves 0.0016-0.0017, 0.0017-0.0022 with the sum of the weights before rounding; 1 % of a
+    // call's time). To keep all of a weight costs more than it gives: as the sum of two bf16
+    // numbers 0.00165, but 12000 tokens take 1670 us instead of 1303, 128 requests behind 32000
+    // tokens 172 instead of 151; with the second part in 6 bits, whose products are a quarter as
+    // dear but want the values in 6 bits too, 1641 and 176.
+    // Weights of the second half of the keys may be formed in beside(m) until m = VALUE_MFMAS * 5 / 8.
     template <typename Beside>
-    __device__ __forceinline__ void values(uint32_t vt, int lane, Scores& s, Beside beside) {
+    __device__ __forceinline__ void values(uint32_t vt, int lane, Scores& s, float& l,
+                                           Beside beside) {
         const uint32_t at = value_place(vt, lane);
         bf16x8 p;
 #pragma unroll
@@ -169,6 +186,7 @@ template <int D> struct AttendTile<bf16, D> {
             if (n % NO == 0)
 #pragma unroll
                 for (int i = 0; i < 8; i++) p[i] = (bf16)s.get(n / NO * 8 + i);
+            if (n % NO == NO - 1) l = add(p, l);
             acc[n % NO] = mma(vf[n % (AHEAD + 1)], p, acc[n % NO]);
             beside(n);
             __builtin_amdgcn_sched_barrier(0);
@@ -255,7 +273,11 @@ template <int D> struct AttendTile<float, D> {
     // A step's sums are formed by themselves and added once: a long sequence is then summed in
     // two levels, and the roundings of n / 32 additions reach a result instead of those of n / 4.
     template <typename Beside>
-    __device__ __forceinline__ void values(uint32_t vt, int lane, Scores& s, Beside) {
+    __device__ __forceinline__ void values(uint32_t vt, int lane, Scores& s, float& l, Beside) {
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < N; n++) sum += s.get(n);
+        l += sum;
         constexpr int JN = 2;  // columns of tiles on their way
         const uint32_t at = vt + (lane >> 4) * 4 * ROW + (lane & 15) * 4;
 #pragma unroll
@@ -633,7 +655,7 @@ void paged_attend_kernel(AttendArgs a) {
                     if (m == MS - 2) x.start_values(vt, lane);
                 });
                 if (c + 1 < mine) mask(c + 1, next);
-                x.values(vt, lane, s, [&](int m) {
+                x.values(vt, lane, s, l, [&](int m) {
                     constexpr int L = MV * 5 / 8, HALF = MV / 2;
                     if (m < L)
 #pragma unroll
@@ -641,11 +663,6 @@ void paged_attend_kernel(AttendArgs a) {
                     if (m < HALF) {
                         top = largest(next, m * N / HALF, (m + 1) * N / HALF, top);
                         asm volatile("" : "+v"(top));
-                    } else {
-#pragma unroll
-                        for (int n = (m - HALF) * N / HALF; n < (m + 1 - HALF) * N / HALF; n++)
-                            l += s.get(n);
-                        asm volatile("" : "+v"(l));
                     }
                     if (m == HALF + 1) top = X::max_partners(top) * cs;
                     if (LEAD > 0 && m == MV - 2) x.start_keys(keys_at(c + 2), lane);
@@ -655,11 +672,7 @@ void paged_attend_kernel(AttendArgs a) {
                 for (int n = 0; n < N; n++) weight(s, n);
                 x.scores(kt, lane, next, [](int) {});
                 if (c + 1 < mine) mask(c + 1, next);
-                x.values(vt, lane, s, [](int) {});
-                float sum = 0.f;  // (as the values: a step's by themselves)
-#pragma unroll
-                for (int n = 0; n < N; n++) sum += s.get(n);
-                l += sum;
+                x.values(vt, lane, s, l, [](int) {});
                 top = X::max_partners(largest(next, 0, N, top)) * cs;
             }
             if (c + 1 < mine) refer(top);
