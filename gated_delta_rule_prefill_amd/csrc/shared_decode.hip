@@ -77,8 +77,28 @@ __global__ __launch_bounds__(AT_TABLE_THREADS) void shared_tables_kernel(SharedD
             a.at, ROWS, X::KB, [&](int g) { return apart ? shared_group(a, g).size * per_request : 0; },
             [&](int g, int row0) {
                 const SharedGroup s = shared_group(a, g);
-                return AttendUnit{s.first, s.first * a.at.n_pos, row0, s.size * per_request,
-                                  s.prefix, 0};
+                const int rows = s.size * per_request;
+                // The tile reads the table row of its first request that holds the whole prefix, or
+                // of its longest one, behind whose tokens none of the tile's rows sees a key: a
+                // request that ended has no pages any more.
+                const int b0 = s.first + row0 / per_request;
+                const int b1 = s.first + (row0 + min(ROWS, rows - row0) - 1) / per_request;
+                int holder = b0, held = 0;
+                constexpr int U = 8;  // lengths on their way
+                for (int b = b0; b <= b1 && held < s.prefix; b += U) {
+                    int n[U];
+#pragma unroll
+                    for (int k = 0; k < U; k++) n[k] = a.at.seq_lens[min(b + k, b1)];
+#pragma unroll
+                    for (int k = 0; k < U; k++) {
+                        n[k] = min(max(n[k], 0), s.prefix);
+                        if (n[k] > held) {
+                            holder = min(b + k, b1);
+                            held = n[k];
+                        }
+                    }
+                }
+                return AttendUnit{holder, s.first * a.at.n_pos, row0, rows, max(held, 1), 0};
             });
         return;
     }

@@ -751,7 +751,7 @@ def gdn_paged_shared_decode(q, k_cache, v_cache, block_table, seq_lens, group_cu
                             scale=1.0, min_bytes=-1, o=None, workspace=None, stream=None):
     """gdn_paged_decode for a batch in which groups of requests share a prefix, read once for the
     group: requests group_cu[g] .. group_cu[g + 1] - 1 ([groups + 1] int32) hold the same pages for
-    their first prefix_lens[g] tokens ([groups] int32). Where that spares less than min_bytes of
+    their first prefix_lens[g] tokens ([groups] int32), or fewer of them, or have ended. Where that spares less than min_bytes of
     reads (negative: the library's rule) each request reads its own. Returns o, shaped as q."""
     shape, dt = q.shape, q.dtype
     if len(shape) == 3:  # one position per request

@@ -626,9 +626,9 @@ int gdn_paged_shared_decode_workspace_bytes(const gdn_paged_dims_t* dims, int32_
  *               requests group_cu[g] .. group_cu[g + 1] - 1. Requests before the first and behind
  *               the last group share nothing
  *   prefix_lens [n_groups] int32 (device): the first prefix_lens[g] tokens of a group's requests
- *               lie in the same pages (any number, whole pages or not; those of the row of its
- *               first request are read, whatever its own length). A request may be shorter (a
- *               padded row of length 0 too)
+ *               lie in the same pages (any number, whole pages or not). A request may be shorter,
+ *               or have ended (length 0, its entries null): the pages are taken from the rows of
+ *               requests that hold all of the prefix, or of the longest where none does
  *   min_bytes   the prefixes are attended apart if that spares this many bytes of reads in all
  *               (sum over the groups of (size - 1) x prefix x 2 num_kv_heads d elements), else each
  *               request reads its own; negative: the library's rule (128 MiB; with fp32 256 MiB, and
