@@ -434,7 +434,8 @@ __global__ __launch_bounds__(PG_THREADS) void paged_copy_kernel(CopyArgs a, int 
     for (int64_t x = blockIdx.x; x < items; x += gridDim.x) {
         const int i = (int)(x / chunks);
         const int src = a.src[i], dst = a.dst[i];
-        if (src < 0 || src >= a.n_blocks || dst < 0 || dst >= a.n_blocks) continue;
+        // (a page onto itself is left alone: another pair may be writing it)
+        if (src < 0 || src >= a.n_blocks || dst < 0 || dst >= a.n_blocks || src == dst) continue;
         const int64_t p0 = (x - (int64_t)i * chunks) * COPY_PIECES + threadIdx.x;
         const i32x4* from = reinterpret_cast<const i32x4*>(pool + src * a.page_bytes);
         i32x4* to = reinterpret_cast<i32x4*>(pool + dst * a.page_bytes);

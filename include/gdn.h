@@ -609,8 +609,9 @@ int gdn_paged_compact(const int32_t* seq_lens, int32_t n_rows, int32_t* block_ta
 /* Copies pages copy_src[i] to pages copy_dst[i] within each of several pools, in one launch.
  *   caches     [n_caches] HOST array of device pointers, each to n_blocks pages of page_bytes
  *              bytes (a multiple of 16): key, value or latent caches of the layers, or state pools
- *   copy_src, copy_dst [n] int32 (device). A pair with a page outside [0, n_blocks) is skipped.
- *              Destinations are distinct and no source is one (the debug library checks)
+ *   copy_src, copy_dst [n] int32 (device). A pair with a page outside [0, n_blocks), or of one
+ *              page with itself, is skipped. Of the others, destinations are distinct and no source
+ *              is one (the debug library checks)
  *   count      [1] int32 (device) or NULL: pairs from *count on are not looked at */
 int gdn_paged_copy(void* const* caches, int32_t n_caches, int64_t page_bytes, int32_t n_blocks,
                    const int32_t* copy_src, const int32_t* copy_dst, int32_t n,
