@@ -325,6 +325,7 @@ constexpr int ATTEND_EXTRA = 2;
 // be joined, cost as much (three turns of 5 to 200 tokens, fp32: 29.7 us a call with 1, 25.7 with 2,
 // 28.4 with 3, 30.7 with 4, 42.5 with 8).
 constexpr int ATTEND_MIN_RUN = 2;
+static_assert(ATTEND_MIN_RUN <= ATTEND_EXTRA, "a stream of one unit has a run");
 
 // The stream of all units (total positions) cut over the workers, the longer runs spread evenly
 // among them: where units are equally long and their number divides the workers', as with one
@@ -334,7 +335,7 @@ struct AttendCut {
     int64_t total;
     int n;
     __device__ __forceinline__ static AttendCut of(int64_t total, int workers) {
-        const int64_t n = (total + ATTEND_MIN_RUN - 1) / ATTEND_MIN_RUN;
+        const int64_t n = total / ATTEND_MIN_RUN;  // (a unit alone has ATTEND_EXTRA positions)
         return {total, (int)(n < workers ? n : workers)};
     }
     __device__ __forceinline__ int64_t start(int w) const { return w * total / n; }
