@@ -19,15 +19,18 @@
 // softmax (vector pipe), with one barrier a step. Rows that do not exist are loaded from a row of
 // zeros: a zero weight would not cancel what a page's unused rows hold.
 //
-// Bound (bf16): the matrix pipe at the clock that the chip keeps under this load. 12000 tokens, 32
-// heads, 8 KV heads, d = 128 (1.18 TFLOP): 1230-1290 us, 0.91-0.96 PFLOP/s (a 16384^3 product on the
-// same chips 1.37-1.57); counters: matrix pipe busy for half of the cycles, the vector pipe for as many,
-// LDS for 40 %; 1.8 GHz. With a quarter of the CUs at work a step takes 1.84 us instead of 2.28. Leaving
-// work out moves the time little: no tile loads 10 %, no exponentials 5 %, no score products 15 %. 24
-// turns of 3 to 1500 tokens behind up to 16000, 32 heads, 4 KV heads: 600-620 us, 0.76 PFLOP/s; 128
-// requests behind 32000 shared tokens 85 us, 0.8; groups of 6 behind 500 to 16000 tokens, 16 heads of
-// 256, 50 us. fp32 is bound by its matrix instructions (a step of 32 keys 1.8 us at d = 64 and full
-// tiles, by their rate).
+// Bound (bf16): by no unit alone. 12000 tokens, 32 heads, 8 KV heads, d = 128 (1.18 TFLOP): 1250-1360
+// us, 0.87-0.94 PFLOP/s (a 16384^3 product on the same chips 1.37-1.57); counters: matrix pipe busy for
+// 49 % of the cycles, the vector pipe for 47 %, LDS for 39 %. A step is 2048 cycles of matrix work a SIMD
+// and takes 4200, at 1.8 GHz with all CUs at work (2.28 us) as at the higher clock of a quarter of them
+// (1.84 us): both waves of a SIMD pass the same barrier and are in the same phase, so that a step's
+// scores, softmax and values wait for each other. Leaving work out therefore moves the time little: no
+// tile loads 10 %, no exponentials 5 %, no score products 15 %; more of it adds its part (products for
+// the rests of the weights 16 %, forming those 7 %). 24 turns of 3 to 1500 tokens behind up to 16000,
+// 32 heads, 4 KV heads: 610-665 us, 0.70-0.77 PFLOP/s; 128 requests behind 32000 shared tokens 84-89
+// us, 0.8 (matrix pipe 40 %); groups of 6 behind 500 to 16000 tokens, 16 heads of 256, 52-53 us (18 %: one
+// wave a SIMD, and second tiles of few rows that take a whole unit's steps). fp32 is bound by its
+// matrix instructions (a step of 32 keys 1.8 us at d = 64 and full tiles, by their rate).
 #pragma once
 #include "attn_launch.h"
 #include "gdn_common.h"
@@ -323,7 +326,7 @@ constexpr int ATTEND_ROWS = AttendTile<T, D>::WAVES * AttendTile<T, D>::WAVE_ROW
 constexpr int ATTEND_EXTRA = 2;
 // No worker is given fewer positions than this: a run's start, and the parts that a cut leaves to
 // be joined, cost as much (three turns of 5 to 200 tokens, fp32: 29.7 us a call with 1, 25.7 with 2,
-// 28.4 with 3, 30.7 with 4, 42.5 with 8).
+// 28.4 with 3, 30.7 with 4, 42.5 with 8; not measured elsewhere: longer streams have longer runs).
 constexpr int ATTEND_MIN_RUN = 2;
 static_assert(ATTEND_MIN_RUN <= ATTEND_EXTRA, "a stream of one unit has a run");
 
@@ -621,7 +624,7 @@ void paged_attend_kernel(AttendArgs a) {
         int page = 0;
         // One step: the weights of s (masked, their references known), its values added; meanwhile
         // the next step's scores and their maximum. Beside the MFMAs of the scores go 5 in 8 of the
-        // weights, beside those of the values the others, the maximum and the sums: about as many
+        // weights, beside those of the values the others, the sums and the maximum: about as many
         // cycles of the vector pipe as of the matrix pipe in both halves.
         auto step = [&](int c, Scores& s, Scores& next) {
             lds_loads_done();

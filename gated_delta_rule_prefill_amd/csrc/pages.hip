@@ -60,9 +60,9 @@ inline unsigned row_pieces_grid(int64_t n, int max_blocks) {
 // entered into row dst and each page named by one has a holder more; with x mod b > 0 entry
 // `whole` becomes the next page of the free list, and (source page, new page) a copy to make.
 //
-// Bound: launch latency (8 bytes an entry). Measured: 4 forks of 1000 tokens 3.4 us; 256 forks of 100
-// to 20000 tokens 5 us a call beside 49 for their copies. So one launch: the first workgroup deals out the free
-// pages, which takes a prefix sum over the forks; the others share whole pages, which takes none.
+// Bound: launch latency (8 bytes an entry). Measured: 4 forks of 1000 tokens 3.3 us; 256 forks of 100
+// to 20000 tokens 5.2 us beside 49 for their copies. So one launch: the first workgroup deals out the
+// free pages, which takes a prefix sum over the forks; the others share whole pages, which takes none.
 // The counts are atomic additions of whole numbers, whose order does not matter.
 __global__ __launch_bounds__(PG_THREADS) void paged_fork_kernel(ForkArgs a) {
     const int tid = threadIdx.x;
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(PG_THREADS) void paged_fork_kernel(ForkArgs a) {
 // all counts in the order of the ids, set it to zero again.
 //
 // Bound: launch latency, and the pool's counts (4 bytes a page). Measured: 256 requests, 70000 entries,
-// a pool of 300000 pages 6.5 + 2.6 + 4.3 us; one request of 9000 tokens, 9000 pages 7.1.
+// a pool of 300000 pages 7.2 + 2.8 + 4.4 us; one request of 9000 tokens, 9000 pages 7.4.
 __device__ __forceinline__ void drop_entry(const FreeArgs& a, int32_t* entry) {
     const int page = atomicExch(entry, -1);
     if (page >= 0 && page < a.n_blocks) atomicSub(a.shares + page, 1);
@@ -246,7 +246,8 @@ __global__ __launch_bounds__(FREE_ONE_THREADS) void paged_free_one_kernel(FreeAr
 // the copies do not depend on each other.
 //
 // Bound: launch latency and the table (4 bytes an entry, read twice). Measured: 120 rows, 29000 pages
-// 2 + 5.3 + 5.6 + 4 us in the four launches below; 10 rows, 600 pages 8.0 in one. U is a bit per page in the
+// 4.3 + 6 + 5.7 + 4.8 us in the four launches below (least 1.8 + 5.6 + 5.2 + 3.8); 10 rows, 600 pages 8.3
+// in one. U is a bit per page in the
 // workspace: cleared, marked from the table, counted and listed, and the table rewritten, each in
 // a launch of its own, since each needs all of the one before.
 __global__ __launch_bounds__(PG_THREADS) void compact_clear_kernel(CompactArgs a) {
@@ -299,7 +300,8 @@ __device__ __forceinline__ void list_page(const CompactArgs& a, int id, bool liv
 }
 
 // A workgroup lists the pages of LIST_WORDS words, and counts all words itself (4 KB of them for
-// 32768 pages, out of the L2) instead of waiting for a launch that would. A thread takes a page at a
+// 32768 pages, out of the L2) instead of waiting for a launch that would: reads that grow with the
+// square of the pool, for a million pages 512 workgroups of 128 KB. A thread takes a page at a
 // time: a word at a time, its pages one after another, 29000 pages took 8.5 us.
 constexpr int LIST_WORDS = 64;
 __global__ __launch_bounds__(PG_THREADS) void compact_list_kernel(CompactArgs a) {
@@ -421,8 +423,8 @@ __global__ __launch_bounds__(COMPACT_ONE_THREADS) void compact_one_kernel(Compac
 
 // ------------------------------------------------------------------------------------ copy
 // Pages copied within each of up to COPY_CACHES pools, 16 bytes a thread at a time. Bound: HBM.
-// Measured: 6300 pages of 16 KiB in 4 pools (826 MB read and written) 157 us, 5.2 TB/s, which is what
-// a large copy reaches.
+// Measured: 6300 pages of 16 KiB in 4 pools (826 MB read and written) 152-160 us, 5.2-5.4 TB/s, which is
+// what a large copy reaches.
 constexpr int COPY_PER = 4;                              // 16-byte pieces of a thread on their way
 constexpr int COPY_PIECES = PG_THREADS * COPY_PER;       // pieces a workgroup takes at a time
 

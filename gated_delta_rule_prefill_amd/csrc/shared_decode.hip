@@ -8,12 +8,13 @@
 //   o = (e^{m1 - M} acc1 + e^{m2 - M} acc2) / (e^{m1 - M} l1 + e^{m2 - M} l2).
 // Four launches: tables, prefixes, own keys, join.
 //
-// Bound: the prefixes by the matrix pipe (paged_attend.h), the own keys by HBM and their units'
-// starts, the join by its parts. 128 requests, 32 heads, 4 KV heads, d = 128, behind one prefix of 32000
-// tokens, 30 to 2000 tokens of their own, bf16: 4 + 85 + 37 + 17 us, 141-151 a call; gdn_paged_decode 619.
+// Bound: the prefixes by their steps (paged_attend.h), the own keys by HBM and their units' starts,
+// the join by its parts. 128 requests, 32 heads, 4 KV heads, d = 128, behind one prefix of 32000
+// tokens, 30 to 2000 tokens of their own, bf16: 6 + 89 + 40 + 21 us (least 5 + 84 + 38 + 18), 145-153 a
+// call; gdn_paged_decode 619.
 // (Own keys of up to 128 or 256 tokens taken by a wave alone, without a cut or a merge: no quicker.)
-// 48 requests of 4 positions, 16 heads of 256, in 8 groups behind 500 to 16000 tokens: 4 + 51 + 20 + 14
-// us, 88 a call; gdn_paged_decode 105.
+// 48 requests of 4 positions, 16 heads of 256, in 8 groups behind 500 to 16000 tokens: 6 + 53 + 20 + 13
+// us, 88-90 a call; gdn_paged_decode 105.
 #include "paged_attend.h"
 
 namespace gdn {
@@ -22,7 +23,7 @@ namespace {
 
 // Workgroups of the joining launch a CU, and groups of lanes that share a row of up to 32 parts (128
 // requests, 17 parts a row: 148 us a call with 8 and 4, 157 with 16 and 4, 153 with 8 and 2, 151 with
-// 16 and 8).
+// 16 and 8; rows of other numbers of parts were not measured).
 constexpr int JOIN_WGS = 8, JOIN_ROW_GROUPS = 4;
 
 // Prefixes are attended apart where that spares reads of so many bytes in all: the prefix kernel's
@@ -31,6 +32,13 @@ constexpr int JOIN_WGS = 8, JOIN_ROW_GROUPS = 4;
 // 4 heads of 128, 59 MB 29 and 23, 235 MB 36 and 49; 4 groups of 2, 134 MB 49 and 53; 64 requests, 4
 // heads, 132 MB 42 and 23, 529 MB 49 and 49, 2114 MB 62 and 156; 7 requests, 4 heads of 64, 101 MB 27
 // and 28. fp32: 8 requests, 8 heads of 128, 235 MB 49 and 48, 940 MB 100 and 146.
+// Bytes alone do not tell the two apart: what many requests read again comes out of the caches
+// faster, so that 32 to 128 requests are better apart from about 250 to 500 MB on only, and are up to
+// 1.4 times slower by this rule in between (4 heads of 128: 32 requests behind 4096 tokens 40 and 39,
+// 64 behind 2048 46 and 34, 128 behind 1024 43 and 36; 64, 2 heads of 256, behind 2048 43 and 40). A caller
+// that knows its batch names min_bytes. Not apart, a call takes 5 to 7 us more than gdn_paged_decode
+// (tables, an empty prefix launch, a join of units that need none: 8 requests behind 512 tokens 17
+// and 11, 64 behind 4096 50 and 44).
 constexpr int64_t SHARED_LEAST_BF16 = (int64_t)128 << 20, SHARED_LEAST_F32 = (int64_t)256 << 20;
 // In fp32 a wave's 16 rows take as long as the reads of several requests: 4 groups of 2 requests (16
 // rows), 268 MB, 166 us apart, 92 not; 8 requests (64 rows), 470 MB, 69 and 82.

@@ -722,8 +722,8 @@ def gdn_paged_compact(seq_lens, block_table, block_size, shares, max_copies=None
 def gdn_paged_copy(caches, copy_src, copy_dst, count=None, stream=None):
     """Pages copy_src[i] copied to pages copy_dst[i] ([n] int32; -1, or the same: none) within each of
     the caches: contiguous tensors of one length (pages) and one number of bytes a page, of any type
-    and shape (key, value and latent caches, state pools). count [1] int32 on the GPU, or None:
-    pairs from it on are not looked at."""
+    and shape (key, value and latent caches, state pools), GDN_COPY_MAX_CACHES of them at most. count
+    [1] int32 on the GPU, or None: pairs from it on are not looked at."""
     n, dev = copy_src.numel(), _gpu(copy_src)
     addresses, like = [], None
     for c in caches:
