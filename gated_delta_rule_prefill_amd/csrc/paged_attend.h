@@ -22,9 +22,9 @@
 // Bound (bf16): by no unit alone. 12000 tokens, 32 heads, 8 KV heads, d = 128 (1.18 TFLOP): 1250-1360
 // us, 0.87-0.94 PFLOP/s (a 16384^3 product on the same chips 1.37-1.57); counters: matrix pipe busy for
 // 49 % of the cycles, the vector pipe for 47 %, LDS for 39 %. A step is 2048 cycles of matrix work a SIMD
-// and takes 4200, at 1.8 GHz with all CUs at work (2.28 us) as at the higher clock of a quarter of them
-// (1.84 us): both waves of a SIMD pass the same barrier and are in the same phase, so that a step's
-// scores, softmax and values wait for each other. Leaving work out therefore moves the time little: no
+// and takes 4200 (2.28 us at the 1.8 GHz of a full chip; with a quarter of the CUs at work 1.84 us, which
+// is as many at 2.3 GHz): both waves of a SIMD pass the same barrier and are in the same phase, so that
+// a step's scores, softmax and values wait for each other. Leaving work out therefore moves the time little: no
 // tile loads 10 %, no exponentials 5 %, no score products 15 %; more of it adds its part (products for
 // the rests of the weights 16 %, forming those 7 %). 24 turns of 3 to 1500 tokens behind up to 16000,
 // 32 heads, 4 KV heads: 610-665 us, 0.70-0.77 PFLOP/s; 128 requests behind 32000 shared tokens 84-89

@@ -122,7 +122,8 @@ def prefill(q, k_cache, v_cache, table, cu, lens, scale):
 
 def shared_decode(q, k_cache, v_cache, table, lens, group_cu, prefix_lens, scale):
     """q [B, P, H, d]; the first prefix_lens[g] keys of a group's requests are those of the row of
-    the first request that holds them all, or of the longest. Returns (o, mean |v|, absolute score sums [B, P, H])."""
+    the first request that holds them all, or of the longest. Returns (o, mean |v|, absolute score
+    sums [B, P, H])."""
     q, kc, vc = _f64(q), _f64(k_cache), _f64(v_cache)
     table, lens = _i32(table).copy(), _i32(lens)
     B, P, H, d = q.shape
@@ -132,9 +133,9 @@ def shared_decode(q, k_cache, v_cache, table, lens, group_cu, prefix_lens, scale
     for g, x in enumerate(_i32(prefix_lens)):
         for b in range(int(group_cu[g]), int(group_cu[g + 1])):
             first[b], skip[b] = int(group_cu[g]), x
-        held = [min(max(int(lens[b]), 0), int(x)) for b in range(int(group_cu[g]), int(group_cu[g + 1]))]
-        if held:
-            first[int(group_cu[g]):int(group_cu[g + 1])] += held.index(max(held))
+        rows = slice(int(group_cu[g]), int(group_cu[g + 1]))
+        if rows.stop > rows.start:  # the first of those that hold the most of it
+            first[rows] += int(np.argmax(np.clip(lens[rows], 0, x)))
     o, mag, top = np.zeros_like(q), np.zeros_like(q), np.zeros((B, P, H))
     for b in range(B):
         n = int(lens[b])
